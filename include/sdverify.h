@@ -361,6 +361,116 @@ sd_status sd_attn_decode(const float *q, const void *k_cache, const void *v_cach
 sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, int64_t S_max, int64_t L, int32_t M,
                        const int32_t *path, const int32_t *count, sd_stream_t stream);
 
+/*
+ * A KV cache in pages, for a batch of sequences.  The pages name no such cache beyond the contiguous one of
+ * sd_kv_append / sd_attn_decode / sd_kv_commit, of which these calls are the batched form: several
+ * conversations share one pool, forks share pages, and a drafter's cache may be a window.
+ *
+ * sd_kv_pages (HOST struct, device pointers) describes one layer's pool.  Row r of page p, KV head h:
+ * D elements from p * page_stride + h * head_stride + r * row_stride (elements, multiples of 16 bytes, the same
+ * for k and v), 0 <= r < page_rows; either the heads' rows apart (head_stride >= page_rows * row_stride) or
+ * together (row_stride >= H_kv * head_stride).  page_rows is 8, 16, 32 or a multiple of 64; D 64, 128 or
+ * 256.  type: SD_KV_F16, SD_KV_BF16, or SD_KV_I8: int8 codes with one fp32 scale per row and head,
+ * k_scale / v_scale [n_pages][H_kv][page_rows] (16-byte aligned; ignored otherwise); value = code * scale.
+ *
+ * table int32 [B][width]: entry s of sequence b is the page of its rows [s * page_rows, (s+1) * page_rows),
+ * -1 where it holds none.  lens int32 [B]: committed rows.  n_new int32 [B] (or NULL: M for all): the
+ * new rows of each sequence, 0 <= n_new[b] <= M, at positions lens[b] .. lens[b] + n_new[b] - 1; a sequence with
+ * none is left alone.  refs int32 [n_pages]: how many table entries name each page; a page is free iff its count
+ * is 0.  All of these are device arrays, so that a whole cycle can be captured in a CUDA graph.
+ * B <= 1024 (else SD_EUNSUPPORTED); width * page_rows < 2^31 - 128.
+ *
+ * Every kernel checks lens, n_new and table entries against these bounds before it uses them: what fails is
+ * skipped (for the attention a missing page reads as zeros) and records SD_EDEVICE in the status word.
+ * The calls of one workspace are ordered on one stream; a graph that may run beside another call needs its own.
+ *
+ * sd_paged_append: k_new, v_new fp32, row i of sequence b at b * seq_stride + i * row_stride (elements,
+ * multiples of 4, 16-byte aligned), its H_kv heads of D contiguous: they may be columns of a fused projection.  Rounded to
+ * the nearest (even) fp16 / bf16; SD_KV_I8: scale = amax|x| / 127 per row and head, code = x / scale rounded half away
+ * from zero, 0 if the row is zero (the arithmetic of sd_rmsnorm_quant_acts per row of D); a row that holds a
+ * NaN or an infinity gets that as its scale.  M >= 1 of any size.
+ *
+ * sd_paged_attn: q, out fp32, row i of sequence b at b * seq_stride + i * row_stride, its H heads of D
+ * contiguous (H a multiple of H_kv; head h reads KV head h / (H / H_kv)); 1 <= M <= 16.  parent int32 [B][M]
+ * as for sd_attn_decode (NULL: chains).  Row i stands at position lens[b] + depth(i) (its index in a chain).
+ *   out[i][h] = sum_j softmax_j(q[i][h] . k_j / sqrt(D)) v_j
+ * over the committed rows and the new rows on i's path.  window > 0: of these only the rows whose position is
+ * greater than i's minus window, or less than sinks (StreamingLLM-style first tokens that stay visible); pages
+ * wholly behind the window and past the sinks are not read and may be released (sd_pages_trim).  Rows that a
+ * position does not see never reach its output, whatever they hold.  Rows n_new[b] .. M-1 of out are left
+ * as they were.  fp32 arithmetic; the same call on the same inputs repeats bit for bit, but the split over
+ * the keys follows the whole batch, so a sequence's last bits depend on its neighbours.
+ * workspace: sd_paged_attn_workspace_bytes, zero-filled by the caller once (counters that every call returns
+ * to zero, then scratch); one workspace serves every batch, context and type of the same D or smaller.
+ *
+ * sd_paged_commit: as sd_kv_commit for every sequence with count[b] >= 1: row lens[b] + path[b][t] moves to row
+ * lens[b] + t for t < count[b] (path int32 [B][M], increasing, path[b][0] >= 0, M <= 16; NULL: chains, nothing
+ * moves and M is unbounded), then lens[b] += count[b].  count[b] = 0 leaves the sequence alone; count[b] > M, a
+ * bad path or a missing page records SD_EDEVICE and leaves the sequence alone.
+ */
+typedef enum { SD_KV_F16 = 0, SD_KV_BF16 = 1, SD_KV_I8 = 2 } sd_kv_type;
+
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale; /* SD_KV_I8 */
+    int32_t type;
+    int32_t n_pages, page_rows, H_kv, D;
+    int64_t page_stride, head_stride, row_stride; /* elements */
+} sd_kv_pages;
+
+sd_status sd_paged_append(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
+                          const int32_t *n_new, int32_t B, int32_t M, const float *k_new, const float *v_new,
+                          int64_t seq_stride, int64_t row_stride, sd_stream_t stream);
+size_t sd_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D);
+sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
+                        const int32_t *n_new, int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride,
+                        int64_t q_row_stride, const int32_t *parent, int32_t window, int32_t sinks, float *out,
+                        int64_t out_seq_stride, int64_t out_row_stride, void *workspace, size_t ws_bytes,
+                        sd_stream_t stream);
+sd_status sd_paged_commit(const sd_kv_pages *pages, const int32_t *table, int32_t width, int32_t *lens, int32_t B,
+                          int32_t M, const int32_t *path, const int32_t *count, sd_stream_t stream);
+
+/*
+ * Pages of the pool: taking, sharing, releasing and moving them.  Sequences that share pages hold the same
+ * page in their tables; nothing writes to a page that another sequence holds, because sd_pages_reserve
+ * gives the writer a copy first.
+ *
+ * sd_pages_reserve: makes every slot that rows lens[b] .. lens[b] + n_new[b] - 1 touch a page that its
+ * sequence alone holds.  An empty slot takes a free page.  A slot whose page others hold too takes a free page,
+ * the rows below lens[b] are copied into it (the rest of it is left as it was), and the old page's count
+ * goes down; when all of a page's holders are in the call, the last of them (highest sequence) keeps it.  Free
+ * pages are taken lowest index first, in the order of (sequence, slot).  All or nothing: with fewer free pages
+ * than needed nothing changes and *missing (device) is how many were short; else *missing = 0.  All sequences of the
+ * table that may write to a shared page should be in one call, or in calls one after the other.
+ * sd_pages_fork: for i < n, sequence dst[i] becomes a copy of sequence src[i]: its own pages are released, the
+ * slots of src[i]'s committed rows are shared (counts + 1), lens is copied.  A source may be named many
+ * times; a dst named twice, or as a source too, and an index outside [0, B) are skipped and record SD_EDEVICE.
+ * sd_pages_free: for i < n, sequence seqs[i] releases the pages of its rows from keep[i] on (whole pages: slots
+ * s with s * page_rows >= keep[i]; keep NULL: all) and lens = min(lens, keep[i]).  A sequence may be named twice.
+ * After a commit, keep = lens gives back the pages of rejected drafts.
+ * sd_pages_trim: every sequence b < B releases the pages that lie wholly in [sinks, lens[b] - window + 1): rows
+ * that no later row of sd_paged_attn with that window and those sinks sees.
+ * sd_pages_compact: moves the live pages at index >= n_live = the number of live pages into the free ones below,
+ * both in increasing order; tables and counts follow, remap int32 [n_pages] receives each page's new index (-1:
+ * it was free) and *n_live the count, so that pages n_live .. n_pages-1 are free.
+ * Page contents (all layers) follow the tables: a pool of several layers calls sd_pages_reserve / _compact on
+ * the first and sd_pages_copy with the same workspace on the others, before the workspace is used again.
+ * workspace: sd_pages_workspace_bytes(n_pages, B, width), zero-filled by the caller once.
+ */
+size_t sd_pages_workspace_bytes(int32_t n_pages, int32_t B, int32_t width);
+sd_status sd_pages_reserve(const sd_kv_pages *pages, int32_t *refs, int32_t *table, int32_t width, const int32_t *lens,
+                           const int32_t *n_new, int32_t B, int32_t M, int32_t *missing, void *workspace,
+                           size_t ws_bytes, sd_stream_t stream);
+sd_status sd_pages_copy(const sd_kv_pages *pages, const void *workspace, size_t ws_bytes, sd_stream_t stream);
+sd_status sd_pages_fork(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens, int32_t B,
+                        int32_t page_rows, const int32_t *src, const int32_t *dst, int32_t n, sd_stream_t stream);
+sd_status sd_pages_free(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens, int32_t B,
+                        int32_t page_rows, const int32_t *seqs, const int32_t *keep, int32_t n, sd_stream_t stream);
+sd_status sd_pages_trim(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, const int32_t *lens, int32_t B,
+                        int32_t page_rows, int32_t window, int32_t sinks, sd_stream_t stream);
+sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *table, int32_t width, int32_t B,
+                           int32_t *remap, int32_t *n_live, void *workspace, size_t ws_bytes, sd_stream_t stream);
+
 sd_status sd_shortlist_build(const void *head_blocks, int64_t vocab, int64_t hidden, void *copy_blocks, float *bound,
                              float *wnorm, sd_stream_t stream);
 size_t sd_shortlist_workspace_bytes(int64_t vocab, int64_t hidden);

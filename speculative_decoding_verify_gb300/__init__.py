@@ -68,6 +68,13 @@ class SdDepthState(ctypes.Structure):
                 ("pause_left", ctypes.c_int32), ("misses", ctypes.c_int32)]
 
 
+class SdKvPages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("type", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_rows", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
 class SdError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {STATUS.get(code, code)} ({code})")
@@ -83,6 +90,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, I32, I64, U32, U64, F, SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int32, ctypes.c_int64,
                                            ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float, ctypes.c_size_t)
+        PG = ctypes.POINTER(SdKvPages)
         sig = {
             "sd_status_string": ([I], ctypes.c_char_p),
             "sd_abi_version": ([], I),
@@ -103,6 +111,17 @@ def lib():
             "sd_kv_append": ([P, P, I32, I32, I32, P, P, I64, I64, P], I),
             "sd_attn_decode": ([P, P, P, I32, I32, I32, I32, I64, I64, P, P, P, SZ, P], I),
             "sd_kv_commit": ([P, P, I32, I32, I64, I64, I32, P, P, P], I),
+            "sd_paged_append": ([PG, P, I32, P, P, I32, I32, P, P, I64, I64, P], I),
+            "sd_paged_attn_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+            "sd_paged_attn": ([PG, P, I32, P, P, I32, I32, I32, P, I64, I64, P, I32, I32, P, I64, I64, P, SZ, P], I),
+            "sd_paged_commit": ([PG, P, I32, P, I32, I32, P, P, P], I),
+            "sd_pages_workspace_bytes": ([I32, I32, I32], SZ),
+            "sd_pages_reserve": ([PG, P, P, I32, P, P, I32, I32, P, P, SZ, P], I),
+            "sd_pages_copy": ([PG, P, SZ, P], I),
+            "sd_pages_fork": ([P, I32, P, I32, P, I32, I32, P, P, I32, P], I),
+            "sd_pages_free": ([P, I32, P, I32, P, I32, I32, P, P, I32, P], I),
+            "sd_pages_trim": ([P, I32, P, I32, P, I32, I32, I32, I32, P], I),
+            "sd_pages_compact": ([PG, P, P, I32, I32, P, P, P, SZ, P], I),
             "sd_shortlist_build": ([P, I64, I64, P, P, P, P], I),
             "sd_shortlist_workspace_bytes": ([I64, I64], SZ),
             "sd_head_shortlist": ([P, P, P, P, I64, I64, P, P, I32, P, P, P, SZ, P], I),
@@ -285,6 +304,186 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, L: int, M: int, coun
     H_kv, S_max, D = k_cache.shape
     _check(lib().sd_kv_commit(_p(k_cache), _p(v_cache), H_kv, D, S_max, L, M, _p(path), _p(count), _stream()),
            "sd_kv_commit")
+
+
+# ---------------------------------------------------------------------------
+# a KV cache in pages
+# ---------------------------------------------------------------------------
+
+KV_F16, KV_BF16, KV_I8 = 0, 1, 2
+_KV_TYPES = {torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.int8: KV_I8}
+
+
+def _here(t, dtype, name, shape):
+    """The tensor's address: a contiguous tensor of that type and shape on the current device."""
+    if (t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda
+            or t.get_device() != torch.cuda.current_device()):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on the current CUDA device, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows_of(t, name, B, M, heads, D):
+    """(address, sequence stride, row stride) of fp32 rows [B][M][heads][D] whose heads are contiguous."""
+    sb, sm, sh, sd = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
+    if (t.dtype is not torch.float32 or tuple(t.shape) != (B, M, heads, D) or sd != 1 or (sh != D and heads > 1)
+            or not t.is_cuda or t.get_device() != torch.cuda.current_device()):
+        raise ValueError(f"{name}: expected fp32 {(B, M, heads, D)} with contiguous heads on the current CUDA device, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    # a dimension of one entry has no stride of its own
+    sm = sm if M > 1 else heads * D
+    return t.data_ptr(), sb if B > 1 else sm, sm
+
+
+class KvPages:
+    """One layer's pool of pages: k and v [n_pages][H_kv][page_rows][D], fp16, bf16 or int8, of the same
+    strides (the last one 1): views, so the rows of all heads may lie together ([n_pages][page_rows][H_kv][D]
+    permuted) or K and V beside each other.  int8 codes need k_scale and v_scale, fp32 [n_pages][H_kv][page_rows]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype or k.dtype not in _KV_TYPES:
+            raise ValueError("k and v: expected fp16, bf16 or int8 pages [n_pages][H_kv][page_rows][D] of one shape")
+        if not k.is_cuda or k.device != v.device:
+            raise ValueError("k and v: expected CUDA tensors on one device")
+        n, h, p, d = k.shape
+
+        def strides(t):  # a dimension of one entry has no stride of its own
+            s = list(t.stride())
+            s[2] = s[2] if p > 1 else d
+            s[1] = s[1] if h > 1 else max(s[2] * p, d)
+            s[0] = s[0] if n > 1 else max(s[1] * h, s[2] * p)
+            return s
+
+        s = strides(k)
+        if s != strides(v) or s[3] != 1:
+            raise ValueError("k and v: expected the same strides, the last one 1")
+        i8 = k.dtype is torch.int8
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if i8 and (t is None or t.dtype is not torch.float32 or tuple(t.shape) != (n, h, p)
+                       or not t.is_contiguous() or t.device != k.device):
+                raise ValueError(f"{name}: expected a contiguous fp32 tensor {(n, h, p)} beside the pages")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale if i8 else None, v_scale if i8 else None
+        self.n_pages, self.H_kv, self.page_rows, self.D = n, h, p, d
+        self.device_index = k.get_device()
+        self.desc = SdKvPages(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if i8 else None,
+                              v_scale.data_ptr() if i8 else None, _KV_TYPES[k.dtype], n, p, h, d, s[0], s[1], s[2])
+        self._ref = ctypes.byref(self.desc)
+
+    def _arg(self):
+        if self.device_index != torch.cuda.current_device():
+            raise ValueError("the pages are not on the current CUDA device")
+        return self._ref
+
+
+def _opt(t, dtype, name, shape):
+    return None if t is None else _here(t, dtype, name, shape)
+
+
+def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, pages: KvPages, table: torch.Tensor, lens: torch.Tensor,
+                 n_new: torch.Tensor | None = None):
+    """k_new, v_new fp32 [B][M][H_kv][D] (heads contiguous, other strides free) -> rows lens[b] .. of the pages
+    that table int32 [B][width] names; n_new int32 [B]: how many rows of each sequence (None: all M)."""
+    B, M = k_new.shape[:2]
+    w = table.shape[-1]
+    kp, sb, sm = _rows_of(k_new, "k_new", B, M, pages.H_kv, pages.D)
+    vp, vb, vm = _rows_of(v_new, "v_new", B, M, pages.H_kv, pages.D)
+    if (vb, vm) != (sb, sm):
+        raise ValueError("k_new and v_new: expected the same strides")
+    _check(lib().sd_paged_append(pages._arg(), _here(table, torch.int32, "table", (B, w)), w,
+                                 _here(lens, torch.int32, "lens", (B,)), _opt(n_new, torch.int32, "n_new", (B,)), B, M,
+                                 kp, vp, sb, sm, _stream()), "sd_paged_append")
+
+
+def paged_attn_workspace_bytes(B: int, M: int, H: int, H_kv: int, D: int) -> int:
+    return int(lib().sd_paged_attn_workspace_bytes(B, M, H, H_kv, D))
+
+
+def paged_attn(q: torch.Tensor, pages: KvPages, table: torch.Tensor, lens: torch.Tensor, out: torch.Tensor,
+               ws: torch.Tensor, n_new: torch.Tensor | None = None, parent: torch.Tensor | None = None,
+               window: int = 0, sinks: int = 0):
+    """q fp32 [B][M][H][D] -> out, over each sequence's lens[b] committed and n_new[b] new rows (chains, or trees by
+    parent int32 [B][M]); window > 0: only the rows less than window behind and the first sinks."""
+    B, M, H = q.shape[:3]
+    w = table.shape[-1]
+    qp, qb, qm = _rows_of(q, "q", B, M, H, pages.D)
+    op, ob, om = _rows_of(out, "out", B, M, H, pages.D)
+    _check(lib().sd_paged_attn(pages._arg(), _here(table, torch.int32, "table", (B, w)), w,
+                               _here(lens, torch.int32, "lens", (B,)), _opt(n_new, torch.int32, "n_new", (B,)), B, M, H,
+                               qp, qb, qm, _opt(parent, torch.int32, "parent", (B, M)), window, sinks, op, ob, om,
+                               ws.data_ptr(), ws.numel() * ws.element_size(), _stream()), "sd_paged_attn")
+
+
+def paged_commit(pages: KvPages, table: torch.Tensor, lens: torch.Tensor, M: int, count: torch.Tensor,
+                 path: torch.Tensor | None = None):
+    """Keep the accepted rows of each sequence (path int32 [B][M], None: chains) and lens += count."""
+    B, w = table.shape
+    _check(lib().sd_paged_commit(pages._arg(), _here(table, torch.int32, "table", (B, w)), w,
+                                 _here(lens, torch.int32, "lens", (B,)), B, M, _opt(path, torch.int32, "path", (B, M)),
+                                 _here(count, torch.int32, "count", (B,)), _stream()), "sd_paged_commit")
+
+
+def pages_workspace_bytes(n_pages: int, B: int, width: int) -> int:
+    return int(lib().sd_pages_workspace_bytes(n_pages, B, width))
+
+
+def pages_reserve(pages: KvPages, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, M: int,
+                  missing: torch.Tensor, ws: torch.Tensor, n_new: torch.Tensor | None = None):
+    """A page of its own for every slot that the next n_new[b] (None: M) rows touch; shared ones are copied.
+    missing int32 [1]: how many free pages were short (then nothing changed)."""
+    B, w = table.shape
+    _check(lib().sd_pages_reserve(pages._arg(), _here(refs, torch.int32, "refs", (pages.n_pages,)),
+                                  _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)),
+                                  _opt(n_new, torch.int32, "n_new", (B,)), B, M,
+                                  _here(missing, torch.int32, "missing", (1,)), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _stream()), "sd_pages_reserve")
+
+
+def pages_copy(pages: KvPages, ws: torch.Tensor):
+    """The copies of the workspace's last pages_reserve or pages_compact again, for another layer's pool."""
+    _check(lib().sd_pages_copy(pages._arg(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream()), "sd_pages_copy")
+
+
+def pages_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page_rows: int, src: torch.Tensor,
+               dst: torch.Tensor):
+    """Sequence dst[i] becomes a copy of src[i] that shares its pages."""
+    B, w = table.shape
+    n = src.numel()
+    _check(lib().sd_pages_fork(_here(refs, torch.int32, "refs", tuple(refs.shape)), refs.numel(),
+                               _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)), B,
+                               page_rows, _here(src, torch.int32, "src", (n,)), _here(dst, torch.int32, "dst", (n,)), n,
+                               _stream()), "sd_pages_fork")
+
+
+def pages_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page_rows: int, seqs: torch.Tensor,
+               keep: torch.Tensor | None = None):
+    """The named sequences release the pages behind their first keep[i] rows (None: all)."""
+    B, w = table.shape
+    n = seqs.numel()
+    _check(lib().sd_pages_free(_here(refs, torch.int32, "refs", tuple(refs.shape)), refs.numel(),
+                               _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)), B,
+                               page_rows, _here(seqs, torch.int32, "seqs", (n,)),
+                               _opt(keep, torch.int32, "keep", (n,)), n, _stream()), "sd_pages_free")
+
+
+def pages_trim(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page_rows: int, window: int,
+               sinks: int = 0):
+    """Every sequence releases the pages between its first sinks rows and its window."""
+    B, w = table.shape
+    _check(lib().sd_pages_trim(_here(refs, torch.int32, "refs", tuple(refs.shape)), refs.numel(),
+                               _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)), B,
+                               page_rows, window, sinks, _stream()), "sd_pages_trim")
+
+
+def pages_compact(pages: KvPages, refs: torch.Tensor, table: torch.Tensor, remap: torch.Tensor, n_live: torch.Tensor,
+                  ws: torch.Tensor):
+    """The live pages to the front of the pool; remap int32 [n_pages]: each page's new index (-1: free)."""
+    B, w = table.shape
+    _check(lib().sd_pages_compact(pages._arg(), _here(refs, torch.int32, "refs", (pages.n_pages,)),
+                                  _here(table, torch.int32, "table", (B, w)), w, B,
+                                  _here(remap, torch.int32, "remap", (pages.n_pages,)),
+                                  _here(n_live, torch.int32, "n_live", (1,)), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _stream()), "sd_pages_compact")
 
 
 def shortlist_build(head_blocks: torch.Tensor, vocab: int, hidden: int):

@@ -1,0 +1,943 @@
+// sdv_paged_attn.cu - attention of the new rows of a batch of sequences over a cache in pages.
+//
+// Row i of sequence b (i < n_new[b]) stands at position len[b] + depth(i) and sees
+//   the committed rows j < len[b] with j > its position - window (all of them without a window), and
+//   the first `sinks` rows, and the new rows on its own path that the same rule lets it see;
+// out = softmax(q k^T / sqrt(D)) v over what it sees, query head h reading KV head h / g, g = H / H_kv.
+//
+// The work of one (sequence, KV head, group of 8 NT query rows) is a run of 64-key tiles (with a window: the
+// tiles of the first rows, then those from the window's start on).  All runs laid end to end are cut into
+// one equal piece per CTA of a persistent grid, so that lengths that differ balance whatever the batch is, and
+// a single long context spreads over the whole GPU.  A run inside one CTA is written out at once; a run cut between
+// CTAs leaves (max, sum, unnormalised output) partials in the workspace, and the CTA that arrives last joins
+// them in the order of their keys: a counter decides who joins, never in which order, so results repeat.
+//
+// Inside a CTA: one producer warp, its lanes fetching the tile's pages (a tensor copy per page, K or V and
+// 128 bytes of row, 128-byte swizzled) into a ring of 64-key stages that runs ahead over the piece's runs; four
+// consumer warps with 16 keys each.  S^T = K Q^T and O^T += V^T P^T on mma m16n8k16 with fp32 accumulation.  The
+// fp32 operands are split so that a product keeps about 2^-22 of relative error: into two fp16 parts
+// for fp16 and 8-bit rows (codes are exact in fp16; the row scales multiply scores and weights in
+// fp32), into three bf16 parts for bf16 rows.  Softmax statistics are fp32 in exp2 units.  A tile's product
+// starts from zero and is added to the rescaled outputs by fp32 FMAs: the tensor cores' own accumulation
+// truncates, a bias that grows with the tiles (1.2e-5 of the result at 40000 rows against 64 bits).
+#include "sdv_paged.cuh"
+
+namespace sdv {
+
+constexpr int PA_KT = 64;          // keys per tile
+constexpr int PA_CW = 4;           // consumer warps, 16 keys of a tile each
+constexpr int PA_THREADS = 32 * (PA_CW + 1);
+constexpr float PA_NEG = -3.402823466e38f;  // running-max start: finite, below every score
+constexpr float PA_PS = 16384.0f;  // fp16 weights are scaled by 2^14 (exact)
+constexpr uint64_t PA_WAIT_NS = 2000000000ull;
+
+struct PagedArgs {
+    const float *q;  // row i of sequence b at b * q_sb + i * q_sm, heads contiguous
+    float *out;
+    const int32_t *table, *lens, *n_new, *parent;
+    const float *k_scale, *v_scale;  // 8-bit rows: [n_pages][H_kv][P]
+    int64_t q_sb, q_sm, o_sb, o_sm;
+    int32_t B, M, H, H_kv, g, P, n_pages, width, window, sinks;
+    int32_t nst;          // ring stages
+    float qscale;         // log2(e) / sqrt(D)
+    float *part_o;        // [2 * grid][8 NT][D]
+    float2 *part_ml;      // [2 * grid][8 NT]
+    int32_t *counters;    // [grid], zero between calls
+    int *status;
+};
+
+template <int T, int D>
+struct PaLayout {
+    static constexpr int ELT = T == SD_KV_I8 ? 1 : 2;
+    static constexpr int ROWB = D * ELT < 128 ? D * ELT : 128;  // bytes of a row in one tensor tile
+    static constexpr int NB = D * ELT / ROWB;                   // tensor tiles across a row
+    static constexpr int TILE = PA_KT * ROWB;
+    static constexpr int KV = NB * TILE;                        // K (or V) rows of a stage
+    static constexpr int SCALES = T == SD_KV_I8 ? 1024 : 0;     // 64 + 64 row scales, padded to the swizzle's alignment
+    static constexpr int STAGE = 2 * KV + SCALES;
+    static constexpr int SW = ROWB / 16 - 1;                    // swizzle mask over the 16-byte chunks
+    static constexpr int SSH = ROWB == 128 ? 0 : 1;             // 64-byte rows: two rows per 128-byte line
+};
+
+// byte offset inside a stage's K (or V) rows of the 16-byte chunk that holds bytes x .. of row r
+template <int T, int D>
+__device__ __forceinline__ uint32_t pa_off(int r, int x) {
+    using L = PaLayout<T, D>;
+    return static_cast<uint32_t>((x / L::ROWB) * L::TILE + r * L::ROWB + ((((x % L::ROWB) >> 4) ^ ((r >> L::SSH) & L::SW)) << 4));
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *tm, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void pa_ldsm(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void pa_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pa_movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <int T>
+__device__ __forceinline__ void pa_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (T == SD_KV_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An fp32 pair as 16-bit parts that add up to it: two fp16 (each halves the rounding 2^-11 left by the part
+// before: 2^-22 in all) or three bf16 (2^-8 each: 2^-24).
+template <int T>
+struct Parts {
+    static constexpr int N = T == SD_KV_BF16 ? 3 : 2;
+    uint32_t r[N];
+};
+template <int T>
+__device__ __forceinline__ Parts<T> split2(float x0, float x1) {
+    Parts<T> p;
+#pragma unroll
+    for (int i = 0; i < Parts<T>::N; ++i) {
+        if constexpr (T == SD_KV_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+            const float2 f = __bfloat1622float2(h);
+            p.r[i] = *reinterpret_cast<const uint32_t *>(&h);
+            x0 -= f.x;
+            x1 -= f.y;
+        } else {
+            const __half2 h = __floats2half2_rn(x0, x1);
+            const float2 f = __half22float2(h);
+            p.r[i] = *reinterpret_cast<const uint32_t *>(&h);
+            x0 -= f.x;
+            x1 -= f.y;
+        }
+    }
+    return p;
+}
+
+// two of a word's four int8 codes (bytes picked by sel, as selector nibbles 0..3) as an exact fp16 pair:
+// the code plus 128 in the mantissa of 1024, minus 1152
+template <int B0, int B1>
+__device__ __forceinline__ uint32_t codes2(uint32_t biased) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(biased), "r"(0x64646464u), "n"(B0 | (4 << 4) | (B1 << 8) | (4 << 12)));
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&r), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The tiles of one sequence: [0, n_sink) and from tile lo_tile on, T in all.
+struct SeqTiles {
+    int32_t n_sink, lo_tile, T;
+};
+__device__ __forceinline__ SeqTiles seq_tiles(int len, int n, int window, int sinks) {
+    SeqTiles s;
+    const int total = len + n;
+    int lo = 0;
+    if (window > 0 && len - window + 1 > 0) lo = len - window + 1;  // the first row (depth 0) reaches furthest back
+    s.lo_tile = lo / PA_KT;
+    const int st = window > 0 ? min((min(sinks, lo) + PA_KT - 1) / PA_KT, s.lo_tile) : 0;
+    s.n_sink = st;
+    s.T = st + (total + PA_KT - 1) / PA_KT - s.lo_tile;
+    return s;
+}
+
+// new rows that position i of a sequence sees: its path, cut by the window (the path's k-th node stands at depth k)
+__device__ __forceinline__ uint32_t new_rows_seen(const PagedArgs &a, int b, int i, int len, int &depth) {
+    uint32_t path = 0;
+    if (!a.parent) {
+        path = (2u << i) - 1u;
+    } else {
+        int x = i;
+        for (int step = 0; step <= i && x >= 0; ++step) {
+            path |= 1u << x;
+            const int p = a.parent[static_cast<int64_t>(b) * a.M + x];
+            if (p >= x) {  // parents come before their children; anything else is a bad tree
+                set_status(a.status, SD_EDEVICE);
+                break;
+            }
+            x = p;
+        }
+    }
+    depth = __popc(path) - 1;
+    if (a.window > 0) {
+        uint32_t keep = 0, left = path;
+        for (int k = 0; left; ++k) {
+            const uint32_t bit = left & (0u - left);
+            left ^= bit;
+            if (k > depth - a.window || len + k < a.sinks) keep |= bit;
+        }
+        path = keep;
+    }
+    return path;
+}
+
+// One piece of a CTA's share: tiles [t0, t1) of the run of (b, kh, rg).
+struct Piece {
+    int32_t b, kh, rg, t0, t1, len, n;
+    SeqTiles st;
+    int64_t run0;  // the run's first tile in the whole line
+};
+
+struct Sched {
+    const int64_t *prefix;  // [B + 1]: tiles of the sequences before
+    const int2 *ln;         // [B]: (len, n_new), n_new 0 where nothing is to be done
+    int64_t u0, u1, W;
+    int32_t G;              // CTAs that share the line
+};
+
+template <int RPG>
+__device__ __forceinline__ Piece piece_at(const PagedArgs &a, const Sched &s, int64_t u, int b) {
+    Piece p;
+    while (s.prefix[b + 1] <= u) ++b;
+    p.b = b;
+    const int2 ln = s.ln[b];
+    p.len = ln.x;
+    p.n = ln.y;
+    p.st = seq_tiles(p.len, p.n, a.window, a.sinks);
+    const int64_t rem = u - s.prefix[b];
+    const int64_t run = rem / p.st.T;
+    p.t0 = static_cast<int32_t>(rem - run * p.st.T);
+    p.run0 = u - p.t0;
+    const int RG = (p.n * a.g + RPG - 1) / RPG;
+    p.kh = static_cast<int32_t>(run / RG);
+    p.rg = static_cast<int32_t>(run - static_cast<int64_t>(p.kh) * RG);
+    const int64_t left = s.u1 - u;
+    p.t1 = left < p.st.T - p.t0 ? p.t0 + static_cast<int32_t>(left) : p.st.T;
+    return p;
+}
+__device__ __forceinline__ int cta_of(const Sched &s, int64_t u) { return static_cast<int>(((u + 1) * s.G - 1) / s.W); }
+
+template <int T, int D, int NT>
+__global__ void __launch_bounds__(PA_THREADS) paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
+                                                                const __grid_constant__ CUtensorMap tmv) {
+    using LY = PaLayout<T, D>;
+    constexpr int KS = D / 16, RPG = 8 * NT, NP = Parts<T>::N, SD = 64 + 4;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // the swizzle wants 1024 B
+    float *sm_o = reinterpret_cast<float *>(ring + static_cast<size_t>(a.nst) * LY::STAGE);  // [PA_CW][8][SD]: 64 columns of the warps' outputs
+    float *sm_m = sm_o + PA_CW * 8 * SD, *sm_l = sm_m + PA_CW * RPG;                         // [PA_CW][RPG]
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm_l + PA_CW * RPG), *empty = full + a.nst;
+    int64_t *prefix = reinterpret_cast<int64_t *>(empty + a.nst);
+    int2 *ln = reinterpret_cast<int2 *>(prefix + a.B + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(ln + a.B);
+    volatile int *last = abort + 1;
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, c = lane & 3;
+
+    if (tid == 0) {
+        for (int i = 0; i < a.nst; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], PA_CW);
+        }
+        *abort = 0;
+        fence_barrier_init();
+        prefix[0] = 0;
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    // the schedule: tiles per sequence, then their running sum
+    for (int b = tid; b < a.B; b += PA_THREADS) {
+        int len = a.lens[b], n = a.n_new ? a.n_new[b] : a.M;
+        if (len < 0 || n < 0 || n > a.M || static_cast<int64_t>(len) + n > static_cast<int64_t>(a.width) * a.P) {
+            set_status(a.status, SD_EDEVICE);
+            n = 0;
+        }
+        int64_t cost = 0;
+        if (n > 0)
+            cost = static_cast<int64_t>(seq_tiles(len, n, a.window, a.sinks).T) * ((n * a.g + RPG - 1) / RPG) * a.H_kv;
+        ln[b] = make_int2(len, n);
+        prefix[b + 1] = cost;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t run = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + lane;
+            int64_t v = b < a.B ? prefix[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
+            }
+            if (b < a.B) prefix[b + 1] = run + v;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    Sched sc;
+    sc.prefix = prefix;
+    sc.ln = ln;
+    sc.W = prefix[a.B];
+    sc.G = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), sc.W));
+    if (static_cast<int64_t>(blockIdx.x) >= sc.W) return;
+    sc.u0 = static_cast<int64_t>(blockIdx.x) * sc.W / sc.G;
+    sc.u1 = static_cast<int64_t>(blockIdx.x + 1) * sc.W / sc.G;
+
+    if (warp == PA_CW) {
+        // ---- producer warp: lane l issues copies l, l + 32, .. of a tile (page, K or V, 128 bytes of row)
+        const int rows = min(a.P, PA_KT), npt = PA_KT / rows;  // rows of a page in a tile, pages per tile
+        const int ncopy = npt * 2 * LY::NB;
+        int64_t u = sc.u0;
+        int b = 0, slot = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        while (ok && u < sc.u1) {
+            const Piece p = piece_at<RPG>(a, sc, u, b);
+            b = p.b;
+            const int32_t *tab = a.table + static_cast<int64_t>(b) * a.width;
+            const int total = p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
+            // page of this lane's place in tile t (a place without rows, or an entry that is no page, reads as zeros)
+            auto page_of = [&](int t) {
+                const int key = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT + (lane % npt) * rows;
+                if (key >= total) return a.n_pages;
+                const int pg = tab[key / a.P];
+                if (pg >= 0 && pg < a.n_pages) return pg;
+                if (key + rows > lo || key < sink) set_status(a.status, SD_EDEVICE);  // a row of it is visible
+                return a.n_pages;
+            };
+            int pg = page_of(p.t0);
+            for (int t = p.t0; t < p.t1; ++t) {
+                const int next = t + 1 < p.t1 ? page_of(t + 1) : 0;  // in flight while this tile waits for its stage
+                const int key0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT;
+                if (issued >= a.nst && !mbar_wait_bounded(&empty[slot], ph ^ 1u, PA_WAIT_NS, abort)) {
+                    set_status(a.status, SD_ETIMEOUT);
+                    *abort = 1;
+                }
+                if (!__all_sync(0xffffffffu, *abort == 0)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *stp = ring + static_cast<size_t>(slot) * LY::STAGE;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[slot], 2 * LY::KV + (T == SD_KV_I8 ? 2 * PA_KT * 4 : 0));
+                __syncwarp();
+                for (int i = lane; i < ncopy; i += 32) {
+                    // page place i % npt: this lane's own (npt divides 32)
+                    const int place = i % npt, half = (i / npt) % LY::NB, kv = i / npt / LY::NB;
+                    const uint32_t dst = smem_u32(stp) + kv * LY::KV + half * LY::TILE + place * rows * LY::ROWB;
+                    tma_4d(dst, kv ? &tmv : &tmk, half * (LY::ROWB / LY::ELT), key0 % a.P, p.kh, pg, &full[slot]);
+                }
+                if constexpr (T == SD_KV_I8) {
+                    if (lane < 2 * npt) {
+                        const int place = lane % npt, kv = lane / npt;
+                        const int64_t page = pg < a.n_pages ? pg : 0;  // a place without rows: any page's scales
+                        const float *src = (kv ? a.v_scale : a.k_scale) + (page * a.H_kv + p.kh) * a.P + key0 % a.P;
+                        bulk_g2s_l2keep(stp + 2 * LY::KV + kv * PA_KT * 4 + place * rows * 4, src, rows * 4, &full[slot]);
+                    }
+                }
+                ++issued;
+                if (++slot == a.nst) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
+                pg = next;
+            }
+            u += p.t1 - p.t0;
+        }
+        if (!ok && lane == 0) {  // never leave with copies in flight
+            for (int i = max(0, issued - a.nst); i < issued; ++i)
+                mbar_wait_bounded(&full[i % a.nst], (i / a.nst) & 1u, PA_WAIT_NS);
+        }
+        __syncwarp();
+        return;
+    }
+
+    // ---- consumer warps
+    const uint32_t sbase = smem_u32(ring);
+    // ldmatrix row addresses of this lane: K (keys x d) and, transposed, V
+    const int kr = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8, kx = (lane >> 4) * 16;
+    const int vr = 16 * warp + (lane & 7) + (T == SD_KV_I8 ? ((lane >> 3) & 1) : (lane >> 4)) * 8;
+    const int vx = (T == SD_KV_I8 ? (lane >> 4) : ((lane >> 3) & 1)) * 16;
+    int64_t u = sc.u0;
+    int b = 0, slot = 0;
+    uint32_t ph = 0;
+    while (u < sc.u1) {
+        const Piece p = piece_at<RPG>(a, sc, u, b);
+        b = p.b;
+        const int rows = p.n * a.g, total = p.len + p.n;
+        // B fragments of query row g of each 8-row tile, in parts; fp16 parts of a row scaled by 2^(11-e) for
+        // max |q| in [2^(e-1), 2^e), so that neither part is subnormal
+        uint32_t qf[NT][KS][2][NP];
+        float rs[NT][2];            // the scale back of rows 2c, 2c+1
+        uint32_t vis[NT][2];        // new rows that rows 2c, 2c+1 see
+        int low[NT][2];             // the first row of their window
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int tg = p.rg * RPG + nt * 8 + g;
+            const bool real = tg < rows;
+            const int i = real ? tg / a.g : 0, h = p.kh * a.g + (real ? tg % a.g : 0);
+            const float *qp = a.q + p.b * a.q_sb + i * a.q_sm + static_cast<int64_t>(h) * D;
+            float qv[KS][4];
+            float mx = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                float2 x, y;
+                if constexpr (T == SD_KV_I8) {  // the order in which a word of four codes is unpacked
+                    const float4 f = *reinterpret_cast<const float4 *>(qp + 16 * ks + 4 * c);
+                    x = make_float2(f.x, f.y);
+                    y = make_float2(f.z, f.w);
+                } else {
+                    x = *reinterpret_cast<const float2 *>(qp + 16 * ks + 2 * c);
+                    y = *reinterpret_cast<const float2 *>(qp + 16 * ks + 2 * c + 8);
+                }
+                qv[ks][0] = real ? x.x * a.qscale : 0.0f;
+                qv[ks][1] = real ? x.y * a.qscale : 0.0f;
+                qv[ks][2] = real ? y.x * a.qscale : 0.0f;
+                qv[ks][3] = real ? y.y * a.qscale : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(qv[ks][e]));
+            }
+            float up = 1.0f, back = 1.0f;
+            if constexpr (T != SD_KV_BF16) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                int ex = 0;
+                if (mx > 0.0f && mx < INFINITY) (void)frexpf(mx, &ex);
+                ex = max(ex, -100);  // below that the parts may go subnormal: such scores are 0 anyway
+                up = ldexpf(1.0f, 11 - ex);
+                back = ldexpf(1.0f, ex - 11);
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const Parts<T> f0 = split2<T>(qv[ks][0] * up, qv[ks][1] * up), f1 = split2<T>(qv[ks][2] * up, qv[ks][3] * up);
+#pragma unroll
+                for (int i2 = 0; i2 < NP; ++i2) {
+                    qf[nt][ks][0][i2] = f0.r[i2];
+                    qf[nt][ks][1][i2] = f1.r[i2];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                rs[nt][r] = __shfl_sync(0xffffffffu, back, 8 * c + 4 * r);
+                const int tr = p.rg * RPG + nt * 8 + 2 * c + r;
+                vis[nt][r] = 0;
+                low[nt][r] = INT32_MAX;
+                if (tr < rows) {
+                    int depth;
+                    vis[nt][r] = new_rows_seen(a, p.b, tr / a.g, p.len, depth);
+                    low[nt][r] = a.window > 0 ? p.len + depth - a.window + 1 : 0;
+                }
+            }
+        }
+        float m[NT][2], l[NT][2], o[NT][KS][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = PA_NEG;
+            l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+            for (int dt = 0; dt < KS; ++dt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][dt][e] = 0.0f;
+        }
+        int ve = -200;  // 8-bit rows: the outputs are in units of 2^ve, at least every V scale so far
+        // keys from full_lo on (or below full_sink) and below p.len are seen by every row
+        const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
+        bool ok = true;
+        for (int t = p.t0; t < p.t1; ++t) {
+            const bool ready = mbar_wait_bounded(&full[slot], ph, PA_WAIT_NS, abort);
+            if (!__all_sync(0xffffffffu, ready)) {
+                if (lane == 0) {
+                    set_status(a.status, SD_ETIMEOUT);
+                    *abort = 1;
+                }
+                ok = false;
+                break;
+            }
+            const uint32_t st = sbase + static_cast<uint32_t>(slot) * LY::STAGE;
+            const int key0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT;
+            float s[NT][4];
+            {
+                float sa[NT][2][4] = {};  // two accumulator chains (even / odd k step)
+#pragma unroll
+                for (int k0 = 0; k0 < KS; k0 += (T == SD_KV_I8 ? 2 : 1)) {
+                    uint32_t ka[4];
+                    pa_ldsm(st + pa_off<T, D>(kr, (T == SD_KV_I8 ? 16 : 32) * k0 + kx), ka);
+                    if constexpr (T == SD_KV_I8) {
+                        const uint32_t w0 = ka[0] ^ 0x80808080u, w1 = ka[1] ^ 0x80808080u, w2 = ka[2] ^ 0x80808080u, w3 = ka[3] ^ 0x80808080u;
+                        const uint32_t k1[4] = {codes2<0, 1>(w0), codes2<0, 1>(w1), codes2<2, 3>(w0), codes2<2, 3>(w1)};
+                        const uint32_t k2[4] = {codes2<0, 1>(w2), codes2<0, 1>(w3), codes2<2, 3>(w2), codes2<2, 3>(w3)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int x = 0; x < NP; ++x) {
+                                pa_mma<T>(sa[nt][0], k1, qf[nt][k0][0][x], qf[nt][k0][1][x]);
+                                pa_mma<T>(sa[nt][1], k2, qf[nt][k0 + 1][0][x], qf[nt][k0 + 1][1][x]);
+                            }
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int x = 0; x < NP; ++x) pa_mma<T>(sa[nt][k0 & 1], ka, qf[nt][k0][0][x], qf[nt][k0][1][x]);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[nt][e] = (sa[nt][0][e] + sa[nt][1][e]) * rs[nt][e & 1];
+            }
+            const int ja = key0 + 16 * warp + g, jb = ja + 8;  // s[.][0..1]: key ja, rows 2c, 2c+1; s[.][2..3]: key jb
+            float vs0 = 1.0f, vs1 = 1.0f;
+            if constexpr (T == SD_KV_I8) {
+                const float *scales = reinterpret_cast<const float *>(ring + static_cast<size_t>(slot) * LY::STAGE + 2 * LY::KV);
+                float ks0 = scales[16 * warp + g], ks1 = scales[16 * warp + g + 8];
+                ks0 += 0.0f * ks0;  // an infinite scale makes a row of NaN (0 codes times infinity), not a score of -inf
+                ks1 += 0.0f * ks1;
+                vs0 = scales[PA_KT + 16 * warp + g];
+                vs1 = scales[PA_KT + 16 * warp + g + 8];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    s[nt][0] *= ks0;
+                    s[nt][1] *= ks0;
+                    s[nt][2] *= ks1;
+                    s[nt][3] *= ks1;
+                }
+            }
+            const bool whole = key0 + PA_KT <= p.len && (key0 >= full_lo || key0 + PA_KT <= full_sink);
+            if (!whole) {
+                auto seen = [&](int j, int nt, int r) {
+                    if (j >= p.len) return j < total && ((vis[nt][r] >> (j - p.len)) & 1u) != 0;
+                    return j >= low[nt][r] || (j < full_sink && low[nt][r] != INT32_MAX);
+                };
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (!seen(ja, nt, 0)) s[nt][0] = -INFINITY;
+                    if (!seen(ja, nt, 1)) s[nt][1] = -INFINITY;
+                    if (!seen(jb, nt, 0)) s[nt][2] = -INFINITY;
+                    if (!seen(jb, nt, 1)) s[nt][3] = -INFINITY;
+                }
+            }
+            float vmul0 = 1.0f, vmul1 = 1.0f, shrink = 1.0f;
+            if constexpr (T == SD_KV_I8) {
+                int e = -200;
+                int x;
+                if (vs0 > 0.0f && vs0 < INFINITY) {
+                    (void)frexpf(vs0, &x);
+                    e = x;
+                }
+                if (vs1 > 0.0f && vs1 < INFINITY) {
+                    (void)frexpf(vs1, &x);
+                    e = max(e, x);
+                }
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, off));
+                e = max(e, -126);
+                if (e > ve) {
+                    shrink = ve > -200 ? ldexpf(1.0f, ve - e) : 0.0f;
+                    ve = e;
+                }
+                const float down = ldexpf(1.0f, -ve);
+                vmul0 = vs0 * down;
+                vmul1 = vs1 * down;
+            }
+            // weights of the keys, running max and sum
+            float pr[NT][4], al[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float x0 = fmaxf(s[nt][0], s[nt][2]), x1 = fmaxf(s[nt][1], s[nt][3]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+                }
+                const float n0 = fmaxf(m[nt][0], x0), n1 = fmaxf(m[nt][1], x1);
+                const float al0 = exp2f(m[nt][0] - n0), al1 = exp2f(m[nt][1] - n1);
+                pr[nt][0] = exp2f(s[nt][0] - n0);
+                pr[nt][1] = exp2f(s[nt][1] - n1);
+                pr[nt][2] = exp2f(s[nt][2] - n0);
+                pr[nt][3] = exp2f(s[nt][3] - n1);
+                l[nt][0] = fmaf(l[nt][0], al0, pr[nt][0] + pr[nt][2]);  // this lane's keys; lanes are added at the end
+                l[nt][1] = fmaf(l[nt][1], al1, pr[nt][1] + pr[nt][3]);
+                m[nt][0] = n0;
+                m[nt][1] = n1;
+                al[nt][0] = T == SD_KV_I8 ? al0 * shrink : al0;
+                al[nt][1] = T == SD_KV_I8 ? al1 * shrink : al1;
+                if constexpr (T == SD_KV_I8) {
+                    // a key with no weight keeps none, whatever its scale is
+                    pr[nt][0] = pr[nt][0] > 0.0f ? pr[nt][0] * vmul0 : pr[nt][0];
+                    pr[nt][1] = pr[nt][1] > 0.0f ? pr[nt][1] * vmul0 : pr[nt][1];
+                    pr[nt][2] = pr[nt][2] > 0.0f ? pr[nt][2] * vmul1 : pr[nt][2];
+                    pr[nt][3] = pr[nt][3] > 0.0f ? pr[nt][3] * vmul1 : pr[nt][3];
+                }
+            }
+            const uint32_t vst = st + LY::KV;
+            if constexpr (T != SD_KV_I8) {
+                if (!whole) {
+                    // a row that some query row does not see may hold anything, and 0 times a NaN or infinity is no 0: such
+                    // rows are added here, to the query rows that see them alone, and cleared before the product
+                    uint32_t bad = 0;
+                    for (int i = lane; i < 16 * LY::NB * (LY::ROWB / 16); i += 32) {
+                        const int r = i % 16, x = (i / 16) * 16;
+                        uint4 v;
+                        const uint32_t ad = vst + pa_off<T, D>(16 * warp + r, x);
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ad) : "memory");
+                        constexpr uint32_t EX = T == SD_KV_BF16 ? 0x7f80u : 0x7c00u;
+                        bool any = false;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t q = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+                            any |= (q & EX) == EX || ((q >> 16) & EX) == EX;
+                        }
+                        if (any) bad |= 1u << r;
+                    }
+                    bad = __reduce_or_sync(0xffffffffu, bad);
+                    if (bad) {  // the rescale that the product below makes otherwise
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                            for (int dt = 0; dt < KS; ++dt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[nt][dt][e] *= al[nt][e & 1];
+                            al[nt][0] = al[nt][1] = 1.0f;
+                        }
+                    }
+                    for (uint32_t left = bad; left; left &= left - 1) {
+                        const int key = __ffs(left) - 1, src = (key & 7) * 4 + c;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float w0 = __shfl_sync(0xffffffffu, key < 8 ? pr[nt][0] : pr[nt][2], src);
+                            const float w1 = __shfl_sync(0xffffffffu, key < 8 ? pr[nt][1] : pr[nt][3], src);
+                            const float f = T == SD_KV_BF16 ? 1.0f : PA_PS;
+#pragma unroll
+                            for (int dt = 0; dt < KS; ++dt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int x = 2 * (16 * dt + g + 8 * e);
+                                    uint16_t raw;
+                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(vst + pa_off<T, D>(16 * warp + key, x) + (x & 15)) : "memory");
+                                    float v;
+                                    if constexpr (T == SD_KV_BF16) v = __bfloat162float(__ushort_as_bfloat16(raw));
+                                    else v = __half2float(__ushort_as_half(raw));
+                                    if (w0 > 0.0f) o[nt][dt][2 * e] += w0 * f * v;
+                                    if (w1 > 0.0f) o[nt][dt][2 * e + 1] += w1 * f * v;
+                                }
+                        }
+                        __syncwarp();
+                        for (int x = 16 * lane; x < 2 * D; x += 512)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vst + pa_off<T, D>(16 * warp + key, x)), "r"(0u) : "memory");
+                        __syncwarp();
+                    }
+                    if (bad) fence_proxy_async_shared();  // before the stage's next copy
+                }
+            }
+            uint32_t b0[NT][NP], b1[NT][NP];  // the weights as B fragments (keys x rows), in parts
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                constexpr float PS = T == SD_KV_BF16 ? 1.0f : PA_PS;
+                const Parts<T> pa = split2<T>(pr[nt][0] * PS, pr[nt][1] * PS), pb = split2<T>(pr[nt][2] * PS, pr[nt][3] * PS);
+#pragma unroll
+                for (int x = 0; x < NP; ++x) {
+                    b0[nt][x] = pa_movm(pa.r[x]);
+                    b1[nt][x] = pa_movm(pb.r[x]);
+                }
+            }
+#pragma unroll
+            for (int dt = 0; dt < KS; dt += (T == SD_KV_I8 ? 2 : 1)) {
+                uint32_t va[4];
+                pa_ldsm_t(vst + pa_off<T, D>(vr, (T == SD_KV_I8 ? 16 : 32) * dt + vx), va);
+                if constexpr (T == SD_KV_I8) {
+                    const uint32_t w0 = va[0] ^ 0x80808080u, w1 = va[1] ^ 0x80808080u, w2 = va[2] ^ 0x80808080u, w3 = va[3] ^ 0x80808080u;
+                    const uint32_t v1[4] = {codes2<0, 2>(w0), codes2<1, 3>(w0), codes2<0, 2>(w1), codes2<1, 3>(w1)};
+                    const uint32_t v2[4] = {codes2<0, 2>(w2), codes2<1, 3>(w2), codes2<0, 2>(w3), codes2<1, 3>(w3)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                            float y1[4] = {}, y2[4] = {};
+#pragma unroll
+                            for (int x = 0; x < NP; ++x) {
+                                pa_mma<T>(y1, v1, b0[nt][x], b1[nt][x]);
+                                pa_mma<T>(y2, v2, b0[nt][x], b1[nt][x]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                o[nt][dt][e] = fmaf(o[nt][dt][e], al[nt][e & 1], y1[e]);
+                                o[nt][dt + 1][e] = fmaf(o[nt][dt + 1][e], al[nt][e & 1], y2[e]);
+                            }
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float y[4] = {};
+#pragma unroll
+                        for (int x = 0; x < NP; ++x) pa_mma<T>(y, va, b0[nt][x], b1[nt][x]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[nt][dt][e] = fmaf(o[nt][dt][e], al[nt][e & 1], y[e]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (++slot == a.nst) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        }
+        if (bar_any(1, 32 * PA_CW, !ok)) return;  // every consumer warp leaves together
+        // ---- join the warps' states and write the piece: rows that are whole go out, others become partials
+        const bool complete = p.t0 == 0 && p.t1 == p.st.T;
+        const int pslot = 2 * static_cast<int>(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
+        const float unit = T == SD_KV_BF16 ? 1.0f : T == SD_KV_I8 ? (ve > -200 ? ldexpf(1.0f / PA_PS, ve) : 0.0f) : 1.0f / PA_PS;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x = l[nt][r];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+                if (g == 0) {
+                    sm_m[warp * RPG + nt * 8 + 2 * c + r] = m[nt][r];
+                    sm_l[warp * RPG + nt * 8 + 2 * c + r] = x;
+                }
+            }
+            const int r = tid >> 4, tr = nt * 8 + r, tg = p.rg * RPG + tr;
+            float f[PA_CW], mx = PA_NEG, lv = 0.0f, inv = 0.0f;
+#pragma unroll
+            for (int cc = 0; cc < D / 64; ++cc) {  // 64 columns at a time
+                float *ow = sm_o + warp * 8 * SD;
+#pragma unroll
+                for (int dx = 0; dx < 4; ++dx) {
+                    const int dt = 4 * cc + dx;
+                    const int d0 = 16 * dx + (T == SD_KV_I8 ? 2 * g : g), d1 = d0 + (T == SD_KV_I8 ? 1 : 8);
+                    ow[(2 * c) * SD + d0] = o[nt][dt][0] * unit;
+                    ow[(2 * c + 1) * SD + d0] = o[nt][dt][1] * unit;
+                    ow[(2 * c) * SD + d1] = o[nt][dt][2] * unit;
+                    ow[(2 * c + 1) * SD + d1] = o[nt][dt][3] * unit;
+                }
+                named_bar_sync(1, 32 * PA_CW);
+                if (cc == 0) {
+#pragma unroll
+                    for (int w = 0; w < PA_CW; ++w) mx = fmaxf(mx, sm_m[w * RPG + tr]);
+#pragma unroll
+                    for (int w = 0; w < PA_CW; ++w) {
+                        f[w] = exp2f(sm_m[w * RPG + tr] - mx);
+                        lv = fmaf(sm_l[w * RPG + tr], f[w], lv);
+                    }
+                    inv = lv == 0.0f ? 0.0f : 1.0f / lv;
+                    if (!complete && tg < rows && (tid & 15) == 0) a.part_ml[pslot * RPG + tr] = make_float2(mx, lv);
+                }
+                if (tg < rows) {
+                    const int i = tg / a.g, h = p.kh * a.g + tg % a.g, d = 4 * (tid & 15);
+                    float *op = complete ? a.out + p.b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D
+                                         : a.part_o + (static_cast<int64_t>(pslot) * RPG + tr) * D;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int w = 0; w < PA_CW; ++w) {
+                        const float4 x = *reinterpret_cast<const float4 *>(sm_o + (w * 8 + r) * SD + d);
+                        v.x = fmaf(x.x, f[w], v.x);
+                        v.y = fmaf(x.y, f[w], v.y);
+                        v.z = fmaf(x.z, f[w], v.z);
+                        v.w = fmaf(x.w, f[w], v.w);
+                    }
+                    if (complete) v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    *reinterpret_cast<float4 *>(op + 64 * cc + d) = v;
+                }
+                named_bar_sync(1, 32 * PA_CW);
+            }
+        }
+        if (!complete) {
+            // the last of the run's CTAs to come here joins their partials, in the order of their keys
+            const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
+            __threadfence();
+            named_bar_sync(1, 32 * PA_CW);
+            if (tid == 0) {
+                const int was = atomicAdd(&a.counters[c0], 1);
+                *last = was == c1 - c0;
+                if (was == c1 - c0) a.counters[c0] = 0;
+            }
+            named_bar_sync(1, 32 * PA_CW);
+            if (*last) {
+                __threadfence();
+                for (int idx = tid; idx < RPG * (D / 4); idx += 32 * PA_CW) {
+                    const int tr = idx / (D / 4), d = idx % (D / 4) * 4, tg = p.rg * RPG + tr;
+                    if (tg >= rows) break;
+                    float mx = PA_NEG;
+                    for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(&a.part_ml[(2 * x + (x == c0)) * RPG + tr]).x);
+                    float lv = 0.0f;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int x = c0; x <= c1; ++x) {
+                        const int sl = 2 * x + (x == c0);
+                        const float2 ml = __ldcg(&a.part_ml[sl * RPG + tr]);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (static_cast<int64_t>(sl) * RPG + tr) * D + d));
+                        const float fx = exp2f(ml.x - mx);
+                        lv = fmaf(ml.y, fx, lv);
+                        v.x = fmaf(y.x, fx, v.x);
+                        v.y = fmaf(y.y, fx, v.y);
+                        v.z = fmaf(y.z, fx, v.z);
+                        v.w = fmaf(y.w, fx, v.w);
+                    }
+                    const float inv = lv == 0.0f ? 0.0f : 1.0f / lv;
+                    const int i = tg / a.g, h = p.kh * a.g + tg % a.g;
+                    *reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D + d) =
+                        make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                }
+            }
+        }
+        u += p.t1 - p.t0;
+    }
+}
+
+struct PaPlan {
+    int nt, grid, nst;
+    size_t smem, off_ml, off_o, total;
+};
+
+static size_t pa_stage(int type, int D) { return 2 * static_cast<size_t>(PA_KT) * D * kv_type_bytes(type) + (type == SD_KV_I8 ? 1024 : 0); }
+
+// Rows beside each other in one 8- or 16-row group; a persistent grid of two CTAs per SM, or one where
+// three stages of the ring do not fit twice.
+static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
+    const int sms = num_sms();
+    if (sms < 1) return false;
+    const int rows = M * (H / H_kv);
+    p.nt = rows > 8 && D <= 128 ? 2 : 1;
+    const size_t fixed = 1024 + static_cast<size_t>(PA_CW) * 8 * 68 * 4 + 2 * static_cast<size_t>(PA_CW) * 8 * p.nt * 4 +
+                         (static_cast<size_t>(B) + 1) * 8 + static_cast<size_t>(B) * 8 + 16;
+    const size_t per = pa_stage(type, D) + 16;
+    const size_t half = (228 * 1024) / 2 - 1024, whole = 227 * 1024;
+    int per_sm = 2;
+    int64_t n = (static_cast<int64_t>(half) - static_cast<int64_t>(fixed)) / static_cast<int64_t>(per);
+    if (n < 2) {
+        per_sm = 1;
+        n = (whole - fixed) / per;
+    }
+    p.nst = static_cast<int>(n < 8 ? n : 8);
+    p.grid = per_sm * sms;
+    p.smem = fixed + per * p.nst;
+    return true;
+}
+
+// workspace: counters of the largest grid, then the partials of 16-row groups
+static size_t pa_workspace(int D, size_t *off_ml, size_t *off_o) {
+    const size_t G = 2 * static_cast<size_t>(num_sms() > 0 ? num_sms() : 0);
+    if (!G) return 0;
+    const size_t ml = (G * 4 + 255) / 256 * 256, o = ml + (2 * G * 16 * 8 + 255) / 256 * 256;
+    if (off_ml) *off_ml = ml;
+    if (off_o) *off_o = o;
+    return o + 2 * G * 16 * static_cast<size_t>(D) * 4;
+}
+
+// K or V pages as a 4-d tensor (x = element of a row, y = row in its page, z = KV head, w = page): boxes of
+// up to 64 rows of one page by 128 bytes, zeros for a page past the last
+static bool pages_map(CUtensorMap *tm, const sd_kv_pages *p, void *base) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int eb = kv_type_bytes(p->type);
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p->D), static_cast<cuuint64_t>(p->page_rows),
+                                static_cast<cuuint64_t>(p->H_kv), static_cast<cuuint64_t>(p->n_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p->row_stride) * eb, static_cast<cuuint64_t>(p->head_stride) * eb,
+                                   static_cast<cuuint64_t>(p->page_stride) * eb};
+    const int rowb = p->D * eb < 128 ? p->D * eb : 128;
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(rowb / eb), static_cast<cuuint32_t>(p->page_rows < PA_KT ? p->page_rows : PA_KT), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType dt = p->type == SD_KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                   : p->type == SD_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return enc(tm, dt, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               rowb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int T, int D, int NT>
+static cudaError_t pa_launch(const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t s) {
+    const cudaError_t e = allow_max_dynamic_smem(paged_attn_kernel<T, D, NT>);
+    if (e != cudaSuccess) return e;
+    return launch(paged_attn_kernel<T, D, NT>, dim3(p.grid), dim3(PA_THREADS), p.smem, s, a, tmk, tmv);
+}
+template <int T>
+static cudaError_t pa_launch_d(int D, const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t s) {
+    if (D == 256) return pa_launch<T, 256, 1>(p, a, tmk, tmv, s);
+    if (D == 128) return p.nt == 1 ? pa_launch<T, 128, 1>(p, a, tmk, tmv, s) : pa_launch<T, 128, 2>(p, a, tmk, tmv, s);
+    return p.nt == 1 ? pa_launch<T, 64, 1>(p, a, tmk, tmv, s) : pa_launch<T, 64, 2>(p, a, tmk, tmv, s);
+}
+
+}  // namespace sdv
+
+using namespace sdv;
+
+extern "C" {
+
+size_t sd_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D) {
+    if (B < 1 || B > PG_MAX_B || M < 1 || M > 16 || H_kv < 1 || H < H_kv || H % H_kv || (D != 64 && D != 128 && D != 256)) return 0;
+    return pa_workspace(D, nullptr, nullptr);
+}
+
+sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
+                        int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride, int64_t q_row_stride,
+                        const int32_t *parent, int32_t window, int32_t sinks, float *out, int64_t out_seq_stride,
+                        int64_t out_row_stride, void *workspace, size_t ws_bytes, sd_stream_t stream) {
+    SD_NVTX("sd_paged_attn");
+    const sd_status st = pages_check(pages);
+    if (st != SD_OK) return st;
+    const int H_kv = pages->H_kv, D = pages->D;
+    if (!table || !lens || !q || !out || !workspace || width < 1) return SD_EINVAL;
+    if (B < 1 || M < 1 || H < H_kv || H % H_kv || window < 0 || sinks < 0) return SD_EINVAL;
+    if (M > 16 || B > PG_MAX_B) return SD_EUNSUPPORTED;
+    const int64_t line = static_cast<int64_t>(H) * D;
+    if (q_row_stride < line || out_row_stride < line || q_row_stride % 4 || out_row_stride % 4 || q_seq_stride % 4 || out_seq_stride % 4)
+        return SD_EINVAL;
+    if (B > 1 && (q_seq_stride < line || out_seq_stride < line)) return SD_EINVAL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return SD_EINVAL;
+    if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 2 * PA_KT) return SD_EUNSUPPORTED;  // positions are 32-bit
+    PaPlan p;
+    size_t off_ml, off_o;
+    const size_t need = pa_workspace(D, &off_ml, &off_o);
+    if (!need || !pa_plan(pages->type, B, M, H, H_kv, D, p)) return SD_ECUDA;
+    if (ws_bytes < need) return SD_EINVAL;
+    CUtensorMap tmk, tmv;
+    if (!pages_map(&tmk, pages, pages->k) || !pages_map(&tmv, pages, pages->v)) return SD_ECUDA;
+    int *status = status_ptr();
+    if (!status) return SD_ECUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    PagedArgs a = {};
+    a.q = q;
+    a.out = out;
+    a.table = table;
+    a.lens = lens;
+    a.n_new = n_new;
+    a.parent = parent;
+    a.k_scale = pages->k_scale;
+    a.v_scale = pages->v_scale;
+    a.q_sb = q_seq_stride;
+    a.q_sm = q_row_stride;
+    a.o_sb = out_seq_stride;
+    a.o_sm = out_row_stride;
+    a.B = B;
+    a.M = M;
+    a.H = H;
+    a.H_kv = H_kv;
+    a.g = H / H_kv;
+    a.P = pages->page_rows;
+    a.n_pages = pages->n_pages;
+    a.width = width;
+    a.window = window;
+    a.sinks = sinks;
+    a.nst = p.nst;
+    a.qscale = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+    a.counters = reinterpret_cast<int32_t *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(ws + off_ml);
+    a.part_o = reinterpret_cast<float *>(ws + off_o);
+    a.status = status;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = pages->type == SD_KV_F16    ? pa_launch_d<SD_KV_F16>(D, p, a, tmk, tmv, s)
+                          : pages->type == SD_KV_BF16 ? pa_launch_d<SD_KV_BF16>(D, p, a, tmk, tmv, s)
+                                                      : pa_launch_d<SD_KV_I8>(D, p, a, tmk, tmv, s);
+    return e == cudaSuccess ? SD_OK : SD_ECUDA;
+}
+
+}  // extern "C"
