@@ -20,210 +20,9 @@
 // fp32), into three bf16 parts for bf16 rows.  Softmax statistics are fp32 in exp2 units.  A tile's product
 // starts from zero and is added to the rescaled outputs by fp32 FMAs: the tensor cores' own accumulation
 // truncates, a bias that grows with the tiles (1.2e-5 of the result at 40000 rows against 64 bits).
-#include "sdv_paged.cuh"
+#include "sdv_paged_attn.cuh"
 
 namespace sdv {
-
-constexpr int PA_KT = 64;          // keys per tile
-constexpr int PA_CW = 4;           // consumer warps, 16 keys of a tile each
-constexpr int PA_THREADS = 32 * (PA_CW + 1);
-constexpr float PA_NEG = -3.402823466e38f;  // running-max start: finite, below every score
-constexpr float PA_PS = 16384.0f;  // fp16 weights are scaled by 2^14 (exact)
-constexpr uint64_t PA_WAIT_NS = 2000000000ull;
-
-struct PagedArgs {
-    const float *q;  // row i of sequence b at b * q_sb + i * q_sm, heads contiguous
-    float *out;
-    const int32_t *table, *lens, *n_new, *parent;
-    const float *k_scale, *v_scale;  // 8-bit rows: [n_pages][H_kv][P]
-    int64_t q_sb, q_sm, o_sb, o_sm;
-    int32_t B, M, H, H_kv, g, P, n_pages, width, window, sinks;
-    int32_t nst;          // ring stages
-    float qscale;         // log2(e) / sqrt(D)
-    float *part_o;        // [2 * grid][8 NT][D]
-    float2 *part_ml;      // [2 * grid][8 NT]
-    int32_t *counters;    // [grid], zero between calls
-    int *status;
-};
-
-template <int T, int D>
-struct PaLayout {
-    static constexpr int ELT = T == SD_KV_I8 ? 1 : 2;
-    static constexpr int ROWB = D * ELT < 128 ? D * ELT : 128;  // bytes of a row in one tensor tile
-    static constexpr int NB = D * ELT / ROWB;                   // tensor tiles across a row
-    static constexpr int TILE = PA_KT * ROWB;
-    static constexpr int KV = NB * TILE;                        // K (or V) rows of a stage
-    static constexpr int SCALES = T == SD_KV_I8 ? 1024 : 0;     // 64 + 64 row scales, padded to the swizzle's alignment
-    static constexpr int STAGE = 2 * KV + SCALES;
-    static constexpr int SW = ROWB / 16 - 1;                    // swizzle mask over the 16-byte chunks
-    static constexpr int SSH = ROWB == 128 ? 0 : 1;             // 64-byte rows: two rows per 128-byte line
-};
-
-// byte offset inside a stage's K (or V) rows of the 16-byte chunk that holds bytes x .. of row r
-template <int T, int D>
-__device__ __forceinline__ uint32_t pa_off(int r, int x) {
-    using L = PaLayout<T, D>;
-    return static_cast<uint32_t>((x / L::ROWB) * L::TILE + r * L::ROWB + ((((x % L::ROWB) >> 4) ^ ((r >> L::SSH) & L::SW)) << 4));
-}
-
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *tm, int x, int y, int z, int w, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void pa_ldsm(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void pa_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t pa_movm(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-template <int T>
-__device__ __forceinline__ void pa_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (T == SD_KV_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// An fp32 pair as 16-bit parts that add up to it: two fp16 (each halves the rounding 2^-11 left by the part
-// before: 2^-22 in all) or three bf16 (2^-8 each: 2^-24).
-template <int T>
-struct Parts {
-    static constexpr int N = T == SD_KV_BF16 ? 3 : 2;
-    uint32_t r[N];
-};
-template <int T>
-__device__ __forceinline__ Parts<T> split2(float x0, float x1) {
-    Parts<T> p;
-#pragma unroll
-    for (int i = 0; i < Parts<T>::N; ++i) {
-        if constexpr (T == SD_KV_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-            const float2 f = __bfloat1622float2(h);
-            p.r[i] = *reinterpret_cast<const uint32_t *>(&h);
-            x0 -= f.x;
-            x1 -= f.y;
-        } else {
-            const __half2 h = __floats2half2_rn(x0, x1);
-            const float2 f = __half22float2(h);
-            p.r[i] = *reinterpret_cast<const uint32_t *>(&h);
-            x0 -= f.x;
-            x1 -= f.y;
-        }
-    }
-    return p;
-}
-
-// two of a word's four int8 codes (bytes picked by sel, as selector nibbles 0..3) as an exact fp16 pair:
-// the code plus 128 in the mantissa of 1024, minus 1152
-template <int B0, int B1>
-__device__ __forceinline__ uint32_t codes2(uint32_t biased) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(biased), "r"(0x64646464u), "n"(B0 | (4 << 4) | (B1 << 8) | (4 << 12)));
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&r), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// The tiles of one sequence: [0, n_sink) and from tile lo_tile on, T in all.
-struct SeqTiles {
-    int32_t n_sink, lo_tile, T;
-};
-__device__ __forceinline__ SeqTiles seq_tiles(int len, int n, int window, int sinks) {
-    SeqTiles s;
-    const int total = len + n;
-    int lo = 0;
-    if (window > 0 && len - window + 1 > 0) lo = len - window + 1;  // the first row (depth 0) reaches furthest back
-    s.lo_tile = lo / PA_KT;
-    const int st = window > 0 ? min((min(sinks, lo) + PA_KT - 1) / PA_KT, s.lo_tile) : 0;
-    s.n_sink = st;
-    s.T = st + (total + PA_KT - 1) / PA_KT - s.lo_tile;
-    return s;
-}
-
-// new rows that position i of a sequence sees: its path, cut by the window (the path's k-th node stands at depth k)
-__device__ __forceinline__ uint32_t new_rows_seen(const PagedArgs &a, int b, int i, int len, int &depth) {
-    uint32_t path = 0;
-    if (!a.parent) {
-        path = (2u << i) - 1u;
-    } else {
-        int x = i;
-        for (int step = 0; step <= i && x >= 0; ++step) {
-            path |= 1u << x;
-            const int p = a.parent[static_cast<int64_t>(b) * a.M + x];
-            if (p >= x) {  // parents come before their children; anything else is a bad tree
-                set_status(a.status, SD_EDEVICE);
-                break;
-            }
-            x = p;
-        }
-    }
-    depth = __popc(path) - 1;
-    if (a.window > 0) {
-        uint32_t keep = 0, left = path;
-        for (int k = 0; left; ++k) {
-            const uint32_t bit = left & (0u - left);
-            left ^= bit;
-            if (k > depth - a.window || len + k < a.sinks) keep |= bit;
-        }
-        path = keep;
-    }
-    return path;
-}
-
-// One piece of a CTA's share: tiles [t0, t1) of the run of (b, kh, rg).
-struct Piece {
-    int32_t b, kh, rg, t0, t1, len, n;
-    SeqTiles st;
-    int64_t run0;  // the run's first tile in the whole line
-};
-
-struct Sched {
-    const int64_t *prefix;  // [B + 1]: tiles of the sequences before
-    const int2 *ln;         // [B]: (len, n_new), n_new 0 where nothing is to be done
-    int64_t u0, u1, W;
-    int32_t G;              // CTAs that share the line
-};
-
-template <int RPG>
-__device__ __forceinline__ Piece piece_at(const PagedArgs &a, const Sched &s, int64_t u, int b) {
-    Piece p;
-    while (s.prefix[b + 1] <= u) ++b;
-    p.b = b;
-    const int2 ln = s.ln[b];
-    p.len = ln.x;
-    p.n = ln.y;
-    p.st = seq_tiles(p.len, p.n, a.window, a.sinks);
-    const int64_t rem = u - s.prefix[b];
-    const int64_t run = rem / p.st.T;
-    p.t0 = static_cast<int32_t>(rem - run * p.st.T);
-    p.run0 = u - p.t0;
-    const int RG = (p.n * a.g + RPG - 1) / RPG;
-    p.kh = static_cast<int32_t>(run / RG);
-    p.rg = static_cast<int32_t>(run - static_cast<int64_t>(p.kh) * RG);
-    const int64_t left = s.u1 - u;
-    p.t1 = left < p.st.T - p.t0 ? p.t0 + static_cast<int32_t>(left) : p.st.T;
-    return p;
-}
-__device__ __forceinline__ int cta_of(const Sched &s, int64_t u) { return static_cast<int>(((u + 1) * s.G - 1) / s.W); }
 
 template <int T, int D, int NT>
 __global__ void __launch_bounds__(PA_THREADS) paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
@@ -249,114 +48,14 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attn_kernel(const PagedArgs 
         }
         *abort = 0;
         fence_barrier_init();
-        prefix[0] = 0;
     }
     pdl_wait();
     pdl_launch_dependents();
-    // the schedule: tiles per sequence, then their running sum
-    for (int b = tid; b < a.B; b += PA_THREADS) {
-        int len = a.lens[b], n = a.n_new ? a.n_new[b] : a.M;
-        if (len < 0 || n < 0 || n > a.M || static_cast<int64_t>(len) + n > static_cast<int64_t>(a.width) * a.P) {
-            set_status(a.status, SD_EDEVICE);
-            n = 0;
-        }
-        int64_t cost = 0;
-        if (n > 0)
-            cost = static_cast<int64_t>(seq_tiles(len, n, a.window, a.sinks).T) * ((n * a.g + RPG - 1) / RPG) * a.H_kv;
-        ln[b] = make_int2(len, n);
-        prefix[b + 1] = cost;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int64_t run = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int b = b0 + lane;
-            int64_t v = b < a.B ? prefix[b + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += y;
-            }
-            if (b < a.B) prefix[b + 1] = run + v;
-            run += __shfl_sync(0xffffffffu, v, 31);
-        }
-    }
-    __syncthreads();
     Sched sc;
-    sc.prefix = prefix;
-    sc.ln = ln;
-    sc.W = prefix[a.B];
-    sc.G = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), sc.W));
-    if (static_cast<int64_t>(blockIdx.x) >= sc.W) return;
-    sc.u0 = static_cast<int64_t>(blockIdx.x) * sc.W / sc.G;
-    sc.u1 = static_cast<int64_t>(blockIdx.x + 1) * sc.W / sc.G;
+    if (!make_sched<RPG, PA_THREADS>(a, prefix, ln, sc)) return;
 
     if (warp == PA_CW) {
-        // ---- producer warp: lane l issues copies l, l + 32, .. of a tile (page, K or V, 128 bytes of row)
-        const int rows = min(a.P, PA_KT), npt = PA_KT / rows;  // rows of a page in a tile, pages per tile
-        const int ncopy = npt * 2 * LY::NB;
-        int64_t u = sc.u0;
-        int b = 0, slot = 0, issued = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        while (ok && u < sc.u1) {
-            const Piece p = piece_at<RPG>(a, sc, u, b);
-            b = p.b;
-            const int32_t *tab = a.table + static_cast<int64_t>(b) * a.width;
-            const int total = p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
-            // page of this lane's place in tile t (a place without rows, or an entry that is no page, reads as zeros)
-            auto page_of = [&](int t) {
-                const int key = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT + (lane % npt) * rows;
-                if (key >= total) return a.n_pages;
-                const int pg = tab[key / a.P];
-                if (pg >= 0 && pg < a.n_pages) return pg;
-                if (key + rows > lo || key < sink) set_status(a.status, SD_EDEVICE);  // a row of it is visible
-                return a.n_pages;
-            };
-            int pg = page_of(p.t0);
-            for (int t = p.t0; t < p.t1; ++t) {
-                const int next = t + 1 < p.t1 ? page_of(t + 1) : 0;  // in flight while this tile waits for its stage
-                const int key0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT;
-                if (issued >= a.nst && !mbar_wait_bounded(&empty[slot], ph ^ 1u, PA_WAIT_NS, abort)) {
-                    set_status(a.status, SD_ETIMEOUT);
-                    *abort = 1;
-                }
-                if (!__all_sync(0xffffffffu, *abort == 0)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *stp = ring + static_cast<size_t>(slot) * LY::STAGE;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&full[slot], 2 * LY::KV + (T == SD_KV_I8 ? 2 * PA_KT * 4 : 0));
-                __syncwarp();
-                for (int i = lane; i < ncopy; i += 32) {
-                    // page place i % npt: this lane's own (npt divides 32)
-                    const int place = i % npt, half = (i / npt) % LY::NB, kv = i / npt / LY::NB;
-                    const uint32_t dst = smem_u32(stp) + kv * LY::KV + half * LY::TILE + place * rows * LY::ROWB;
-                    tma_4d(dst, kv ? &tmv : &tmk, half * (LY::ROWB / LY::ELT), key0 % a.P, p.kh, pg, &full[slot]);
-                }
-                if constexpr (T == SD_KV_I8) {
-                    if (lane < 2 * npt) {
-                        const int place = lane % npt, kv = lane / npt;
-                        const int64_t page = pg < a.n_pages ? pg : 0;  // a place without rows: any page's scales
-                        const float *src = (kv ? a.v_scale : a.k_scale) + (page * a.H_kv + p.kh) * a.P + key0 % a.P;
-                        bulk_g2s_l2keep(stp + 2 * LY::KV + kv * PA_KT * 4 + place * rows * 4, src, rows * 4, &full[slot]);
-                    }
-                }
-                ++issued;
-                if (++slot == a.nst) {
-                    slot = 0;
-                    ph ^= 1u;
-                }
-                pg = next;
-            }
-            u += p.t1 - p.t0;
-        }
-        if (!ok && lane == 0) {  // never leave with copies in flight
-            for (int i = max(0, issued - a.nst); i < issued; ++i)
-                mbar_wait_bounded(&full[i % a.nst], (i / a.nst) & 1u, PA_WAIT_NS);
-        }
-        __syncwarp();
+        produce_tiles<T, D, RPG>(a, sc, &tmk, &tmv, ring, a.nst, full, empty, abort);
         return;
     }
 
@@ -762,31 +461,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attn_kernel(const PagedArgs 
             }
             named_bar_sync(1, 32 * PA_CW);
             if (*last) {
-                __threadfence();
-                for (int idx = tid; idx < RPG * (D / 4); idx += 32 * PA_CW) {
-                    const int tr = idx / (D / 4), d = idx % (D / 4) * 4, tg = p.rg * RPG + tr;
-                    if (tg >= rows) break;
-                    float mx = PA_NEG;
-                    for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(&a.part_ml[(2 * x + (x == c0)) * RPG + tr]).x);
-                    float lv = 0.0f;
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int x = c0; x <= c1; ++x) {
-                        const int sl = 2 * x + (x == c0);
-                        const float2 ml = __ldcg(&a.part_ml[sl * RPG + tr]);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (static_cast<int64_t>(sl) * RPG + tr) * D + d));
-                        const float fx = exp2f(ml.x - mx);
-                        lv = fmaf(ml.y, fx, lv);
-                        v.x = fmaf(y.x, fx, v.x);
-                        v.y = fmaf(y.y, fx, v.y);
-                        v.z = fmaf(y.z, fx, v.z);
-                        v.w = fmaf(y.w, fx, v.w);
-                    }
-                    const float inv = lv == 0.0f ? 0.0f : 1.0f / lv;
-                    const int i = tg / a.g, h = p.kh * a.g + tg % a.g;
-                    *reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D + d) =
-                        make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                }
+                join_partials<RPG, D, 32 * PA_CW>(a, p, c0, c1, tid);
             }
         }
         u += p.t1 - p.t0;
@@ -823,14 +498,21 @@ static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
     return true;
 }
 
-// workspace: counters of the largest grid, then the partials of 16-row groups
+// Query rows of a KV head above which the tensor-memory kernel runs.
+constexpr int PA_WIDE_ROWS = 8;
+
+static bool pa_wide(int rows, int D) { return rows > PA_WIDE_ROWS && D <= 128; }
+
+// workspace: counters of the largest grid, then the partials: two per CTA, of 16 rows on two CTAs per SM or
+// of 128 rows on one
 static size_t pa_workspace(int D, size_t *off_ml, size_t *off_o) {
-    const size_t G = 2 * static_cast<size_t>(num_sms() > 0 ? num_sms() : 0);
-    if (!G) return 0;
-    const size_t ml = (G * 4 + 255) / 256 * 256, o = ml + (2 * G * 16 * 8 + 255) / 256 * 256;
+    const size_t sms = num_sms() > 0 ? num_sms() : 0;
+    if (!sms) return 0;
+    const size_t rows = sms * 2 * 128;  // 4 x 16 rows per SM take less
+    const size_t ml = (2 * sms * 4 + 255) / 256 * 256, o = ml + (rows * 8 + 255) / 256 * 256;
     if (off_ml) *off_ml = ml;
     if (off_o) *off_o = o;
-    return o + 2 * G * 16 * static_cast<size_t>(D) * 4;
+    return o + rows * static_cast<size_t>(D) * 4;
 }
 
 // K or V pages as a 4-d tensor (x = element of a row, y = row in its page, z = KV head, w = page): boxes of
@@ -934,6 +616,11 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     a.part_o = reinterpret_cast<float *>(ws + off_o);
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int rows = M * a.g;
+    if (pa_wide(rows, D)) {
+        const auto run = pages->type == SD_KV_F16 ? paged_wide_f16 : pages->type == SD_KV_BF16 ? paged_wide_bf16 : paged_wide_i8;
+        return run(a, tmk, tmv, D, rows, num_sms(), s) == cudaSuccess ? SD_OK : SD_ECUDA;
+    }
     const cudaError_t e = pages->type == SD_KV_F16    ? pa_launch_d<SD_KV_F16>(D, p, a, tmk, tmv, s)
                           : pages->type == SD_KV_BF16 ? pa_launch_d<SD_KV_BF16>(D, p, a, tmk, tmv, s)
                                                       : pa_launch_d<SD_KV_I8>(D, p, a, tmk, tmv, s);

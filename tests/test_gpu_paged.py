@@ -148,6 +148,23 @@ def test_windows_and_sinks(sdv, dtype, window, sinks, tree):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("M,H,H_kv,D", [(3, 3, 1, 128), (5, 10, 2, 64), (11, 3, 1, 128), (16, 4, 1, 64), (13, 10, 2, 128), (16, 8, 1, 64),
+                                        (9, 15, 1, 128), (16, 40, 1, 64), (16, 64, 1, 128)])
+def test_many_rows_per_kv_head(sdv, dtype, M, H, H_kv, D):
+    """From 9 to 1024 query rows of a KV head, some sequences with fewer, contexts over tile and CTA borders."""
+    lens, news = [0, 62, 64, 130, 1500], [M, 1, M - 1, 0, M]
+    check_attn(sdv, M * H, lens, news, M, H, H_kv, D, 16, dtype)
+    check_attn(sdv, M * H + 1, [400, 90], [M, M], M, H, H_kv, D, 32, dtype, nhd=True, parents=[binary(M)] * 2, window=100, sinks=3)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("H", [1, 4])
+def test_many_rows_over_long_contexts(sdv, dtype, H):
+    """Runs of more tiles than any ring holds, cut between CTAs."""
+    check_attn(sdv, 77, [30011, 5000], [16, 9], 16, H * 4, 1, 128, 64, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
 def test_long_contexts_are_split_and_joined(sdv, dtype):
     check_attn(sdv, 9, [20011, 0, 64, 9000], [3, 1, 3, 2], 3, 4, 1, 128, 64, dtype)
 
@@ -174,13 +191,14 @@ def test_many_sequences(sdv):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
 @pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
-def test_unseen_rows_may_hold_anything(sdv, dtype, what):
+@pytest.mark.parametrize("H", [1, 2, 7, 15, 30])
+def test_unseen_rows_may_hold_anything(sdv, dtype, what, H):
     """A tree's sibling and a row behind one position's window hold NaN or infinities in K and V: the positions that do not
     see them are exact, the others are not numbers (or infinite) where V is."""
     rng = np.random.default_rng(4)
     L, M, window, parent = 100, 5, 40, [-1, 0, 0, 1, 2]
     c = Cache(sdv, rng, [L], [M], M, 1, 128, 16, dtype)
-    q = rng.standard_normal((1, M, 2, 128)).astype(np.float32)
+    q = rng.standard_normal((1, M, H, 128)).astype(np.float32)
     see = plain.seen_rows(L, M, parent, window, 4)
     bad_old, bad_new = L - window + 1, L + 4  # the first only the root sees, the second only node 4
     assert see[:, bad_old].tolist() == [True, False, False, False, False] and see[:, bad_new].tolist() == [False] * 4 + [True]
@@ -198,12 +216,13 @@ def test_unseen_rows_may_hold_anything(sdv, dtype, what):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-def test_infinite_values_reach_the_rows_that_see_them_alone(sdv, dtype):
+@pytest.mark.parametrize("H", [1, 3, 10, 25])
+def test_infinite_values_reach_the_rows_that_see_them_alone(sdv, dtype, H):
     """V alone holds an infinity in one column of a new row: the same column of the positions that see it, and nothing else."""
     rng = np.random.default_rng(14)
     L, M = 30, 4
     c = Cache(sdv, rng, [L], [M], M, 1, 64, 8, dtype)
-    q = rng.standard_normal((1, M, 3, 64)).astype(np.float32)
+    q = rng.standard_normal((1, M, H, 64)).astype(np.float32)
     j = L + 2
     c.v[int(c.table[0, j // 8]), 0, j % 8, 11] = float("inf")
     out = run_attn(sdv, c, q, [L], [M], M, None, 0, 0)[0]
