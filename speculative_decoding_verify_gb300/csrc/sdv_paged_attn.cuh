@@ -323,35 +323,43 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
     __syncwarp();
 }
 
-// The partials of one run's CTAs c0 .. c1, joined in the order of their keys by the NTHR threads that call it.
+// The partials of one run's CTAs c0 .. c1, joined in the order of their keys by the NTHR threads that call it: NTHR / RPG
+// threads (at most D / 4) per row, each with every so-many-th 4 columns and all of them in flight.
 template <int RPG, int D, int NTHR>
 __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1, int tid) {
-    const int rows = p.n * a.g;
+    constexpr int TR = NTHR / RPG < D / 4 ? NTHR / RPG : D / 4, NV = D / 4 / TR;
+    const int tr = tid / TR, tg = p.rg * RPG + tr, q = tid % TR;
+    if (tr >= RPG || tg >= p.n * a.g) return;
     __threadfence();
-    for (int idx = tid; idx < RPG * (D / 4); idx += NTHR) {
-        const int tr = idx / (D / 4), d = idx % (D / 4) * 4, tg = p.rg * RPG + tr;
-        if (tg >= rows) break;
-        float mx = PA_NEG;
-        for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(&a.part_ml[(2 * x + (x == c0)) * RPG + tr]).x);
-        float lv = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int x = c0; x <= c1; ++x) {
-            const int sl = 2 * x + (x == c0);
-            const float2 ml = __ldcg(&a.part_ml[sl * RPG + tr]);
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (static_cast<int64_t>(sl) * RPG + tr) * D + d));
-            const float fx = exp2f(ml.x - mx);
-            lv = fmaf(ml.y, fx, lv);
-            v.x = fmaf(y.x, fx, v.x);
-            v.y = fmaf(y.y, fx, v.y);
-            v.z = fmaf(y.z, fx, v.z);
-            v.w = fmaf(y.w, fx, v.w);
+    float mx = PA_NEG;
+#pragma unroll 8
+    for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(&a.part_ml[(2 * x + (x == c0)) * RPG + tr]).x);
+    float lv = 0.0f;
+    float4 v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll(NV >= 8 ? 1 : 4)
+    for (int x = c0; x <= c1; ++x) {
+        const int64_t row = static_cast<int64_t>(2 * x + (x == c0)) * RPG + tr;
+        const float2 ml = __ldcg(&a.part_ml[row]);
+        const float4 *src = reinterpret_cast<const float4 *>(a.part_o + row * D) + q;
+        float4 y[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) y[i] = __ldcg(src + i * TR);
+        const float f = exp2f(ml.x - mx);
+        lv = fmaf(ml.y, f, lv);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            v[i].x = fmaf(y[i].x, f, v[i].x);
+            v[i].y = fmaf(y[i].y, f, v[i].y);
+            v[i].z = fmaf(y[i].z, f, v[i].z);
+            v[i].w = fmaf(y[i].w, f, v[i].w);
         }
-        const float inv = lv == 0.0f ? 0.0f : 1.0f / lv;
-        const int i = tg / a.g, h = p.kh * a.g + tg % a.g;
-        *reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D + d) =
-            make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     }
+    const float inv = lv == 0.0f ? 0.0f : 1.0f / lv;
+    float4 *to = reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + (tg / a.g) * a.o_sm + static_cast<int64_t>(p.kh * a.g + tg % a.g) * D) + q;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) to[i * TR] = make_float4(v[i].x * inv, v[i].y * inv, v[i].z * inv, v[i].w * inv);
 }
 
 // The many-row kernel (sdv_paged_wide.cuh): D = 64 or 128, `rows` the most query rows of a KV head, one CTA per SM.
