@@ -155,9 +155,45 @@ struct WideLayout {
     static constexpr int NBAR = 2 * NOP + 2 * NRAW + 8 + 3;
     static constexpr size_t fixed() { return 1024 + static_cast<size_t>(NOP) * OSTAGE + static_cast<size_t>(NRAW) * PaLayout<T, D>::STAGE + SCRATCH + NBAR * 8 + 64; }
     // registers per thread as launched, then of the softmax, of producer and MMA, of the converting warps
-    static constexpr int REG_L = I8 ? 128 : 168, REG_S = I8 ? 184 : 208, REG_P = I8 ? 72 : 88, REG_C = 72;
+    static constexpr int REG_L = I8 ? 128 : 168, REG_S = I8 ? 192 : 224, REG_P = I8 ? 64 : 56, REG_C = 64;
     static_assert(PW_SOFT * REG_S + 128 * REG_P + (I8 ? 128 * REG_C : 0) <= THREADS * REG_L, "registers");
 };
+
+// bits e < 32 of the keys key0 + e in [lo, hi)
+__device__ __forceinline__ uint32_t key_range(int key0, int lo, int hi) {
+    const int l = min(max(lo - key0, 0), 32), h = min(max(hi - key0, 0), 32);
+    return h <= l ? 0u : (0xffffffffu >> (32 - (h - l))) << l;
+}
+// bits e < 32: whether a row sees key key0 + e.  low: the first committed row of its window (INT32_MAX: no row at
+// all), sink: the first rows that stay visible, vis: the new rows on its path
+__device__ __forceinline__ uint32_t seen_keys(int key0, int len, int low, int sink, uint32_t vis) {
+    uint32_t m = key_range(key0, low, len);
+    if (low != INT32_MAX) m |= key_range(key0, 0, min(sink, len));
+    const int d = len - key0;
+    return m | (d >= 32 || d <= -32 ? 0u : d >= 0 ? vis << d : vis >> -d);
+}
+
+// What V rows with a NaN or infinity (bits of bad) add to the outputs acc of this thread: weight times value where the row
+// sees the key and has a weight for it, and nothing elsewhere.  Rare: kept out of the tile's code.
+template <int T, int D, int DO>
+__device__ __noinline__ void add_bad_rows(float *acc, const uint8_t *v_rows, uint2 bad, uint2 seen, uint32_t scores, float back, float off, int d0) {
+    for (int j = 0; j < PA_KT; ++j) {
+        if (!(((j < 32 ? bad.x : bad.y) >> (j & 31)) & 1u)) continue;
+        uint32_t y;
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(y) : "r"(scores + j) : "memory");
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(y)::"memory");
+        const float w = ((j < 32 ? seen.x : seen.y) >> (j & 31)) & 1u ? ex2(fmaf(__uint_as_float(y), back, off)) : 0.0f;
+#pragma unroll 1
+        for (int d = 0; d < DO; ++d) {
+            const int x = 2 * (d0 + d);
+            const uint16_t h = *reinterpret_cast<const volatile uint16_t *>(v_rows + pa_off<T, D>(j, x) + (x & 15));
+            float v;
+            if constexpr (T == SD_KV_BF16) v = __bfloat162float(__ushort_as_bfloat16(h));
+            else v = __half2float(__ushort_as_half(h));
+            if (w > 0.0f) acc[d] += w * v;
+        }
+    }
+}
 
 template <int R>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
@@ -276,8 +312,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 ok = scores() && (n < 2 || scores());
                 for (int i = 0; ok && i < n; ++i) {
                     const uint32_t sb = npv & 1u, ob2 = npv % W::NPV;
-                    ok = wait(&p_ready[sb], (npv >> 1) & 1u);
-                    if (ok && npv >= W::NPV) ok = wait(&pv_free[(npv - W::NPV) & 1u], ((npv - W::NPV) >> 1) & 1u);
+                    ok = npv < W::NPV || wait(&pv_free[(npv - W::NPV) & 1u], ((npv - W::NPV) >> 1) & 1u);
+                    ok = ok && wait(&p_ready[sb], (npv >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t vb = ob + pv_slot * W::OSTAGE + W::OKV, d = tm + W::TO + ob2 * D, pa = tm + W::TS + sb * W::SCOLS;
@@ -400,7 +436,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         while (u < sc.u1) {
             const Piece p = piece_at<RP>(a, sc, u, b);
             b = p.b;
-            const int rows = p.n * a.g, total = p.len + p.n, tg = p.rg * RP + r;
+            const int rows = p.n * a.g, tg = p.rg * RP + r;
             const bool real = tg < rows;
             float2 o[W::DO / 2];
             float back = 1.0f;
@@ -457,8 +493,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
             // adds this thread's columns of the product of tile number i to the outputs
             auto add_product = [&](uint32_t i) {
-                const bool got = wait(&pv_full[i & 1u], (i >> 1) & 1u);
-                if (!__all_sync(0xffffffffu, got)) return false;
+                if (!__all_sync(0xffffffffu, wait(&pv_full[i & 1u], (i >> 1) & 1u))) return false;
                 tc_fence_after();
                 const uint32_t at = tq + W::TO + (i % W::NPV) * D + grp * W::DO;
                 uint32_t y[W::DO / 32][32];
@@ -513,13 +548,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     }
                 }
                 if (!whole) {
+                    const uint32_t seen = seen_keys(key0, p.len, low, full_sink, vis);
 #pragma unroll
-                    for (int e = 0; e < NC; ++e) {
-                        const int j = key0 + e;
-                        const bool seen = j >= p.len ? j < total && ((vis >> (j - p.len)) & 1u) != 0
-                                                     : j >= low || (j < full_sink && low != INT32_MAX);
-                        if (!seen) (e & 1 ? s[e / 2].y : s[e / 2].x) = -INFINITY;
-                    }
+                    for (int e = 0; e < NC; ++e)
+                        if (!((seen >> e) & 1u)) (e & 1 ? s[e / 2].y : s[e / 2].x) = -INFINITY;
                 }
                 float x2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -533,6 +565,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     if (!whole) {
                         // V rows with a NaN or infinity reach the rows that see them alone: added here, and cleared before the product
                         uint32_t bw[2] = {0, 0};
+#pragma unroll 1
                         for (int x = tid; x < PA_KT * (2 * D / 16); x += PW_SOFT) {
                             const int vr = x % PA_KT;
                             const uint4 v = *reinterpret_cast<const uint4 *>(stage + W::OKV + pa_off<T, D>(vr, (x / PA_KT) * 16));
@@ -554,29 +587,21 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         if (tid == 0) other[0] = other[1] = 0;  // read by all before the barrier above
                         if (ok && (bad[0] | bad[1])) {
                             if (t > p.t0) ok = add_product(nt - 1);
+                            float acc[W::DO];
 #pragma unroll
-                            for (int d = 0; d < W::DO / 2; ++d) o[d] = fmul2_rn(o[d], make_float2(an, an));
-                            rescaled = true;
-                            for (int j = 0; j < PA_KT; ++j) {
-                                if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
-                                uint32_t y;  // this row's weight of key j, from its score
-                                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(y) : "r"(sc_at + j) : "memory");
-                                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(y)::"memory");
-                                const int jj = tile0 + j;
-                                const bool seen = jj >= p.len ? jj < total && ((vis >> (jj - p.len)) & 1u) != 0
-                                                              : jj >= low || (jj < full_sink && low != INT32_MAX);
-                                const float w = seen && part == 0 && j >= l_at && j < l_at + W::KL ? ex2(fmaf(__uint_as_float(y), back, off)) : 0.0f;
-#pragma unroll
-                                for (int d = 0; d < W::DO; ++d) {
-                                    const int x = 2 * (grp * W::DO + d);
-                                    const uint16_t h = *reinterpret_cast<const volatile uint16_t *>(stage + W::OKV + pa_off<T, D>(j, x) + (x & 15));
-                                    float v;
-                                    if constexpr (T == SD_KV_BF16) v = __bfloat162float(__ushort_as_bfloat16(h));
-                                    else v = __half2float(__ushort_as_half(h));
-                                    if (w > 0.0f) (d & 1 ? o[d / 2].y : o[d / 2].x) += w * v;
-                                }
+                            for (int d = 0; d < W::DO / 2; ++d) {
+                                acc[2 * d] = o[d].x * an;
+                                acc[2 * d + 1] = o[d].y * an;
                             }
+                            rescaled = true;
+                            uint2 seen = make_uint2(seen_keys(tile0, p.len, low, full_sink, vis), seen_keys(tile0 + 32, p.len, low, full_sink, vis));
+                            seen.x &= part == 0 ? key_range(0, l_at, l_at + W::KL) : 0u;  // this lane's keys, once for all parts
+                            seen.y &= part == 0 ? key_range(32, l_at, l_at + W::KL) : 0u;
+                            add_bad_rows<T, D, W::DO>(acc, stage + W::OKV, make_uint2(bad[0], bad[1]), seen, sc_at, back, off, grp * W::DO);
+#pragma unroll
+                            for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(acc[2 * d], acc[2 * d + 1]);
                             ok = sync_all() && ok;
+#pragma unroll 1
                             for (int x = tid; x < PA_KT * (2 * D / 16); x += PW_SOFT) {
                                 const int vr = x % PA_KT;
                                 if ((bad[vr >> 5] >> (vr & 31)) & 1u)
