@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attn_kernel(const PagedArgs 
             }
             named_bar_sync(1, 32 * PA_CW);
             if (*last) {
-                join_partials<RPG, D, 32 * PA_CW>(a, p, c0, c1, tid);
+                join_partials<RPG, D, 32 * PA_CW>(a, p, c0, c1, tid, sm_o, 1);
             }
         }
         u += p.t1 - p.t0;
@@ -498,10 +498,11 @@ static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
     return true;
 }
 
-// Query rows of a KV head above which the tensor-memory kernel runs.
-constexpr int PA_WIDE_ROWS = 8;
+// Query rows of a KV head above which the tensor-memory kernel runs; its shared memory holds the schedule of PA_WIDE_B
+// sequences.
+constexpr int PA_WIDE_ROWS = 8, PA_WIDE_B = 512;
 
-static bool pa_wide(int rows, int D) { return rows > PA_WIDE_ROWS && D <= 128; }
+static bool pa_wide(int rows, int D, int B) { return rows > PA_WIDE_ROWS && D <= 128 && B <= PA_WIDE_B; }
 
 // workspace: counters of the largest grid, then the partials: two per CTA, of 16 rows on two CTAs per SM or
 // of 128 rows on one
@@ -617,7 +618,7 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int rows = M * a.g;
-    if (pa_wide(rows, D)) {
+    if (pa_wide(rows, D, B)) {
         const auto run = pages->type == SD_KV_F16 ? paged_wide_f16 : pages->type == SD_KV_BF16 ? paged_wide_bf16 : paged_wide_i8;
         return run(a, tmk, tmv, D, rows, num_sms(), s) == cudaSuccess ? SD_OK : SD_ECUDA;
     }

@@ -323,43 +323,84 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
     __syncwarp();
 }
 
-// The partials of one run's CTAs c0 .. c1, joined in the order of their keys by the NTHR threads that call it: NTHR / RPG
-// threads (at most D / 4) per row, each with every so-many-th 4 columns and all of them in flight.
+// The partials of one run's CTAs c0 .. c1, joined in the order of their keys by the NTHR threads that call it (named
+// barrier `bar` among them).  A warp reads whole rows (a row of D = 64 half a warp), JC CTAs at a time: the weights of all
+// rows come first, through shared memory (RPG * (JC + 2) floats), then every load of a pass is in flight at once.
+constexpr int JC = 8;
 template <int RPG, int D, int NTHR>
-__device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1, int tid) {
-    constexpr int TR = NTHR / RPG < D / 4 ? NTHR / RPG : D / 4, NV = D / 4 / TR;
-    const int tr = tid / TR, tg = p.rg * RPG + tr, q = tid % TR;
-    if (tr >= RPG || tg >= p.n * a.g) return;
+__device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1, int tid, float *sm, int bar) {
+    constexpr int LR = D / 4 < 32 ? D / 4 : 32, NV = D / 4 / LR;  // lanes of a row, 16-byte columns per lane
+    constexpr int RT = NTHR / LR, NR = (RPG + RT - 1) / RT;       // rows at a time, rows per thread
+    constexpr int XU = 16 / (NR * NV) > 0 ? (16 / (NR * NV) < JC ? 16 / (NR * NV) : JC) : 1;
+    const int rows = min(RPG, p.n * a.g - p.rg * RPG);
+    float *mx_of = sm, *sum_of = sm + RPG, *weight = sm + 2 * RPG;  // weight [JC][RPG]
     __threadfence();
-    float mx = PA_NEG;
+    auto ml_of = [&](int x, int tr) { return __ldcg(&a.part_ml[static_cast<int64_t>(2 * x + (x == c0)) * RPG + tr]); };
+    if (tid < rows) {
+        float mx = PA_NEG, lv = 0.0f;
 #pragma unroll 8
-    for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(&a.part_ml[(2 * x + (x == c0)) * RPG + tr]).x);
-    float lv = 0.0f;
-    float4 v[NV];
+        for (int x = c0; x <= c1; ++x) {
+            const float2 ml = ml_of(x, tid);
+            const float n = fmaxf(mx, ml.x);
+            lv = fmaf(lv, exp2f(mx - n), ml.y * exp2f(ml.x - n));
+            mx = n;
+        }
+        mx_of[tid] = mx;
+        sum_of[tid] = lv == 0.0f ? 0.0f : 1.0f / lv;
+    }
+    const int r0 = tid / LR, col = tid % LR;
+    float4 v[NR][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll(NV >= 8 ? 1 : 4)
-    for (int x = c0; x <= c1; ++x) {
-        const int64_t row = static_cast<int64_t>(2 * x + (x == c0)) * RPG + tr;
-        const float2 ml = __ldcg(&a.part_ml[row]);
-        const float4 *src = reinterpret_cast<const float4 *>(a.part_o + row * D) + q;
-        float4 y[NV];
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) y[i] = __ldcg(src + i * TR);
-        const float f = exp2f(ml.x - mx);
-        lv = fmaf(ml.y, f, lv);
+        for (int k = 0; k < NV; ++k) v[i][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int x0 = c0; x0 <= c1; x0 += JC) {
+        const int nx = min(JC, c1 - x0 + 1);
+        named_bar_sync(bar, NTHR);
+        for (int i = tid; i < nx * rows; i += NTHR) {
+            const int x = i / rows, tr = i - x * rows;
+            weight[x * RPG + tr] = exp2f(ml_of(x0 + x, tr).x - mx_of[tr]);
+        }
+        named_bar_sync(bar, NTHR);
+        for (int xs = 0; xs < nx; xs += XU) {
+            float4 y[XU][NR][NV];
+            float f[XU][NR];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            v[i].x = fmaf(y[i].x, f, v[i].x);
-            v[i].y = fmaf(y[i].y, f, v[i].y);
-            v[i].z = fmaf(y[i].z, f, v[i].z);
-            v[i].w = fmaf(y[i].w, f, v[i].w);
+            for (int x = 0; x < XU; ++x)
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const int tr = r0 + i * RT, xc = x0 + xs + x;
+                    const bool on = xs + x < nx && tr < rows;
+                    f[x][i] = on ? weight[(xs + x) * RPG + tr] : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+                        y[x][i][k] = on ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + (static_cast<int64_t>(2 * xc + (xc == c0)) * RPG + tr) * D) + col + k * LR)
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+            for (int x = 0; x < XU; ++x)
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        v[i][k].x = fmaf(y[x][i][k].x, f[x][i], v[i][k].x);
+                        v[i][k].y = fmaf(y[x][i][k].y, f[x][i], v[i][k].y);
+                        v[i][k].z = fmaf(y[x][i][k].z, f[x][i], v[i][k].z);
+                        v[i][k].w = fmaf(y[x][i][k].w, f[x][i], v[i][k].w);
+                    }
         }
     }
-    const float inv = lv == 0.0f ? 0.0f : 1.0f / lv;
-    float4 *to = reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + (tg / a.g) * a.o_sm + static_cast<int64_t>(p.kh * a.g + tg % a.g) * D) + q;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) to[i * TR] = make_float4(v[i].x * inv, v[i].y * inv, v[i].z * inv, v[i].w * inv);
+    for (int i = 0; i < NR; ++i) {
+        const int tr = r0 + i * RT, tg = p.rg * RPG + tr;
+        if (tr < rows) {
+            const float inv = sum_of[tr];
+            float4 *to = reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + (tg / a.g) * a.o_sm + static_cast<int64_t>(p.kh * a.g + tg % a.g) * D) + col;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) to[k * LR] = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
+        }
+    }
+    named_bar_sync(bar, NTHR);
 }
 
 // The many-row kernel (sdv_paged_wide.cuh): D = 64 or 128, `rows` the most query rows of a KV head, one CTA per SM.

@@ -150,8 +150,8 @@ struct WideLayout {
     static constexpr int NPV = QCOLS + 2 * SCOLS + 2 * D <= 512 ? 2 : 1;  // product buffers
     static constexpr int TO = TS + 2 * SCOLS;
     static_assert(TO + NPV * D <= 512, "tensor memory");
-    // shared memory after the rings: 8 columns of every softmax thread's outputs, the threads' maxima (two turns) and sums
-    static constexpr int SCRATCH = PW_SOFT * 12 * 4 + 3 * PW_SOFT * 4;
+    // shared memory after the rings: 16 columns of every softmax thread's outputs, the threads' maxima (two turns) and sums
+    static constexpr int SCRATCH = PW_SOFT * 20 * 4 + 3 * PW_SOFT * 4;
     static constexpr int NBAR = 2 * NOP + 2 * NRAW + 8 + 3;
     static constexpr size_t fixed() { return 1024 + static_cast<size_t>(NOP) * OSTAGE + static_cast<size_t>(NRAW) * PaLayout<T, D>::STAGE + SCRATCH + NBAR * 8 + 64; }
     // registers per thread as launched, then of the softmax, of producer and MMA, of the converting warps
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
     uint8_t *ops = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *raw = ops + static_cast<size_t>(W::NOP) * W::OSTAGE;  // 8-bit rows: the copies' ring
     float *scratch = reinterpret_cast<float *>(raw + static_cast<size_t>(W::NRAW) * LY::STAGE);
-    float *sm_m = scratch + PW_SOFT * 12, *sm_l = sm_m + 2 * PW_SOFT;
+    float *sm_m = scratch + PW_SOFT * 20, *sm_l = sm_m + 2 * PW_SOFT;
     uint64_t *op_full = reinterpret_cast<uint64_t *>(sm_l + PW_SOFT), *op_empty = op_full + W::NOP;
     uint64_t *raw_full = op_empty + W::NOP, *raw_empty = raw_full + W::NRAW;
     // in turns of two tiles, whatever the number of product buffers
@@ -442,17 +442,37 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             float back = 1.0f;
             {
                 // this thread's columns of the row's query into tensor memory, in parts; fp16 parts scaled by a power of two as in
-                // paged_attn_kernel
-                const float4 *qp = reinterpret_cast<const float4 *>(a.q + p.b * a.q_sb + (real ? tg / a.g : 0) * a.q_sm +
-                                                                    static_cast<int64_t>(p.kh * a.g + (real ? tg % a.g : 0)) * D + grp * W::DO);
+                // paged_attn_kernel.  The rows are read 64 bytes at a time by four threads and turned through shared memory
+                constexpr int LQ = RP * 4 / PW_SOFT > 0 ? RP * 4 / PW_SOFT : 1;  // 16-byte loads of a thread per 16 columns
+                float4 in[D / 16][LQ];
+#pragma unroll
+                for (int k = 0; k < LQ; ++k) {
+                    const int tr = (tid >> 2) + k * (PW_SOFT / 4), y = p.rg * RP + tr;
+                    const bool on = tr < RP && y < rows;
+                    const float4 *qp = reinterpret_cast<const float4 *>(a.q + p.b * a.q_sb + (on ? y / a.g : 0) * a.q_sm +
+                                                                        static_cast<int64_t>(p.kh * a.g + (on ? y % a.g : 0)) * D) + (tid & 3);
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) in[c][k] = on ? qp[4 * c] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
                 float mx = 0.0f;
 #pragma unroll
-                for (int d = 0; d < W::DO; d += 4) {
-                    const float4 f = real ? qp[d / 4] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    o[d / 2] = make_float2(f.x * a.qscale, f.y * a.qscale);
-                    o[d / 2 + 1] = make_float2(f.z * a.qscale, f.w * a.qscale);
+                for (int c = 0; c < D / 16; ++c) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) mx = fmaxf(mx, fmaxf(fabsf(o[d / 2 + e].x), fabsf(o[d / 2 + e].y)));
+                    for (int k = 0; k < LQ; ++k) {
+                        const int tr = (tid >> 2) + k * (PW_SOFT / 4);
+                        if (tr < RP) *reinterpret_cast<float4 *>(scratch + ((c & 1) * 128 + tr) * 20 + 4 * (tid & 3)) = in[c][k];
+                    }
+                    named_bar_sync(5, PW_SOFT);  // (two turns of the scratch: the next round's writes need no second barrier)
+                    if (c / (W::DO / 16) == grp) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 f = *reinterpret_cast<const float4 *>(scratch + ((c & 1) * 128 + r) * 20 + 4 * e);
+                            float2 *to = o + (c % (W::DO / 16)) * 8 + 2 * e;
+                            to[0] = make_float2(f.x * a.qscale, f.y * a.qscale);
+                            to[1] = make_float2(f.z * a.qscale, f.w * a.qscale);
+                            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(to[0].x), fabsf(to[0].y)), fmaxf(fabsf(to[1].x), fabsf(to[1].y))));
+                        }
+                    }
                 }
                 float up = 1.0f;
                 if constexpr (T != SD_KV_BF16) {
@@ -684,10 +704,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             }
             const float f = ex2(m - mx) * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
-            // 8 columns of every group at a time through shared memory: thread = 4 columns of row (tid / 8) (and of the rows 64
-            // further on), group (tid / 2) % 4
-            constexpr int RW = PW_SOFT / (2 * PW_NG), NK = (RP + RW - 1) / RW;
-            const int wg = (tid >> 1) % PW_NG, wc = wg * W::DO + 4 * (tid & 1), wr = tid / (2 * PW_NG);
+            // 16 columns of every group at a time through shared memory: thread = 4 columns of row tid / 8 (and of the rows RW
+            // further on), group (tid / 4) % 2
+            constexpr int RW = PW_SOFT / (4 * PW_NG), NK = (RP + RW - 1) / RW;
+            const int wg = (tid >> 2) % PW_NG, wc = wg * W::DO + 4 * (tid & 3), wr = tid / (4 * PW_NG);
             float *to[NK];
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
@@ -697,11 +717,11 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                                    : a.part_o + (static_cast<int64_t>(pslot) * RP + tr) * D + wc;
             }
 #pragma unroll
-            for (int d = 0; d < W::DO; d += 8) {
+            for (int d = 0; d < W::DO; d += 16) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     const float2 x = fmul2_rn(o[d / 2 + 2 * e], make_float2(f, f)), y = fmul2_rn(o[d / 2 + 2 * e + 1], make_float2(f, f));
-                    *reinterpret_cast<float4 *>(scratch + tid * 12 + 4 * e) = make_float4(x.x, x.y, y.x, y.y);
+                    *reinterpret_cast<float4 *>(scratch + tid * 20 + 4 * e) = make_float4(x.x, x.y, y.x, y.y);
                 }
                 named_bar_sync(5, PW_SOFT);
 #pragma unroll
@@ -710,7 +730,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                         for (int j = 0; j < C; ++j) {
-                            const float4 x = *reinterpret_cast<const float4 *>(scratch + (wg * 128 + j * RP + wr + RW * k) * 12 + 4 * (tid & 1));
+                            const float4 x = *reinterpret_cast<const float4 *>(scratch + (wg * 128 + j * RP + wr + RW * k) * 20 + 4 * (tid & 3));
                             v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
                         }
                         *reinterpret_cast<float4 *>(to[k] + d) = v;
@@ -727,7 +747,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     if (was == c1 - c0) a.counters[c0] = 0;
                 }
                 named_bar_sync(5, PW_SOFT);
-                if (*last) join_partials<RP, D, PW_SOFT>(a, p, c0, c1, tid);
+                if (*last) join_partials<RP, D, PW_SOFT>(a, p, c0, c1, tid, scratch, 5);
             }
             u += p.t1 - p.t0;
         }
