@@ -314,24 +314,41 @@ KV_F16, KV_BF16, KV_I8 = 0, 1, 2
 _KV_TYPES = {torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.int8: KV_I8}
 
 
-def _here(t, dtype, name, shape):
-    """The tensor's address: a contiguous tensor of that type and shape on the current device."""
-    if (t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda
-            or t.get_device() != torch.cuda.current_device()):
+def _where():
+    """(current device, its current stream): one look per call, in the form that costs the least host time."""
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _here(t, dtype, name, shape, dev):
+    """The tensor's address: a contiguous tensor of that type and shape on device dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on the current CUDA device, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows_of(t, name, B, M, heads, D):
+def _opt(t, dtype, name, shape, dev):
+    return None if t is None else _here(t, dtype, name, shape, dev)
+
+
+def _space(ws, dev):
+    """(address, bytes) of a workspace on device dev."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous workspace on the current CUDA device, got one on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _rows_of(t, name, shape, dev):
     """(address, sequence stride, row stride) of fp32 rows [B][M][heads][D] whose heads are contiguous."""
+    B, M, heads, D = shape
     sb, sm, sh, sd = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
-    if (t.dtype is not torch.float32 or tuple(t.shape) != (B, M, heads, D) or sd != 1 or (sh != D and heads > 1)
-            or not t.is_cuda or t.get_device() != torch.cuda.current_device()):
-        raise ValueError(f"{name}: expected fp32 {(B, M, heads, D)} with contiguous heads on the current CUDA device, "
+    if t.dtype is not torch.float32 or t.shape != shape or sd != 1 or (sh != D and heads > 1) or t.get_device() != dev:
+        raise ValueError(f"{name}: expected fp32 {shape} with contiguous heads on the current CUDA device, "
                          f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     # a dimension of one entry has no stride of its own
-    sm = sm if M > 1 else heads * D
+    if M == 1:
+        sm = heads * D
     return t.data_ptr(), sb if B > 1 else sm, sm
 
 
@@ -370,29 +387,28 @@ class KvPages:
                               v_scale.data_ptr() if i8 else None, _KV_TYPES[k.dtype], n, p, h, d, s[0], s[1], s[2])
         self._ref = ctypes.byref(self.desc)
 
-    def _arg(self):
-        if self.device_index != torch.cuda.current_device():
+    def _arg(self, dev):
+        if self.device_index != dev:
             raise ValueError("the pages are not on the current CUDA device")
         return self._ref
-
-
-def _opt(t, dtype, name, shape):
-    return None if t is None else _here(t, dtype, name, shape)
 
 
 def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, pages: KvPages, table: torch.Tensor, lens: torch.Tensor,
                  n_new: torch.Tensor | None = None):
     """k_new, v_new fp32 [B][M][H_kv][D] (heads contiguous, other strides free) -> rows lens[b] .. of the pages
     that table int32 [B][width] names; n_new int32 [B]: how many rows of each sequence (None: all M)."""
+    dev, stream = _where()
     B, M = k_new.shape[:2]
     w = table.shape[-1]
-    kp, sb, sm = _rows_of(k_new, "k_new", B, M, pages.H_kv, pages.D)
-    vp, vb, vm = _rows_of(v_new, "v_new", B, M, pages.H_kv, pages.D)
+    shape = (B, M, pages.H_kv, pages.D)
+    kp, sb, sm = _rows_of(k_new, "k_new", shape, dev)
+    vp, vb, vm = _rows_of(v_new, "v_new", shape, dev)
     if (vb, vm) != (sb, sm):
         raise ValueError("k_new and v_new: expected the same strides")
-    _check(lib().sd_paged_append(pages._arg(), _here(table, torch.int32, "table", (B, w)), w,
-                                 _here(lens, torch.int32, "lens", (B,)), _opt(n_new, torch.int32, "n_new", (B,)), B, M,
-                                 kp, vp, sb, sm, _stream()), "sd_paged_append")
+    _check(lib().sd_paged_append(pages._arg(dev), _here(table, torch.int32, "table", (B, w), dev), w,
+                                 _here(lens, torch.int32, "lens", (B,), dev),
+                                 _opt(n_new, torch.int32, "n_new", (B,), dev), B, M,
+                                 kp, vp, sb, sm, stream), "sd_paged_append")
 
 
 def paged_attn_workspace_bytes(B: int, M: int, H: int, H_kv: int, D: int) -> int:
@@ -404,23 +420,29 @@ def paged_attn(q: torch.Tensor, pages: KvPages, table: torch.Tensor, lens: torch
                window: int = 0, sinks: int = 0):
     """q fp32 [B][M][H][D] -> out, over each sequence's lens[b] committed and n_new[b] new rows (chains, or trees by
     parent int32 [B][M]); window > 0: only the rows less than window behind and the first sinks."""
+    dev, stream = _where()
     B, M, H = q.shape[:3]
     w = table.shape[-1]
-    qp, qb, qm = _rows_of(q, "q", B, M, H, pages.D)
-    op, ob, om = _rows_of(out, "out", B, M, H, pages.D)
-    _check(lib().sd_paged_attn(pages._arg(), _here(table, torch.int32, "table", (B, w)), w,
-                               _here(lens, torch.int32, "lens", (B,)), _opt(n_new, torch.int32, "n_new", (B,)), B, M, H,
-                               qp, qb, qm, _opt(parent, torch.int32, "parent", (B, M)), window, sinks, op, ob, om,
-                               ws.data_ptr(), ws.numel() * ws.element_size(), _stream()), "sd_paged_attn")
+    shape = (B, M, H, pages.D)
+    qp, qb, qm = _rows_of(q, "q", shape, dev)
+    op, ob, om = _rows_of(out, "out", shape, dev)
+    _check(lib().sd_paged_attn(pages._arg(dev), _here(table, torch.int32, "table", (B, w), dev), w,
+                               _here(lens, torch.int32, "lens", (B,), dev),
+                               _opt(n_new, torch.int32, "n_new", (B,), dev), B, M, H,
+                               qp, qb, qm,
+                               _opt(parent, torch.int32, "parent", (B, M), dev), window, sinks, op, ob, om,
+                               *_space(ws, dev), stream), "sd_paged_attn")
 
 
 def paged_commit(pages: KvPages, table: torch.Tensor, lens: torch.Tensor, M: int, count: torch.Tensor,
                  path: torch.Tensor | None = None):
     """Keep the accepted rows of each sequence (path int32 [B][M], None: chains) and lens += count."""
+    dev, stream = _where()
     B, w = table.shape
-    _check(lib().sd_paged_commit(pages._arg(), _here(table, torch.int32, "table", (B, w)), w,
-                                 _here(lens, torch.int32, "lens", (B,)), B, M, _opt(path, torch.int32, "path", (B, M)),
-                                 _here(count, torch.int32, "count", (B,)), _stream()), "sd_paged_commit")
+    _check(lib().sd_paged_commit(pages._arg(dev), _here(table, torch.int32, "table", (B, w), dev), w,
+                                 _here(lens, torch.int32, "lens", (B,), dev), B, M,
+                                 _opt(path, torch.int32, "path", (B, M), dev),
+                                 _here(count, torch.int32, "count", (B,), dev), stream), "sd_paged_commit")
 
 
 def pages_workspace_bytes(n_pages: int, B: int, width: int) -> int:
@@ -431,59 +453,70 @@ def pages_reserve(pages: KvPages, refs: torch.Tensor, table: torch.Tensor, lens:
                   missing: torch.Tensor, ws: torch.Tensor, n_new: torch.Tensor | None = None):
     """A page of its own for every slot that the next n_new[b] (None: M) rows touch; shared ones are copied.
     missing int32 [1]: how many free pages were short (then nothing changed)."""
+    dev, stream = _where()
     B, w = table.shape
-    _check(lib().sd_pages_reserve(pages._arg(), _here(refs, torch.int32, "refs", (pages.n_pages,)),
-                                  _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)),
-                                  _opt(n_new, torch.int32, "n_new", (B,)), B, M,
-                                  _here(missing, torch.int32, "missing", (1,)), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), _stream()), "sd_pages_reserve")
+    _check(lib().sd_pages_reserve(pages._arg(dev), _here(refs, torch.int32, "refs", (pages.n_pages,), dev),
+                                  _here(table, torch.int32, "table", (B, w), dev), w,
+                                  _here(lens, torch.int32, "lens", (B,), dev),
+                                  _opt(n_new, torch.int32, "n_new", (B,), dev), B, M,
+
+                                                                   _here(missing, torch.int32, "missing", (1,), dev), *_space(ws, dev), stream), "sd_pages_reserve")
 
 
 def pages_copy(pages: KvPages, ws: torch.Tensor):
     """The copies of the workspace's last pages_reserve or pages_compact again, for another layer's pool."""
-    _check(lib().sd_pages_copy(pages._arg(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream()), "sd_pages_copy")
+    dev, stream = _where()
+    _check(lib().sd_pages_copy(pages._arg(dev), *_space(ws, dev), stream), "sd_pages_copy")
 
 
 def pages_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page_rows: int, src: torch.Tensor,
                dst: torch.Tensor):
     """Sequence dst[i] becomes a copy of src[i] that shares its pages."""
+    dev, stream = _where()
     B, w = table.shape
     n = src.numel()
-    _check(lib().sd_pages_fork(_here(refs, torch.int32, "refs", tuple(refs.shape)), refs.numel(),
-                               _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)), B,
-                               page_rows, _here(src, torch.int32, "src", (n,)), _here(dst, torch.int32, "dst", (n,)), n,
-                               _stream()), "sd_pages_fork")
+    _check(lib().sd_pages_fork(_here(refs, torch.int32, "refs", (refs.numel(),), dev), refs.numel(),
+                               _here(table, torch.int32, "table", (B, w), dev), w,
+                               _here(lens, torch.int32, "lens", (B,), dev), B,
+                               page_rows, _here(src, torch.int32, "src", (n,), dev),
+                               _here(dst, torch.int32, "dst", (n,), dev), n,
+                               stream), "sd_pages_fork")
 
 
 def pages_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page_rows: int, seqs: torch.Tensor,
                keep: torch.Tensor | None = None):
     """The named sequences release the pages behind their first keep[i] rows (None: all)."""
+    dev, stream = _where()
     B, w = table.shape
     n = seqs.numel()
-    _check(lib().sd_pages_free(_here(refs, torch.int32, "refs", tuple(refs.shape)), refs.numel(),
-                               _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)), B,
-                               page_rows, _here(seqs, torch.int32, "seqs", (n,)),
-                               _opt(keep, torch.int32, "keep", (n,)), n, _stream()), "sd_pages_free")
+    _check(lib().sd_pages_free(_here(refs, torch.int32, "refs", (refs.numel(),), dev), refs.numel(),
+                               _here(table, torch.int32, "table", (B, w), dev), w,
+                               _here(lens, torch.int32, "lens", (B,), dev), B,
+                               page_rows, _here(seqs, torch.int32, "seqs", (n,), dev),
+                               _opt(keep, torch.int32, "keep", (n,), dev), n, stream), "sd_pages_free")
 
 
 def pages_trim(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page_rows: int, window: int,
                sinks: int = 0):
     """Every sequence releases the pages between its first sinks rows and its window."""
+    dev, stream = _where()
     B, w = table.shape
-    _check(lib().sd_pages_trim(_here(refs, torch.int32, "refs", tuple(refs.shape)), refs.numel(),
-                               _here(table, torch.int32, "table", (B, w)), w, _here(lens, torch.int32, "lens", (B,)), B,
-                               page_rows, window, sinks, _stream()), "sd_pages_trim")
+    _check(lib().sd_pages_trim(_here(refs, torch.int32, "refs", (refs.numel(),), dev), refs.numel(),
+                               _here(table, torch.int32, "table", (B, w), dev), w,
+                               _here(lens, torch.int32, "lens", (B,), dev), B,
+                               page_rows, window, sinks, stream), "sd_pages_trim")
 
 
 def pages_compact(pages: KvPages, refs: torch.Tensor, table: torch.Tensor, remap: torch.Tensor, n_live: torch.Tensor,
                   ws: torch.Tensor):
     """The live pages to the front of the pool; remap int32 [n_pages]: each page's new index (-1: free)."""
+    dev, stream = _where()
     B, w = table.shape
-    _check(lib().sd_pages_compact(pages._arg(), _here(refs, torch.int32, "refs", (pages.n_pages,)),
-                                  _here(table, torch.int32, "table", (B, w)), w, B,
-                                  _here(remap, torch.int32, "remap", (pages.n_pages,)),
-                                  _here(n_live, torch.int32, "n_live", (1,)), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), _stream()), "sd_pages_compact")
+    _check(lib().sd_pages_compact(pages._arg(dev), _here(refs, torch.int32, "refs", (pages.n_pages,), dev),
+                                  _here(table, torch.int32, "table", (B, w), dev), w, B,
+                                  _here(remap, torch.int32, "remap", (pages.n_pages,), dev),
+
+                                                                   _here(n_live, torch.int32, "n_live", (1,), dev), *_space(ws, dev), stream), "sd_pages_compact")
 
 
 def shortlist_build(head_blocks: torch.Tensor, vocab: int, hidden: int):
