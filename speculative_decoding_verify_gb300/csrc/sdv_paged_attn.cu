@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attn_kernel(const PagedArgs 
     if (!make_sched<RPG, PA_THREADS>(a, prefix, ln, sc)) return;
 
     if (warp == PA_CW) {
-        produce_tiles<T, D, RPG>(a, sc, &tmk, &tmv, ring, a.nst, full, empty, abort);
+        produce_tiles<T, D, RPG, 0, 1>(a, sc, &tmk, &tmv, ring, a.nst, full, empty, abort);
         return;
     }
 

@@ -251,7 +251,9 @@ __device__ bool make_sched(const PagedArgs &a, int64_t *prefix, int2 *ln, Sched 
 }
 
 // The producer warp's loop: the tiles of the CTA's pieces into the ring's stages, running ahead of whoever empties them.
-template <int T, int D, int RPG>
+// QS > 0: each piece's query rows come first, in QS stages of QR rows, each row D floats and 16 bytes apart (so that threads
+// of consecutive rows read them without bank conflicts).
+template <int T, int D, int RPG, int QS, int QR>
 __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring, int nst,
                               uint64_t *full, uint64_t *empty, volatile int *abort) {
     using LY = PaLayout<T, D>;
@@ -263,9 +265,41 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
     int b = 0, slot = 0, issued = 0;
     uint32_t ph = 0;
     bool ok = true;
+    // the next stage, free; false: given up
+    auto take = [&]() {
+        if (issued >= nst && !mbar_wait_bounded(&empty[slot], ph ^ 1u, PA_WAIT_NS, abort)) {
+            set_status(a.status, SD_ETIMEOUT);
+            *abort = 1;
+        }
+        return __all_sync(0xffffffffu, *abort == 0) != 0;
+    };
+    auto taken = [&]() {
+        ++issued;
+        if (++slot == nst) {
+            slot = 0;
+            ph ^= 1u;
+        }
+    };
     while (ok && u < sc.u1) {
         const Piece p = piece_at<RPG>(a, sc, u, b);
         b = p.b;
+        for (int s = 0; ok && s < QS; ++s) {
+            ok = take();
+            if (!ok) break;
+            const int r0 = s * QR, n = max(0, min(min(QR, RPG - r0), p.n * a.g - p.rg * RPG - r0));  // rows of this stage
+            if (lane == 0) {
+                if (n) mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(n) * D * 4);
+                else mbar_arrive(&full[slot]);
+            }
+            __syncwarp();
+            for (int i = lane; i < n; i += 32) {
+                const int tg = p.rg * RPG + r0 + i;
+                bulk_g2s_l2keep(ring + static_cast<size_t>(slot) * LY::STAGE + i * (D * 4 + 16),
+                                a.q + p.b * a.q_sb + (tg / a.g) * a.q_sm + static_cast<int64_t>(p.kh * a.g + tg % a.g) * D, D * 4, &full[slot]);
+            }
+            taken();
+        }
+        if (!ok) break;
         const int32_t *tab = a.table + static_cast<int64_t>(b) * a.width;
         const int total = p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
         // page of this lane's place in tile t (a place without rows, or an entry that is no page, reads as zeros)
@@ -281,14 +315,8 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
         for (int t = p.t0; t < p.t1; ++t) {
             const int next = t + 1 < p.t1 ? page_of(t + 1) : 0;  // in flight while this tile waits for its stage
             const int key0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT;
-            if (issued >= nst && !mbar_wait_bounded(&empty[slot], ph ^ 1u, PA_WAIT_NS, abort)) {
-                set_status(a.status, SD_ETIMEOUT);
-                *abort = 1;
-            }
-            if (!__all_sync(0xffffffffu, *abort == 0)) {
-                ok = false;
-                break;
-            }
+            ok = take();
+            if (!ok) break;
             uint8_t *stp = ring + static_cast<size_t>(slot) * LY::STAGE;
             if (lane == 0)
                 mbar_arrive_expect_tx(&full[slot], 2 * LY::KV + (T == SD_KV_I8 ? 2 * PA_KT * 4 : 0));
@@ -307,11 +335,7 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
                     bulk_g2s_l2keep(stp + 2 * LY::KV + kv * PA_KT * 4 + place * rows * 4, src, rows * 4, &full[slot]);
                 }
             }
-            ++issued;
-            if (++slot == nst) {
-                slot = 0;
-                ph ^= 1u;
-            }
+            taken();
             pg = next;
         }
         u += p.t1 - p.t0;

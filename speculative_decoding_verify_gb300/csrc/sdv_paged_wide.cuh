@@ -141,6 +141,9 @@ struct WideLayout {
     static constexpr int OSTAGE = 2 * OKV + OSCALES;
     static constexpr int NOP = I8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 6);  // operand stages (8-bit rows: written by the converting warps)
     static constexpr int NRAW = I8 ? (D == 64 ? 8 : 5) : 0;                 // 8-bit stages as copied
+    // the query rows of a piece take stages of the copies' ring before its tiles
+    static constexpr int QROW = D * 4 + 16, QR = PaLayout<T, D>::STAGE / QROW < RP ? PaLayout<T, D>::STAGE / QROW : RP, QS = (RP + QR - 1) / QR;
+    static_assert(QS < (I8 ? NRAW : NOP), "a piece's queries fit in the ring");
     static constexpr int THREADS = PW_SOFT + 128 + (I8 ? 128 : 0);
     static constexpr int WARP_P = 4 * PW_NG, WARP_M = WARP_P + 1, WARP_C = WARP_P + 4;  // producer, MMAs, first converting warp
     // tensor memory columns
@@ -268,9 +271,9 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
     if (warp >= W::WARP_P && warp < W::WARP_P + 4) regs_dec<W::REG_P>();
     if (warp == W::WARP_P) {
         if constexpr (W::I8)
-            produce_tiles<T, D, RP>(a, sc, &tmk, &tmv, raw, W::NRAW, raw_full, raw_empty, abort);
+            produce_tiles<T, D, RP, W::QS, W::QR>(a, sc, &tmk, &tmv, raw, W::NRAW, raw_full, raw_empty, abort);
         else
-            produce_tiles<T, D, RP>(a, sc, &tmk, &tmv, ops, W::NOP, op_full, op_empty, abort);
+            produce_tiles<T, D, RP, W::QS, W::QR>(a, sc, &tmk, &tmv, ops, W::NOP, op_full, op_empty, abort);
     } else if (warp == W::WARP_M) {
         // ---- the thread that issues the MMAs: tiles are numbered over the whole share
         if (elect_one()) {
@@ -289,6 +292,15 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 const int n = p.t1 - p.t0;
                 if (!wait(q_ready, np & 1u)) break;
                 ++np;
+                if constexpr (!W::I8)
+                    for (int s = 0; s < W::QS; ++s) {  // the queries' stages are read
+                        mbar_arrive(&op_empty[qk_slot]);
+                        if (++qk_slot == W::NOP) {
+                            qk_slot = 0;
+                            qk_ph ^= 1u;
+                        }
+                        if (++pv_slot == W::NOP) pv_slot = 0;
+                    }
                 auto scores = [&]() {
                     if (!wait(&op_full[qk_slot], qk_ph)) return false;
                     tc_fence_after();
@@ -344,9 +356,29 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             // ---- 8-bit rows to fp16 operands: thread ct takes row ct % 64 of K (ct < 64) or V
             const int ct = tid - 32 * W::WARP_C, row = ct & 63;
             const bool isv = ct >= 64;
-            const int64_t tiles = sc.u1 - sc.u0;
-            uint32_t rs = 0, rph = 0, os = 0, oph = 0;
-            for (int64_t i = 0; i < tiles; ++i) {
+            uint32_t rs = 0, rph = 0, os = 0, oph = 0, np = 0;
+            int64_t u = sc.u0, i = 0;
+            int b = 0, left = 0;  // tiles of the piece still to come
+            for (; left > 0 || u < sc.u1; ++i, --left) {
+                if (left == 0) {  // the next piece: its queries' stages go back once they are read
+                    const Piece p = piece_at<RP>(a, sc, u, b);
+                    b = p.b;
+                    left = p.t1 - p.t0;
+                    u += left;
+                    const bool got = mbar_wait_bounded(q_ready, np++ & 1u, PA_WAIT_NS, abort);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        set_status(a.status, SD_ETIMEOUT);
+                        *abort = 1;
+                        break;
+                    }
+                    for (int s = 0; s < W::QS; ++s) {
+                        if (lane == 0) mbar_arrive(&raw_empty[rs]);
+                        if (++rs == W::NRAW) {
+                            rs = 0;
+                            rph ^= 1u;
+                        }
+                    }
+                }
                 bool ok = mbar_wait_bounded(&raw_full[rs], rph, PA_WAIT_NS, abort);
                 if (ok && i >= W::NOP) ok = mbar_wait_bounded(&op_empty[os], oph ^ 1u, PA_WAIT_NS, abort);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -415,7 +447,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         const int part = lg % W::CP, l_at = (lg / W::CP) * W::KL, k_at = l_at + grp * NC;  // this lane's part and keys; this thread's keys
         int64_t u = sc.u0;
         int b = 0;
-        uint32_t nt = 0, nsync = 0, nmask = 0, nmax = 0, slot_n = 0, slot_ph = 0;
+        uint32_t nt = 0, nsync = 0, nmask = 0, nmax = 0, slot_n = 0, slot_ph = 0, q_slot = 0, q_ph = 0;
         bool ok = true;
         auto sync_all = [&]() {  // all softmax warps (an mbarrier: waits that give up)
             __syncwarp();
@@ -442,37 +474,30 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             float back = 1.0f;
             {
                 // this thread's columns of the row's query into tensor memory, in parts; fp16 parts scaled by a power of two as in
-                // paged_attn_kernel.  The rows are read 64 bytes at a time by four threads and turned through shared memory
-                constexpr int LQ = RP * 4 / PW_SOFT > 0 ? RP * 4 / PW_SOFT : 1;  // 16-byte loads of a thread per 16 columns
-                float4 in[D / 16][LQ];
+                // paged_attn_kernel.  The producer has put the rows into the first stages of the piece
+                if constexpr (!W::I8) q_slot = slot_n, q_ph = slot_ph;
+                uint64_t *qfull = W::I8 ? raw_full : op_full;
+                const uint8_t *qring = W::I8 ? raw : ops;
+                const float4 *qp = nullptr;
 #pragma unroll
-                for (int k = 0; k < LQ; ++k) {
-                    const int tr = (tid >> 2) + k * (PW_SOFT / 4), y = p.rg * RP + tr;
-                    const bool on = tr < RP && y < rows;
-                    const float4 *qp = reinterpret_cast<const float4 *>(a.q + p.b * a.q_sb + (on ? y / a.g : 0) * a.q_sm +
-                                                                        static_cast<int64_t>(p.kh * a.g + (on ? y % a.g : 0)) * D) + (tid & 3);
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) in[c][k] = on ? qp[4 * c] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int s = 0; s < W::QS; ++s) {
+                    ok = ok && __all_sync(0xffffffffu, wait(&qfull[q_slot], q_ph));
+                    if (r / W::QR == s)
+                        qp = reinterpret_cast<const float4 *>(qring + static_cast<size_t>(q_slot) * LY::STAGE + (r - s * W::QR) * W::QROW + grp * W::DO * 4);
+                    if (++q_slot == (W::I8 ? W::NRAW : W::NOP)) {
+                        q_slot = 0;
+                        q_ph ^= 1u;
+                    }
                 }
+                if constexpr (!W::I8) slot_n = q_slot, slot_ph = q_ph;
                 float mx = 0.0f;
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
+                for (int d = 0; d < W::DO; d += 4) {
+                    const float4 f = real && ok ? qp[d / 4] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    o[d / 2] = make_float2(f.x * a.qscale, f.y * a.qscale);
+                    o[d / 2 + 1] = make_float2(f.z * a.qscale, f.w * a.qscale);
 #pragma unroll
-                    for (int k = 0; k < LQ; ++k) {
-                        const int tr = (tid >> 2) + k * (PW_SOFT / 4);
-                        if (tr < RP) *reinterpret_cast<float4 *>(scratch + ((c & 1) * 128 + tr) * 20 + 4 * (tid & 3)) = in[c][k];
-                    }
-                    named_bar_sync(5, PW_SOFT);  // (two turns of the scratch: the next round's writes need no second barrier)
-                    if (c / (W::DO / 16) == grp) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 f = *reinterpret_cast<const float4 *>(scratch + ((c & 1) * 128 + r) * 20 + 4 * e);
-                            float2 *to = o + (c % (W::DO / 16)) * 8 + 2 * e;
-                            to[0] = make_float2(f.x * a.qscale, f.y * a.qscale);
-                            to[1] = make_float2(f.z * a.qscale, f.w * a.qscale);
-                            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(to[0].x), fabsf(to[0].y)), fmaxf(fabsf(to[1].x), fabsf(to[1].y))));
-                        }
-                    }
+                    for (int e = 0; e < 2; ++e) mx = fmaxf(mx, fmaxf(fabsf(o[d / 2 + e].x), fabsf(o[d / 2 + e].y)));
                 }
                 float up = 1.0f;
                 if constexpr (T != SD_KV_BF16) {
@@ -539,6 +564,12 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 if (++slot_n == W::NOP) {
                     slot_n = 0;
                     slot_ph ^= 1u;
+                }
+                if constexpr (W::I8) {  // the copies' ring, which holds the queries, goes on beside the operands'
+                    if (++q_slot == W::NRAW) {
+                        q_slot = 0;
+                        q_ph ^= 1u;
+                    }
                 }
                 ok = ok && __all_sync(0xffffffffu, wait(&s_full[sb], (nt >> 1) & 1u));
                 tc_fence_after();
@@ -704,38 +735,50 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             }
             const float f = ex2(m - mx) * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
-            // 16 columns of every group at a time through shared memory: thread = 4 columns of row tid / 8 (and of the rows RW
-            // further on), group (tid / 4) % 2
-            constexpr int RW = PW_SOFT / (4 * PW_NG), NK = (RP + RW - 1) / RW;
-            const int wg = (tid >> 2) % PW_NG, wc = wg * W::DO + 4 * (tid & 3), wr = tid / (4 * PW_NG);
-            float *to[NK];
+            // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared memory: thread = 4
+            // columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
+            auto write_rows = [&](bool final, float fac) {
+                constexpr int RW = PW_SOFT / (4 * PW_NG), NK = (RP + RW - 1) / RW;
+                const int wg = (tid >> 2) % PW_NG, wc = wg * W::DO + 4 * (tid & 3), wr = tid / (4 * PW_NG);
+                float *to[NK];
 #pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                const int tr = wr + RW * k, y = p.rg * RP + tr;
-                to[k] = tr >= RP || y >= rows ? nullptr
-                        : complete ? a.out + p.b * a.o_sb + (y / a.g) * a.o_sm + static_cast<int64_t>(p.kh * a.g + y % a.g) * D + wc
-                                   : a.part_o + (static_cast<int64_t>(pslot) * RP + tr) * D + wc;
-            }
-#pragma unroll
-            for (int d = 0; d < W::DO; d += 16) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 x = fmul2_rn(o[d / 2 + 2 * e], make_float2(f, f)), y = fmul2_rn(o[d / 2 + 2 * e + 1], make_float2(f, f));
-                    *reinterpret_cast<float4 *>(scratch + tid * 20 + 4 * e) = make_float4(x.x, x.y, y.x, y.y);
+                for (int k = 0; k < NK; ++k) {
+                    const int tr = wr + RW * k, y = p.rg * RP + tr;
+                    to[k] = tr >= RP || y >= rows ? nullptr
+                            : final ? a.out + p.b * a.o_sb + (y / a.g) * a.o_sm + static_cast<int64_t>(p.kh * a.g + y % a.g) * D + wc
+                                    : a.part_o + (static_cast<int64_t>(pslot) * RP + tr) * D + wc;
                 }
-                named_bar_sync(5, PW_SOFT);
 #pragma unroll
-                for (int k = 0; k < NK; ++k)
-                    if (to[k]) {
-                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int d = 0; d < W::DO; d += 16) {
 #pragma unroll
-                        for (int j = 0; j < C; ++j) {
-                            const float4 x = *reinterpret_cast<const float4 *>(scratch + (wg * 128 + j * RP + wr + RW * k) * 20 + 4 * (tid & 3));
-                            v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
-                        }
-                        *reinterpret_cast<float4 *>(to[k] + d) = v;
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = fmul2_rn(o[d / 2 + 2 * e], make_float2(fac, fac)), y = fmul2_rn(o[d / 2 + 2 * e + 1], make_float2(fac, fac));
+                        *reinterpret_cast<float4 *>(scratch + tid * 20 + 4 * e) = make_float4(x.x, x.y, y.x, y.y);
                     }
-                named_bar_sync(5, PW_SOFT);
+                    named_bar_sync(5, PW_SOFT);
+#pragma unroll
+                    for (int k = 0; k < NK; ++k)
+                        if (to[k]) {
+                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                            for (int j = 0; j < C; ++j) {
+                                const float4 x = *reinterpret_cast<const float4 *>(scratch + (wg * 128 + j * RP + wr + RW * k) * 20 + 4 * (tid & 3));
+                                v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+                            }
+                            *reinterpret_cast<float4 *>(to[k] + d) = v;
+                        }
+                    named_bar_sync(5, PW_SOFT);
+                }
+            };
+            // C = 1: a thread's columns of a partial as they are, [D / 4][128] 16-byte columns (lanes beside each other: whole lines, no
+            // exchange); the joining CTA's threads read the same places
+            float4 *lanes = reinterpret_cast<float4 *>(a.part_o) + grp * (W::DO / 4) * 128 + lt;
+            if (C > 1 || complete) {
+                write_rows(complete, f);
+            } else {
+#pragma unroll
+                for (int d = 0; d < W::DO / 4; ++d)
+                    lanes[static_cast<int64_t>(pslot) * (RP * D / 4) + d * 128] = make_float4(o[2 * d].x, o[2 * d].y, o[2 * d + 1].x, o[2 * d + 1].y);
             }
             if (!complete) {
                 const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
@@ -747,7 +790,34 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     if (was == c1 - c0) a.counters[c0] = 0;
                 }
                 named_bar_sync(5, PW_SOFT);
-                if (*last) join_partials<RP, D, PW_SOFT>(a, p, c0, c1, tid, scratch, 5);
+                if (*last) {
+                    if constexpr (C > 1) {
+                        join_partials<RP, D, PW_SOFT>(a, p, c0, c1, tid, scratch, 5);
+                    } else {
+                        // as join_partials: in the order of the keys, a row's weights from its maxima
+                        __threadfence();
+                        float jm = PA_NEG, jl = 0.0f;
+#pragma unroll 4
+                        for (int x = c0; x <= c1; ++x) jm = fmaxf(jm, __ldcg(&a.part_ml[(2 * x + (x == c0)) * RP + r]).x);
+#pragma unroll
+                        for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
+                        for (int x = c0; x <= c1; ++x) {
+                            const int64_t sl = 2 * x + (x == c0);
+                            const float2 ml = __ldcg(&a.part_ml[sl * RP + r]);
+                            float4 y[W::DO / 4];
+#pragma unroll
+                            for (int d = 0; d < W::DO / 4; ++d) y[d] = __ldcg(lanes + sl * (RP * D / 4) + d * 128);
+                            const float w = ex2(ml.x - jm);
+                            jl = fmaf(ml.y, w, jl);
+#pragma unroll
+                            for (int d = 0; d < W::DO / 4; ++d) {
+                                o[2 * d] = ffma2_rn(make_float2(y[d].x, y[d].y), make_float2(w, w), o[2 * d]);
+                                o[2 * d + 1] = ffma2_rn(make_float2(y[d].z, y[d].w), make_float2(w, w), o[2 * d + 1]);
+                            }
+                        }
+                        write_rows(true, jl == 0.0f ? 0.0f : 1.0f / jl);
+                    }
+                }
             }
             u += p.t1 - p.t0;
         }
