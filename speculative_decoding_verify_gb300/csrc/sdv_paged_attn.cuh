@@ -260,6 +260,7 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
     const int lane = static_cast<int>(threadIdx.x) & 31;
     // lane l issues copies l, l + 32, .. of a tile (page, K or V, 128 bytes of row)
     const int rows = min(a.P, PA_KT), npt = PA_KT / rows;  // rows of a page in a tile, pages per tile
+    const int lg = __ffs(npt) - 1;
     const int ncopy = npt * 2 * LY::NB;
     int64_t u = sc.u0;
     int b = 0, slot = 0, issued = 0;
@@ -302,18 +303,26 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
         if (!ok) break;
         const int32_t *tab = a.table + static_cast<int64_t>(b) * a.width;
         const int total = p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
-        // page of this lane's place in tile t (a place without rows, or an entry that is no page, reads as zeros)
-        auto page_of = [&](int t) {
-            const int key = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT + (lane % npt) * rows;
+        // the pages of the piece's places in order, npt to a tile, 32 at a time and 32 more on their way: a table entry fetched per tile
+        // would cost the tile its latency.  (A place without rows, or an entry that is no page, reads as zeros.)
+        auto page_of = [&](int e) {
+            const int t = p.t0 + (e >> lg);
+            if (t >= p.t1) return a.n_pages;
+            const int key = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT + (e & (npt - 1)) * rows;
             if (key >= total) return a.n_pages;
             const int pg = tab[key / a.P];
             if (pg >= 0 && pg < a.n_pages) return pg;
             if (key + rows > lo || key < sink) set_status(a.status, SD_EDEVICE);  // a row of it is visible
             return a.n_pages;
         };
-        int pg = page_of(p.t0);
+        int pages = page_of(lane), later = page_of(32 + lane);
         for (int t = p.t0; t < p.t1; ++t) {
-            const int next = t + 1 < p.t1 ? page_of(t + 1) : 0;  // in flight while this tile waits for its stage
+            const int e = (t - p.t0) << lg;
+            if (e && (e & 31) == 0) {
+                pages = later;
+                later = page_of(e + 32 + lane);
+            }
+            const int pg = __shfl_sync(0xffffffffu, pages, (e & 31) + (lane & (npt - 1)));
             const int key0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT;
             ok = take();
             if (!ok) break;
@@ -336,7 +345,6 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
                 }
             }
             taken();
-            pg = next;
         }
         u += p.t1 - p.t0;
     }
