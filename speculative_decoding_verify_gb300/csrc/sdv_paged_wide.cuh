@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
             // adds this thread's columns of the product of tile number i to the outputs
             auto add_product = [&](uint32_t i) {
-                if (!__all_sync(0xffffffffu, wait(&pv_full[i & 1u], (i >> 1) & 1u))) return false;
+                const bool got = wait(&pv_full[i & 1u], (i >> 1) & 1u);
                 tc_fence_after();
                 const uint32_t at = tq + W::TO + (i % W::NPV) * D + grp * W::DO;
                 uint32_t y[W::DO / 32][32];
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pv_free[i & 1u]);
-                return true;
+                return got;
             };
             for (int t = p.t0; t < p.t1; ++t, ++nt) {
                 const uint32_t sb = nt & 1u, slot = slot_n, slot_par = slot_ph;
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         q_ph ^= 1u;
                     }
                 }
-                ok = ok && __all_sync(0xffffffffu, wait(&s_full[sb], (nt >> 1) & 1u));
+                ok = wait(&s_full[sb], (nt >> 1) & 1u) && ok;  // (each lane's own answer: lane_max brings them together)
                 tc_fence_after();
                 const uint32_t sc_at = tq + W::TS + sb * W::SCOLS;
                 const int tile0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT, key0 = tile0 + k_at;
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 const float *scales = reinterpret_cast<const float *>(stage + 2 * W::OKV);
                 const bool whole = tile0 + PA_KT <= p.len && (tile0 >= full_lo || tile0 + PA_KT <= full_sink);
                 if (W::I8 || !whole)  // what stands in the stage is read below: its barrier makes it visible here too
-                    ok = ok && __all_sync(0xffffffffu, wait(&op_full[slot], slot_par));
+                    ok = wait(&op_full[slot], slot_par) && ok;
                 float tunit = 1.0f;
                 if constexpr (W::I8) tunit = scales[2 * PA_KT];
                 float2 s[NC / 2];
@@ -633,11 +633,11 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                             const uint32_t any = __reduce_or_sync(0xffffffffu, bw[w]);
                             if (lane == 0 && any) atomicOr(&words[w], any);
                         }
-                        ok = sync_all();
+                        ok = sync_all() && ok;
                         const uint32_t bad[2] = {*reinterpret_cast<volatile uint32_t *>(&words[0]), *reinterpret_cast<volatile uint32_t *>(&words[1])};
                         if (tid == 0) other[0] = other[1] = 0;  // read by all before the barrier above
-                        if (ok && (bad[0] | bad[1])) {
-                            if (t > p.t0) ok = add_product(nt - 1);
+                        if (__all_sync(0xffffffffu, ok) && (bad[0] | bad[1])) {
+                            if (t > p.t0) ok = add_product(nt - 1) && ok;
                             float acc[W::DO];
 #pragma unroll
                             for (int d = 0; d < W::DO / 2; ++d) {
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 al = rescaled ? 1.0f : an;
                 unit = tunit;
             }
-            if (ok) ok = add_product(nt - 1);
+            ok = add_product(nt - 1) && ok;
             if (bar_any(5, PW_SOFT, !ok)) break;  // all softmax warps leave together
             // ---- write the piece: a run that is whole goes out, others become partials
             const bool complete = p.t0 == 0 && p.t1 == p.st.T;
