@@ -24,8 +24,10 @@
 
 namespace sdv {
 
+// (Five warps a CTA put three of ten on one scheduler: above 168 registers one CTA runs per SM.  At D = 64 the 16-row form is held to
+// that, 162 -> 125 us for 16 sequences of 16000 bf16 rows; at D = 128 it would spill 60 registers and take 20 % longer.)
 template <int T, int D, int NT>
-__global__ void __launch_bounds__(PA_THREADS) paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
+__global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
                                                                 const __grid_constant__ CUtensorMap tmv) {
     using LY = PaLayout<T, D>;
     constexpr int KS = D / 16, RPG = 8 * NT, NP = Parts<T>::N, SD = 64 + 4;
@@ -498,11 +500,13 @@ static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
     return true;
 }
 
-// Query rows of a KV head above which the tensor-memory kernel runs; its shared memory holds the schedule of PA_WIDE_B
-// sequences.
-constexpr int PA_WIDE_ROWS = 8, PA_WIDE_B = 512;
+// Query rows of a KV head above which the tensor-memory kernel runs: its cost per 64-key tile hardly depends on D or on the
+// rows (up to 32 of them), the other's grows with both.  16 sequences of 16000 rows, 8 KV heads, 16 query rows, this kernel /
+// the tensor-memory one: D = 64 fp16 100 / 147 us; D = 128 fp16 205 / 178, bf16 258 / 223, int8 250 / 252.  The other's shared
+// memory holds the schedule of PA_WIDE_B sequences.
+constexpr int PA_WIDE_ROWS = 8, PA_WIDE_ROWS_64 = 16, PA_WIDE_B = 512;
 
-static bool pa_wide(int rows, int D, int B) { return rows > PA_WIDE_ROWS && D <= 128 && B <= PA_WIDE_B; }
+static bool pa_wide(int rows, int D, int B) { return rows > (D == 64 ? PA_WIDE_ROWS_64 : PA_WIDE_ROWS) && D <= 128 && B <= PA_WIDE_B; }
 
 // workspace: counters of the largest grid, then the partials: two per CTA, of 16 rows on two CTAs per SM or
 // of 128 rows on one

@@ -137,7 +137,7 @@ struct WideLayout {
     static constexpr int NR = (NP + CP - 1) / CP;   // parts that a lane holds: passes of the product
     static constexpr int OTILE = PA_KT * 128;       // 64 keys x 64 halves
     static constexpr int OKV = D / 64 * OTILE;      // K (or V) operand of a tile
-    static constexpr int OSCALES = I8 ? 1024 : 0;   // scales of K [64], of V [64] in units of the tile's, that unit
+    static constexpr int OSCALES = I8 ? 1024 : 0;   // scales of K [64], of V [64] in the piece's unit so far, its change, the unit
     static constexpr int OSTAGE = 2 * OKV + OSCALES;
     static constexpr int NOP = I8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 6);  // operand stages (8-bit rows: written by the converting warps)
     static constexpr int NRAW = I8 ? (D == 64 ? 8 : 5) : 0;                 // 8-bit stages as copied
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             uint32_t rs = 0, rph = 0, os = 0, oph = 0, np = 0;
             int64_t u = sc.u0, i = 0;
             int b = 0, left = 0;  // tiles of the piece still to come
+            int ve = -126;        // exponent of the unit of the V scales so far in the piece
             for (; left > 0 || u < sc.u1; ++i, --left) {
                 if (left == 0) {  // the next piece: its queries' stages go back once they are read
                     const Piece p = piece_at<RP>(a, sc, u, b);
@@ -366,11 +367,11 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     left = p.t1 - p.t0;
                     u += left;
                     const bool got = mbar_wait_bounded(q_ready, np++ & 1u, PA_WAIT_NS, abort);
-                    if (!__all_sync(0xffffffffu, got)) {
+                    if (!got) {
                         set_status(a.status, SD_ETIMEOUT);
                         *abort = 1;
-                        break;
                     }
+                    ve = -126;
                     for (int s = 0; s < W::QS; ++s) {
                         if (lane == 0) mbar_arrive(&raw_empty[rs]);
                         if (++rs == W::NRAW) {
@@ -381,10 +382,9 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 }
                 bool ok = mbar_wait_bounded(&raw_full[rs], rph, PA_WAIT_NS, abort);
                 if (ok && i >= W::NOP) ok = mbar_wait_bounded(&op_empty[os], oph ^ 1u, PA_WAIT_NS, abort);
-                if (!__all_sync(0xffffffffu, ok)) {
+                if (!ok) {  // (the loop goes on: every later wait gives up at once)
                     set_status(a.status, SD_ETIMEOUT);
                     *abort = 1;
-                    break;
                 }
                 const uint8_t *src = raw + static_cast<size_t>(rs) * LY::STAGE;
                 uint8_t *dst = ops + static_cast<size_t>(os) * W::OSTAGE + (isv ? W::OKV : 0);
@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         const float s = ss[lane + 32 * y];
                         ds[lane + 32 * y] = s + 0.0f * s;
                     }
-                } else if (ct < 64) {  // V scales in units of a power of two that none exceeds
+                } else if (ct < 64) {  // V scales in units of a power of two that none so far in the piece exceeds
                     float s[2] = {ss[PA_KT + lane], ss[PA_KT + 32 + lane]};
-                    int e = -126;
+                    int e = ve;
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
                         if (s[y] > 0.0f && s[y] < INFINITY) {
@@ -419,7 +419,11 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     const float down = ldexpf(1.0f, -e);
                     ds[PA_KT + lane] = s[0] * down;
                     ds[PA_KT + 32 + lane] = s[1] * down;
-                    if (lane == 0) ds[2 * PA_KT] = ldexpf(1.0f, e);
+                    if (lane == 0) {
+                        ds[2 * PA_KT] = ldexpf(1.0f, ve - e);  // what the outputs so far shrink by
+                        ds[2 * PA_KT + 1] = ldexpf(1.0f, e);   // the unit
+                    }
+                    ve = e;
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 low = a.window > 0 ? p.len + depth - a.window + 1 : 0;
             }
             const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
-            float m = PA_NEG, l = 0.0f, al = 0.0f, unit = 1.0f;  // al, unit: rescale of the outputs and unit of the product still to be added
+            float m = PA_NEG, l = 0.0f, al = 0.0f, unit = 1.0f;  // al: rescale of the outputs before the product still to be added; unit: theirs (8-bit rows)
 #pragma unroll
             for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
             // adds this thread's columns of the product of tile number i to the outputs
@@ -549,9 +553,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     tc_wait_ld(y[d]);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        float2 f = make_float2(__uint_as_float(y[d][2 * e]), __uint_as_float(y[d][2 * e + 1]));
-                        if constexpr (W::I8) f = fmul2_rn(f, make_float2(unit, unit));
-                        o[16 * d + e] = ffma2_rn(o[16 * d + e], make_float2(al, al), f);
+                        const float2 f = make_float2(__uint_as_float(y[d][2 * e]), __uint_as_float(y[d][2 * e + 1]));
+                            o[16 * d + e] = ffma2_rn(o[16 * d + e], make_float2(al, al), f);
                     }
                 }
                 tc_fence_before();
@@ -580,8 +583,11 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 const bool whole = tile0 + PA_KT <= p.len && (tile0 >= full_lo || tile0 + PA_KT <= full_sink);
                 if (W::I8 || !whole)  // what stands in the stage is read below: its barrier makes it visible here too
                     ok = wait(&op_full[slot], slot_par) && ok;
-                float tunit = 1.0f;
-                if constexpr (W::I8) tunit = scales[2 * PA_KT];
+                float shrink = 1.0f;
+                if constexpr (W::I8) {
+                    shrink = scales[2 * PA_KT];
+                    unit = scales[2 * PA_KT + 1];
+                }
                 float2 s[NC / 2];
                 {
                     uint32_t y[NC];
@@ -676,9 +682,13 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < NC / 2; e += 2) {
                         const float4 f = *reinterpret_cast<const float4 *>(scales + PA_KT + k_at + 2 * e);
-                        // a key with no weight keeps none, whatever its scale is
-                        s[e] = make_float2(s[e].x > 0.0f ? s[e].x * f.x : s[e].x, s[e].y > 0.0f ? s[e].y * f.y : s[e].y);
-                        s[e + 1] = make_float2(s[e + 1].x > 0.0f ? s[e + 1].x * f.z : s[e + 1].x, s[e + 1].y > 0.0f ? s[e + 1].y * f.w : s[e + 1].y);
+                        const float2 was = s[e], was1 = s[e + 1];
+                        s[e] = fmul2_rn(s[e], make_float2(f.x, f.y));
+                        s[e + 1] = fmul2_rn(s[e + 1], make_float2(f.z, f.w));
+                        if (!whole) {  // a key with no weight keeps none, whatever its scale is
+                            s[e] = make_float2(was.x > 0.0f ? s[e].x : was.x, was.y > 0.0f ? s[e].y : was.y);
+                            s[e + 1] = make_float2(was1.x > 0.0f ? s[e + 1].x : was1.x, was1.y > 0.0f ? s[e + 1].y : was1.y);
+                        }
                     }
                 }
 #pragma unroll
@@ -711,8 +721,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 if (lane == 0) mbar_arrive(&p_ready[sb]);
                 // the product of the tile before, while this one's runs
                 if (t > p.t0 && !rescaled) ok = add_product(nt - 1) && ok;
-                al = rescaled ? 1.0f : an;
-                unit = tunit;
+                al = rescaled ? 1.0f : W::I8 ? an * shrink : an;
             }
             ok = add_product(nt - 1) && ok;
             if (bar_any(5, PW_SOFT, !ok)) break;  // all softmax warps leave together
@@ -733,7 +742,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 for (int g = 0; g < PW_NG; ++g) x += sm_l[g * 128 + j * RP + r];
                 lv = fmaf(x, ex2(sm_m[j * RP + r] - mx), lv);
             }
-            const float f = ex2(m - mx) * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
+            const float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
             // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared memory: thread = 4
             // columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
@@ -778,7 +787,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             } else {
 #pragma unroll
                 for (int d = 0; d < W::DO / 4; ++d)
-                    lanes[static_cast<int64_t>(pslot) * (RP * D / 4) + d * 128] = make_float4(o[2 * d].x, o[2 * d].y, o[2 * d + 1].x, o[2 * d + 1].y);
+                    lanes[static_cast<int64_t>(pslot) * (RP * D / 4) + d * 128] = make_float4(o[2 * d].x * unit, o[2 * d].y * unit, o[2 * d + 1].x * unit, o[2 * d + 1].y * unit);
             }
             if (!complete) {
                 const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
@@ -842,7 +851,10 @@ cudaError_t wide_launch(const PagedArgs &a, const CUtensorMap &tmk, const CUtens
 template <int T, int D>
 cudaError_t wide_launch_c(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int rows, int grid, cudaStream_t s) {
     if (rows <= 32) return wide_launch<T, D, 4>(a, tmk, tmv, grid, s);
-    if (rows <= 64) return wide_launch<T, D, 2>(a, tmk, tmv, grid, s);
+    // (two lane groups for three bf16 parts make two passes of the product: 346 us against 264 us with one group, 64 rows,
+    // 16 sequences of 16000 rows)
+    if constexpr (T != SD_KV_BF16)
+        if (rows <= 64) return wide_launch<T, D, 2>(a, tmk, tmv, grid, s);
     return wide_launch<T, D, 1>(a, tmk, tmv, grid, s);
 }
 
