@@ -546,7 +546,7 @@ static cudaError_t append_launch(const sd_kv_pages *p, const int32_t *table, int
 
 static cudaError_t copy_launch(const sd_kv_pages *p, const PagesWs &ws, int32_t *table, int64_t entries, const int32_t *remap, cudaStream_t s) {
     const bool i8 = p->type == SD_KV_I8;
-    return launch(pages_copy_kernel, dim3(static_cast<unsigned>(num_sms()) * 8), dim3(CP_T), 0, s, page_view(p), static_cast<uint8_t *>(p->k),
+    return launch(pages_copy_kernel, dim3(static_cast<unsigned>(num_sms()) * 16), dim3(CP_T), 0, s, page_view(p), static_cast<uint8_t *>(p->k),
                   static_cast<uint8_t *>(p->v), i8 ? p->k_scale : nullptr, i8 ? p->v_scale : nullptr, kv_type_bytes(p->type),
                   static_cast<const int32_t *>(ws.n_copies), static_cast<const int4 *>(ws.list), table, entries, remap);
 }
