@@ -306,8 +306,9 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     tc_fence_after();
                     const uint32_t kb = ob + qk_slot * W::OSTAGE, d = tm + W::TS + (nqk & 1u) * W::SCOLS;
                     bool acc = false;
+                    // the smallest parts first: the accumulation truncates at the size that the sum has by then
 #pragma unroll
-                    for (int x = 0; x < NP; ++x)
+                    for (int x = NP - 1; x >= 0; --x)
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
                             tc_mma_ts(d, tm + W::TQ + x * (D / 2) + ks * 8, sw128_desc(kb + (ks >> 2) * W::OTILE + (ks & 3) * 32, 0), ID_QK, acc);
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     const uint32_t vb = ob + pv_slot * W::OSTAGE + W::OKV, d = tm + W::TO + ob2 * D, pa = tm + W::TS + sb * W::SCOLS;
                     bool acc = false;
 #pragma unroll
-                    for (int x = 0; x < W::NR; ++x)
+                    for (int x = W::NR - 1; x >= 0; --x)
 #pragma unroll
                         for (int ks = 0; ks < PA_KT / 16; ++ks) {
                             tc_mma_ts(d, pa + x * 32 + ks * 8, sw128_desc(vb + ks * 2048, W::OTILE), ID_PV, acc);
