@@ -383,6 +383,7 @@ sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, in
  * Every kernel checks lens, n_new and table entries against these bounds before it uses them: what fails is
  * skipped (for the attention a missing page reads as zeros) and records SD_EDEVICE in the status word.
  * The calls of one workspace are ordered on one stream; a graph that may run beside another call needs its own.
+ * After an SD_ETIMEOUT a workspace must be zero-filled again.
  *
  * sd_paged_append: k_new, v_new fp32, row i of sequence b at b * seq_stride + i * row_stride (elements,
  * multiples of 4, 16-byte aligned), its H_kv heads of D contiguous: they may be columns of a fused projection.  Rounded to
@@ -447,14 +448,15 @@ sd_status sd_paged_commit(const sd_kv_pages *pages, const int32_t *table, int32_
  * times; a dst named twice, or as a source too, and an index outside [0, B) are skipped and record SD_EDEVICE.
  * sd_pages_free: for i < n, sequence seqs[i] releases the pages of its rows from keep[i] on (whole pages: slots
  * s with s * page_rows >= keep[i]; keep NULL: all) and lens = min(lens, keep[i]).  A sequence may be named twice.
- * After a commit, keep = lens gives back the pages of rejected drafts.
+ * After a commit, seqs = 0 .. B-1 and keep = lens give back the pages of rejected drafts.
  * sd_pages_trim: every sequence b < B releases the pages that lie wholly in [sinks, lens[b] - window + 1): rows
  * that no later row of sd_paged_attn with that window and those sinks sees.
  * sd_pages_compact: moves the live pages at index >= n_live = the number of live pages into the free ones below,
  * both in increasing order; tables and counts follow, remap int32 [n_pages] receives each page's new index (-1:
  * it was free) and *n_live the count, so that pages n_live .. n_pages-1 are free.
  * Page contents (all layers) follow the tables: a pool of several layers calls sd_pages_reserve / _compact on
- * the first and sd_pages_copy with the same workspace on the others, before the workspace is used again.
+ * the first and sd_pages_copy with the same workspace on the others (pools of as many pages and rows), before the
+ * workspace is used again.
  * workspace: sd_pages_workspace_bytes(n_pages, B, width), zero-filled by the caller once.
  */
 size_t sd_pages_workspace_bytes(int32_t n_pages, int32_t B, int32_t width);

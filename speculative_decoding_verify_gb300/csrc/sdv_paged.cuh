@@ -11,6 +11,7 @@
 namespace sdv {
 
 constexpr int PG_MAX_B = 1024;  // sequences per call (their schedule is held in shared memory)
+constexpr int PG_MAX_PAGES = 1 << 30;
 
 // The driver's tensor-map encoder (sdv_attn.cu), looked up once; null if the driver has none.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
@@ -22,7 +23,7 @@ inline int kv_type_bytes(int type) { return type == SD_KV_I8 ? 1 : 2; }
 inline sd_status pages_check(const sd_kv_pages *p) {
     if (!p || !p->k || !p->v) return SD_EINVAL;
     if (p->type != SD_KV_F16 && p->type != SD_KV_BF16 && p->type != SD_KV_I8) return SD_EUNSUPPORTED;
-    if (p->n_pages < 1 || p->H_kv < 1 || p->page_rows < 1 || p->D < 1) return SD_EINVAL;
+    if (p->n_pages < 1 || p->n_pages > PG_MAX_PAGES || p->H_kv < 1 || p->page_rows < 1 || p->D < 1) return SD_EINVAL;
     if (p->D != 64 && p->D != 128 && p->D != 256) return SD_EUNSUPPORTED;
     if (!(p->page_rows == 8 || p->page_rows == 16 || p->page_rows == 32 || p->page_rows % 64 == 0))
         return SD_EUNSUPPORTED;

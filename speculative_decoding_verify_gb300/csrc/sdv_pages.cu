@@ -401,7 +401,7 @@ constexpr int CP_T = 256, CP_U = 4;
 
 __global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *k, uint8_t *v, float *k_scale, float *v_scale, int eb,
                                                           const int32_t *n_copies, const int4 *list, int32_t *table, int64_t entries,
-                                                          const int32_t *remap) {
+                                                          const int32_t *remap, int *status) {
     pdl_wait();
     pdl_launch_dependents();
     if (table)
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *
             const int t = table[x];
             if (t >= 0 && t < pv.n_pages) table[x] = remap[t];
         }
-    const int n = *n_copies;
+    const int n = min(*n_copies, pv.n_pages);  // a plan lists a page at most once as a target
     const int cols = pv.D * eb / 16;  // a power of two
     const int cs = __ffs(cols) - 1;
     const int parts = static_cast<int>((static_cast<int64_t>(pv.P) * pv.H_kv * cols + CP_T * CP_U - 1) / (CP_T * CP_U));
@@ -418,6 +418,10 @@ __global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *
         const int64_t y = w / parts;
         const int part = static_cast<int>(w - y * parts);
         const int4 e = list[y >> 1];
+        if (e.x < 0 || e.x >= pv.n_pages || e.y < 0 || e.y >= pv.n_pages || e.z > pv.P) {  // a plan for another pool's sizes
+            set_status(status, SD_EDEVICE);
+            continue;
+        }
         const int total = e.z * pv.H_kv * cols;
         if (part * (CP_T * CP_U) >= total) continue;
         uint8_t *base = (y & 1) ? v : k;
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(256) pages_trim_kernel(int32_t *refs, int32_t 
     pdl_wait();
     pdl_launch_dependents();
     const int b = static_cast<int>(blockIdx.x);
-    const int lo = lens[b] - window + 1;  // the first row that a later row sees
+    const int lo = max(lens[b], 0) - window + 1;  // the first row that a later row sees
     int32_t *t = table + static_cast<int64_t>(b) * width;
     const int end = lo > 0 ? min(lo / P, width) : 0;
     for (int64_t x = (static_cast<int64_t>(sinks) + P - 1) / P + threadIdx.x; x < end; x += blockDim.x) {
@@ -545,14 +549,16 @@ static cudaError_t append_launch(const sd_kv_pages *p, const int32_t *table, int
 }
 
 static cudaError_t copy_launch(const sd_kv_pages *p, const PagesWs &ws, int32_t *table, int64_t entries, const int32_t *remap, cudaStream_t s) {
+    int *status = status_ptr();
+    if (!status) return cudaErrorUnknown;
     const bool i8 = p->type == SD_KV_I8;
     return launch(pages_copy_kernel, dim3(static_cast<unsigned>(num_sms()) * 16), dim3(CP_T), 0, s, page_view(p), static_cast<uint8_t *>(p->k),
                   static_cast<uint8_t *>(p->v), i8 ? p->k_scale : nullptr, i8 ? p->v_scale : nullptr, kv_type_bytes(p->type),
-                  static_cast<const int32_t *>(ws.n_copies), static_cast<const int4 *>(ws.list), table, entries, remap);
+                  static_cast<const int32_t *>(ws.n_copies), static_cast<const int4 *>(ws.list), table, entries, remap, status);
 }
 
 static bool table_ok(const void *refs, int32_t n_pages, const void *table, int32_t width, int32_t B, int32_t P) {
-    return refs && table && n_pages >= 1 && width >= 1 && B >= 1 && P >= 1 &&
+    return refs && table && n_pages >= 1 && n_pages <= PG_MAX_PAGES && width >= 1 && B >= 1 && P >= 1 &&
            static_cast<int64_t>(width) * P <= INT32_MAX - 128;
 }
 

@@ -148,7 +148,7 @@ def test_windows_and_sinks(sdv, dtype, window, sinks, tree):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
-@pytest.mark.parametrize("M,H,H_kv,D", [(3, 3, 1, 128), (5, 10, 2, 64), (11, 3, 1, 128), (16, 4, 1, 64), (13, 10, 2, 128), (16, 8, 1, 64),
+@pytest.mark.parametrize("M,H,H_kv,D", [(3, 3, 1, 128), (3, 3, 1, 64), (4, 8, 2, 64), (4, 5, 1, 256), (5, 10, 2, 64), (11, 3, 1, 128), (16, 4, 1, 64), (13, 10, 2, 128), (16, 8, 1, 64),
                                         (9, 15, 1, 128), (16, 40, 1, 64), (16, 64, 1, 128)])
 def test_many_rows_per_kv_head(sdv, dtype, M, H, H_kv, D):
     """From 9 to 1024 query rows of a KV head, some sequences with fewer, contexts over tile and CTA borders."""
@@ -178,6 +178,24 @@ def test_sharp_scores(sdv, dtype):
 def test_tiny_and_huge_queries(sdv, dtype):
     check_attn(sdv, 12, [300], [2], 2, 2, 1, 128, 16, dtype, scale=1.0, qscale=1e-30)
     check_attn(sdv, 13, [300], [2], 2, 2, 1, 128, 16, dtype, scale=1e-3, qscale=3e3)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_of_many_sequences(sdv, dtype, D):
+    """More sequences than the many-row kernel's schedule holds, and as many as it does."""
+    rng = np.random.default_rng(D)
+    for B in (513, 512):
+        lens = rng.integers(0, 150, B).tolist()
+        news = rng.integers(0, 4, B).tolist()
+        c = Cache(sdv, rng, lens, news, 3, 1, D, 16, dtype)
+        q = rng.standard_normal((B, 3, 5, D)).astype(np.float32)
+        out = run_attn(sdv, c, q, lens, news, 3, None, 40, 3)
+        for b in rng.permutation(B)[:60].tolist():
+            if news[b]:
+                ref, tol = plain.attention(q[b, :news[b]], c.K[b], c.V[b], plain.seen_rows(lens[b], news[b], None, 40, 3))
+                assert np.all(np.abs(out[b, :news[b]] - ref) <= tol)
+            assert np.all(out[b, news[b]:] == 123.0)
 
 
 def test_many_sequences(sdv):
@@ -266,12 +284,13 @@ def test_same_result_as_the_contiguous_cache(sdv):
     assert np.all(np.abs(out - host(flat)) <= 2 * tol)
 
 
-def test_results_repeat_and_the_workspace_is_left_ready(sdv):
+@pytest.mark.parametrize("H", [6, 40])
+def test_results_repeat_and_the_workspace_is_left_ready(sdv, H):
     rng = np.random.default_rng(17)
     lens = [5000, 300, 0, 12000]
     c = Cache(sdv, rng, lens, [2] * 4, 2, 2, 128, 16, "bf16")
-    q = cuda(rng.standard_normal((4, 2, 6, 128)).astype(np.float32))
-    ws = sdv.workspace(sdv.paged_attn_workspace_bytes(4, 2, 6, 2, 128))
+    q = cuda(rng.standard_normal((4, 2, H, 128)).astype(np.float32))
+    ws = sdv.workspace(sdv.paged_attn_workspace_bytes(4, 2, H, 2, 128))
     outs = []
     for _ in range(4):
         out = torch.zeros_like(q)
@@ -638,6 +657,21 @@ def test_other_layers_follow(sdv):
     other.moved(want, copies, None)
 
 
+def test_a_plan_for_a_larger_pool_is_not_followed(sdv):
+    """The copies of a pool of 30 pages on one of 3: those within it are made, the others reported, nothing else is touched."""
+    m = Both(sdv, 30, 4, 4, 16, seed=1)
+    m.reserve([20, 0, 0, 0], 20)
+    m.grow([20, 0, 0, 0])
+    m.fork([(0, 1), (0, 2)])
+    _, copies = plain_copies(m, [3, 3, 3, 0])
+    m.reserve([3, 3, 3, 0], 3)
+    small = Both(sdv, 3, 4, 4, 16, seed=2)
+    want = [t.clone() for t in small.kv]
+    sdv.pages_copy(small.pages, m.ws)
+    assert sdv.device_status() == EDEVICE
+    small.moved(want, [c for c in copies if max(c[:2]) < 3], None)
+
+
 def plain_copies(m, n_new):
     import copy
     return copy.deepcopy(m.pool).reserve(n_new)
@@ -727,19 +761,20 @@ def test_cycles(sdv, dtype, window, captured):
         assert np.array_equal(host(refs), counts)
 
 
-def test_two_streams_with_their_own_workspaces(sdv):
+@pytest.mark.parametrize("H", [4, 32])
+def test_two_streams_with_their_own_workspaces(sdv, H):
     rng = np.random.default_rng(51)
     lens = [3000, 100]
     c = Cache(sdv, rng, lens, [2, 2], 2, 2, 128, 16, "f16")
-    q = [cuda(rng.standard_normal((2, 2, 4, 128)).astype(np.float32)) for _ in range(2)]
+    q = [cuda(rng.standard_normal((2, 2, H, 128)).astype(np.float32)) for _ in range(2)]
     L = i32(lens)
     alone = []
     for x in q:
         o = torch.zeros_like(x)
-        sdv.paged_attn(x, c.pages, c.table, L, o, sdv.workspace(sdv.paged_attn_workspace_bytes(2, 2, 4, 2, 128)))
+        sdv.paged_attn(x, c.pages, c.table, L, o, sdv.workspace(sdv.paged_attn_workspace_bytes(2, 2, H, 2, 128)))
         alone.append(o)
     outs = [torch.zeros_like(x) for x in q]
-    wss = [sdv.workspace(sdv.paged_attn_workspace_bytes(2, 2, 4, 2, 128)) for _ in q]
+    wss = [sdv.workspace(sdv.paged_attn_workspace_bytes(2, 2, H, 2, 128)) for _ in q]
     streams = [torch.cuda.Stream() for _ in q]
     torch.cuda.synchronize()
     for _ in range(20):

@@ -32,7 +32,7 @@ def attn(sdv, p, **kw):
 
 BAD_PAGES = [
     (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(k=A + 8), EINVAL), (dict(type=3), EUNSUPPORTED), (dict(type=-1), EUNSUPPORTED),
-    (dict(n_pages=0), EINVAL), (dict(H_kv=0), EINVAL), (dict(page_rows=0), EINVAL), (dict(page_rows=1), EUNSUPPORTED),
+    (dict(n_pages=0), EINVAL), (dict(n_pages=(1 << 30) + 1), EINVAL), (dict(H_kv=0), EINVAL), (dict(page_rows=0), EINVAL), (dict(page_rows=1), EUNSUPPORTED),
     (dict(page_rows=24), EUNSUPPORTED), (dict(page_rows=96, head_stride=96 * 128, page_stride=4 * 96 * 128), EUNSUPPORTED),
     (dict(D=96), EUNSUPPORTED), (dict(D=512), EUNSUPPORTED),
     (dict(row_stride=64), EINVAL), (dict(row_stride=132), EINVAL), (dict(head_stride=128), EINVAL), (dict(page_stride=128), EINVAL),
