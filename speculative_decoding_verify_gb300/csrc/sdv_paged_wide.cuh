@@ -145,7 +145,7 @@ struct WideLayout {
     static constexpr int QROW = D * 4 + 16, QR = PaLayout<T, D>::STAGE / QROW < RP ? PaLayout<T, D>::STAGE / QROW : RP, QS = (RP + QR - 1) / QR;
     static_assert(QS < (I8 ? NRAW : NOP), "a piece's queries fit in the ring");
     static constexpr int THREADS = PW_SOFT + 128 + (I8 ? 128 : 0);
-    static constexpr int WARP_P = 4 * PW_NG, WARP_M = WARP_P + 1, WARP_C = WARP_P + 4;  // producer, MMAs, first converting warp
+    static constexpr int WARP_P = 4 * PW_NG, WARP_M = WARP_P + 1, WARP_S = WARP_P + 2, WARP_C = WARP_P + 4;  // producer, MMAs, scales and first converting warp (8-bit rows)
     // tensor memory columns
     static constexpr int TQ = 0, QCOLS = NP * D / 2;
     static constexpr int SCOLS = NR == 3 ? 96 : 64;  // scores (64), then the weights' parts over them (32 each)
@@ -229,12 +229,12 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
 
     if (tid == 0) {
         for (int i = 0; i < W::NOP; ++i) {
-            mbar_init(&op_full[i], W::I8 ? 4 : 1);
+            mbar_init(&op_full[i], W::I8 ? 5 : 1);
             mbar_init(&op_empty[i], 1);
         }
         for (int i = 0; i < W::NRAW; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 4);
+            mbar_init(&raw_empty[i], 5);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -351,28 +351,30 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             (void)mbar_wait_bounded(done, 0, PA_WAIT_NS);
         }
         __syncwarp();
-    } else if (warp >= W::WARP_C) {
+    } else if (warp == W::WARP_S || warp >= W::WARP_C) {
         if constexpr (W::I8) {
-            regs_dec<W::REG_C>();
-            // ---- 8-bit rows to fp16 operands: thread ct takes row ct % 64 of K (ct < 64) or V
+            // ---- 8-bit rows to fp16 operands: thread ct takes row ct % 64 of K (ct < 64) or V; a warp of its own writes the scales (on a
+            // converting warp they were the longest way through a tile: 254 -> 221 us for 16 sequences of 16000 rows)
+            if (warp >= W::WARP_C) regs_dec<W::REG_C>();
             const int ct = tid - 32 * W::WARP_C, row = ct & 63;
             const bool isv = ct >= 64;
+            // 16-byte chunk x of a row is at its row's offset with x in the swizzled bits: exclusive-ors of one base
+            const uint32_t from = (isv ? LY::KV : 0) + pa_off<T, D>(row, 0), to = (isv ? W::OKV : 0) + pa_off<SD_KV_F16, D>(row, 0);
             uint32_t rs = 0, rph = 0, os = 0, oph = 0, np = 0;
             int64_t u = sc.u0, i = 0;
-            int b = 0, left = 0;  // tiles of the piece still to come
-            int ve = -126;        // exponent of the unit of the V scales so far in the piece
+            int b = 0, left = 0;        // tiles of the piece still to come
+            uint32_t unit = 0x00800000;  // the unit of the V scales so far in the piece (a power of two, as bits)
             for (; left > 0 || u < sc.u1; ++i, --left) {
                 if (left == 0) {  // the next piece: its queries' stages go back once they are read
                     const Piece p = piece_at<RP>(a, sc, u, b);
                     b = p.b;
                     left = p.t1 - p.t0;
                     u += left;
-                    const bool got = mbar_wait_bounded(q_ready, np++ & 1u, PA_WAIT_NS, abort);
-                    if (!got) {
+                    if (!mbar_wait_bounded(q_ready, np++ & 1u, PA_WAIT_NS, abort)) {
                         set_status(a.status, SD_ETIMEOUT);
                         *abort = 1;
                     }
-                    ve = -126;
+                    unit = 0x00800000;
                     for (int s = 0; s < W::QS; ++s) {
                         if (lane == 0) mbar_arrive(&raw_empty[rs]);
                         if (++rs == W::NRAW) {
@@ -387,44 +389,38 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     set_status(a.status, SD_ETIMEOUT);
                     *abort = 1;
                 }
+                __syncwarp();
                 const uint8_t *src = raw + static_cast<size_t>(rs) * LY::STAGE;
-                uint8_t *dst = ops + static_cast<size_t>(os) * W::OSTAGE + (isv ? W::OKV : 0);
+                uint8_t *dst = ops + static_cast<size_t>(os) * W::OSTAGE;
+                if (warp >= W::WARP_C) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(src + (isv ? LY::KV : 0) + pa_off<T, D>(row, 16 * x));
-                    const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+                    for (int x = 0; x < D / 16; ++x) {
+                        // (a row's 16-byte chunks beyond 128 bytes are in the next tensor tile)
+                        const uint4 v = *reinterpret_cast<const uint4 *>(src + ((from + (x * 16 / LY::ROWB) * LY::TILE) ^ (x * 16 % LY::ROWB)));
+                        const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        *reinterpret_cast<uint4 *>(dst + pa_off<SD_KV_F16, D>(row, 32 * x + 16 * y)) =
-                            make_uint4(codes2<0, 1>(w[2 * y]), codes2<2, 3>(w[2 * y]), codes2<0, 1>(w[2 * y + 1]), codes2<2, 3>(w[2 * y + 1]));
-                }
-                const float *ss = reinterpret_cast<const float *>(src + 2 * LY::KV);
-                float *ds = reinterpret_cast<float *>(ops + static_cast<size_t>(os) * W::OSTAGE + 2 * W::OKV);
-                if (ct < 32) {  // K scales; an infinite one makes a row of NaN
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float s = ss[lane + 32 * y];
-                        ds[lane + 32 * y] = s + 0.0f * s;
+                        for (int y = 0; y < 2; ++y)
+                            *reinterpret_cast<uint4 *>(dst + ((to + ((32 * x + 16 * y) / 128) * W::OTILE) ^ ((32 * x + 16 * y) % 128))) =
+                                make_uint4(codes2<0, 1>(w[2 * y]), codes2<2, 3>(w[2 * y]), codes2<0, 1>(w[2 * y + 1]), codes2<2, 3>(w[2 * y + 1]));
                     }
-                } else if (ct < 64) {  // V scales in units of a power of two that none so far in the piece exceeds
-                    float s[2] = {ss[PA_KT + lane], ss[PA_KT + 32 + lane]};
-                    int e = ve;
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        if (s[y] > 0.0f && s[y] < INFINITY) {
-                            int x;
-                            (void)frexpf(s[y], &x);
-                            e = max(e, x);
-                        }
-                    e = __reduce_max_sync(0xffffffffu, e);
-                    const float down = ldexpf(1.0f, -e);
-                    ds[PA_KT + lane] = s[0] * down;
-                    ds[PA_KT + 32 + lane] = s[1] * down;
+                } else {
+                    const float *ss = reinterpret_cast<const float *>(src + 2 * LY::KV);
+                    float *ds = reinterpret_cast<float *>(dst + 2 * W::OKV);
+                    const float k0 = ss[lane], k1 = ss[lane + 32], v0 = ss[PA_KT + lane], v1 = ss[PA_KT + 32 + lane];
+                    ds[lane] = k0 + 0.0f * k0;  // an infinite K scale makes a row of NaN
+                    ds[lane + 32] = k1 + 0.0f * k1;
+                    // V scales in units of a power of two above all finite ones so far in the piece (positive floats order as their bits)
+                    const uint32_t m0 = v0 > 0.0f && v0 < INFINITY ? __float_as_uint(v0) : 0u, m1 = v1 > 0.0f && v1 < INFINITY ? __float_as_uint(v1) : 0u;
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m0, m1));
+                    const uint32_t was = unit;
+                    unit = min(max(unit, (top & 0x7f800000u) + 0x00800000u), 0x7e800000u);
+                    const float down = __uint_as_float(0x7f000000u - unit);  // 1 / unit (at most 2^126, so that this is a normal number)
+                    ds[PA_KT + lane] = v0 * down;
+                    ds[PA_KT + 32 + lane] = v1 * down;
                     if (lane == 0) {
-                        ds[2 * PA_KT] = ldexpf(1.0f, ve - e);  // what the outputs so far shrink by
-                        ds[2 * PA_KT + 1] = ldexpf(1.0f, e);   // the unit
+                        ds[2 * PA_KT] = __uint_as_float(was) * down;  // what the outputs so far shrink by
+                        ds[2 * PA_KT + 1] = __uint_as_float(unit);
                     }
-                    ve = e;
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
