@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][dt][e] = 0.0f;
         }
-        int ve = -200;  // 8-bit rows: the outputs are in units of 2^ve, at least every V scale so far
+        uint32_t vunit = 0x00800000u;  // 8-bit rows: the outputs' unit, a power of two above every V scale so far (its bits)
         // keys from full_lo on (or below full_sink) and below p.len are seen by every row
         const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
         bool ok = true;
@@ -227,24 +227,12 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
             }
             float vmul0 = 1.0f, vmul1 = 1.0f, shrink = 1.0f;
             if constexpr (T == SD_KV_I8) {
-                int e = -200;
-                int x;
-                if (vs0 > 0.0f && vs0 < INFINITY) {
-                    (void)frexpf(vs0, &x);
-                    e = x;
-                }
-                if (vs1 > 0.0f && vs1 < INFINITY) {
-                    (void)frexpf(vs1, &x);
-                    e = max(e, x);
-                }
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, off));
-                e = max(e, -126);
-                if (e > ve) {
-                    shrink = ve > -200 ? ldexpf(1.0f, ve - e) : 0.0f;
-                    ve = e;
-                }
-                const float down = ldexpf(1.0f, -ve);
+                // a power of two above all finite scales so far (positive floats order as their bits)
+                const uint32_t t0 = vs0 > 0.0f && vs0 < INFINITY ? __float_as_uint(vs0) : 0u, t1 = vs1 > 0.0f && vs1 < INFINITY ? __float_as_uint(vs1) : 0u;
+                const uint32_t top = __reduce_max_sync(0xffffffffu, max(t0, t1)), was = vunit;
+                vunit = min(max(vunit, (top & 0x7f800000u) + 0x00800000u), 0x7e800000u);
+                const float down = __uint_as_float(0x7f000000u - vunit);  // its inverse
+                shrink = __uint_as_float(was) * down;
                 vmul0 = vs0 * down;
                 vmul1 = vs1 * down;
             }
@@ -393,7 +381,7 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
         // ---- join the warps' states and write the piece: rows that are whole go out, others become partials
         const bool complete = p.t0 == 0 && p.t1 == p.st.T;
         const int pslot = 2 * static_cast<int>(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
-        const float unit = T == SD_KV_BF16 ? 1.0f : T == SD_KV_I8 ? (ve > -200 ? ldexpf(1.0f / PA_PS, ve) : 0.0f) : 1.0f / PA_PS;
+        const float unit = T == SD_KV_BF16 ? 1.0f : T == SD_KV_I8 ? __uint_as_float(vunit) / PA_PS : 1.0f / PA_PS;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
