@@ -259,11 +259,12 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                 al[nt][0] = T == SD_KV_I8 ? al0 * shrink : al0;
                 al[nt][1] = T == SD_KV_I8 ? al1 * shrink : al1;
                 if constexpr (T == SD_KV_I8) {
+                    const float w0 = pr[nt][0] * vmul0, w1 = pr[nt][1] * vmul0, w2 = pr[nt][2] * vmul1, w3 = pr[nt][3] * vmul1;
                     // a key with no weight keeps none, whatever its scale is
-                    pr[nt][0] = pr[nt][0] > 0.0f ? pr[nt][0] * vmul0 : pr[nt][0];
-                    pr[nt][1] = pr[nt][1] > 0.0f ? pr[nt][1] * vmul0 : pr[nt][1];
-                    pr[nt][2] = pr[nt][2] > 0.0f ? pr[nt][2] * vmul1 : pr[nt][2];
-                    pr[nt][3] = pr[nt][3] > 0.0f ? pr[nt][3] * vmul1 : pr[nt][3];
+                    pr[nt][0] = whole || pr[nt][0] > 0.0f ? w0 : pr[nt][0];
+                    pr[nt][1] = whole || pr[nt][1] > 0.0f ? w1 : pr[nt][1];
+                    pr[nt][2] = whole || pr[nt][2] > 0.0f ? w2 : pr[nt][2];
+                    pr[nt][3] = whole || pr[nt][3] > 0.0f ? w3 : pr[nt][3];
                 }
             }
             const uint32_t vst = st + LY::KV;

@@ -96,23 +96,32 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x to about 2^-22, 0 below 
     return y;
 }
 
-// a pair of weights in 16-bit parts, as split2 (the differences are exact)
+// one 16-bit part of a pair, and what it leaves over
+template <int T>
+__device__ __forceinline__ uint32_t part_bits(float2 x) {
+    if constexpr (T == SD_KV_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x.x, x.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+template <int T>
+__device__ __forceinline__ float2 part_left(float2 x, uint32_t bits) {
+    const float2 f = T == SD_KV_BF16 ? make_float2(__uint_as_float(bits << 16), __uint_as_float(bits & 0xffff0000u))
+                                     : __half22float2(*reinterpret_cast<const __half2 *>(&bits));
+    return ffma2_rn(f, make_float2(-1.0f, -1.0f), x);
+}
+
+// a pair of weights in all its parts, as split2 (the differences are exact)
 template <int T>
 __device__ __forceinline__ Parts<T> split_pair(float2 x) {
     Parts<T> p;
 #pragma unroll
     for (int i = 0; i < Parts<T>::N; ++i) {
-        float2 f;
-        if constexpr (T == SD_KV_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-            p.r[i] = *reinterpret_cast<const uint32_t *>(&h);
-            f = make_float2(__uint_as_float(p.r[i] << 16), __uint_as_float(p.r[i] & 0xffff0000u));
-        } else {
-            const __half2 h = __floats2half2_rn(x.x, x.y);
-            p.r[i] = *reinterpret_cast<const uint32_t *>(&h);
-            f = __half22float2(h);
-        }
-        if (i + 1 < Parts<T>::N) x = ffma2_rn(f, make_float2(-1.0f, -1.0f), x);
+        p.r[i] = part_bits<T>(x);
+        if (i + 1 < Parts<T>::N) x = part_left<T>(x, p.r[i]);
     }
     return p;
 }
@@ -688,19 +697,25 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         }
                     }
                 }
+                if constexpr (W::CP == 1) {
 #pragma unroll
-                for (int e = 0; e < NC / 2; ++e) {
-                    const Parts<T> f = split_pair<T>(s[e]);
+                    for (int e = 0; e < NC / 2; ++e) {
+                        const Parts<T> f = split_pair<T>(s[e]);
 #pragma unroll
-                    for (int x = 0; x < W::NR; ++x) {
-                        if constexpr (W::CP == 1) {
-                            keep[x][e] = f.r[x];
-                        } else {
-                            uint32_t v = 0;
+                        for (int x = 0; x < W::NR; ++x) keep[x][e] = f.r[x];
+                    }
+                } else {
+                    // one part, the same for the whole warp (lane groups are whole warps): part `part` of what the parts before leave
+                    static_assert(W::NR == 1 && RP % 32 == 0, "one part a lane, one lane group a warp");
+                    for (int k = 0; k < part && k < NP - 1; ++k)
 #pragma unroll
-                            for (int y = 0; y < NP; ++y) v = x * W::CP + part == y ? f.r[y] : v;
-                            keep[x][e] = v;
-                        }
+                        for (int e = 0; e < NC / 2; ++e) s[e] = part_left<T>(s[e], part_bits<T>(s[e]));
+                    if (part < NP) {
+#pragma unroll
+                        for (int e = 0; e < NC / 2; ++e) keep[0][e] = part_bits<T>(s[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < NC / 2; ++e) keep[0][e] = 0;
                     }
                 }
 #pragma unroll
