@@ -31,11 +31,14 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                                                                 const __grid_constant__ CUtensorMap tmv) {
     using LY = PaLayout<T, D>;
     constexpr int KS = D / 16, RPG = 8 * NT, NP = Parts<T>::N, SD = 64 + 4;
+    // 16 rows of D = 256: their query fragments do not fit beside the outputs in registers, and all four warps need the same ones
+    constexpr bool QSM = D == 256 && NT == 2;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // the swizzle wants 1024 B
     float *sm_o = reinterpret_cast<float *>(ring + static_cast<size_t>(a.nst) * LY::STAGE);  // [PA_CW][8][SD]: 64 columns of the warps' outputs
     float *sm_m = sm_o + PA_CW * 8 * SD, *sm_l = sm_m + PA_CW * RPG;                         // [PA_CW][RPG]
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm_l + PA_CW * RPG), *empty = full + a.nst;
+    uint32_t *sm_q = reinterpret_cast<uint32_t *>(sm_l + PA_CW * RPG);  // [NT][KS][2 NP][32]
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm_q + (QSM ? NT * KS * 2 * NP * 32 : 0)), *empty = full + a.nst;
     int64_t *prefix = reinterpret_cast<int64_t *>(empty + a.nst);
     int2 *ln = reinterpret_cast<int2 *>(prefix + a.B + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(ln + a.B);
@@ -76,7 +79,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
         const int rows = p.n * a.g, total = p.len + p.n;
         // B fragments of query row g of each 8-row tile, in parts; fp16 parts of a row scaled by 2^(11-e) for
         // max |q| in [2^(e-1), 2^e), so that neither part is subnormal
-        uint32_t qf[NT][KS][2][NP];
+        uint32_t qf[QSM ? 1 : NT][QSM ? 1 : KS][2][NP];
+        if constexpr (QSM) named_bar_sync(1, 32 * PA_CW);  // the piece before is done with them
         float rs[NT][2];            // the scale back of rows 2c, 2c+1
         uint32_t vis[NT][2];        // new rows that rows 2c, 2c+1 see
         int low[NT][2];             // the first row of their window
@@ -121,8 +125,15 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                 const Parts<T> f0 = split2<T>(qv[ks][0] * up, qv[ks][1] * up), f1 = split2<T>(qv[ks][2] * up, qv[ks][3] * up);
 #pragma unroll
                 for (int i2 = 0; i2 < NP; ++i2) {
-                    qf[nt][ks][0][i2] = f0.r[i2];
-                    qf[nt][ks][1][i2] = f1.r[i2];
+                    if constexpr (QSM) {
+                        if (ks % PA_CW == warp) {
+                            sm_q[((nt * KS + ks) * 2 * NP + i2) * 32 + lane] = f0.r[i2];
+                            sm_q[((nt * KS + ks) * 2 * NP + NP + i2) * 32 + lane] = f1.r[i2];
+                        }
+                    } else {
+                        qf[nt][ks][0][i2] = f0.r[i2];
+                        qf[nt][ks][1][i2] = f1.r[i2];
+                    }
                 }
             }
 #pragma unroll
@@ -138,6 +149,12 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                 }
             }
         }
+        if constexpr (QSM) named_bar_sync(1, 32 * PA_CW);
+        // a query fragment in its parts
+        auto q_of = [&](int nt, int ks, int half, int x) {
+            if constexpr (QSM) return sm_q[((nt * KS + ks) * 2 * NP + half * NP + x) * 32 + lane];
+            else return qf[nt][ks][half][x];
+        };
         float m[NT][2], l[NT][2], o[NT][KS][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -179,14 +196,14 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int x = 0; x < NP; ++x) {
-                                pa_mma<T>(sa[nt][0], k1, qf[nt][k0][0][x], qf[nt][k0][1][x]);
-                                pa_mma<T>(sa[nt][1], k2, qf[nt][k0 + 1][0][x], qf[nt][k0 + 1][1][x]);
+                                pa_mma<T>(sa[nt][0], k1, q_of(nt, k0, 0, x), q_of(nt, k0, 1, x));
+                                pa_mma<T>(sa[nt][1], k2, q_of(nt, k0 + 1, 0, x), q_of(nt, k0 + 1, 1, x));
                             }
                     } else {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int x = 0; x < NP; ++x) pa_mma<T>(sa[nt][k0 & 1], ka, qf[nt][k0][0][x], qf[nt][k0][1][x]);
+                            for (int x = 0; x < NP; ++x) pa_mma<T>(sa[nt][k0 & 1], ka, q_of(nt, k0, 0, x), q_of(nt, k0, 1, x));
                     }
                 }
 #pragma unroll
@@ -472,16 +489,19 @@ static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
     const int sms = num_sms();
     if (sms < 1) return false;
     const int rows = M * (H / H_kv);
-    p.nt = rows > 8 && D <= 128 ? 2 : 1;
+    p.nt = rows > 8 ? 2 : 1;
+    const int parts = type == SD_KV_BF16 ? 3 : 2;
     const size_t fixed = 1024 + static_cast<size_t>(PA_CW) * 8 * 68 * 4 + 2 * static_cast<size_t>(PA_CW) * 8 * p.nt * 4 +
+                         (D == 256 && p.nt == 2 ? static_cast<size_t>(2) * (D / 16) * 2 * parts * 32 * 4 : 0) +
                          (static_cast<size_t>(B) + 1) * 8 + static_cast<size_t>(B) * 8 + 16;
     const size_t per = pa_stage(type, D) + 16;
     const size_t half = (228 * 1024) / 2 - 1024, whole = 227 * 1024;
-    int per_sm = 2;
-    int64_t n = (static_cast<int64_t>(half) - static_cast<int64_t>(fixed)) / static_cast<int64_t>(per);
+    // two CTAs where their registers fit (above) and two stages each do
+    int per_sm = D == 256 || (D == 128 && p.nt == 2) ? 1 : 2;
+    int64_t n = (static_cast<int64_t>(per_sm == 2 ? half : whole) - static_cast<int64_t>(fixed)) / static_cast<int64_t>(per);
     if (n < 2) {
         per_sm = 1;
-        n = (whole - fixed) / per;
+        n = (static_cast<int64_t>(whole) - static_cast<int64_t>(fixed)) / static_cast<int64_t>(per);
     }
     p.nst = static_cast<int>(n < 8 ? n : 8);
     p.grid = per_sm * sms;
@@ -537,7 +557,7 @@ static cudaError_t pa_launch(const PaPlan &p, const PagedArgs &a, const CUtensor
 }
 template <int T>
 static cudaError_t pa_launch_d(int D, const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t s) {
-    if (D == 256) return pa_launch<T, 256, 1>(p, a, tmk, tmv, s);
+    if (D == 256) return p.nt == 1 ? pa_launch<T, 256, 1>(p, a, tmk, tmv, s) : pa_launch<T, 256, 2>(p, a, tmk, tmv, s);
     if (D == 128) return p.nt == 1 ? pa_launch<T, 128, 1>(p, a, tmk, tmv, s) : pa_launch<T, 128, 2>(p, a, tmk, tmv, s);
     return p.nt == 1 ? pa_launch<T, 64, 1>(p, a, tmk, tmv, s) : pa_launch<T, 64, 2>(p, a, tmk, tmv, s);
 }

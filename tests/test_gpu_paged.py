@@ -148,7 +148,7 @@ def test_windows_and_sinks(sdv, dtype, window, sinks, tree):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
-@pytest.mark.parametrize("M,H,H_kv,D", [(3, 3, 1, 128), (3, 3, 1, 64), (4, 8, 2, 64), (4, 5, 1, 256), (5, 10, 2, 64), (11, 3, 1, 128), (16, 4, 1, 64), (13, 10, 2, 128), (16, 8, 1, 64),
+@pytest.mark.parametrize("M,H,H_kv,D", [(3, 3, 1, 128), (3, 3, 1, 64), (4, 8, 2, 64), (4, 5, 1, 256), (16, 8, 1, 256), (5, 10, 2, 64), (11, 3, 1, 128), (16, 4, 1, 64), (13, 10, 2, 128), (16, 8, 1, 64),
                                         (9, 15, 1, 128), (16, 40, 1, 64), (16, 64, 1, 128)])
 def test_many_rows_per_kv_head(sdv, dtype, M, H, H_kv, D):
     """From 9 to 1024 query rows of a KV head, some sequences with fewer, contexts over tile and CTA borders."""
