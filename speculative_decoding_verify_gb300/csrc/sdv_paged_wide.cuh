@@ -815,25 +815,34 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     if constexpr (C > 1) {
                         join_partials<RP, D, PW_SOFT>(a, p, c0, c1, tid, scratch, 5);
                     } else {
-                        // as join_partials: in the order of the keys, a row's weights from its maxima
+                        // as join_partials: in the order of the keys, with a running maximum; two partials' loads in flight at once
                         __threadfence();
                         float jm = PA_NEG, jl = 0.0f;
-#pragma unroll 4
-                        for (int x = c0; x <= c1; ++x) jm = fmaxf(jm, __ldcg(&a.part_ml[(2 * x + (x == c0)) * RP + r]).x);
 #pragma unroll
                         for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
-                        for (int x = c0; x <= c1; ++x) {
-                            const int64_t sl = 2 * x + (x == c0);
-                            const float2 ml = __ldcg(&a.part_ml[sl * RP + r]);
-                            float4 y[W::DO / 4];
+                        for (int x0 = c0; x0 <= c1; x0 += 2) {
+                            float2 ml[2];
+                            float4 y[2][W::DO / 4];
 #pragma unroll
-                            for (int d = 0; d < W::DO / 4; ++d) y[d] = __ldcg(lanes + sl * (RP * D / 4) + d * 128);
-                            const float w = ex2(ml.x - jm);
-                            jl = fmaf(ml.y, w, jl);
+                            for (int h = 0; h < 2; ++h) {
+                                const int x = min(x0 + h, c1);  // (past the last: read again, and weighed by 0)
+                                const int64_t sl = 2 * x + (x == c0);
+                                ml[h] = __ldcg(&a.part_ml[sl * RP + r]);
 #pragma unroll
-                            for (int d = 0; d < W::DO / 4; ++d) {
-                                o[2 * d] = ffma2_rn(make_float2(y[d].x, y[d].y), make_float2(w, w), o[2 * d]);
-                                o[2 * d + 1] = ffma2_rn(make_float2(y[d].z, y[d].w), make_float2(w, w), o[2 * d + 1]);
+                                for (int d = 0; d < W::DO / 4; ++d) y[h][d] = __ldcg(lanes + sl * (RP * D / 4) + d * 128);
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (x0 + h > c1) break;
+                                const float n = fmaxf(jm, ml[h].x), w0 = ex2(jm - n), w = ex2(ml[h].x - n);
+                                jm = n;
+                                jl = fmaf(jl, w0, ml[h].y * w);
+#pragma unroll
+                                for (int d = 0; d < W::DO / 4; ++d) {
+                                    const float2 lo = fmul2_rn(o[2 * d], make_float2(w0, w0)), hi = fmul2_rn(o[2 * d + 1], make_float2(w0, w0));
+                                    o[2 * d] = ffma2_rn(make_float2(y[h][d].x, y[h][d].y), make_float2(w, w), lo);
+                                    o[2 * d + 1] = ffma2_rn(make_float2(y[h][d].z, y[h][d].w), make_float2(w, w), hi);
+                                }
                             }
                         }
                         write_rows(true, jl == 0.0f ? 0.0f : 1.0f / jl);
