@@ -13,7 +13,7 @@ namespace sdv {
 constexpr int PG_MAX_B = 1024;  // sequences per call (their schedule is held in shared memory)
 constexpr int PG_MAX_PAGES = 1 << 30;
 
-// The driver's tensor-map encoder (sdv_attn.cu), looked up once; null if the driver has none.
+// The CUDA driver's tensor-map encoder (sdv_attn.cu), looked up once; null if it has none.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 inline int kv_type_bytes(int type) { return type == SD_KV_I8 ? 1 : 2; }

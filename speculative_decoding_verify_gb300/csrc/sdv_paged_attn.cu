@@ -24,18 +24,22 @@
 
 namespace sdv {
 
-// (Five warps a CTA put three of ten on one scheduler: above 168 registers one CTA runs per SM.  At D = 64 the 16-row form is held to
-// that, 162 -> 125 us for 16 sequences of 16000 bf16 rows; at D = 128 it would spill 60 registers and take 20 % longer.)
+// (Five warps a CTA put three of ten on one scheduler: above 168 registers one CTA runs per SM.  At D = 64 the 16-row
+// form is held to that, 162 -> 125 us for 16 sequences of 16000 bf16 rows; at D = 128 it would spill 60 registers and
+// take 20 % longer.)
 template <int T, int D, int NT>
-__global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
-                                                                const __grid_constant__ CUtensorMap tmv) {
+__global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
+    paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv) {
     using LY = PaLayout<T, D>;
     constexpr int KS = D / 16, RPG = 8 * NT, NP = Parts<T>::N, SD = 64 + 4;
-    // 16 rows of D = 256: their query fragments do not fit beside the outputs in registers, and all four warps need the same ones
+    // 16 rows of D = 256: their query fragments do not fit beside the outputs in registers, and all four warps need the
+    // same ones
     constexpr bool QSM = D == 256 && NT == 2;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // the swizzle wants 1024 B
-    float *sm_o = reinterpret_cast<float *>(ring + static_cast<size_t>(a.nst) * LY::STAGE);  // [PA_CW][8][SD]: 64 columns of the warps' outputs
+    // [PA_CW][8][SD]: 64 columns of the warps' outputs
+    float *sm_o = reinterpret_cast<float *>(ring + static_cast<size_t>(a.nst) * LY::STAGE);
     float *sm_m = sm_o + PA_CW * 8 * SD, *sm_l = sm_m + PA_CW * RPG;                         // [PA_CW][RPG]
     uint32_t *sm_q = reinterpret_cast<uint32_t *>(sm_l + PA_CW * RPG);  // [NT][KS][2 NP][32]
     uint64_t *full = reinterpret_cast<uint64_t *>(sm_q + (QSM ? NT * KS * 2 * NP * 32 : 0)), *empty = full + a.nst;
@@ -165,7 +169,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][dt][e] = 0.0f;
         }
-        uint32_t vunit = 0x00800000u;  // 8-bit rows: the outputs' unit, a power of two above every V scale so far (its bits)
+        // 8-bit rows: the outputs' unit, a power of two above every V scale so far (its bits)
+        uint32_t vunit = 0x00800000u;
         // keys from full_lo on (or below full_sink) and below p.len are seen by every row
         const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
         bool ok = true;
@@ -189,7 +194,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                     uint32_t ka[4];
                     pa_ldsm(st + pa_off<T, D>(kr, (T == SD_KV_I8 ? 16 : 32) * k0 + kx), ka);
                     if constexpr (T == SD_KV_I8) {
-                        const uint32_t w0 = ka[0] ^ 0x80808080u, w1 = ka[1] ^ 0x80808080u, w2 = ka[2] ^ 0x80808080u, w3 = ka[3] ^ 0x80808080u;
+                        const uint32_t w0 = ka[0] ^ 0x80808080u, w1 = ka[1] ^ 0x80808080u, w2 = ka[2] ^ 0x80808080u,
+                                       w3 = ka[3] ^ 0x80808080u;
                         const uint32_t k1[4] = {codes2<0, 1>(w0), codes2<0, 1>(w1), codes2<2, 3>(w0), codes2<2, 3>(w1)};
                         const uint32_t k2[4] = {codes2<0, 1>(w2), codes2<0, 1>(w3), codes2<2, 3>(w2), codes2<2, 3>(w3)};
 #pragma unroll
@@ -203,7 +209,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int x = 0; x < NP; ++x) pa_mma<T>(sa[nt][k0 & 1], ka, q_of(nt, k0, 0, x), q_of(nt, k0, 1, x));
+                            for (int x = 0; x < NP; ++x)
+                                pa_mma<T>(sa[nt][k0 & 1], ka, q_of(nt, k0, 0, x), q_of(nt, k0, 1, x));
                     }
                 }
 #pragma unroll
@@ -214,9 +221,11 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
             const int ja = key0 + 16 * warp + g, jb = ja + 8;  // s[.][0..1]: key ja, rows 2c, 2c+1; s[.][2..3]: key jb
             float vs0 = 1.0f, vs1 = 1.0f;
             if constexpr (T == SD_KV_I8) {
-                const float *scales = reinterpret_cast<const float *>(ring + static_cast<size_t>(slot) * LY::STAGE + 2 * LY::KV);
+                const float *scales =
+                    reinterpret_cast<const float *>(ring + static_cast<size_t>(slot) * LY::STAGE + 2 * LY::KV);
                 float ks0 = scales[16 * warp + g], ks1 = scales[16 * warp + g + 8];
-                ks0 += 0.0f * ks0;  // an infinite scale makes a row of NaN (0 codes times infinity), not a score of -inf
+                // an infinite scale makes a row of NaN (0 codes times infinity), not a score of -inf
+                ks0 += 0.0f * ks0;
                 ks1 += 0.0f * ks1;
                 vs0 = scales[PA_KT + 16 * warp + g];
                 vs1 = scales[PA_KT + 16 * warp + g + 8];
@@ -245,7 +254,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
             float vmul0 = 1.0f, vmul1 = 1.0f, shrink = 1.0f;
             if constexpr (T == SD_KV_I8) {
                 // a power of two above all finite scales so far (positive floats order as their bits)
-                const uint32_t t0 = vs0 > 0.0f && vs0 < INFINITY ? __float_as_uint(vs0) : 0u, t1 = vs1 > 0.0f && vs1 < INFINITY ? __float_as_uint(vs1) : 0u;
+                const uint32_t t0 = vs0 > 0.0f && vs0 < INFINITY ? __float_as_uint(vs0) : 0u;
+                const uint32_t t1 = vs1 > 0.0f && vs1 < INFINITY ? __float_as_uint(vs1) : 0u;
                 const uint32_t top = __reduce_max_sync(0xffffffffu, max(t0, t1)), was = vunit;
                 vunit = min(max(vunit, (top & 0x7f800000u) + 0x00800000u), 0x7e800000u);
                 const float down = __uint_as_float(0x7f000000u - vunit);  // its inverse
@@ -287,14 +297,17 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
             const uint32_t vst = st + LY::KV;
             if constexpr (T != SD_KV_I8) {
                 if (!whole) {
-                    // a row that some query row does not see may hold anything, and 0 times a NaN or infinity is no 0: such
-                    // rows are added here, to the query rows that see them alone, and cleared before the product
+                    // a row that some query row does not see may hold anything, and 0 times a NaN or infinity is no 0:
+                    // such rows are added here, to the query rows that see them alone, and cleared before the product
                     uint32_t bad = 0;
                     for (int i = lane; i < 16 * LY::NB * (LY::ROWB / 16); i += 32) {
                         const int r = i % 16, x = (i / 16) * 16;
                         uint4 v;
                         const uint32_t ad = vst + pa_off<T, D>(16 * warp + r, x);
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ad) : "memory");
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(ad)
+                                     : "memory");
                         constexpr uint32_t EX = T == SD_KV_BF16 ? 0x7f80u : 0x7c00u;
                         bool any = false;
 #pragma unroll
@@ -328,7 +341,10 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                                 for (int e = 0; e < 2; ++e) {
                                     const int x = 2 * (16 * dt + g + 8 * e);
                                     uint16_t raw;
-                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(vst + pa_off<T, D>(16 * warp + key, x) + (x & 15)) : "memory");
+                                    asm volatile("ld.shared.u16 %0, [%1];"
+                                                 : "=h"(raw)
+                                                 : "r"(vst + pa_off<T, D>(16 * warp + key, x) + (x & 15))
+                                                 : "memory");
                                     float v;
                                     if constexpr (T == SD_KV_BF16) v = __bfloat162float(__ushort_as_bfloat16(raw));
                                     else v = __half2float(__ushort_as_half(raw));
@@ -338,7 +354,9 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                         }
                         __syncwarp();
                         for (int x = 16 * lane; x < 2 * D; x += 512)
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vst + pa_off<T, D>(16 * warp + key, x)), "r"(0u) : "memory");
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vst + pa_off<T, D>(16 * warp + key, x)),
+                                         "r"(0u)
+                                         : "memory");
                         __syncwarp();
                     }
                     if (bad) fence_proxy_async_shared();  // before the stage's next copy
@@ -360,7 +378,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0) paged_attn_kernel
                 uint32_t va[4];
                 pa_ldsm_t(vst + pa_off<T, D>(vr, (T == SD_KV_I8 ? 16 : 32) * dt + vx), va);
                 if constexpr (T == SD_KV_I8) {
-                    const uint32_t w0 = va[0] ^ 0x80808080u, w1 = va[1] ^ 0x80808080u, w2 = va[2] ^ 0x80808080u, w3 = va[3] ^ 0x80808080u;
+                    const uint32_t w0 = va[0] ^ 0x80808080u, w1 = va[1] ^ 0x80808080u, w2 = va[2] ^ 0x80808080u,
+                                   w3 = va[3] ^ 0x80808080u;
                     const uint32_t v1[4] = {codes2<0, 2>(w0), codes2<1, 3>(w0), codes2<0, 2>(w1), codes2<1, 3>(w1)};
                     const uint32_t v2[4] = {codes2<0, 2>(w2), codes2<1, 3>(w2), codes2<0, 2>(w3), codes2<1, 3>(w3)};
 #pragma unroll
@@ -481,7 +500,9 @@ struct PaPlan {
     size_t smem, off_ml, off_o, total;
 };
 
-static size_t pa_stage(int type, int D) { return 2 * static_cast<size_t>(PA_KT) * D * kv_type_bytes(type) + (type == SD_KV_I8 ? 1024 : 0); }
+static size_t pa_stage(int type, int D) {
+    return 2 * static_cast<size_t>(PA_KT) * D * kv_type_bytes(type) + (type == SD_KV_I8 ? 1024 : 0);
+}
 
 // Rows beside each other in one 8- or 16-row group; a persistent grid of two CTAs per SM, or one where
 // three stages of the ring do not fit twice.
@@ -509,13 +530,15 @@ static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
     return true;
 }
 
-// Query rows of a KV head above which the tensor-memory kernel runs: its cost per 64-key tile hardly depends on D or on the
-// rows (up to 32 of them), the other's grows with both.  16 sequences of 16000 rows, 8 KV heads, 16 query rows, this kernel /
-// the tensor-memory one: D = 64 fp16 100 / 147 us; D = 128 fp16 205 / 178, bf16 258 / 223, int8 250 / 252.  The other's shared
-// memory holds the schedule of PA_WIDE_B sequences.
+// Query rows of a KV head above which the tensor-memory kernel runs: its cost per 64-key tile hardly depends on D or on
+// the rows (up to 32 of them), the other's grows with both.  16 sequences of 16000 rows, 8 KV heads, 16 query rows,
+// this kernel / the tensor-memory one: D = 64 fp16 100 / 156 us; D = 128 fp16 186 / 188, bf16 246 / 232, int8
+// 223 / 217.  The other's shared memory holds the schedule of PA_WIDE_B sequences.
 constexpr int PA_WIDE_ROWS = 8, PA_WIDE_ROWS_64 = 16, PA_WIDE_B = 512;
 
-static bool pa_wide(int rows, int D, int B) { return rows > (D == 64 ? PA_WIDE_ROWS_64 : PA_WIDE_ROWS) && D <= 128 && B <= PA_WIDE_B; }
+static bool pa_wide(int rows, int D, int B) {
+    return rows > (D == 64 ? PA_WIDE_ROWS_64 : PA_WIDE_ROWS) && D <= 128 && B <= PA_WIDE_B;
+}
 
 // workspace: counters of the largest grid, then the partials: two per CTA, of 16 rows on two CTAs per SM or
 // of 128 rows on one
@@ -540,7 +563,8 @@ static bool pages_map(CUtensorMap *tm, const sd_kv_pages *p, void *base) {
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p->row_stride) * eb, static_cast<cuuint64_t>(p->head_stride) * eb,
                                    static_cast<cuuint64_t>(p->page_stride) * eb};
     const int rowb = p->D * eb < 128 ? p->D * eb : 128;
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(rowb / eb), static_cast<cuuint32_t>(p->page_rows < PA_KT ? p->page_rows : PA_KT), 1, 1};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(rowb / eb),
+                               static_cast<cuuint32_t>(p->page_rows < PA_KT ? p->page_rows : PA_KT), 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUtensorMapDataType dt = p->type == SD_KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                    : p->type == SD_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -550,13 +574,15 @@ static bool pages_map(CUtensorMap *tm, const sd_kv_pages *p, void *base) {
 }
 
 template <int T, int D, int NT>
-static cudaError_t pa_launch(const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t s) {
+static cudaError_t pa_launch(const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                             cudaStream_t s) {
     const cudaError_t e = allow_max_dynamic_smem(paged_attn_kernel<T, D, NT>);
     if (e != cudaSuccess) return e;
     return launch(paged_attn_kernel<T, D, NT>, dim3(p.grid), dim3(PA_THREADS), p.smem, s, a, tmk, tmv);
 }
 template <int T>
-static cudaError_t pa_launch_d(int D, const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t s) {
+static cudaError_t pa_launch_d(int D, const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk,
+                               const CUtensorMap &tmv, cudaStream_t s) {
     if (D == 256) return p.nt == 1 ? pa_launch<T, 256, 1>(p, a, tmk, tmv, s) : pa_launch<T, 256, 2>(p, a, tmk, tmv, s);
     if (D == 128) return p.nt == 1 ? pa_launch<T, 128, 1>(p, a, tmk, tmv, s) : pa_launch<T, 128, 2>(p, a, tmk, tmv, s);
     return p.nt == 1 ? pa_launch<T, 64, 1>(p, a, tmk, tmv, s) : pa_launch<T, 64, 2>(p, a, tmk, tmv, s);
@@ -569,14 +595,16 @@ using namespace sdv;
 extern "C" {
 
 size_t sd_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D) {
-    if (B < 1 || B > PG_MAX_B || M < 1 || M > 16 || H_kv < 1 || H < H_kv || H % H_kv || (D != 64 && D != 128 && D != 256)) return 0;
+    if (B < 1 || B > PG_MAX_B || M < 1 || M > 16 || H_kv < 1 || H < H_kv || H % H_kv || (D != 64 && D != 128 && D != 256))
+        return 0;
     return pa_workspace(D, nullptr, nullptr);
 }
 
-sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
-                        int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride, int64_t q_row_stride,
-                        const int32_t *parent, int32_t window, int32_t sinks, float *out, int64_t out_seq_stride,
-                        int64_t out_row_stride, void *workspace, size_t ws_bytes, sd_stream_t stream) {
+sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
+                        const int32_t *n_new, int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride,
+                        int64_t q_row_stride, const int32_t *parent, int32_t window, int32_t sinks, float *out,
+                        int64_t out_seq_stride, int64_t out_row_stride, void *workspace, size_t ws_bytes,
+                        sd_stream_t stream) {
     SD_NVTX("sd_paged_attn");
     const sd_status st = pages_check(pages);
     if (st != SD_OK) return st;
@@ -585,11 +613,13 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     if (B < 1 || M < 1 || H < H_kv || H % H_kv || window < 0 || sinks < 0) return SD_EINVAL;
     if (M > 16 || B > PG_MAX_B) return SD_EUNSUPPORTED;
     const int64_t line = static_cast<int64_t>(H) * D;
-    if (q_row_stride < line || out_row_stride < line || q_row_stride % 4 || out_row_stride % 4 || q_seq_stride % 4 || out_seq_stride % 4)
+    if (q_row_stride < line || out_row_stride < line || q_row_stride % 4 || out_row_stride % 4 ||
+        q_seq_stride % 4 || out_seq_stride % 4)
         return SD_EINVAL;
     if (B > 1 && (q_seq_stride < line || out_seq_stride < line)) return SD_EINVAL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return SD_EINVAL;
-    if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 2 * PA_KT) return SD_EUNSUPPORTED;  // positions are 32-bit
+    // positions are 32-bit
+    if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 2 * PA_KT) return SD_EUNSUPPORTED;
     PaPlan p;
     size_t off_ml, off_o;
     const size_t need = pa_workspace(D, &off_ml, &off_o);
@@ -632,7 +662,9 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int rows = M * a.g;
     if (pa_wide(rows, D, B)) {
-        const auto run = pages->type == SD_KV_F16 ? paged_wide_f16 : pages->type == SD_KV_BF16 ? paged_wide_bf16 : paged_wide_i8;
+        const auto run = pages->type == SD_KV_F16 ? paged_wide_f16
+                         : pages->type == SD_KV_BF16 ? paged_wide_bf16
+                                                      : paged_wide_i8;
         return run(a, tmk, tmv, D, rows, num_sms(), s) == cudaSuccess ? SD_OK : SD_ECUDA;
     }
     const cudaError_t e = pages->type == SD_KV_F16    ? pa_launch_d<SD_KV_F16>(D, p, a, tmk, tmv, s)

@@ -45,7 +45,8 @@ struct PaLayout {
 template <int T, int D>
 __device__ __forceinline__ uint32_t pa_off(int r, int x) {
     using L = PaLayout<T, D>;
-    return static_cast<uint32_t>((x / L::ROWB) * L::TILE + r * L::ROWB + ((((x % L::ROWB) >> 4) ^ ((r >> L::SSH) & L::SW)) << 4));
+    return static_cast<uint32_t>((x / L::ROWB) * L::TILE + r * L::ROWB +
+                                 ((((x % L::ROWB) >> 4) ^ ((r >> L::SSH) & L::SW)) << 4));
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *tm, int x, int y, int z, int w, uint64_t *bar) {
@@ -250,12 +251,12 @@ __device__ bool make_sched(const PagedArgs &a, int64_t *prefix, int2 *ln, Sched 
     return true;
 }
 
-// The producer warp's loop: the tiles of the CTA's pieces into the ring's stages, running ahead of whoever empties them.
-// QS > 0: each piece's query rows come first, in QS stages of QR rows, each row D floats and 16 bytes apart (so that threads
-// of consecutive rows read them without bank conflicts).
+// The producer warp's loop: the tiles of the CTA's pieces into the ring's stages, running ahead of whoever empties
+// them.  QS > 0: each piece's query rows come first, in QS stages of QR rows, each row D floats and 16 bytes apart (so
+// that threads of consecutive rows read them without bank conflicts).
 template <int T, int D, int RPG, int QS, int QR>
-__device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring, int nst,
-                              uint64_t *full, uint64_t *empty, volatile int *abort) {
+__device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtensorMap *tmk, const CUtensorMap *tmv,
+                              uint8_t *ring, int nst, uint64_t *full, uint64_t *empty, volatile int *abort) {
     using LY = PaLayout<T, D>;
     const int lane = static_cast<int>(threadIdx.x) & 31;
     // lane l issues copies l, l + 32, .. of a tile (page, K or V, 128 bytes of row)
@@ -287,7 +288,8 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
         for (int s = 0; ok && s < QS; ++s) {
             ok = take();
             if (!ok) break;
-            const int r0 = s * QR, n = max(0, min(min(QR, RPG - r0), p.n * a.g - p.rg * RPG - r0));  // rows of this stage
+            // rows of this stage
+            const int r0 = s * QR, n = max(0, min(min(QR, RPG - r0), p.n * a.g - p.rg * RPG - r0));
             if (lane == 0) {
                 if (n) mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(n) * D * 4);
                 else mbar_arrive(&full[slot]);
@@ -296,15 +298,18 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
             for (int i = lane; i < n; i += 32) {
                 const int tg = p.rg * RPG + r0 + i;
                 bulk_g2s_l2keep(ring + static_cast<size_t>(slot) * LY::STAGE + i * (D * 4 + 16),
-                                a.q + p.b * a.q_sb + (tg / a.g) * a.q_sm + static_cast<int64_t>(p.kh * a.g + tg % a.g) * D, D * 4, &full[slot]);
+                                a.q + p.b * a.q_sb + (tg / a.g) * a.q_sm +
+                                    static_cast<int64_t>(p.kh * a.g + tg % a.g) * D,
+                                D * 4, &full[slot]);
             }
             taken();
         }
         if (!ok) break;
         const int32_t *tab = a.table + static_cast<int64_t>(b) * a.width;
         const int total = p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
-        // the pages of the piece's places in order, npt to a tile, 32 at a time and 32 more on their way: a table entry fetched per tile
-        // would cost the tile its latency.  (A place without rows, or an entry that is no page, reads as zeros.)
+        // the pages of the piece's places in order, npt to a tile, 32 at a time and 32 more on their way: a table entry
+        // fetched per tile would cost the tile its latency.  (A place without rows, or an entry that is no page, reads
+        // as zeros.)
         auto page_of = [&](int e) {
             const int t = p.t0 + (e >> lg);
             if (t >= p.t1) return a.n_pages;
@@ -356,8 +361,8 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
 }
 
 // The partials of one run's CTAs c0 .. c1, joined in the order of their keys by the NTHR threads that call it (named
-// barrier `bar` among them).  A warp reads whole rows (a row of D = 64 half a warp), JC CTAs at a time: the weights of all
-// rows come first, through shared memory (RPG * (JC + 2) floats), then every load of a pass is in flight at once.
+// barrier `bar` among them).  A warp reads whole rows (a row of D = 64 half a warp), JC CTAs at a time: the weights of
+// all rows come first, through shared memory (RPG * (JC + 2) floats), then every load of a pass is in flight at once.
 constexpr int JC = 8;
 template <int RPG, int D, int NTHR>
 __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1, int tid, float *sm, int bar) {
@@ -404,10 +409,13 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
                     const int tr = r0 + i * RT, xc = x0 + xs + x;
                     const bool on = xs + x < nx && tr < rows;
                     f[x][i] = on ? weight[(xs + x) * RPG + tr] : 0.0f;
+                    const float4 *from =
+                        reinterpret_cast<const float4 *>(
+                            a.part_o + (static_cast<int64_t>(2 * xc + (xc == c0)) * RPG + tr) * D) +
+                        col;
 #pragma unroll
                     for (int k = 0; k < NV; ++k)
-                        y[x][i][k] = on ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + (static_cast<int64_t>(2 * xc + (xc == c0)) * RPG + tr) * D) + col + k * LR)
-                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        y[x][i][k] = on ? __ldcg(from + k * LR) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
 #pragma unroll
             for (int x = 0; x < XU; ++x)
@@ -427,17 +435,22 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
         const int tr = r0 + i * RT, tg = p.rg * RPG + tr;
         if (tr < rows) {
             const float inv = sum_of[tr];
-            float4 *to = reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + (tg / a.g) * a.o_sm + static_cast<int64_t>(p.kh * a.g + tg % a.g) * D) + col;
+            float4 *to = reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + (tg / a.g) * a.o_sm +
+                                                    static_cast<int64_t>(p.kh * a.g + tg % a.g) * D) + col;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) to[k * LR] = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
+            for (int k = 0; k < NV; ++k)
+                to[k * LR] = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
         }
     }
     named_bar_sync(bar, NTHR);
 }
 
 // The many-row kernel (sdv_paged_wide.cuh): D = 64 or 128, `rows` the most query rows of a KV head, one CTA per SM.
-cudaError_t paged_wide_f16(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows, int grid, cudaStream_t s);
-cudaError_t paged_wide_bf16(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows, int grid, cudaStream_t s);
-cudaError_t paged_wide_i8(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows, int grid, cudaStream_t s);
+cudaError_t paged_wide_f16(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows,
+                           int grid, cudaStream_t s);
+cudaError_t paged_wide_bf16(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows,
+                            int grid, cudaStream_t s);
+cudaError_t paged_wide_i8(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows, int grid,
+                          cudaStream_t s);
 
 }  // namespace sdv

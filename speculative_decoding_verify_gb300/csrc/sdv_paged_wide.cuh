@@ -2,20 +2,22 @@
 // heads): the same work, cut, masks and partials as paged_attn_kernel, on the 5th-generation tensor cores.
 //
 // The rows of one (sequence, KV head) are the 128 lanes of tensor memory.  With at most 64 (32) of them the lanes hold
-// C = 2 (4) groups of the same rows, which hold different 16-bit parts of the weights (one pass of the product instead of
-// two or three) or weigh different keys of a tile; the lane groups join at the end of a piece as the splits of a run do.
+// C = 2 (4) groups of the same rows, which hold different 16-bit parts of the weights (one pass of the product instead
+// of two or three) or weigh different keys of a tile; the lane groups join at the end of a piece as the splits of a run
+// do.
 //   S = Q K^T: tcgen05.mma kind::f16, M = 128, N = 64, Q in tensor memory as A (written once per piece, in 16-bit parts
 //     that add up to the fp32 value: two fp16, or three bf16), K as B from shared memory as the tensor copy left it
 //     (K-major, 128-byte swizzle);
 //   softmax: four threads per lane, a quarter of the tile's keys each, their maximum shared through shared memory; the
 //     weights go back to tensor memory over the scores, in parts;
 //   O_t = P V: the weights as A, V as B (MN-major, the same swizzle), from zero for each tile; the softmax threads add
-//     a quarter of the columns each to their fp32 outputs in registers with the rescale of the running maximum (a tensor-core accumulator kept
-//     over the tiles would truncate at every step, and rescaling it would cost the same loads and more stores).
+//     a quarter of the columns each to their fp32 outputs in registers with the rescale of the running maximum (a
+//     tensor-core accumulator kept over the tiles would truncate at every step, and rescaling it would cost the same
+//     loads and more stores).
 // One thread issues all MMAs: scores two tiles ahead of the weights, so the tensor cores work while the softmax
-// runs.  Measured on the way (16 sequences of 8000 rows, 8 KV heads, 128 query rows, fp16): one softmax group of four warps
-// 215 us, two that take the tiles in turn 149 us (each waits for its own product: the chain scores - softmax - product
-// is longer than two tiles).  8-bit rows pass through four more warps that write them as fp16 into operand
+// runs.  Measured on the way (16 sequences of 8000 rows, 8 KV heads, 128 query rows, fp16): one softmax group of four
+// warps 215 us, two that take the tiles in turn 149 us (each waits for its own product: the chain scores - softmax -
+// product is longer than two tiles).  8-bit rows pass through four more warps that write them as fp16 into operand
 // buffers (exact) and their scales beside them.
 //
 // What bounds it: at 128 rows of D = 128 a 64-key fp16 tile is 32 KB of HBM (about 1400 SM cycles of one SM's share)
@@ -49,9 +51,12 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-#define PW_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
-#define PW_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
-#define PW_W8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+#define PW_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), \
+                    "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define PW_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), \
+                    "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+#define PW_W8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), \
+                    "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
 
 // N consecutive columns of this warp's lanes; the values are there after tc_wait_ld on the same registers
 __device__ __forceinline__ void tc_ld(uint32_t (&r)[8], uint32_t addr) {
@@ -80,7 +85,9 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : PW_W8(r, 0), PW_W8(r, 8), PW_W8(r, 16), PW_W8(r, 24)::"memory");
 }
 __device__ __forceinline__ void tc_st(const uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 __device__ __forceinline__ void tc_st(const uint32_t (&r)[8], uint32_t addr) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), PW_I8(r, 0) : "memory");
@@ -146,15 +153,19 @@ struct WideLayout {
     static constexpr int NR = (NP + CP - 1) / CP;   // parts that a lane holds: passes of the product
     static constexpr int OTILE = PA_KT * 128;       // 64 keys x 64 halves
     static constexpr int OKV = D / 64 * OTILE;      // K (or V) operand of a tile
-    static constexpr int OSCALES = I8 ? 1024 : 0;   // scales of K [64], of V [64] in the piece's unit so far, its change, the unit
+    // scales of K [64], of V [64] in the piece's unit so far, its change, the unit
+    static constexpr int OSCALES = I8 ? 1024 : 0;
     static constexpr int OSTAGE = 2 * OKV + OSCALES;
-    static constexpr int NOP = I8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 6);  // operand stages (8-bit rows: written by the converting warps)
+    // operand stages (8-bit rows: written by the converting warps)
+    static constexpr int NOP = I8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 6);
     static constexpr int NRAW = I8 ? (D == 64 ? 8 : 5) : 0;                 // 8-bit stages as copied
     // the query rows of a piece take stages of the copies' ring before its tiles
-    static constexpr int QROW = D * 4 + 16, QR = PaLayout<T, D>::STAGE / QROW < RP ? PaLayout<T, D>::STAGE / QROW : RP, QS = (RP + QR - 1) / QR;
+    static constexpr int QROW = D * 4 + 16;
+    static constexpr int QR = PaLayout<T, D>::STAGE / QROW < RP ? PaLayout<T, D>::STAGE / QROW : RP, QS = (RP + QR - 1) / QR;
     static_assert(QS < (I8 ? NRAW : NOP), "a piece's queries fit in the ring");
     static constexpr int THREADS = PW_SOFT + 128 + (I8 ? 128 : 0);
-    static constexpr int WARP_P = 4 * PW_NG, WARP_M = WARP_P + 1, WARP_S = WARP_P + 2, WARP_C = WARP_P + 4;  // producer, MMAs, scales and first converting warp (8-bit rows)
+    // producer, MMAs, scales and first converting warp (8-bit rows)
+    static constexpr int WARP_P = 4 * PW_NG, WARP_M = WARP_P + 1, WARP_S = WARP_P + 2, WARP_C = WARP_P + 4;
     // tensor memory columns
     static constexpr int TQ = 0, QCOLS = NP * D / 2;
     static constexpr int SCOLS = NR == 3 ? 96 : 64;  // scores (64), then the weights' parts over them (32 each)
@@ -162,10 +173,14 @@ struct WideLayout {
     static constexpr int NPV = QCOLS + 2 * SCOLS + 2 * D <= 512 ? 2 : 1;  // product buffers
     static constexpr int TO = TS + 2 * SCOLS;
     static_assert(TO + NPV * D <= 512, "tensor memory");
-    // shared memory after the rings: 16 columns of every softmax thread's outputs, the threads' maxima (two turns) and sums
+    // shared memory after the rings: 16 columns of every softmax thread's outputs, the threads' maxima (two turns) and
+    // sums
     static constexpr int SCRATCH = PW_SOFT * 20 * 4 + 3 * PW_SOFT * 4;
     static constexpr int NBAR = 2 * NOP + 2 * NRAW + 8 + 3;
-    static constexpr size_t fixed() { return 1024 + static_cast<size_t>(NOP) * OSTAGE + static_cast<size_t>(NRAW) * PaLayout<T, D>::STAGE + SCRATCH + NBAR * 8 + 64; }
+    static constexpr size_t fixed() {
+        return 1024 + static_cast<size_t>(NOP) * OSTAGE +
+               static_cast<size_t>(NRAW) * PaLayout<T, D>::STAGE + SCRATCH + NBAR * 8 + 64;
+    }
     // registers per thread as launched, then of the softmax, of producer and MMA, of the converting warps
     static constexpr int REG_L = I8 ? 128 : 168, REG_S = I8 ? 192 : 224, REG_P = I8 ? 64 : 56, REG_C = 64;
     static_assert(PW_SOFT * REG_S + 128 * REG_P + (I8 ? 128 * REG_C : 0) <= THREADS * REG_L, "registers");
@@ -185,10 +200,11 @@ __device__ __forceinline__ uint32_t seen_keys(int key0, int len, int low, int si
     return m | (d >= 32 || d <= -32 ? 0u : d >= 0 ? vis << d : vis >> -d);
 }
 
-// What V rows with a NaN or infinity (bits of bad) add to the outputs acc of this thread: weight times value where the row
-// sees the key and has a weight for it, and nothing elsewhere.  Rare: kept out of the tile's code.
+// What V rows with a NaN or infinity (bits of bad) add to the outputs acc of this thread: weight times value where the
+// row sees the key and has a weight for it, and nothing elsewhere.  Rare: kept out of the tile's code.
 template <int T, int D, int DO>
-__device__ __noinline__ void add_bad_rows(float *acc, const uint8_t *v_rows, uint2 bad, uint2 seen, uint32_t scores, float back, float off, int d0) {
+__device__ __noinline__ void add_bad_rows(float *acc, const uint8_t *v_rows, uint2 bad, uint2 seen, uint32_t scores,
+                                          float back, float off, int d0) {
     for (int j = 0; j < PA_KT; ++j) {
         if (!(((j < 32 ? bad.x : bad.y) >> (j & 31)) & 1u)) continue;
         uint32_t y;
@@ -214,7 +230,8 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 
 template <int T, int D, int C>
 __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
-    paged_wide_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    paged_wide_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv) {
     using W = WideLayout<T, D, C>;
     using LY = PaLayout<T, D>;
     constexpr int NP = W::NP, RP = W::RP, NC = W::NC, KS = D / 16;
@@ -288,7 +305,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         if (elect_one()) {
             constexpr uint32_t FMT = T == SD_KV_BF16 ? 1u : 0u;
             constexpr uint32_t ID = (1u << 4) | (FMT << 7) | (FMT << 10) | (8u << 24);  // fp32 sums, M = 128
-            constexpr uint32_t ID_QK = ID | (PA_KT / 8 << 17), ID_PV = ID | (1u << 16) | (D / 8 << 17);  // B K-major; B MN-major
+            // B K-major; B MN-major
+            constexpr uint32_t ID_QK = ID | (PA_KT / 8 << 17), ID_PV = ID | (1u << 16) | (D / 8 << 17);
             const uint32_t ob = smem_u32(ops);
             int64_t u = sc.u0;
             int b = 0;
@@ -320,7 +338,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     for (int x = NP - 1; x >= 0; --x)
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
-                            tc_mma_ts(d, tm + W::TQ + x * (D / 2) + ks * 8, sw128_desc(kb + (ks >> 2) * W::OTILE + (ks & 3) * 32, 0), ID_QK, acc);
+                            tc_mma_ts(d, tm + W::TQ + x * (D / 2) + ks * 8,
+                                      sw128_desc(kb + (ks >> 2) * W::OTILE + (ks & 3) * 32, 0), ID_QK, acc);
                             acc = true;
                         }
                     tc_commit(&s_full[nqk & 1u]);
@@ -338,7 +357,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     ok = ok && wait(&p_ready[sb], (npv >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t vb = ob + pv_slot * W::OSTAGE + W::OKV, d = tm + W::TO + ob2 * D, pa = tm + W::TS + sb * W::SCOLS;
+                    const uint32_t vb = ob + pv_slot * W::OSTAGE + W::OKV, d = tm + W::TO + ob2 * D,
+                                   pa = tm + W::TS + sb * W::SCOLS;
                     bool acc = false;
 #pragma unroll
                     for (int x = W::NR - 1; x >= 0; --x)
@@ -362,13 +382,15 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         __syncwarp();
     } else if (warp == W::WARP_S || warp >= W::WARP_C) {
         if constexpr (W::I8) {
-            // ---- 8-bit rows to fp16 operands: thread ct takes row ct % 64 of K (ct < 64) or V; a warp of its own writes the scales (on a
-            // converting warp they were the longest way through a tile: 254 -> 221 us for 16 sequences of 16000 rows)
+            // ---- 8-bit rows to fp16 operands: thread ct takes row ct % 64 of K (ct < 64) or V; a warp of its own
+            // writes the scales (on a converting warp they were the longest way through a tile: 254 -> 221 us for 16
+            // sequences of 16000 rows)
             if (warp >= W::WARP_C) regs_dec<W::REG_C>();
             const int ct = tid - 32 * W::WARP_C, row = ct & 63;
             const bool isv = ct >= 64;
             // 16-byte chunk x of a row is at its row's offset with x in the swizzled bits: exclusive-ors of one base
-            const uint32_t from = (isv ? LY::KV : 0) + pa_off<T, D>(row, 0), to = (isv ? W::OKV : 0) + pa_off<SD_KV_F16, D>(row, 0);
+            const uint32_t from = (isv ? LY::KV : 0) + pa_off<T, D>(row, 0);
+            const uint32_t to = (isv ? W::OKV : 0) + pa_off<SD_KV_F16, D>(row, 0);
             uint32_t rs = 0, rph = 0, os = 0, oph = 0, np = 0;
             int64_t u = sc.u0, i = 0;
             int b = 0, left = 0;        // tiles of the piece still to come
@@ -405,12 +427,15 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
                         // (a row's 16-byte chunks beyond 128 bytes are in the next tensor tile)
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src + ((from + (x * 16 / LY::ROWB) * LY::TILE) ^ (x * 16 % LY::ROWB)));
+                        const uint4 v =
+                            *reinterpret_cast<const uint4 *>(src + ((from + (x * 16 / LY::ROWB) * LY::TILE) ^ (x * 16 % LY::ROWB)));
                         const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
 #pragma unroll
                         for (int y = 0; y < 2; ++y)
-                            *reinterpret_cast<uint4 *>(dst + ((to + ((32 * x + 16 * y) / 128) * W::OTILE) ^ ((32 * x + 16 * y) % 128))) =
-                                make_uint4(codes2<0, 1>(w[2 * y]), codes2<2, 3>(w[2 * y]), codes2<0, 1>(w[2 * y + 1]), codes2<2, 3>(w[2 * y + 1]));
+                            *reinterpret_cast<uint4 *>(
+                                dst + ((to + ((32 * x + 16 * y) / 128) * W::OTILE) ^ ((32 * x + 16 * y) % 128))) =
+                                make_uint4(codes2<0, 1>(w[2 * y]), codes2<2, 3>(w[2 * y]), codes2<0, 1>(w[2 * y + 1]),
+                                           codes2<2, 3>(w[2 * y + 1]));
                     }
                 } else {
                     const float *ss = reinterpret_cast<const float *>(src + 2 * LY::KV);
@@ -418,12 +443,15 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     const float k0 = ss[lane], k1 = ss[lane + 32], v0 = ss[PA_KT + lane], v1 = ss[PA_KT + 32 + lane];
                     ds[lane] = k0 + 0.0f * k0;  // an infinite K scale makes a row of NaN
                     ds[lane + 32] = k1 + 0.0f * k1;
-                    // V scales in units of a power of two above all finite ones so far in the piece (positive floats order as their bits)
-                    const uint32_t m0 = v0 > 0.0f && v0 < INFINITY ? __float_as_uint(v0) : 0u, m1 = v1 > 0.0f && v1 < INFINITY ? __float_as_uint(v1) : 0u;
+                    // V scales in units of a power of two above all finite ones so far in the piece (positive floats
+                    // order as their bits)
+                    const uint32_t m0 = v0 > 0.0f && v0 < INFINITY ? __float_as_uint(v0) : 0u;
+                    const uint32_t m1 = v1 > 0.0f && v1 < INFINITY ? __float_as_uint(v1) : 0u;
                     const uint32_t top = __reduce_max_sync(0xffffffffu, max(m0, m1));
                     const uint32_t was = unit;
                     unit = min(max(unit, (top & 0x7f800000u) + 0x00800000u), 0x7e800000u);
-                    const float down = __uint_as_float(0x7f000000u - unit);  // 1 / unit (at most 2^126, so that this is a normal number)
+                    // 1 / unit (at most 2^126, so that this is a normal number)
+                    const float down = __uint_as_float(0x7f000000u - unit);
                     ds[PA_KT + lane] = v0 * down;
                     ds[PA_KT + 32 + lane] = v1 * down;
                     if (lane == 0) {
@@ -449,12 +477,14 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         }
     } else if (warp < 4 * PW_NG) {
         regs_inc<W::REG_S>();
-        // ---- softmax: thread = lane of tensor memory (row lt % RP, lane group lt / RP), of which each of the PW_NG groups weighs
-        // some keys of every tile and adds some columns of its product; a lane's maximum is shared by its PW_NG threads
+        // ---- softmax: thread = lane of tensor memory (row lt % RP, lane group lt / RP), of which each of the PW_NG
+        // groups weighs some keys of every tile and adds some columns of its product; a lane's maximum is shared by its
+        // PW_NG threads
         const int grp = warp >> 2, lt = tid & 127, quarter = warp & 3;
         const uint32_t tq = tm + (static_cast<uint32_t>(32 * quarter) << 16);
         const int lg = lt / RP, r = lt % RP;
-        const int part = lg % W::CP, l_at = (lg / W::CP) * W::KL, k_at = l_at + grp * NC;  // this lane's part and keys; this thread's keys
+        // this lane's part and keys; this thread's keys
+        const int part = lg % W::CP, l_at = (lg / W::CP) * W::KL, k_at = l_at + grp * NC;
         int64_t u = sc.u0;
         int b = 0;
         uint32_t nt = 0, nsync = 0, nmask = 0, nmax = 0, slot_n = 0, slot_ph = 0, q_slot = 0, q_ph = 0;
@@ -464,7 +494,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             if (lane == 0) mbar_arrive(mask_bar);
             return __all_sync(0xffffffffu, wait(mask_bar, nsync++ & 1u)) != 0;
         };
-        // the largest of a lane's PW_NG values; `ok` false in any of its warps makes it false in all: they leave together
+        // the largest of a lane's PW_NG values; `ok` false in any of its warps makes it false in all: they leave
+        // together
         auto lane_max = [&](float x) {
             float *turn = sm_m + (nmax++ & 1u) * PW_SOFT;
             turn[tid] = x;
@@ -483,8 +514,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             float2 o[W::DO / 2];
             float back = 1.0f;
             {
-                // this thread's columns of the row's query into tensor memory, in parts; fp16 parts scaled by a power of two as in
-                // paged_attn_kernel.  The producer has put the rows into the first stages of the piece
+                // this thread's columns of the row's query into tensor memory, in parts; fp16 parts scaled by a power
+                // of two as in paged_attn_kernel.  The producer has put the rows into the first stages of the piece
                 if constexpr (!W::I8) q_slot = slot_n, q_ph = slot_ph;
                 uint64_t *qfull = W::I8 ? raw_full : op_full;
                 const uint8_t *qring = W::I8 ? raw : ops;
@@ -493,7 +524,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 for (int s = 0; s < W::QS; ++s) {
                     ok = ok && __all_sync(0xffffffffu, wait(&qfull[q_slot], q_ph));
                     if (r / W::QR == s)
-                        qp = reinterpret_cast<const float4 *>(qring + static_cast<size_t>(q_slot) * LY::STAGE + (r - s * W::QR) * W::QROW + grp * W::DO * 4);
+                        qp = reinterpret_cast<const float4 *>(qring + static_cast<size_t>(q_slot) * LY::STAGE +
+                                                              (r - s * W::QR) * W::QROW + grp * W::DO * 4);
                     if (++q_slot == (W::I8 ? W::NRAW : W::NOP)) {
                         q_slot = 0;
                         q_ph ^= 1u;
@@ -543,7 +575,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 low = a.window > 0 ? p.len + depth - a.window + 1 : 0;
             }
             const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
-            float m = PA_NEG, l = 0.0f, al = 0.0f, unit = 1.0f;  // al: rescale of the outputs before the product still to be added; unit: theirs (8-bit rows)
+            // al: rescale of the outputs before the product still to be added; unit: theirs (8-bit rows)
+            float m = PA_NEG, l = 0.0f, al = 0.0f, unit = 1.0f;
 #pragma unroll
             for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
             // adds this thread's columns of the product of tile number i to the outputs
@@ -580,7 +613,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         q_ph ^= 1u;
                     }
                 }
-                ok = wait(&s_full[sb], (nt >> 1) & 1u) && ok;  // (each lane's own answer: lane_max brings them together)
+                // (each lane's own answer: lane_max brings them together)
+                ok = wait(&s_full[sb], (nt >> 1) & 1u) && ok;
                 tc_fence_after();
                 const uint32_t sc_at = tq + W::TS + sb * W::SCOLS;
                 const int tile0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT, key0 = tile0 + k_at;
@@ -600,7 +634,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     tc_ld(y, sc_at + k_at);
                     tc_wait_ld(y);
 #pragma unroll
-                    for (int e = 0; e < NC / 2; ++e) s[e] = make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                    for (int e = 0; e < NC / 2; ++e)
+                        s[e] = make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
                 }
                 if constexpr (W::I8) {
 #pragma unroll
@@ -626,12 +661,14 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 bool rescaled = false;
                 if constexpr (!W::I8) {
                     if (!whole) {
-                        // V rows with a NaN or infinity reach the rows that see them alone: added here, and cleared before the product
+                        // V rows with a NaN or infinity reach the rows that see them alone: added here, and cleared
+                        // before the product
                         uint32_t bw[2] = {0, 0};
 #pragma unroll 1
                         for (int x = tid; x < PA_KT * (2 * D / 16); x += PW_SOFT) {
                             const int vr = x % PA_KT;
-                            const uint4 v = *reinterpret_cast<const uint4 *>(stage + W::OKV + pa_off<T, D>(vr, (x / PA_KT) * 16));
+                            const uint4 v =
+                                *reinterpret_cast<const uint4 *>(stage + W::OKV + pa_off<T, D>(vr, (x / PA_KT) * 16));
                             constexpr uint32_t EX = T == SD_KV_BF16 ? 0x7f80u : 0x7c00u;
                             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -646,7 +683,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                             if (lane == 0 && any) atomicOr(&words[w], any);
                         }
                         ok = sync_all() && ok;
-                        const uint32_t bad[2] = {*reinterpret_cast<volatile uint32_t *>(&words[0]), *reinterpret_cast<volatile uint32_t *>(&words[1])};
+                        const uint32_t bad[2] = {*reinterpret_cast<volatile uint32_t *>(&words[0]),
+                                                 *reinterpret_cast<volatile uint32_t *>(&words[1])};
                         if (tid == 0) other[0] = other[1] = 0;  // read by all before the barrier above
                         if (__all_sync(0xffffffffu, ok) && (bad[0] | bad[1])) {
                             if (t > p.t0) ok = add_product(nt - 1) && ok;
@@ -657,10 +695,13 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                                 acc[2 * d + 1] = o[d].y * an;
                             }
                             rescaled = true;
-                            uint2 seen = make_uint2(seen_keys(tile0, p.len, low, full_sink, vis), seen_keys(tile0 + 32, p.len, low, full_sink, vis));
-                            seen.x &= part == 0 ? key_range(0, l_at, l_at + W::KL) : 0u;  // this lane's keys, once for all parts
+                            uint2 seen = make_uint2(seen_keys(tile0, p.len, low, full_sink, vis),
+                                                    seen_keys(tile0 + 32, p.len, low, full_sink, vis));
+                            // this lane's keys, once for all parts
+                            seen.x &= part == 0 ? key_range(0, l_at, l_at + W::KL) : 0u;
                             seen.y &= part == 0 ? key_range(32, l_at, l_at + W::KL) : 0u;
-                            add_bad_rows<T, D, W::DO>(acc, stage + W::OKV, make_uint2(bad[0], bad[1]), seen, sc_at, back, off, grp * W::DO);
+                            add_bad_rows<T, D, W::DO>(acc, stage + W::OKV, make_uint2(bad[0], bad[1]), seen, sc_at,
+                                                      back, off, grp * W::DO);
 #pragma unroll
                             for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(acc[2 * d], acc[2 * d + 1]);
                             ok = sync_all() && ok;
@@ -668,13 +709,16 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                             for (int x = tid; x < PA_KT * (2 * D / 16); x += PW_SOFT) {
                                 const int vr = x % PA_KT;
                                 if ((bad[vr >> 5] >> (vr & 31)) & 1u)
-                                    *reinterpret_cast<uint4 *>(const_cast<uint8_t *>(stage) + W::OKV + pa_off<T, D>(vr, (x / PA_KT) * 16)) = make_uint4(0, 0, 0, 0);
+                                    *reinterpret_cast<uint4 *>(const_cast<uint8_t *>(stage) + W::OKV +
+                                                               pa_off<T, D>(vr, (x / PA_KT) * 16)) =
+                                        make_uint4(0, 0, 0, 0);
                             }
                             fence_proxy_async_shared();
                         }
                     }
                 }
-                // weights in parts, over the scores: the lane's threads read theirs before any writes (lane_max is behind them)
+                // weights in parts, over the scores: the lane's threads read theirs before any writes (lane_max is
+                // behind them)
                 float2 l2 = make_float2(0.0f, 0.0f);
                 uint32_t keep[W::NR][NC / 2];
 #pragma unroll
@@ -705,7 +749,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         for (int x = 0; x < W::NR; ++x) keep[x][e] = f.r[x];
                     }
                 } else {
-                    // one part, the same for the whole warp (lane groups are whole warps): part `part` of what the parts before leave
+                    // one part, the same for the whole warp (lane groups are whole warps): part `part` of what the
+                    // parts before leave
                     static_assert(W::NR == 1 && RP % 32 == 0, "one part a lane, one lane group a warp");
                     for (int k = 0; k < part && k < NP - 1; ++k)
 #pragma unroll
@@ -756,8 +801,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             }
             const float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
-            // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared memory: thread = 4
-            // columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
+            // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared
+            // memory: thread = 4 columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
             auto write_rows = [&](bool final, float fac) {
                 constexpr int RW = PW_SOFT / (4 * PW_NG), NK = (RP + RW - 1) / RW;
                 const int wg = (tid >> 2) % PW_NG, wc = wg * W::DO + 4 * (tid & 3), wr = tid / (4 * PW_NG);
@@ -766,14 +811,16 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 for (int k = 0; k < NK; ++k) {
                     const int tr = wr + RW * k, y = p.rg * RP + tr;
                     to[k] = tr >= RP || y >= rows ? nullptr
-                            : final ? a.out + p.b * a.o_sb + (y / a.g) * a.o_sm + static_cast<int64_t>(p.kh * a.g + y % a.g) * D + wc
+                            : final ? a.out + p.b * a.o_sb + (y / a.g) * a.o_sm +
+                                          static_cast<int64_t>(p.kh * a.g + y % a.g) * D + wc
                                     : a.part_o + (static_cast<int64_t>(pslot) * RP + tr) * D + wc;
                 }
 #pragma unroll
                 for (int d = 0; d < W::DO; d += 16) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 x = fmul2_rn(o[d / 2 + 2 * e], make_float2(fac, fac)), y = fmul2_rn(o[d / 2 + 2 * e + 1], make_float2(fac, fac));
+                        const float2 x = fmul2_rn(o[d / 2 + 2 * e], make_float2(fac, fac));
+                        const float2 y = fmul2_rn(o[d / 2 + 2 * e + 1], make_float2(fac, fac));
                         *reinterpret_cast<float4 *>(scratch + tid * 20 + 4 * e) = make_float4(x.x, x.y, y.x, y.y);
                     }
                     named_bar_sync(5, PW_SOFT);
@@ -783,7 +830,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                             for (int j = 0; j < C; ++j) {
-                                const float4 x = *reinterpret_cast<const float4 *>(scratch + (wg * 128 + j * RP + wr + RW * k) * 20 + 4 * (tid & 3));
+                                const float4 x = *reinterpret_cast<const float4 *>(
+                                    scratch + (wg * 128 + j * RP + wr + RW * k) * 20 + 4 * (tid & 3));
                                 v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
                             }
                             *reinterpret_cast<float4 *>(to[k] + d) = v;
@@ -791,15 +839,16 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     named_bar_sync(5, PW_SOFT);
                 }
             };
-            // C = 1: a thread's columns of a partial as they are, [D / 4][128] 16-byte columns (lanes beside each other: whole lines, no
-            // exchange); the joining CTA's threads read the same places
+            // C = 1: a thread's columns of a partial as they are, [D / 4][128] 16-byte columns (lanes beside each
+            // other: whole lines, no exchange); the joining CTA's threads read the same places
             float4 *lanes = reinterpret_cast<float4 *>(a.part_o) + grp * (W::DO / 4) * 128 + lt;
             if (C > 1 || complete) {
                 write_rows(complete, f);
             } else {
 #pragma unroll
                 for (int d = 0; d < W::DO / 4; ++d)
-                    lanes[static_cast<int64_t>(pslot) * (RP * D / 4) + d * 128] = make_float4(o[2 * d].x * unit, o[2 * d].y * unit, o[2 * d + 1].x * unit, o[2 * d + 1].y * unit);
+                    lanes[static_cast<int64_t>(pslot) * (RP * D / 4) + d * 128] =
+                        make_float4(o[2 * d].x * unit, o[2 * d].y * unit, o[2 * d + 1].x * unit, o[2 * d + 1].y * unit);
             }
             if (!complete) {
                 const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
@@ -815,7 +864,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     if constexpr (C > 1) {
                         join_partials<RP, D, PW_SOFT>(a, p, c0, c1, tid, scratch, 5);
                     } else {
-                        // as join_partials: in the order of the keys, with a running maximum; two partials' loads in flight at once
+                        // as join_partials: in the order of the keys, with a running maximum; two partials' loads in
+                        // flight at once
                         __threadfence();
                         float jm = PA_NEG, jl = 0.0f;
 #pragma unroll
@@ -829,7 +879,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                                 const int64_t sl = 2 * x + (x == c0);
                                 ml[h] = __ldcg(&a.part_ml[sl * RP + r]);
 #pragma unroll
-                                for (int d = 0; d < W::DO / 4; ++d) y[h][d] = __ldcg(lanes + sl * (RP * D / 4) + d * 128);
+                                for (int d = 0; d < W::DO / 4; ++d)
+                                    y[h][d] = __ldcg(lanes + sl * (RP * D / 4) + d * 128);
                             }
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -839,7 +890,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                                 jl = fmaf(jl, w0, ml[h].y * w);
 #pragma unroll
                                 for (int d = 0; d < W::DO / 4; ++d) {
-                                    const float2 lo = fmul2_rn(o[2 * d], make_float2(w0, w0)), hi = fmul2_rn(o[2 * d + 1], make_float2(w0, w0));
+                                    const float2 lo = fmul2_rn(o[2 * d], make_float2(w0, w0));
+                                    const float2 hi = fmul2_rn(o[2 * d + 1], make_float2(w0, w0));
                                     o[2 * d] = ffma2_rn(make_float2(y[h][d].x, y[h][d].y), make_float2(w, w), lo);
                                     o[2 * d + 1] = ffma2_rn(make_float2(y[h][d].z, y[h][d].w), make_float2(w, w), hi);
                                 }
@@ -870,10 +922,11 @@ cudaError_t wide_launch(const PagedArgs &a, const CUtensorMap &tmk, const CUtens
     return launch(paged_wide_kernel<T, D, C>, dim3(grid), dim3(W::THREADS), smem, s, a, tmk, tmv);
 }
 template <int T, int D>
-cudaError_t wide_launch_c(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int rows, int grid, cudaStream_t s) {
+cudaError_t wide_launch_c(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int rows, int grid,
+                          cudaStream_t s) {
     if (rows <= 32) return wide_launch<T, D, 4>(a, tmk, tmv, grid, s);
-    // (two lane groups for three bf16 parts make two passes of the product: 346 us against 264 us with one group, 64 rows,
-    // 16 sequences of 16000 rows)
+    // (two lane groups for three bf16 parts make two passes of the product: 346 us against 264 us with one group, 64
+    // rows, 16 sequences of 16000 rows)
     if constexpr (T != SD_KV_BF16)
         if (rows <= 64) return wide_launch<T, D, 2>(a, tmk, tmv, grid, s);
     return wide_launch<T, D, 1>(a, tmk, tmv, grid, s);

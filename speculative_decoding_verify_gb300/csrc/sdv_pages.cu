@@ -28,21 +28,24 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float d) {
     return make_uint2(w[0], w[1]);
 }
 
-// One group of D / 8 lanes per (sequence, row, KV head): K and V, 8 elements a lane (two 16-byte loads, one store each).
-// Bound by HBM: 4 bytes read and `elt` written per element; the row's page is looked up once per group.
+// One group of D / 8 lanes per (sequence, row, KV head): K and V, 8 elements a lane (two 16-byte loads, one store
+// each).  Bound by HBM: 4 bytes read and `elt` written per element; the row's page is looked up once per group.
 template <int T, int D>
-__global__ void __launch_bounds__(256) paged_append_kernel(PageView pv, void *k, void *v, float *k_scale, float *v_scale,
-                                                           const int32_t *table, int32_t width, const int32_t *lens,
-                                                           const int32_t *n_new, int32_t B, int32_t M, const float *k_new,
-                                                           const float *v_new, int64_t sb, int64_t sm, int *status) {
+__global__ void __launch_bounds__(256) paged_append_kernel(PageView pv, void *k, void *v, float *k_scale,
+                                                           float *v_scale, const int32_t *table, int32_t width,
+                                                           const int32_t *lens, const int32_t *n_new, int32_t B,
+                                                           int32_t M, const float *k_new, const float *v_new,
+                                                           int64_t sb, int64_t sm, int *status) {
     constexpr int LR = D / 8, RB = 256 / LR;  // lanes per row, rows per block
     pdl_wait();
     pdl_launch_dependents();
     const int l = static_cast<int>(threadIdx.x) % LR;
     const int64_t items = static_cast<int64_t>(B) * M * pv.H_kv;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * RB + threadIdx.x / LR; it < items; it += static_cast<int64_t>(gridDim.x) * RB) {
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * RB + threadIdx.x / LR; it < items;
+         it += static_cast<int64_t>(gridDim.x) * RB) {
         const int64_t y = it / pv.H_kv;
-        const int h = static_cast<int>(it - y * pv.H_kv), b = static_cast<int>(y / M), i = static_cast<int>(y - static_cast<int64_t>(b) * M);
+        const int h = static_cast<int>(it - y * pv.H_kv), b = static_cast<int>(y / M);
+        const int i = static_cast<int>(y - static_cast<int64_t>(b) * M);
         const int n = n_new ? n_new[b] : M;
         const int len = lens[b];
         if (n < 0 || n > M || len < 0 || static_cast<int64_t>(len) + n > static_cast<int64_t>(width) * pv.P) {
@@ -102,12 +105,13 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PageView pv, void *k,
     }
 }
 
-// One CTA per sequence, a thread per 16-byte column of a row (K and V of all heads).  path increases and path[t] >= t, so
-// moving the rows in the order of t never overwrites a row that is still to be read: no staging.  The row addresses
+// One CTA per sequence, a thread per 16-byte column of a row (K and V of all heads).  path increases and path[t] >= t,
+// so moving the rows in the order of t never overwrites a row that is still to be read: no staging.  The row addresses
 // are looked up once by the first threads.
-__global__ void __launch_bounds__(256) paged_commit_kernel(PageView pv, uint8_t *k, uint8_t *v, float *k_scale, float *v_scale, int eb,
-                                                           const int32_t *table, int32_t width, int32_t *lens, int32_t M,
-                                                           const int32_t *path, const int32_t *count, int *status) {
+__global__ void __launch_bounds__(256) paged_commit_kernel(PageView pv, uint8_t *k, uint8_t *v, float *k_scale,
+                                                           float *v_scale, int eb, const int32_t *table, int32_t width,
+                                                           int32_t *lens, int32_t M, const int32_t *path,
+                                                           const int32_t *count, int *status) {
     __shared__ int32_t from[16], spage[16], srow[16], dpage[16], drow[16];
     pdl_wait();
     pdl_launch_dependents();
@@ -146,7 +150,8 @@ __global__ void __launch_bounds__(256) paged_commit_kernel(PageView pv, uint8_t 
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (i0 + j < n && from[i0 + j] != i0 + j)
-                        r[j] = *reinterpret_cast<const uint4 *>(base + (spage[i0 + j] * pv.ps + srow[i0 + j] * pv.rs) * eb + at);
+                        r[j] =
+                            *reinterpret_cast<const uint4 *>(base + (spage[i0 + j] * pv.ps + srow[i0 + j] * pv.rs) * eb + at);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (i0 + j < n && from[i0 + j] != i0 + j)
@@ -222,7 +227,8 @@ __device__ __forceinline__ int warps_before(int x, int *sh, int &sum) {
     return __shfl_sync(0xffffffffu, inc - v, warp);
 }
 
-// pages p in [lo, hi) with (refs[p] > 0) == live, in order, into out[at ..]; stops once `most` are there.  Returns how many.
+// pages p in [lo, hi) with (refs[p] > 0) == live, in order, into out[at ..]; stops once `most` are there.  Returns how
+// many.
 __device__ int list_pages(const int32_t *refs, int lo, int hi, bool live, int32_t *out, int most, int *sh) {
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
     int at = 0;
@@ -255,8 +261,9 @@ __device__ int list_pages(const int32_t *refs, int lo, int hi, bool live, int32_
     return at;
 }
 
-__global__ void __launch_bounds__(PL_T) pages_reserve_kernel(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t P,
-                                                             const int32_t *lens, const int32_t *n_new, int32_t B, int32_t M, int32_t per,
+__global__ void __launch_bounds__(PL_T) pages_reserve_kernel(int32_t *refs, int32_t n_pages, int32_t *table,
+                                                             int32_t width, int32_t P, const int32_t *lens,
+                                                             const int32_t *n_new, int32_t B, int32_t M, int32_t per,
                                                              int32_t *missing, PagesWs ws, int *status) {
     __shared__ int sh[33];
     __shared__ int n_list;
@@ -301,7 +308,8 @@ __global__ void __launch_bounds__(PL_T) pages_reserve_kernel(int32_t *refs, int3
             int b, slot, len;
             const int pg = look(it, b, slot, len);
             if (pg == -1) d = 1;
-            else if (pg >= 0 && refs[pg] > 1 && !(__ldcg(&ws.cnt[pg]) == refs[pg] && __ldcg(&ws.last[pg]) == it + 1)) d = 2;
+            else if (pg >= 0 && refs[pg] > 1 && !(__ldcg(&ws.cnt[pg]) == refs[pg] && __ldcg(&ws.last[pg]) == it + 1))
+                d = 2;
             ws.dec[it] = d;
         }
         int sum;
@@ -354,8 +362,8 @@ __global__ void __launch_bounds__(PL_T) pages_reserve_kernel(int32_t *refs, int3
     }
 }
 
-__global__ void __launch_bounds__(PL_T) pages_compact_kernel(int32_t *refs, int32_t n_pages, int32_t P, int32_t *remap, int32_t *n_live,
-                                                             PagesWs ws) {
+__global__ void __launch_bounds__(PL_T) pages_compact_kernel(int32_t *refs, int32_t n_pages, int32_t P, int32_t *remap,
+                                                             int32_t *n_live, PagesWs ws) {
     __shared__ int sh[33];
     pdl_wait();
     pdl_launch_dependents();
@@ -399,13 +407,15 @@ __global__ void __launch_bounds__(PL_T) pages_compact_kernel(int32_t *refs, int3
 // where they lie together.  With a table, its entries follow remap.  HBM-bound: every byte read and written once.
 constexpr int CP_T = 256, CP_U = 4;
 
-__global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *k, uint8_t *v, float *k_scale, float *v_scale, int eb,
-                                                          const int32_t *n_copies, const int4 *list, int32_t *table, int64_t entries,
+__global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *k, uint8_t *v, float *k_scale,
+                                                          float *v_scale, int eb, const int32_t *n_copies,
+                                                          const int4 *list, int32_t *table, int64_t entries,
                                                           const int32_t *remap, int *status) {
     pdl_wait();
     pdl_launch_dependents();
     if (table)
-        for (int64_t x = static_cast<int64_t>(blockIdx.x) * CP_T + threadIdx.x; x < entries; x += static_cast<int64_t>(gridDim.x) * CP_T) {
+        for (int64_t x = static_cast<int64_t>(blockIdx.x) * CP_T + threadIdx.x; x < entries;
+             x += static_cast<int64_t>(gridDim.x) * CP_T) {
             const int t = table[x];
             if (t >= 0 && t < pv.n_pages) table[x] = remap[t];
         }
@@ -418,7 +428,8 @@ __global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *
         const int64_t y = w / parts;
         const int part = static_cast<int>(w - y * parts);
         const int4 e = list[y >> 1];
-        if (e.x < 0 || e.x >= pv.n_pages || e.y < 0 || e.y >= pv.n_pages || e.z > pv.P) {  // a plan for another pool's sizes
+        // a plan for another pool's sizes
+        if (e.x < 0 || e.x >= pv.n_pages || e.y < 0 || e.y >= pv.n_pages || e.z > pv.P) {
             set_status(status, SD_EDEVICE);
             continue;
         }
@@ -474,8 +485,9 @@ __device__ __forceinline__ void drop_page(int32_t *refs, int32_t n_pages, int pg
 }
 
 // one CTA per pair
-__global__ void __launch_bounds__(256) pages_fork_kernel(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens,
-                                                         int32_t B, int32_t P, const int32_t *src, const int32_t *dst, int32_t n, int *status) {
+__global__ void __launch_bounds__(256) pages_fork_kernel(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width,
+                                                         int32_t *lens, int32_t B, int32_t P, const int32_t *src,
+                                                         const int32_t *dst, int32_t n, int *status) {
     pdl_wait();
     pdl_launch_dependents();
     const int i = static_cast<int>(blockIdx.x), s = src[i], d = dst[i];
@@ -502,8 +514,9 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(int32_t *refs, int32_t 
 }
 
 // one CTA per named sequence; entries are exchanged, so that a sequence named twice releases its pages once
-__global__ void __launch_bounds__(256) pages_free_kernel(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens,
-                                                         int32_t B, int32_t P, const int32_t *seqs, const int32_t *keep, int *status) {
+__global__ void __launch_bounds__(256) pages_free_kernel(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width,
+                                                         int32_t *lens, int32_t B, int32_t P, const int32_t *seqs,
+                                                         const int32_t *keep, int *status) {
     pdl_wait();
     pdl_launch_dependents();
     const int b = seqs[blockIdx.x], rows = keep ? keep[blockIdx.x] : 0;
@@ -518,8 +531,9 @@ __global__ void __launch_bounds__(256) pages_free_kernel(int32_t *refs, int32_t 
 }
 
 // one CTA per sequence
-__global__ void __launch_bounds__(256) pages_trim_kernel(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, const int32_t *lens,
-                                                         int32_t P, int32_t window, int32_t sinks, int *status) {
+__global__ void __launch_bounds__(256) pages_trim_kernel(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width,
+                                                         const int32_t *lens, int32_t P, int32_t window, int32_t sinks,
+                                                         int *status) {
     pdl_wait();
     pdl_launch_dependents();
     const int b = static_cast<int>(blockIdx.x);
@@ -535,24 +549,32 @@ __global__ void __launch_bounds__(256) pages_trim_kernel(int32_t *refs, int32_t 
 }
 
 template <int T>
-static cudaError_t append_launch(const sd_kv_pages *p, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
-                                 int32_t B, int32_t M, const float *kn, const float *vn, int64_t sb, int64_t sm, int *status, cudaStream_t s) {
+static cudaError_t append_launch(const sd_kv_pages *p, const int32_t *table, int32_t width, const int32_t *lens,
+                                 const int32_t *n_new, int32_t B, int32_t M, const float *kn, const float *vn,
+                                 int64_t sb, int64_t sm, int *status, cudaStream_t s) {
     const int rb = 256 / (p->D / 8);
     const int64_t blocks = (static_cast<int64_t>(B) * M * p->H_kv + rb - 1) / rb;
     const int64_t cap = static_cast<int64_t>(num_sms()) * 32;
     const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap));
     const PageView pv = page_view(p);
     float *ks = T == SD_KV_I8 ? p->k_scale : nullptr, *vs = T == SD_KV_I8 ? p->v_scale : nullptr;
-    if (p->D == 64) return launch(paged_append_kernel<T, 64>, grid, dim3(256), 0, s, pv, p->k, p->v, ks, vs, table, width, lens, n_new, B, M, kn, vn, sb, sm, status);
-    if (p->D == 128) return launch(paged_append_kernel<T, 128>, grid, dim3(256), 0, s, pv, p->k, p->v, ks, vs, table, width, lens, n_new, B, M, kn, vn, sb, sm, status);
-    return launch(paged_append_kernel<T, 256>, grid, dim3(256), 0, s, pv, p->k, p->v, ks, vs, table, width, lens, n_new, B, M, kn, vn, sb, sm, status);
+    if (p->D == 64)
+        return launch(paged_append_kernel<T, 64>, grid, dim3(256), 0, s, pv,
+                      p->k, p->v, ks, vs, table, width, lens, n_new, B, M, kn, vn, sb, sm, status);
+    if (p->D == 128)
+        return launch(paged_append_kernel<T, 128>, grid, dim3(256), 0, s, pv,
+                      p->k, p->v, ks, vs, table, width, lens, n_new, B, M, kn, vn, sb, sm, status);
+    return launch(paged_append_kernel<T, 256>, grid, dim3(256), 0, s, pv,
+                  p->k, p->v, ks, vs, table, width, lens, n_new, B, M, kn, vn, sb, sm, status);
 }
 
-static cudaError_t copy_launch(const sd_kv_pages *p, const PagesWs &ws, int32_t *table, int64_t entries, const int32_t *remap, cudaStream_t s) {
+static cudaError_t copy_launch(const sd_kv_pages *p, const PagesWs &ws, int32_t *table, int64_t entries,
+                               const int32_t *remap, cudaStream_t s) {
     int *status = status_ptr();
     if (!status) return cudaErrorUnknown;
     const bool i8 = p->type == SD_KV_I8;
-    return launch(pages_copy_kernel, dim3(static_cast<unsigned>(num_sms()) * 16), dim3(CP_T), 0, s, page_view(p), static_cast<uint8_t *>(p->k),
+    return launch(pages_copy_kernel, dim3(static_cast<unsigned>(num_sms()) * 16), dim3(CP_T), 0, s, page_view(p),
+                  static_cast<uint8_t *>(p->k),
                   static_cast<uint8_t *>(p->v), i8 ? p->k_scale : nullptr, i8 ? p->v_scale : nullptr, kv_type_bytes(p->type),
                   static_cast<const int32_t *>(ws.n_copies), static_cast<const int4 *>(ws.list), table, entries, remap, status);
 }
@@ -568,30 +590,34 @@ using namespace sdv;
 
 extern "C" {
 
-sd_status sd_paged_append(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
-                          int32_t B, int32_t M, const float *k_new, const float *v_new, int64_t seq_stride, int64_t row_stride,
-                          sd_stream_t stream) {
+sd_status sd_paged_append(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
+                          const int32_t *n_new, int32_t B, int32_t M, const float *k_new, const float *v_new,
+                          int64_t seq_stride, int64_t row_stride, sd_stream_t stream) {
     SD_NVTX("sd_paged_append");
     const sd_status st = pages_check(pages);
     if (st != SD_OK) return st;
     if (!table || !lens || !k_new || !v_new || width < 1 || B < 1 || M < 1) return SD_EINVAL;
     if (B > PG_MAX_B) return SD_EUNSUPPORTED;
     const int64_t line = static_cast<int64_t>(pages->H_kv) * pages->D;
-    if ((M > 1 && row_stride < line) || (B > 1 && seq_stride < line) || row_stride % 4 || seq_stride % 4) return SD_EINVAL;
+    if ((M > 1 && row_stride < line) || (B > 1 && seq_stride < line) || row_stride % 4 || seq_stride % 4)
+        return SD_EINVAL;
     if (!aligned(k_new, 16) || !aligned(v_new, 16)) return SD_EINVAL;
     if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 128) return SD_EUNSUPPORTED;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        pages->type == SD_KV_F16    ? append_launch<SD_KV_F16>(pages, table, width, lens, n_new, B, M, k_new, v_new, seq_stride, row_stride, status, s)
-        : pages->type == SD_KV_BF16 ? append_launch<SD_KV_BF16>(pages, table, width, lens, n_new, B, M, k_new, v_new, seq_stride, row_stride, status, s)
-                                    : append_launch<SD_KV_I8>(pages, table, width, lens, n_new, B, M, k_new, v_new, seq_stride, row_stride, status, s);
+        pages->type == SD_KV_F16    ? append_launch<SD_KV_F16>(pages, table, width, lens, n_new, B, M, k_new, v_new,
+                                                               seq_stride, row_stride, status, s)
+        : pages->type == SD_KV_BF16 ? append_launch<SD_KV_BF16>(pages, table, width, lens, n_new, B, M, k_new, v_new,
+                                                                seq_stride, row_stride, status, s)
+                                    : append_launch<SD_KV_I8>(pages, table, width, lens, n_new, B, M, k_new, v_new,
+                                                              seq_stride, row_stride, status, s);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
-sd_status sd_paged_commit(const sd_kv_pages *pages, const int32_t *table, int32_t width, int32_t *lens, int32_t B, int32_t M,
-                          const int32_t *path, const int32_t *count, sd_stream_t stream) {
+sd_status sd_paged_commit(const sd_kv_pages *pages, const int32_t *table, int32_t width, int32_t *lens, int32_t B,
+                          int32_t M, const int32_t *path, const int32_t *count, sd_stream_t stream) {
     SD_NVTX("sd_paged_commit");
     const sd_status st = pages_check(pages);
     if (st != SD_OK) return st;
@@ -601,9 +627,11 @@ sd_status sd_paged_commit(const sd_kv_pages *pages, const int32_t *table, int32_
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     const bool i8 = pages->type == SD_KV_I8;
-    const cudaError_t e = launch(paged_commit_kernel, dim3(B), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), page_view(pages),
-                                 static_cast<uint8_t *>(pages->k), static_cast<uint8_t *>(pages->v), i8 ? pages->k_scale : nullptr,
-                                 i8 ? pages->v_scale : nullptr, kv_type_bytes(pages->type), table, width, lens, M, path, count, status);
+    const cudaError_t e = launch(paged_commit_kernel, dim3(B), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream),
+                                 page_view(pages),
+                                 static_cast<uint8_t *>(pages->k), static_cast<uint8_t *>(pages->v),
+                                 i8 ? pages->k_scale : nullptr, i8 ? pages->v_scale : nullptr,
+                                 kv_type_bytes(pages->type), table, width, lens, M, path, count, status);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
@@ -619,7 +647,8 @@ sd_status sd_pages_reserve(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
     const sd_status st = pages_check(pages);
     if (st != SD_OK) return st;
     const int P = pages->page_rows;
-    if (!table_ok(refs, pages->n_pages, table, width, B, P) || !lens || !missing || !workspace || M < 1) return SD_EINVAL;
+    if (!table_ok(refs, pages->n_pages, table, width, B, P) || !lens || !missing || !workspace || M < 1)
+        return SD_EINVAL;
     if (!aligned(workspace, 256) || ws_bytes < sd_pages_workspace_bytes(pages->n_pages, B, width)) return SD_EINVAL;
     // slots that M rows can touch; items are counted in 32 bits
     const int64_t most = (static_cast<int64_t>(M) + P - 2) / P + 1, per = most < width ? most : width;
@@ -628,8 +657,9 @@ sd_status sd_pages_reserve(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
     if (!status) return SD_ECUDA;
     const PagesWs ws = pages_ws(workspace, pages->n_pages, static_cast<int64_t>(B) * width);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(pages_reserve_kernel, dim3(1), dim3(PL_T), 0, s, refs, pages->n_pages, table, width, P, lens, n_new, B, M,
-                           static_cast<int32_t>(per), missing, ws, status);
+    cudaError_t e = launch(pages_reserve_kernel, dim3(1), dim3(PL_T), 0, s, refs,
+                           pages->n_pages, table, width, P, lens, n_new, B, M, static_cast<int32_t>(per), missing,
+                           ws, status);
     if (e == cudaSuccess) e = copy_launch(pages, ws, nullptr, 0, nullptr, s);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
@@ -638,60 +668,65 @@ sd_status sd_pages_copy(const sd_kv_pages *pages, const void *workspace, size_t 
     SD_NVTX("sd_pages_copy");
     const sd_status st = pages_check(pages);
     if (st != SD_OK) return st;
-    if (!workspace || !aligned(workspace, 256) || ws_bytes < sd_pages_workspace_bytes(pages->n_pages, 1, 1)) return SD_EINVAL;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < sd_pages_workspace_bytes(pages->n_pages, 1, 1))
+        return SD_EINVAL;
     const PagesWs ws = pages_ws(const_cast<void *>(workspace), pages->n_pages, 1);
-    return copy_launch(pages, ws, nullptr, 0, nullptr, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SD_OK : SD_ECUDA;
+    return copy_launch(pages, ws, nullptr, 0, nullptr,
+                       reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
-sd_status sd_pages_fork(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens, int32_t B, int32_t page_rows,
-                        const int32_t *src, const int32_t *dst, int32_t n, sd_stream_t stream) {
+sd_status sd_pages_fork(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens, int32_t B,
+                        int32_t page_rows, const int32_t *src, const int32_t *dst, int32_t n, sd_stream_t stream) {
     SD_NVTX("sd_pages_fork");
-    if (!table_ok(refs, n_pages, table, width, B, page_rows) || !lens || n < 0 || (n > 0 && (!src || !dst))) return SD_EINVAL;
+    if (!table_ok(refs, n_pages, table, width, B, page_rows) || !lens || n < 0 || (n > 0 && (!src || !dst)))
+        return SD_EINVAL;
     if (n == 0) return SD_OK;
     if (n > B) return SD_EINVAL;  // some dst would be named twice
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
-    return launch(pages_fork_kernel, dim3(n), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), refs, n_pages, table, width, lens, B,
-                  page_rows, src, dst, n, status) == cudaSuccess
+    return launch(pages_fork_kernel, dim3(n), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), refs, n_pages,
+                  table, width, lens, B, page_rows, src, dst, n, status) == cudaSuccess
                ? SD_OK
                : SD_ECUDA;
 }
 
-sd_status sd_pages_free(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens, int32_t B, int32_t page_rows,
-                        const int32_t *seqs, const int32_t *keep, int32_t n, sd_stream_t stream) {
+sd_status sd_pages_free(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, int32_t *lens, int32_t B,
+                        int32_t page_rows, const int32_t *seqs, const int32_t *keep, int32_t n, sd_stream_t stream) {
     SD_NVTX("sd_pages_free");
     if (!table_ok(refs, n_pages, table, width, B, page_rows) || !lens || n < 0 || (n > 0 && !seqs)) return SD_EINVAL;
     if (n == 0) return SD_OK;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
-    return launch(pages_free_kernel, dim3(n), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), refs, n_pages, table, width, lens, B,
-                  page_rows, seqs, keep, status) == cudaSuccess
+    return launch(pages_free_kernel, dim3(n), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), refs, n_pages,
+                  table, width, lens, B, page_rows, seqs, keep, status) == cudaSuccess
                ? SD_OK
                : SD_ECUDA;
 }
 
-sd_status sd_pages_trim(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, const int32_t *lens, int32_t B, int32_t page_rows,
-                        int32_t window, int32_t sinks, sd_stream_t stream) {
+sd_status sd_pages_trim(int32_t *refs, int32_t n_pages, int32_t *table, int32_t width, const int32_t *lens, int32_t B,
+                        int32_t page_rows, int32_t window, int32_t sinks, sd_stream_t stream) {
     SD_NVTX("sd_pages_trim");
     if (!table_ok(refs, n_pages, table, width, B, page_rows) || !lens || window < 1 || sinks < 0) return SD_EINVAL;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
-    return launch(pages_trim_kernel, dim3(B), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), refs, n_pages, table, width, lens,
-                  page_rows, window, sinks, status) == cudaSuccess
+    return launch(pages_trim_kernel, dim3(B), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), refs, n_pages,
+                  table, width, lens, page_rows, window, sinks, status) == cudaSuccess
                ? SD_OK
                : SD_ECUDA;
 }
 
-sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *table, int32_t width, int32_t B, int32_t *remap,
-                           int32_t *n_live, void *workspace, size_t ws_bytes, sd_stream_t stream) {
+sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *table, int32_t width, int32_t B,
+                           int32_t *remap, int32_t *n_live, void *workspace, size_t ws_bytes, sd_stream_t stream) {
     SD_NVTX("sd_pages_compact");
     const sd_status st = pages_check(pages);
     if (st != SD_OK) return st;
-    if (!table_ok(refs, pages->n_pages, table, width, B, pages->page_rows) || !remap || !n_live || !workspace) return SD_EINVAL;
+    if (!table_ok(refs, pages->n_pages, table, width, B, pages->page_rows) || !remap || !n_live || !workspace)
+        return SD_EINVAL;
     if (!aligned(workspace, 256) || ws_bytes < sd_pages_workspace_bytes(pages->n_pages, B, width)) return SD_EINVAL;
     const PagesWs ws = pages_ws(workspace, pages->n_pages, static_cast<int64_t>(B) * width);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(pages_compact_kernel, dim3(1), dim3(PL_T), 0, s, refs, pages->n_pages, pages->page_rows, remap, n_live, ws);
+    cudaError_t e = launch(pages_compact_kernel, dim3(1), dim3(PL_T), 0, s, refs,
+                           pages->n_pages, pages->page_rows, remap, n_live, ws);
     if (e == cudaSuccess) e = copy_launch(pages, ws, table, static_cast<int64_t>(B) * width, remap, s);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
