@@ -386,8 +386,8 @@ sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, in
  * After an SD_ETIMEOUT a workspace must be zero-filled again.
  *
  * sd_paged_append: k_new, v_new fp32, row i of sequence b at b * seq_stride + i * row_stride (elements,
- * multiples of 4, 16-byte aligned), its H_kv heads of D contiguous: they may be columns of a fused projection.  Rounded to
- * the nearest (even) fp16 / bf16; SD_KV_I8: scale = amax|x| / 127 per row and head, code = x / scale rounded half away
+ * multiples of 4, 16-byte aligned), its H_kv heads of D contiguous: they may be columns of a fused projection.
+ * Rounded to the nearest (even) fp16 / bf16; SD_KV_I8: scale = amax|x| / 127 per row and head, code = x / scale rounded half away
  * from zero, 0 if the row is zero (the arithmetic of sd_rmsnorm_quant_acts per row of D); a row that holds a
  * NaN or an infinity gets that as its scale.  M >= 1 of any size.
  *
@@ -398,8 +398,8 @@ sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, in
  * over the committed rows and the new rows on i's path.  window > 0: of these only the rows whose position is
  * greater than i's minus window, or less than sinks (StreamingLLM-style first tokens that stay visible); pages
  * wholly behind the window and past the sinks are not read and may be released (sd_pages_trim).  Rows that a
- * position does not see never reach its output, whatever they hold.  Rows n_new[b] .. M-1 of out are left
- * as they were.  fp32 arithmetic; the same call on the same inputs repeats bit for bit, but the split over
+ * position does not see never reach its output, whatever they hold; a row that it sees and whose K holds a NaN
+ * or an infinity may make the output NaN.  Rows n_new[b] .. M-1 of out are left as they were.  fp32 arithmetic; the same call on the same inputs repeats bit for bit, but the split over
  * the keys follows the whole batch, so a sequence's last bits depend on its neighbours.
  * workspace: sd_paged_attn_workspace_bytes, zero-filled by the caller once (counters that every call returns
  * to zero, then scratch); one workspace serves every batch, context and type of the same D or smaller.

@@ -459,8 +459,8 @@ def pages_reserve(pages: KvPages, refs: torch.Tensor, table: torch.Tensor, lens:
                                   _here(table, torch.int32, "table", (B, w), dev), w,
                                   _here(lens, torch.int32, "lens", (B,), dev),
                                   _opt(n_new, torch.int32, "n_new", (B,), dev), B, M,
-
-                                  _here(missing, torch.int32, "missing", (1,), dev), *_space(ws, dev), stream), "sd_pages_reserve")
+                                  _here(missing, torch.int32, "missing", (1,), dev), *_space(ws, dev), stream),
+           "sd_pages_reserve")
 
 
 def pages_copy(pages: KvPages, ws: torch.Tensor):
@@ -515,8 +515,8 @@ def pages_compact(pages: KvPages, refs: torch.Tensor, table: torch.Tensor, remap
     _check(lib().sd_pages_compact(pages._arg(dev), _here(refs, torch.int32, "refs", (pages.n_pages,), dev),
                                   _here(table, torch.int32, "table", (B, w), dev), w, B,
                                   _here(remap, torch.int32, "remap", (pages.n_pages,), dev),
-
-                                  _here(n_live, torch.int32, "n_live", (1,), dev), *_space(ws, dev), stream), "sd_pages_compact")
+                                  _here(n_live, torch.int32, "n_live", (1,), dev), *_space(ws, dev), stream),
+           "sd_pages_compact")
 
 
 def shortlist_build(head_blocks: torch.Tensor, vocab: int, hidden: int):
