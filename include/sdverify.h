@@ -387,9 +387,9 @@ sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, in
  *
  * sd_paged_append: k_new, v_new fp32, row i of sequence b at b * seq_stride + i * row_stride (elements,
  * multiples of 4, 16-byte aligned), its H_kv heads of D contiguous: they may be columns of a fused projection.
- * Rounded to the nearest (even) fp16 / bf16; SD_KV_I8: scale = amax|x| / 127 per row and head, code = x / scale rounded half away
- * from zero, 0 if the row is zero (the arithmetic of sd_rmsnorm_quant_acts per row of D); a row that holds a
- * NaN or an infinity gets that as its scale.  M >= 1 of any size.
+ * Rounded to the nearest (even) fp16 / bf16; SD_KV_I8: scale = amax|x| / 127 per row and head, code = x / scale rounded
+ * half away from zero, 0 if the row is zero (the arithmetic of sd_rmsnorm_quant_acts per row of D); a row that
+ * holds a NaN or an infinity gets that as its scale.  M >= 1 of any size.
  *
  * sd_paged_attn: q, out fp32, row i of sequence b at b * seq_stride + i * row_stride, its H heads of D
  * contiguous (H a multiple of H_kv; head h reads KV head h / (H / H_kv)); 1 <= M <= 16.  parent int32 [B][M]
