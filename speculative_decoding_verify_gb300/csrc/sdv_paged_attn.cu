@@ -169,8 +169,14 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][dt][e] = 0.0f;
         }
-        // 8-bit rows: the outputs' unit, a power of two above every V scale so far (its bits)
+        // 8-bit rows: the unit of a row's outputs, a power of two above every V scale that it has seen so far (its bits).
+        // One for all rows while they have seen the same scales; after a tile that they see parts of one for each
+        // (`apart`, in shared memory): a scale that a row does not see may be of any size, and in a unit above it nothing
+        // would be left of the row's weights.  (A unit per row in every tile: 194 -> 219 us, 16 sequences of 8000 rows of
+        // D = 256, 16 query rows.)
         uint32_t vunit = 0x00800000u;
+        uint32_t *sm_unit = reinterpret_cast<uint32_t *>(sm_m) + warp * RPG;  // (the maxima come there at the piece's end)
+        bool apart = false;
         // keys from full_lo on (or below full_sink) and below p.len are seen by every row
         const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
         bool ok = true;
@@ -251,18 +257,6 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                     if (!seen(jb, nt, 1)) s[nt][3] = -INFINITY;
                 }
             }
-            float vmul0 = 1.0f, vmul1 = 1.0f, shrink = 1.0f;
-            if constexpr (T == SD_KV_I8) {
-                // a power of two above all finite scales so far (positive floats order as their bits)
-                const uint32_t t0 = vs0 > 0.0f && vs0 < INFINITY ? __float_as_uint(vs0) : 0u;
-                const uint32_t t1 = vs1 > 0.0f && vs1 < INFINITY ? __float_as_uint(vs1) : 0u;
-                const uint32_t top = __reduce_max_sync(0xffffffffu, max(t0, t1)), was = vunit;
-                vunit = min(max(vunit, (top & 0x7f800000u) + 0x00800000u), 0x7e800000u);
-                const float down = __uint_as_float(0x7f000000u - vunit);  // its inverse
-                shrink = __uint_as_float(was) * down;
-                vmul0 = vs0 * down;
-                vmul1 = vs1 * down;
-            }
             // weights of the keys, running max and sum
             float pr[NT][4], al[NT][2];
 #pragma unroll
@@ -283,15 +277,51 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                 l[nt][1] = fmaf(l[nt][1], al1, pr[nt][1] + pr[nt][3]);
                 m[nt][0] = n0;
                 m[nt][1] = n1;
-                al[nt][0] = T == SD_KV_I8 ? al0 * shrink : al0;
-                al[nt][1] = T == SD_KV_I8 ? al1 * shrink : al1;
-                if constexpr (T == SD_KV_I8) {
-                    const float w0 = pr[nt][0] * vmul0, w1 = pr[nt][1] * vmul0, w2 = pr[nt][2] * vmul1, w3 = pr[nt][3] * vmul1;
-                    // a key with no weight keeps none, whatever its scale is
-                    pr[nt][0] = whole || pr[nt][0] > 0.0f ? w0 : pr[nt][0];
-                    pr[nt][1] = whole || pr[nt][1] > 0.0f ? w1 : pr[nt][1];
-                    pr[nt][2] = whole || pr[nt][2] > 0.0f ? w2 : pr[nt][2];
-                    pr[nt][3] = whole || pr[nt][3] > 0.0f ? w3 : pr[nt][3];
+                al[nt][0] = al0;
+                al[nt][1] = al1;
+            }
+            if constexpr (T == SD_KV_I8) {
+                const uint32_t t0 = scale_bits(vs0), t1 = scale_bits(vs1);
+                if (whole && !apart) {
+                    const uint32_t was = vunit;
+                    vunit = max(was, unit_above(__reduce_max_sync(0xffffffffu, max(t0, t1))));
+                    const float down = unit_inverse(vunit), shrink = __uint_as_float(was) * down;
+                    const float vmul0 = vs0 * down, vmul1 = vs1 * down;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        al[nt][0] *= shrink;
+                        al[nt][1] *= shrink;
+                        pr[nt][0] *= vmul0;
+                        pr[nt][1] *= vmul0;
+                        pr[nt][2] *= vmul1;
+                        pr[nt][3] *= vmul1;
+                    }
+                } else {
+                    uint32_t hi = 0, lo = 0xffffffffu;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            // the largest scale of a key that the row sees (what it does not see scores -inf)
+                            uint32_t top = max(s[nt][r] == -INFINITY ? 0u : t0, s[nt][2 + r] == -INFINITY ? 0u : t1);
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                            const uint32_t was = apart ? sm_unit[nt * 8 + 2 * c + r] : vunit, now = max(was, unit_above(top));
+                            __syncwarp();
+                            if (g == 0) sm_unit[nt * 8 + 2 * c + r] = now;
+                            if (low[nt][r] != INT32_MAX) {
+                                hi = max(hi, now);
+                                lo = min(lo, now);
+                            }
+                            const float down = unit_inverse(now);
+                            al[nt][r] *= __uint_as_float(was) * down;
+                            // a key with no weight keeps none, whatever its scale is
+                            if (!(pr[nt][r] == 0.0f)) pr[nt][r] *= vs0 * down;
+                            if (!(pr[nt][2 + r] == 0.0f)) pr[nt][2 + r] *= vs1 * down;
+                        }
+                    __syncwarp();
+                    vunit = __reduce_max_sync(0xffffffffu, hi);
+                    apart = __reduce_min_sync(0xffffffffu, lo) != vunit;
                 }
             }
             const uint32_t vst = st + LY::KV;
@@ -418,9 +448,14 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
         // ---- join the warps' states and write the piece: rows that are whole go out, others become partials
         const bool complete = p.t0 == 0 && p.t1 == p.st.T;
         const int pslot = 2 * static_cast<int>(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
-        const float unit = T == SD_KV_BF16 ? 1.0f : T == SD_KV_I8 ? __uint_as_float(vunit) / PA_PS : 1.0f / PA_PS;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            float unit[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                unit[r] = T == SD_KV_BF16 ? 1.0f
+                          : T == SD_KV_I8 ? __uint_as_float(apart ? sm_unit[nt * 8 + 2 * c + r] : vunit) / PA_PS : 1.0f / PA_PS;
+            if constexpr (T == SD_KV_I8) __syncwarp();  // read before the maxima come there
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float x = l[nt][r];
@@ -440,10 +475,10 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                 for (int dx = 0; dx < 4; ++dx) {
                     const int dt = 4 * cc + dx;
                     const int d0 = 16 * dx + (T == SD_KV_I8 ? 2 * g : g), d1 = d0 + (T == SD_KV_I8 ? 1 : 8);
-                    ow[(2 * c) * SD + d0] = o[nt][dt][0] * unit;
-                    ow[(2 * c + 1) * SD + d0] = o[nt][dt][1] * unit;
-                    ow[(2 * c) * SD + d1] = o[nt][dt][2] * unit;
-                    ow[(2 * c + 1) * SD + d1] = o[nt][dt][3] * unit;
+                    ow[(2 * c) * SD + d0] = o[nt][dt][0] * unit[0];
+                    ow[(2 * c + 1) * SD + d0] = o[nt][dt][1] * unit[1];
+                    ow[(2 * c) * SD + d1] = o[nt][dt][2] * unit[0];
+                    ow[(2 * c + 1) * SD + d1] = o[nt][dt][3] * unit[1];
                 }
                 named_bar_sync(1, 32 * PA_CW);
                 if (cc == 0) {

@@ -116,6 +116,14 @@ __device__ __forceinline__ Parts<T> split2(float x0, float x1) {
     return p;
 }
 
+// 8-bit rows: a power of two above a finite scale's magnitude (the least normal number where there is none), at most
+// 2^126 so that its inverse is a normal number too: the unit in which weights times V scales are split
+__device__ __forceinline__ uint32_t unit_above(uint32_t bits) { return min((bits & 0x7f800000u) + 0x00800000u, 0x7e800000u); }
+__device__ __forceinline__ float unit_inverse(uint32_t unit) { return __uint_as_float(0x7f000000u - unit); }
+__device__ __forceinline__ uint32_t scale_bits(float x) {  // (magnitudes order as their bits; 0: counts for nothing)
+    return fabsf(x) < INFINITY ? __float_as_uint(fabsf(x)) : 0u;
+}
+
 // two of a word's four int8 codes (bytes picked by sel, as selector nibbles 0..3) as an exact fp16 pair:
 // the code plus 128 in the mantissa of 1024, minus 1152
 template <int B0, int B1>

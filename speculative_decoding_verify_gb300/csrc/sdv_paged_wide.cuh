@@ -153,7 +153,7 @@ struct WideLayout {
     static constexpr int NR = (NP + CP - 1) / CP;   // parts that a lane holds: passes of the product
     static constexpr int OTILE = PA_KT * 128;       // 64 keys x 64 halves
     static constexpr int OKV = D / 64 * OTILE;      // K (or V) operand of a tile
-    // scales of K [64], of V [64] in the piece's unit so far, its change, the unit
+    // scales of K [64], of V [64] in the tile's unit, that unit
     static constexpr int OSCALES = I8 ? 1024 : 0;
     static constexpr int OSTAGE = 2 * OKV + OSCALES;
     // operand stages (8-bit rows: written by the converting warps)
@@ -393,19 +393,21 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             const uint32_t to = (isv ? W::OKV : 0) + pa_off<SD_KV_F16, D>(row, 0);
             uint32_t rs = 0, rph = 0, os = 0, oph = 0, np = 0;
             int64_t u = sc.u0, i = 0;
-            int b = 0, left = 0;        // tiles of the piece still to come
-            uint32_t unit = 0x00800000;  // the unit of the V scales so far in the piece (a power of two, as bits)
+            int b = 0, left = 0;  // tiles of the piece still to come
+            Piece p = {};
+            // the unit of the tiles of the piece that every row sees, so far: a power of two above their V scales (its bits)
+            uint32_t unit = 0x00800000u;
             for (; left > 0 || u < sc.u1; ++i, --left) {
                 if (left == 0) {  // the next piece: its queries' stages go back once they are read
-                    const Piece p = piece_at<RP>(a, sc, u, b);
+                    p = piece_at<RP>(a, sc, u, b);
                     b = p.b;
                     left = p.t1 - p.t0;
                     u += left;
+                    unit = 0x00800000u;
                     if (!mbar_wait_bounded(q_ready, np++ & 1u, PA_WAIT_NS, abort)) {
                         set_status(a.status, SD_ETIMEOUT);
                         *abort = 1;
                     }
-                    unit = 0x00800000;
                     for (int s = 0; s < W::QS; ++s) {
                         if (lane == 0) mbar_arrive(&raw_empty[rs]);
                         if (++rs == W::NRAW) {
@@ -443,21 +445,17 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     const float k0 = ss[lane], k1 = ss[lane + 32], v0 = ss[PA_KT + lane], v1 = ss[PA_KT + 32 + lane];
                     ds[lane] = k0 + 0.0f * k0;  // an infinite K scale makes a row of NaN
                     ds[lane + 32] = k1 + 0.0f * k1;
-                    // V scales in units of a power of two above all finite ones so far in the piece (positive floats
-                    // order as their bits)
-                    const uint32_t m0 = v0 > 0.0f && v0 < INFINITY ? __float_as_uint(v0) : 0u;
-                    const uint32_t m1 = v1 > 0.0f && v1 < INFINITY ? __float_as_uint(v1) : 0u;
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m0, m1));
-                    const uint32_t was = unit;
-                    unit = min(max(unit, (top & 0x7f800000u) + 0x00800000u), 0x7e800000u);
-                    // 1 / unit (at most 2^126, so that this is a normal number)
-                    const float down = __uint_as_float(0x7f000000u - unit);
+                    // V scales in the tile's unit: of a tile that every row sees a power of two above those of all such tiles
+                    // so far in the piece; of another, whose scales may be of any size where a row does not look, 1
+                    const int t = p.t1 - left, tile0 = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT;
+                    const bool whole = tile0 + PA_KT <= p.len &&
+                                       (a.window == 0 || tile0 >= p.len + p.n - a.window || tile0 + PA_KT <= a.sinks);
+                    const uint32_t above = unit_above(__reduce_max_sync(0xffffffffu, max(scale_bits(v0), scale_bits(v1))));
+                    if (whole) unit = max(unit, above);
+                    const float down = whole ? unit_inverse(unit) : 1.0f;
                     ds[PA_KT + lane] = v0 * down;
                     ds[PA_KT + 32 + lane] = v1 * down;
-                    if (lane == 0) {
-                        ds[2 * PA_KT] = __uint_as_float(was) * down;  // what the outputs so far shrink by
-                        ds[2 * PA_KT + 1] = __uint_as_float(unit);
-                    }
+                    if (lane == 0) ds[2 * PA_KT] = whole ? __uint_as_float(unit) : 1.0f;
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -575,8 +573,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 low = a.window > 0 ? p.len + depth - a.window + 1 : 0;
             }
             const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
-            // al: rescale of the outputs before the product still to be added; unit: theirs (8-bit rows)
-            float m = PA_NEG, l = 0.0f, al = 0.0f, unit = 1.0f;
+            // al: rescale of the outputs before the product still to be added; vunit: their unit (8-bit rows), a power of
+            // two above every V scale that this lane's row has seen so far, as in paged_attn_kernel
+            float m = PA_NEG, l = 0.0f, al = 0.0f;
+            uint32_t vunit = 0x00800000u;
 #pragma unroll
             for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
             // adds this thread's columns of the product of tile number i to the outputs
@@ -623,11 +623,11 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 const bool whole = tile0 + PA_KT <= p.len && (tile0 >= full_lo || tile0 + PA_KT <= full_sink);
                 if (W::I8 || !whole)  // what stands in the stage is read below: its barrier makes it visible here too
                     ok = wait(&op_full[slot], slot_par) && ok;
-                float shrink = 1.0f;
-                if constexpr (W::I8) {
-                    shrink = scales[2 * PA_KT];
-                    unit = scales[2 * PA_KT + 1];
-                }
+                // 8-bit rows: `above` is what the outputs' unit has to reach.  Outputs in a unit 2^k times the tile's take
+                // weights that are smaller by that, in the exponent; the sum of weights gets it back
+                // (k is at most 112 either way, so that no weight that counts leaves the normal numbers)
+                uint32_t above = 0, tile_unit = 0;
+                if constexpr (W::I8) above = tile_unit = __float_as_uint(scales[2 * PA_KT]);
                 float2 s[NC / 2];
                 {
                     uint32_t y[NC];
@@ -650,13 +650,28 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < NC; ++e)
                         if (!((seen >> e) & 1u)) (e & 1 ? s[e / 2].y : s[e / 2].x) = -INFINITY;
+                    if constexpr (W::I8) {  // (the tile's unit is 1)
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int e = 0; e < NC; ++e)
+                            if ((seen >> e) & 1u) top = max(top, scale_bits(scales[PA_KT + k_at + e]));
+                        above = max(unit_above(__float_as_uint(lane_max(__uint_as_float(top)))), tile_unit - (112u << 23));
+                    }
+                }
+                float shrink = 1.0f, k = 0.0f, two_k = 1.0f;
+                if constexpr (W::I8) {
+                    const uint32_t was = vunit;
+                    vunit = min(max(was, above), tile_unit + (112u << 23));
+                    shrink = __uint_as_float(was) * unit_inverse(vunit);
+                    k = static_cast<float>(static_cast<int>(vunit - tile_unit) >> 23);
+                    two_k = __uint_as_float(0x3f800000u + (vunit - tile_unit));
                 }
                 float x2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < NC / 2; ++e) x2[e & 1] = fmaxf(fmaxf(x2[e & 1], s[e].x), s[e].y);
                 const float n = fmaxf(m, lane_max(fmaxf(x2[0], x2[1])) * back);
                 if (!ok) break;
-                const float an = ex2(m - n), off = PW_UP - n;
+                const float an = ex2(m - n), off = PW_UP - k - n;
                 m = n;
                 bool rescaled = false;
                 if constexpr (!W::I8) {
@@ -727,7 +742,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     s[e] = make_float2(ex2(x.x), ex2(x.y));
                     l2 = fadd2_rn(l2, s[e]);
                 }
-                l = fmaf(l, an, l2.x + l2.y);
+                l = fmaf(l, an, W::I8 ? (l2.x + l2.y) * two_k : l2.x + l2.y);
                 if constexpr (W::I8) {
 #pragma unroll
                     for (int e = 0; e < NC / 2; e += 2) {
@@ -799,6 +814,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 for (int g = 0; g < PW_NG; ++g) x += sm_l[g * 128 + j * RP + r];
                 lv = fmaf(x, ex2(sm_m[j * RP + r] - mx), lv);
             }
+            const float unit = W::I8 ? __uint_as_float(vunit) : 1.0f;
             const float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
             // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared

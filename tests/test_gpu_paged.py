@@ -253,6 +253,58 @@ def test_infinite_values_reach_the_rows_that_see_them_alone(sdv, dtype, H):
     assert np.all(np.abs(out - ref) <= tol)
 
 
+@pytest.mark.parametrize("value", [1e4, 1e10, 1e30, 1e38])
+@pytest.mark.parametrize("M,H,D", [(5, 1, 128), (5, 2, 128), (5, 7, 128), (5, 15, 128), (5, 30, 128), (1, 1, 64), (5, 3, 64), (5, 5, 64), (1, 2, 256), (5, 3, 256)])
+def test_large_scales_of_unseen_rows(sdv, value, M, H, D):
+    """int8 rows whose scales are finite and large where a position does not look: unwritten rows and pages, rows behind the
+    window in its first tile (whole tiles come after it), a tree's sibling, a row that the first position alone sees.  The
+    positions that do not see them keep the bound of every other case; those that see one (whose K is as it was) too, but for
+    what the split leaves: weights times scales in two fp16 parts, in units of U 2^-14 where U is at most twice the largest
+    scale that the position sees, are off by half of fp16's least step, 2^-25 of that: 2^-38 of the largest scale seen, times the
+    code, for each row (the softmax sum is at least 1 in the same units)."""
+    rng = np.random.default_rng(D + H)
+    lens, window, sinks, parent = [100, 1000, 70], 40 if M > 1 else 600, 4, [-1, 0, 0, 1, 2][:M]
+    c = Cache(sdv, rng, lens, [M] * 3, M, 1, D, 16, "i8")
+    q = rng.standard_normal((3, M, H, D)).astype(np.float32)
+    for s in (c.ks, c.vs):
+        s[torch.isnan(s)] = value
+    for b, L in enumerate(lens):
+        see = plain.seen_rows(L, M, parent, window, sinks)
+        for j in np.nonzero(~see.all(0))[0].tolist():
+            pg, r = int(c.table[b, j // 16]), j % 16
+            if not see[:, j].any():
+                c.ks[pg, :, r] = c.vs[pg, :, r] = value
+            elif j in (L - window + 1, L + 4):
+                c.vs[pg, :, r] = value
+                c.V[b][:, j] = c.v[pg, :, r].cpu().double().numpy() * float(c.vs[pg, 0, r])
+    out = run_attn(sdv, c, q, lens, [M] * 3, M, [parent] * 3, window, sinks)
+    for b, L in enumerate(lens):
+        see = plain.seen_rows(L, M, parent, window, sinks)
+        ref, tol = plain.attention(q[b], c.K[b], c.V[b], see)
+        j = torch.arange(L + M)
+        pg, r = c.table[b].cpu()[j // 16].long(), j % 16
+        code, scale = c.v.cpu()[pg, 0, r].double().numpy(), c.vs.cpu()[pg, 0, r].double().numpy()
+        for i in range(M):
+            if np.abs(c.V[b][0, see[i]]).max() < 1e37:  # (else the output is past fp32's range)
+                left = 2.0 ** -38 * scale[see[i]].max() * np.abs(code[see[i]]).sum(0)
+                assert np.all(np.abs(out[b, i] - ref[i]) <= tol[i] + left), (b, i)
+
+
+@pytest.mark.parametrize("power", [-100, -60, -20, 20, 60, 100])
+@pytest.mark.parametrize("M,H,D,window", [(3, 1, 128, 0), (3, 4, 128, 0), (5, 10, 128, 300), (5, 30, 64, 300), (5, 2, 64, 70), (3, 4, 256, 300)])
+def test_scales_of_any_size(sdv, power, M, H, D, window):
+    """int8 rows whose V scales are all near a power of two far from 1: the outputs are that much larger or smaller."""
+    rng = np.random.default_rng(D + H)
+    lens = [700, 64, 130]
+    c = Cache(sdv, rng, lens, [M] * 3, M, 1, D, 16, "i8")
+    q = rng.standard_normal((3, M, H, D)).astype(np.float32)
+    c.vs *= 2.0 ** power
+    out = run_attn(sdv, c, q, lens, [M] * 3, M, [binary(M)] * 3, window, 3)
+    for b, L in enumerate(lens):
+        ref, tol = plain.attention(q[b], c.K[b], c.V[b], plain.seen_rows(L, M, binary(M), window, 3))
+        assert np.all(np.abs(out[b] * 2.0 ** -power - ref) <= tol), b
+
+
 def test_strided_queries_and_outputs(sdv):
     """q and out as columns of wider rows, whose other columns stay as they are."""
     rng = np.random.default_rng(15)
