@@ -625,7 +625,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     ok = wait(&op_full[slot], slot_par) && ok;
                 // 8-bit rows: `above` is what the outputs' unit has to reach.  Outputs in a unit 2^k times the tile's take
                 // weights that are smaller by that, in the exponent; the sum of weights gets it back
-                // (k is at most 112 either way, so that no weight that counts leaves the normal numbers)
+                // (k is from -104, where 2^(14 + 104) is left of the largest weights, to 112, where 2^(14 - 112) is: the weights
+                // that count and their sum stay normal numbers)
                 uint32_t above = 0, tile_unit = 0;
                 if constexpr (W::I8) above = tile_unit = __float_as_uint(scales[2 * PA_KT]);
                 float2 s[NC / 2];
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < NC; ++e)
                             if ((seen >> e) & 1u) top = max(top, scale_bits(scales[PA_KT + k_at + e]));
-                        above = max(unit_above(__float_as_uint(lane_max(__uint_as_float(top)))), tile_unit - (112u << 23));
+                        above = max(unit_above(__float_as_uint(lane_max(__uint_as_float(top)))), tile_unit - (104u << 23));
                     }
                 }
                 float shrink = 1.0f, k = 0.0f, two_k = 1.0f;

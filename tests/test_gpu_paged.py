@@ -305,6 +305,23 @@ def test_scales_of_any_size(sdv, power, M, H, D, window):
         assert np.all(np.abs(out[b] * 2.0 ** -power - ref) <= tol), b
 
 
+@pytest.mark.parametrize("M,H,D", [(2, 2, 128), (2, 8, 128), (5, 8, 128), (16, 8, 128), (5, 5, 64), (2, 4, 256)])
+def test_rows_whose_values_are_zero(sdv, M, H, D):
+    """int8 rows with a V scale of 0: all from row 32 on (half a tile and whole ones), all of a sequence, and the new rows alone."""
+    rng = np.random.default_rng(29)
+    lens = [40, 700, 50, 100]
+    c = Cache(sdv, rng, lens, [M] * 4, M, 1, D, 16, "i8")
+    for b, lo in ((0, 32), (1, 32), (2, 0), (3, 100)):
+        j = torch.arange(lo, lens[b] + M)
+        c.vs[c.table[b].cpu()[j // 16].long(), :, j % 16] = 0.0
+        c.V[b][:, lo:] = 0.0
+    q = rng.standard_normal((4, M, H, D)).astype(np.float32)
+    out = run_attn(sdv, c, q, lens, [M] * 4, M, None, 0, 0)
+    for b, L in enumerate(lens):
+        ref, tol = plain.attention(q[b], c.K[b], c.V[b], plain.seen_rows(L, M, None, 0, 0))
+        assert np.all(np.abs(out[b] - ref) <= tol), b
+
+
 def test_strided_queries_and_outputs(sdv):
     """q and out as columns of wider rows, whose other columns stay as they are."""
     rng = np.random.default_rng(15)
