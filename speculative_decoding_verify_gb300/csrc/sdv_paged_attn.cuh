@@ -28,6 +28,9 @@ struct PagedArgs {
     int *status;
 };
 
+// the scales of 8-bit rows where there is no page
+static __device__ __align__(16) float pa_zeros[PA_KT];
+
 template <int T, int D>
 struct PaLayout {
     static constexpr int ELT = T == SD_KV_I8 ? 1 : 2;
@@ -352,8 +355,9 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
             if constexpr (T == SD_KV_I8) {
                 if (lane < 2 * npt) {
                     const int place = lane % npt, kv = lane / npt;
-                    const int64_t page = pg < a.n_pages ? pg : 0;  // a place without rows: any page's scales
-                    const float *src = (kv ? a.v_scale : a.k_scale) + (page * a.H_kv + p.kh) * a.P + key0 % a.P;
+                    const float *src = pg >= a.n_pages ? pa_zeros
+                                                       : (kv ? a.v_scale : a.k_scale) +
+                                                             (static_cast<int64_t>(pg) * a.H_kv + p.kh) * a.P + key0 % a.P;
                     bulk_g2s_l2keep(stp + 2 * LY::KV + kv * PA_KT * 4 + place * rows * 4, src, rows * 4, &full[slot]);
                 }
             }

@@ -393,6 +393,32 @@ def test_bad_entries_are_reported_and_read_as_zeros(sdv):
     assert sdv.device_status() == EDEVICE
 
 
+@pytest.mark.parametrize("H", [2, 8])
+@pytest.mark.parametrize("P", [16, 64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e30])
+def test_missing_pages_of_8_bit_rows_read_as_zeros(sdv, H, P, value):
+    """Entries of visible rows that name no page, in tiles that every position sees and in the last one: zeros, whatever the scales
+    of the pool's first page are."""
+    rng = np.random.default_rng(28)
+    lens, M, D = [700, 130, 40], 2, 128
+    while True:
+        c = Cache(sdv, rng, lens, [M] * 3, M, 1, D, P, "i8")
+        if 0 in c.order[c.used:]:
+            break  # nobody holds the first page
+    c.ks[0] = c.vs[0] = value
+    for b, slot, entry in ((0, 1, -1), (0, 2, c.k.shape[0]), (1, 0, -7), (2, 40 // P, -1)):
+        c.table[b, slot] = entry
+        c.K[b][:, slot * P:(slot + 1) * P] = 0.0
+        c.V[b][:, slot * P:(slot + 1) * P] = 0.0
+    q = rng.standard_normal((3, M, H, D)).astype(np.float32)
+    out = torch.zeros(3, M, H, D, device="cuda")
+    sdv.paged_attn(cuda(q), c.pages, c.table, i32(lens), out, sdv.workspace(sdv.paged_attn_workspace_bytes(3, M, H, 1, D)))
+    assert sdv.device_status() == EDEVICE
+    for b, L in enumerate(lens):
+        ref, tol = plain.attention(q[b], c.K[b], c.V[b], plain.seen_rows(L, M, None, 0, 0))
+        assert np.all(np.abs(host(out[b]) - ref) <= tol), b
+
+
 def test_trimmed_pages_are_not_read(sdv):
     """Pages behind the window are released and their entries cleared: the results stay the same."""
     rng = np.random.default_rng(19)
