@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
     uint32_t *tbase = reinterpret_cast<uint32_t *>(mask_bar + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tbase + 1);
     volatile int *last = abort + 1;
-    uint32_t *badw = tbase + 4;  // [turn][2]: rows of a tile with a NaN or infinity in V
-    int64_t *prefix = reinterpret_cast<int64_t *>(tbase + 8);
+    uint32_t *badw = tbase + 4;  // [3 turns][2]: rows of a tile with a NaN or infinity in V
+    int64_t *prefix = reinterpret_cast<int64_t *>(tbase + 10);
     int2 *ln = reinterpret_cast<int2 *>(prefix + a.B + 1);
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
 
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         mbar_init(q_ready, 4 * PW_NG);
         mbar_init(done, 1);
         *abort = 0;
-        for (int i = 0; i < 4; ++i) badw[i] = 0;
+        for (int i = 0; i < 6; ++i) badw[i] = 0;
         fence_barrier_init();
     }
     pdl_wait();
@@ -691,8 +691,11 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                             for (int w = 0; w < 4; ++w)
                                 if ((q[w] & EX) == EX || ((q[w] >> 16) & EX) == EX) bw[vr >> 5] |= 1u << (vr & 31);
                         }
-                        uint32_t *words = badw + 2 * (nmask & 1u), *other = badw + 2 * ((nmask + 1) & 1u);
-                        ++nmask;
+                        // the words of the next turn are cleared ahead of this one's barrier: they were read before the last
+                        // one, and are written behind this one
+                        uint32_t *words = badw + 2 * nmask;
+                        nmask = nmask == 2 ? 0 : nmask + 1;
+                        if (tid == 0) badw[2 * nmask] = badw[2 * nmask + 1] = 0;
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
                             const uint32_t any = __reduce_or_sync(0xffffffffu, bw[w]);
@@ -701,7 +704,6 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         ok = sync_all() && ok;
                         const uint32_t bad[2] = {*reinterpret_cast<volatile uint32_t *>(&words[0]),
                                                  *reinterpret_cast<volatile uint32_t *>(&words[1])};
-                        if (tid == 0) other[0] = other[1] = 0;  // read by all before the barrier above
                         if (__all_sync(0xffffffffu, ok) && (bad[0] | bad[1])) {
                             if (t > p.t0) ok = add_product(nt - 1) && ok;
                             float acc[W::DO];

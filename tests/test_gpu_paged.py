@@ -322,6 +322,33 @@ def test_rows_whose_values_are_zero(sdv, M, H, D):
         assert np.all(np.abs(out[b] - ref) <= tol), b
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H", [1, 3, 8])
+def test_cut_tiles_in_a_row_that_hold_no_numbers(sdv, dtype, H):
+    """Four tiles one after the other of which each position sees a part, all with rows of NaN where it does not look: behind the
+    first rows and the window, siblings, rows past the end.  The same call many times."""
+    rng = np.random.default_rng(30)
+    L, M, window, sinks, parent = 1000, 16, 70, 40, binary(16)
+    c = Cache(sdv, rng, [L] * 3, [M] * 3, M, 1, 128, 16, dtype)
+    see = plain.seen_rows(L, M, parent, window, sinks)
+    for b in range(3):
+        j = torch.tensor(np.nonzero(~see.any(0))[0])
+        c.k[c.table[b].cpu()[j // 16].long(), :, j % 16] = float("nan")
+        c.v[c.table[b].cpu()[j // 16].long(), :, j % 16] = float("nan")
+        c.v[int(c.table[b, (L + M - 1) // 16]), :, (L + M - 1) % 16, 3] = float("inf")  # the last row: a sibling of the others
+    q = cuda(rng.standard_normal((3, M, H, 128)).astype(np.float32))
+    ws = sdv.workspace(sdv.paged_attn_workspace_bytes(3, M, H, 1, 128))
+    outs = torch.zeros(100, 3, M, H, 128, device="cuda")
+    lens, par = i32([L] * 3), i32([parent] * 3)
+    for o in outs:
+        sdv.paged_attn(q, c.pages, c.table, lens, o, ws, parent=par, window=window, sinks=sinks)
+    status_ok()
+    assert torch.equal(outs.nan_to_num(7.0), outs[:1].nan_to_num(7.0).expand_as(outs))
+    for b in range(3):
+        ref, tol = plain.attention(host(q[b]), c.K[b], c.V[b], see)
+        assert np.all(np.abs(host(outs[0, b]) - ref)[:-1] <= tol[:-1]), b
+
+
 def test_strided_queries_and_outputs(sdv):
     """q and out as columns of wider rows, whose other columns stay as they are."""
     rng = np.random.default_rng(15)
