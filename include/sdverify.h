@@ -399,7 +399,11 @@ sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, in
  * greater than i's minus window, or less than sinks (StreamingLLM-style first tokens that stay visible); pages
  * wholly behind the window and past the sinks are not read and may be released (sd_pages_trim).  Rows that a
  * position does not see never reach its output, whatever they hold; a row that it sees and whose K holds a NaN
- * or an infinity may make the output NaN.  Rows n_new[b] .. M-1 of out are left as they were.  fp32 arithmetic;
+ * or an infinity may make the output NaN.  An infinity in V of a row that it sees makes that column of its output
+ * infinite or, where the row is weighed in parts (a 64-row tile of committed rows that all new rows see), NaN;
+ * never a number (unless the row's weight is below fp32's range), and no other column.  SD_KV_I8: a row whose
+ * scale is infinite counts as NaN.
+ * Rows n_new[b] .. M-1 of out are left as they were.  fp32 arithmetic;
  * the same call on the same inputs repeats bit for bit, but the split over the keys follows the whole batch, so a
  * sequence's last bits depend on its neighbours.
  * workspace: sd_paged_attn_workspace_bytes, zero-filled by the caller once (counters that every call returns

@@ -349,6 +349,37 @@ def test_cut_tiles_in_a_row_that_hold_no_numbers(sdv, dtype, H):
         assert np.all(np.abs(host(outs[0, b]) - ref)[:-1] <= tol[:-1]), b
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H,D", [(1, 64), (1, 128), (3, 128), (10, 64), (10, 128), (25, 128), (1, 256), (3, 256)])
+@pytest.mark.parametrize("L,window", [(300, 0), (300, 150), (9000, 0)])
+def test_infinite_values_of_committed_rows(sdv, dtype, H, D, L, window):
+    """V holds infinities and NaN in rows of tiles that every position sees, and in cut ones: the columns that the formula makes
+    infinite or NaN are no numbers (an infinity has the formula's sign), and the others are exact."""
+    rng = np.random.default_rng(31)
+    M, sinks = 4, 3
+    c = Cache(sdv, rng, [L], [M], M, 1, D, 16, dtype)
+    q = (rng.standard_normal((1, M, H, D)) * 0.3).astype(np.float32)  # (no weight below fp32's range)
+    see = plain.seen_rows(L, M, None, window, sinks)
+    V, want = c.V[0].copy(), np.zeros((M, D))
+    first = max(0, L - window + 1 if window else 0)
+    places = [(first + 70, 5, np.inf), (first + 75, 6, -np.inf), (first + 20, 7, np.inf), (first + 90, 7, -np.inf), (first + 100, 8, np.nan),
+              (L + 1, 9, np.inf), (first + 80, 9, np.inf), (L + 2, 10, -np.inf), (first + 71, 10, np.inf), (first + 60, D - 1, np.inf), (L, 63, -np.inf)]
+    if window:
+        places += [(first, 11, np.inf), (first, 12, np.inf), (first + 90, 12, np.inf), (first - 30, 13, np.inf), (1, 14, -np.inf)]
+    for j, d, x in places:
+        c.v[int(c.table[0, j // 16]), 0, j % 16, d] = float(x)
+        V[0, j, d] = 0.0
+        with np.errstate(invalid="ignore"):
+            want[see[:, j], d] += x
+    out = run_attn(sdv, c, q, [L], [M], M, None, window, sinks)[0]
+    ref, tol = plain.attention(q[0], c.K[0], V, see)
+    for i in range(M):
+        fine = want[i] == 0
+        assert np.all(np.abs(out[i][:, fine] - ref[i][:, fine]) <= tol[i][:, fine])
+        got = out[i][:, ~fine]
+        assert np.all(np.isnan(got) | (got == want[i][~fine])), i
+
+
 def test_strided_queries_and_outputs(sdv):
     """q and out as columns of wider rows, whose other columns stay as they are."""
     rng = np.random.default_rng(15)
