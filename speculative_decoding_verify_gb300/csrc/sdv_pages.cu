@@ -73,18 +73,14 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PageView pv, void *k,
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if constexpr (T == SD_KV_I8) {
-                float a = 0.0f;
-                bool nan = false;
+                // the largest magnitude by its bits, where an infinity is above every number and a NaN above that
+                uint32_t a = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    a = fmaxf(a, fabsf(x[e][j]));
-                    nan |= x[e][j] != x[e][j];
-                }
-                if (nan) a = INFINITY;  // a row with a NaN or an infinity is not a number as a whole
+                for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(fabsf(x[e][j])));
                 const unsigned mask = LR == 32 ? 0xffffffffu : ((1u << (LR & 31)) - 1u) << ((threadIdx.x & 31) / LR * LR);
 #pragma unroll
-                for (int o = LR / 2; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
-                const float d = a < INFINITY ? __fdiv_rn(a, 127.0f) : __int_as_float(0x7fc00000);
+                for (int o = LR / 2; o >= 1; o >>= 1) a = max(a, __shfl_xor_sync(mask, a, o));
+                const float d = __fdiv_rn(__uint_as_float(a), 127.0f);
                 *reinterpret_cast<uint2 *>(static_cast<int8_t *>(e ? v : k) + dst) = codes8(x[e], d);
                 if (l == 0) (e ? v_scale : k_scale)[(static_cast<int64_t>(page) * pv.H_kv + h) * pv.P + r] = d;
             } else {

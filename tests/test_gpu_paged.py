@@ -578,6 +578,24 @@ def test_append_of_numbers_that_are_none(sdv):
     assert np.isnan(K[0, :3]).all() and np.isnan(V[0, :3]).all() and np.isfinite(K[0, 3]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_of_appended_rows_that_hold_no_numbers(sdv, D):
+    """A row with a NaN has that as its scale, one with an infinity alone that, and their codes are 0."""
+    rng = np.random.default_rng(34)
+    c = Cache(sdv, rng, [0], [5], 5, 2, D, 16, "i8")
+    x = rng.standard_normal((1, 5, 2, D)).astype(np.float32)
+    x[0, 0, 0, 3], x[0, 1, 0, D - 1], x[0, 2, 0, 0], x[0, 3, 0, 1], x[0, 3, 0, D - 2] = np.nan, np.inf, -np.inf, np.inf, np.nan
+    sdv.paged_append(cuda(x), cuda(-x), c.pages, c.table, i32([0]))
+    status_ok()
+    pg = int(c.table[0, 0])
+    for codes, scales, sign in ((c.k, c.ks, 1), (c.v, c.vs, -1)):
+        assert np.array_equal(host(scales[pg, 0, :4]), np.array([np.nan, np.inf, np.inf, np.nan], np.float32), equal_nan=True)
+        assert not codes[pg, 0, :4].any()
+        for i, h in ((4, 0), (0, 1), (1, 1), (2, 1), (3, 1), (4, 1)):
+            code, scale = plain.codes(sign * x[0, i, h])
+            assert np.array_equal(host(codes[pg, h, i]), code) and float(scales[pg, h, i]) == scale
+
+
 def test_append_reports_missing_pages_and_skips_them(sdv):
     rng = np.random.default_rng(32)
     c = Cache(sdv, rng, [10, 10], [4, 4], 4, 1, 64, 8, "f16")
