@@ -380,8 +380,9 @@ sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, in
  * is 0.  All of these are device arrays, so that a whole cycle can be captured in a CUDA graph.
  * B <= 1024 (else SD_EUNSUPPORTED); width * page_rows < 2^31 - 128.
  *
- * Every kernel checks lens, n_new and table entries against these bounds before it uses them: what fails is
- * skipped (for the attention a missing page reads as zeros) and records SD_EDEVICE in the status word.
+ * Every kernel checks lens (0 .. width * page_rows), n_new and table entries against these bounds before it uses
+ * them: what fails is skipped (for the attention a missing page reads as zeros) and records SD_EDEVICE in the
+ * status word.
  * The calls of one workspace are ordered on one stream; a graph that may run beside another call needs its own.
  * After an SD_ETIMEOUT a workspace must be zero-filled again.
  *

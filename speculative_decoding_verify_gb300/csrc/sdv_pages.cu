@@ -467,6 +467,11 @@ __global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *
 // tables and counts
 // ---------------------------------------------------------------------------------------------------
 
+// whether a sequence's length is one that its table can hold
+__device__ __forceinline__ bool len_ok(int len, int32_t width, int32_t P) {
+    return len >= 0 && len <= static_cast<int64_t>(width) * P;
+}
+
 // one holder fewer; a count that was not there is put back and recorded
 __device__ __forceinline__ void drop_page(int32_t *refs, int32_t n_pages, int pg, int *status) {
     if (pg < 0) return;
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(int32_t *refs, int32_t 
     pdl_wait();
     pdl_launch_dependents();
     const int i = static_cast<int>(blockIdx.x), s = src[i], d = dst[i];
-    bool bad = s < 0 || s >= B || d < 0 || d >= B;
+    bool bad = s < 0 || s >= B || d < 0 || d >= B || !len_ok(lens[s], width, P);
     for (int j = threadIdx.x; j < n; j += blockDim.x) bad |= src[j] == d || (j != i && dst[j] == d);
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) set_status(status, SD_EDEVICE);
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(256) pages_free_kernel(int32_t *refs, int32_t 
     pdl_wait();
     pdl_launch_dependents();
     const int b = seqs[blockIdx.x], rows = keep ? keep[blockIdx.x] : 0;
-    if (b < 0 || b >= B || rows < 0) {
+    if (b < 0 || b >= B || rows < 0 || !len_ok(lens[b], width, P)) {
         if (threadIdx.x == 0) set_status(status, SD_EDEVICE);
         return;
     }
@@ -533,7 +538,11 @@ __global__ void __launch_bounds__(256) pages_trim_kernel(int32_t *refs, int32_t 
     pdl_wait();
     pdl_launch_dependents();
     const int b = static_cast<int>(blockIdx.x);
-    const int lo = max(lens[b], 0) - window + 1;  // the first row that a later row sees
+    if (!len_ok(lens[b], width, P)) {
+        if (threadIdx.x == 0) set_status(status, SD_EDEVICE);
+        return;
+    }
+    const int lo = lens[b] - window + 1;  // the first row that a later row sees
     int32_t *t = table + static_cast<int64_t>(b) * width;
     const int end = lo > 0 ? min(lo / P, width) : 0;
     for (int64_t x = (static_cast<int64_t>(sinks) + P - 1) / P + threadIdx.x; x < end; x += blockDim.x) {

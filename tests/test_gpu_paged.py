@@ -803,6 +803,28 @@ def test_fork_refuses_what_overlaps(sdv):
             assert (m.refs.tolist(), m.table.tolist()) == before
 
 
+@pytest.mark.parametrize("length", [-1, -2 ** 31, 33, 2 ** 31 - 1])
+def test_page_calls_skip_a_length_that_no_table_holds(sdv, length):
+    m = Both(sdv, 20, 4, 4, 8)
+    m.reserve([20, 10, 8, 0], 20)
+    m.grow([20, 10, 8, 0])
+    m.fork([(0, 3)])
+    status_ok()
+    m.same()
+    m.lens[1] = length
+    before = m.refs.tolist(), m.table.tolist(), m.lens.tolist()
+    sdv.pages_fork(m.refs, m.table, m.lens, 8, i32([1]), i32([2]))
+    assert sdv.device_status() == EDEVICE and (m.refs.tolist(), m.table.tolist(), m.lens.tolist()) == before
+    sdv.pages_free(m.refs, m.table, m.lens, 8, i32([1]), i32([4]))
+    assert sdv.device_status() == EDEVICE and (m.refs.tolist(), m.table.tolist(), m.lens.tolist()) == before
+    m.pool.lens[1] = 0  # the plain pool skips it, and trims the others
+    m.pool.trim(3, 0)
+    m.pool.lens[1] = length
+    sdv.pages_trim(m.refs, m.table, m.lens, 8, 3)
+    assert sdv.device_status() == EDEVICE
+    m.same()
+
+
 def test_a_count_that_is_not_there_is_reported(sdv):
     m = Both(sdv, 10, 2, 4, 8)
     m.table[0, 0] = 3  # a page that nobody counted, and one past the pool
