@@ -413,7 +413,7 @@ sd_status sd_kv_commit(void *k_cache, void *v_cache, int32_t H_kv, int32_t D, in
  * sd_paged_commit: as sd_kv_commit for every sequence with count[b] >= 1: row lens[b] + path[b][t] moves to row
  * lens[b] + t for t < count[b] (path int32 [B][M], increasing, path[b][0] >= 0, M <= 16; NULL: chains, nothing
  * moves and M is unbounded), then lens[b] += count[b].  count[b] = 0 leaves the sequence alone; count[b] > M, a
- * bad path or a missing page records SD_EDEVICE and leaves the sequence alone.
+ * bad path or a page missing where a row moves from or to records SD_EDEVICE and leaves the sequence alone.
  */
 typedef enum { SD_KV_F16 = 0, SD_KV_BF16 = 1, SD_KV_I8 = 2 } sd_kv_type;
 
