@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                     inv = lv == 0.0f ? 0.0f : 1.0f / lv;
                     if (!complete && tg < rows && (tid & 15) == 0) a.part_ml[pslot * RPG + tr] = make_float2(mx, lv);
                 }
-                if (tg < rows) {
+                if (tg < rows && SD_INB(p.b < a.B && tg / a.g < a.M && p.kh < a.H_kv && (complete || (pslot + 1) * RPG <= a.part_rows),
+                                        a.status, 117)) {  // site 117: rows of a piece
                     const int i = tg / a.g, h = p.kh * a.g + tg % a.g, d = 4 * (tid & 15);
                     float *op = complete ? a.out + p.b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D
                                          : a.part_o + (static_cast<int64_t>(pslot) * RPG + tr) * D;
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
             const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
             __threadfence();
             named_bar_sync(1, 32 * PA_CW);
-            if (tid == 0) {
+            if (tid == 0 && SD_INB(c0 >= 0 && c0 <= c1 && c1 < static_cast<int>(gridDim.x), a.status, 118)) {  // site 118: counter
                 const int was = atomicAdd(&a.counters[c0], 1);
                 *last = was == c1 - c0;
                 if (was == c1 - c0) a.counters[c0] = 0;
@@ -691,6 +692,7 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     a.nst = p.nst;
     a.qscale = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     a.counters = reinterpret_cast<int32_t *>(ws);
+    a.part_rows = static_cast<int32_t>((need - off_o) / (static_cast<size_t>(D) * 4));
     a.part_ml = reinterpret_cast<float2 *>(ws + off_ml);
     a.part_o = reinterpret_cast<float *>(ws + off_o);
     a.status = status;

@@ -25,6 +25,7 @@ struct PagedArgs {
     float *part_o;        // [2 * grid][8 NT][D]
     float2 *part_ml;      // [2 * grid][8 NT]
     int32_t *counters;    // [grid], zero between calls
+    int32_t part_rows;    // rows of D floats that part_o holds (part_ml: as many pairs)
     int *status;
 };
 
@@ -308,6 +309,9 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
             __syncwarp();
             for (int i = lane; i < n; i += 32) {
                 const int tg = p.rg * RPG + r0 + i;
+                if (!SD_INB(p.b >= 0 && p.b < a.B && tg >= 0 && tg / a.g < a.M && p.kh >= 0 && p.kh < a.H_kv && slot < nst,
+                            a.status, 113))  // site 113: query row
+                    continue;
                 bulk_g2s_l2keep(ring + static_cast<size_t>(slot) * LY::STAGE + i * (D * 4 + 16),
                                 a.q + p.b * a.q_sb + (tg / a.g) * a.q_sm +
                                     static_cast<int64_t>(p.kh * a.g + tg % a.g) * D,
@@ -326,6 +330,7 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
             if (t >= p.t1) return a.n_pages;
             const int key = (t < p.st.n_sink ? t : t - p.st.n_sink + p.st.lo_tile) * PA_KT + (e & (npt - 1)) * rows;
             if (key >= total) return a.n_pages;
+            if (!SD_INB(key >= 0 && key / a.P < a.width && b < a.B, a.status, 114)) return a.n_pages;  // site 114: table entry
             const int pg = tab[key / a.P];
             if (pg >= 0 && pg < a.n_pages) return pg;
             if (key + rows > lo || key < sink) set_status(a.status, SD_EDEVICE);  // a row of it is visible
@@ -350,6 +355,10 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
                 // page place i % npt: this lane's own (npt divides 32)
                 const int place = i % npt, half = (i / npt) % LY::NB, kv = i / npt / LY::NB;
                 const uint32_t dst = smem_u32(stp) + kv * LY::KV + half * LY::TILE + place * rows * LY::ROWB;
+                if (!SD_INB(slot < nst && key0 >= 0 && key0 % a.P + rows <= a.P && p.kh >= 0 && p.kh < a.H_kv && pg >= 0 &&
+                                pg <= a.n_pages && kv < 2 && (place + 1) * rows <= PA_KT,
+                            a.status, 115))  // site 115: a page's rows (and its scales)
+                    continue;
                 tma_4d(dst, kv ? tmv : tmk, half * (LY::ROWB / LY::ELT), key0 % a.P, p.kh, pg, &full[slot]);
             }
             if constexpr (T == SD_KV_I8) {
@@ -403,6 +412,10 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
     for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int k = 0; k < NV; ++k) v[i][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RPG <= a.part_rows && rows <= RPG &&
+                    (p.rg * RPG + rows - 1) / a.g < a.M,
+                a.status, 116))  // site 116: partials of a join, its output rows
+        c1 = c0 - 1;
     for (int x0 = c0; x0 <= c1; x0 += JC) {
         const int nx = min(JC, c1 - x0 + 1);
         named_bar_sync(bar, NTHR);

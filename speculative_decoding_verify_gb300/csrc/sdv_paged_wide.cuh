@@ -845,7 +845,9 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     named_bar_sync(5, PW_SOFT);
 #pragma unroll
                     for (int k = 0; k < NK; ++k)
-                        if (to[k]) {
+                        if (to[k] && SD_INB(p.b < a.B && (p.rg * RP + wr + RW * k) / a.g < a.M && p.kh < a.H_kv &&
+                                                (final || (pslot + 1) * RP <= a.part_rows),
+                                            a.status, 117)) {  // site 117: rows of a piece
                             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                             for (int j = 0; j < C; ++j) {
@@ -873,7 +875,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
                 __threadfence();
                 named_bar_sync(5, PW_SOFT);
-                if (tid == 0) {
+                if (tid == 0 && SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RP <= a.part_rows,
+                                       a.status, 118)) {  // site 118: counter, partials
                     const int was = atomicAdd(&a.counters[c0], 1);
                     *last = was == c1 - c0;
                     if (was == c1 - c0) a.counters[c0] = 0;

@@ -60,6 +60,9 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PageView pv, void *k,
             continue;
         }
         const int r = pos - slot * pv.P;
+        if (!SD_INB(b < B && i < M && h >= 0 && h < pv.H_kv && slot >= 0 && slot < width && r >= 0 && r < pv.P && 8 * l + 8 <= D,
+                    status, 109))  // site 109: appended row
+            continue;
         const int64_t src = b * sb + i * sm + static_cast<int64_t>(h) * D + 8 * l;
         const int64_t dst = page * pv.ps + h * pv.hs + r * pv.rs + 8 * l;
         float x[2][8];
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(256) paged_commit_kernel(PageView pv, uint8_t 
         bad = f < t || f >= M || (t > 0 && f <= path[static_cast<int64_t>(b) * M + t - 1]);
         if (!bad) {
             const int sp = len + f, dp = len + t;
-            bad = sp / pv.P >= width;
+            bad = sp / pv.P >= width || !SD_INB(f < M && t < 16 && t <= f && dp / pv.P < width, status, 110);  // site 110: moved row
             if (!bad) {
                 from[t] = f;
                 spage[t] = table[static_cast<int64_t>(b) * width + sp / pv.P];
@@ -340,6 +343,10 @@ __global__ void __launch_bounds__(PL_T) pages_reserve_kernel(int32_t *refs, int3
         at += sum;
         if (d) {
             const int b = it / per, slot = lens[b] / P + it % per;
+            if (!SD_INB(b < B && slot >= 0 && slot < width && o >= 0 && o < found && o < n_pages && ws.freel[o] >= 0 &&
+                            ws.freel[o] < n_pages,
+                        status, 111))  // site 111: a plan's pages
+                continue;
             int32_t *e = table + static_cast<int64_t>(b) * width + slot;
             const int to = ws.freel[o];
             if (d == 2) {
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(PL_T) pages_reserve_kernel(int32_t *refs, int3
 }
 
 __global__ void __launch_bounds__(PL_T) pages_compact_kernel(int32_t *refs, int32_t n_pages, int32_t P, int32_t *remap,
-                                                             int32_t *n_live, PagesWs ws) {
+                                                             int32_t *n_live, PagesWs ws, int *status) {
     __shared__ int sh[33];
     pdl_wait();
     pdl_launch_dependents();
@@ -383,6 +390,7 @@ __global__ void __launch_bounds__(PL_T) pages_compact_kernel(int32_t *refs, int3
     __syncthreads();
     for (int i = tid; i < holes; i += PL_T) {  // as many movers as holes: live pages = live
         const int from = ws.movers[i], to = ws.freel[i];
+        if (!SD_INB(i < n_pages && from >= live && from < n_pages && to >= 0 && to < live, status, 111)) continue;
         ws.list[i] = make_int4(from, to, P, 0);
         remap[from] = to;
         refs[to] = refs[from];
@@ -445,6 +453,7 @@ __global__ void __launch_bounds__(CP_T) pages_copy_kernel(PageView pv, uint8_t *
                 const int div = together ? pv.H_kv : e.z;
                 const int hi = z / div, low = z - hi * div;
                 const int h = together ? low : hi, row = together ? hi : low;
+                if (!SD_INB(h >= 0 && h < pv.H_kv && row >= 0 && row < e.z && c < cols, status, 112)) continue;  // site 112: copy
                 off[u] = (h * pv.hs + row * pv.rs) * eb + 16 * c;
                 r[u] = __ldcs(reinterpret_cast<const uint4 *>(src + off[u]));
             }
@@ -728,10 +737,12 @@ sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
     if (!table_ok(refs, pages->n_pages, table, width, B, pages->page_rows) || !remap || !n_live || !workspace)
         return SD_EINVAL;
     if (!aligned(workspace, 256) || ws_bytes < sd_pages_workspace_bytes(pages->n_pages, B, width)) return SD_EINVAL;
+    int *status = status_ptr();
+    if (!status) return SD_ECUDA;
     const PagesWs ws = pages_ws(workspace, pages->n_pages, static_cast<int64_t>(B) * width);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch(pages_compact_kernel, dim3(1), dim3(PL_T), 0, s, refs,
-                           pages->n_pages, pages->page_rows, remap, n_live, ws);
+                           pages->n_pages, pages->page_rows, remap, n_live, ws, status);
     if (e == cudaSuccess) e = copy_launch(pages, ws, table, static_cast<int64_t>(B) * width, remap, s);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }

@@ -112,3 +112,14 @@ def test_python_refuses_tensors_that_are_not_on_the_gpu(sdv):
         sdv.KvPages(torch.zeros(4, 2, 16, 64, dtype=torch.float16), torch.zeros(4, 2, 16, 64, dtype=torch.float16))
     with pytest.raises(ValueError):
         sdv.KvPages(torch.zeros(4, 2, 16, 64), torch.zeros(4, 2, 16, 64))
+
+
+@pytest.mark.parametrize("name", ["sdv_pages.cu", "sdv_paged_attn.cuh", "sdv_paged_attn.cu", "sdv_paged_wide.cuh"])
+def test_the_bounds_checked_build_checks_the_paged_kernels(sdv, name):
+    """Each file with paged kernels has its sites (109 to 118), which the bounds-checked suite runs."""
+    import os
+    import re
+    from speculative_decoding_verify_gb300 import build as b
+    text = open(os.path.join(b.CSRC, name)).read()
+    sites = {int(s) for s in re.findall(r"status,\s*(1\d\d)\)", text)}
+    assert sites and sites <= set(range(109, 119))
