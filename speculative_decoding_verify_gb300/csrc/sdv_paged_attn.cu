@@ -540,8 +540,8 @@ static size_t pa_stage(int type, int D) {
     return 2 * static_cast<size_t>(PA_KT) * D * kv_type_bytes(type) + (type == SD_KV_I8 ? 1024 : 0);
 }
 
-// Rows beside each other in one 8- or 16-row group; a persistent grid of two CTAs per SM, or one where
-// three stages of the ring do not fit twice.
+// Rows beside each other in one 8- or 16-row group; a persistent grid of two CTAs per SM, or one where their registers
+// or two stages of the ring each do not fit.
 static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
     const int sms = num_sms();
     if (sms < 1) return false;

@@ -22,8 +22,10 @@ struct PagedArgs {
     int32_t B, M, H, H_kv, g, P, n_pages, width, window, sinks;
     int32_t nst;          // ring stages
     float qscale;         // log2(e) / sqrt(D)
-    float *part_o;        // [2 * grid][8 NT][D]
-    float2 *part_ml;      // [2 * grid][8 NT]
+    // partials, two per CTA (of a run cut at the start of its share, and at the end), RPG query rows each (8 NT, or the
+    // many-row kernel's 128 / C, whose 128-row partials keep the order of lanes, [D / 4][128] columns of four)
+    float *part_o;        // [2 * grid][RPG][D]
+    float2 *part_ml;      // [2 * grid][RPG]: maximum and sum
     int32_t *counters;    // [grid], zero between calls
     int32_t part_rows;    // rows of D floats that part_o holds (part_ml: as many pairs)
     int *status;

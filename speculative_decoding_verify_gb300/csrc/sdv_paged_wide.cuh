@@ -8,10 +8,10 @@
 //   S = Q K^T: tcgen05.mma kind::f16, M = 128, N = 64, Q in tensor memory as A (written once per piece, in 16-bit parts
 //     that add up to the fp32 value: two fp16, or three bf16), K as B from shared memory as the tensor copy left it
 //     (K-major, 128-byte swizzle);
-//   softmax: four threads per lane, a quarter of the tile's keys each, their maximum shared through shared memory; the
+//   softmax: two threads per lane, half of the lane's keys each, their maximum shared through shared memory; the
 //     weights go back to tensor memory over the scores, in parts;
 //   O_t = P V: the weights as A, V as B (MN-major, the same swizzle), from zero for each tile; the softmax threads add
-//     a quarter of the columns each to their fp32 outputs in registers with the rescale of the running maximum (a
+//     half of the columns each to their fp32 outputs in registers with the rescale of the running maximum (a
 //     tensor-core accumulator kept over the tiles would truncate at every step, and rescaling it would cost the same
 //     loads and more stores).
 // One thread issues all MMAs: scores two tiles ahead of the weights, so the tensor cores work while the softmax
@@ -59,12 +59,6 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
                     "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
 
 // N consecutive columns of this warp's lanes; the values are there after tc_wait_ld on the same registers
-__device__ __forceinline__ void tc_ld(uint32_t (&r)[8], uint32_t addr) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : PW_R8(r, 0) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : PW_W8(r, 0)::"memory");
-}
 __device__ __forceinline__ void tc_ld(uint32_t (&r)[16], uint32_t addr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : PW_R8(r, 0), PW_R8(r, 8)
@@ -83,11 +77,6 @@ __device__ __forceinline__ void tc_ld(uint32_t (&r)[32], uint32_t addr) {
 }
 __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : PW_W8(r, 0), PW_W8(r, 8), PW_W8(r, 16), PW_W8(r, 24)::"memory");
-}
-__device__ __forceinline__ void tc_st(const uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
 }
 __device__ __forceinline__ void tc_st(const uint32_t (&r)[8], uint32_t addr) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), PW_I8(r, 0) : "memory");
