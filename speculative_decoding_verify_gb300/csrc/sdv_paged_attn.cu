@@ -568,13 +568,12 @@ static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
 
 // Query rows of a KV head above which the tensor-memory kernel runs: its cost per 64-key tile hardly depends on D or on
 // the rows (up to 32 of them), the other's grows with both.  16 sequences of 16000 rows, 8 KV heads, 16 query rows,
-// this kernel / the tensor-memory one: D = 64 fp16 100 / 156 us; D = 128 fp16 186 / 188, bf16 246 / 232, int8
-// 223 / 217.  The other's shared memory holds the schedule of PA_WIDE_B sequences.
+// this kernel / the tensor-memory one: D = 64 fp16 100 / 158 us, bf16 125 / 205, int8 117 / 207; D = 128 fp16 184 / 197,
+// bf16 246 / 229, int8 221 / 219.  The other's shared memory holds the schedule of PA_WIDE_B sequences; more are two
+// launches (this kernel in its place took 2731 us for 513 sequences of 500 rows, 128 query rows; 512 take 510).
 constexpr int PA_WIDE_ROWS = 8, PA_WIDE_ROWS_64 = 16, PA_WIDE_B = 512;
 
-static bool pa_wide(int rows, int D, int B) {
-    return rows > (D == 64 ? PA_WIDE_ROWS_64 : PA_WIDE_ROWS) && D <= 128 && B <= PA_WIDE_B;
-}
+static bool pa_wide(int rows, int D) { return rows > (D == 64 ? PA_WIDE_ROWS_64 : PA_WIDE_ROWS) && D <= 128; }
 
 // workspace: counters of the largest grid, then the partials: two per CTA, of 16 rows on two CTAs per SM or
 // of 128 rows on one
@@ -698,11 +697,23 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int rows = M * a.g;
-    if (pa_wide(rows, D, B)) {
+    if (pa_wide(rows, D)) {
         const auto run = pages->type == SD_KV_F16 ? paged_wide_f16
                          : pages->type == SD_KV_BF16 ? paged_wide_bf16
                                                       : paged_wide_i8;
-        return run(a, tmk, tmv, D, rows, num_sms(), s) == cudaSuccess ? SD_OK : SD_ECUDA;
+        const int part = B <= PA_WIDE_B ? B : (B + 1) / 2;
+        static_assert(PG_MAX_B <= 2 * PA_WIDE_B, "two launches hold the most sequences");
+        for (int b0 = 0; b0 < B; b0 += part) {
+            a.B = B - b0 < part ? B - b0 : part;
+            a.table = table + static_cast<int64_t>(b0) * width;
+            a.lens = lens + b0;
+            a.n_new = n_new ? n_new + b0 : nullptr;
+            a.parent = parent ? parent + static_cast<int64_t>(b0) * M : nullptr;
+            a.q = q + b0 * q_seq_stride;
+            a.out = out + b0 * out_seq_stride;
+            if (run(a, tmk, tmv, D, rows, num_sms(), s) != cudaSuccess) return SD_ECUDA;
+        }
+        return SD_OK;
     }
     const cudaError_t e = pages->type == SD_KV_F16    ? pa_launch_d<SD_KV_F16>(D, p, a, tmk, tmv, s)
                           : pages->type == SD_KV_BF16 ? pa_launch_d<SD_KV_BF16>(D, p, a, tmk, tmv, s)

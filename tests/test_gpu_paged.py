@@ -198,6 +198,28 @@ def test_many_rows_of_many_sequences(sdv, dtype, D):
             assert np.all(out[b, news[b]:] == 123.0)
 
 
+@pytest.mark.parametrize("dtype,D,B", [("f16", 128, 1024), ("bf16", 64, 1023), ("i8", 128, 700)])
+def test_trees_of_more_sequences_than_one_launch_takes(sdv, dtype, D, B):
+    """Every argument of the second launch: its tables, lengths, numbers of new rows, trees, strided queries and outputs."""
+    rng = np.random.default_rng(B)
+    M, H = 7, 3
+    lens, news = rng.integers(0, 90, B).tolist(), rng.integers(0, M + 1, B).tolist()
+    c = Cache(sdv, rng, lens, news, M, 1, D, 8, dtype)
+    parents = [[-1] + [int(rng.integers(0, i)) for i in range(1, M)] for _ in range(B)]
+    wide = torch.randn(B, M + 1, 2 * H, D, device="cuda")
+    q, outs = wide[:, :M, H:], torch.full((B, M + 2, H, D), 123.0, device="cuda")
+    ws = sdv.workspace(sdv.paged_attn_workspace_bytes(B, M, H, 1, D))
+    sdv.paged_attn(q, c.pages, c.table, i32(lens), outs[:, 1:M + 1], ws, n_new=i32(news), parent=i32(parents), window=30, sinks=2)
+    status_ok()
+    assert torch.all(outs[:, 0] == 123.0) and torch.all(outs[:, M + 1] == 123.0)
+    out = host(outs)[:, 1:M + 1]
+    for b in rng.permutation(B)[:80].tolist() + [0, (B + 1) // 2 - 1, (B + 1) // 2, B - 1]:
+        if news[b]:
+            ref, tol = plain.attention(host(q[b, :news[b]]), c.K[b], c.V[b], plain.seen_rows(lens[b], news[b], parents[b], 30, 2))
+            assert np.all(np.abs(out[b, :news[b]] - ref) <= tol), b
+        assert np.all(out[b, news[b]:] == 123.0)
+
+
 def test_many_sequences(sdv):
     """As many as a call takes."""
     rng = np.random.default_rng(3)
