@@ -312,6 +312,41 @@ def test_large_scales_of_unseen_rows(sdv, value, M, H, D):
                 assert np.all(np.abs(out[b, i] - ref[i]) <= tol[i] + left), (b, i)
 
 
+@pytest.mark.parametrize("value", [1e4, 1e10, 1e30])
+@pytest.mark.parametrize("M,H,D", [(5, 1, 128), (5, 2, 128), (5, 7, 128), (5, 15, 128), (16, 16, 128), (5, 3, 64), (5, 5, 64), (16, 8, 64), (2, 2, 256), (5, 3, 256)])
+def test_large_scales_ahead_of_whole_tiles(sdv, value, M, H, D):
+    """The first rows of the window and of the sinks, which the first positions alone see, have large V scales, and tiles that every
+    position sees come after them, some with zeros for scales: each position keeps its bound (that of the split, where it sees
+    one: 2^-38 of the largest scale seen, as above)."""
+    rng = np.random.default_rng(D + H)
+    lens, window, sinks, parent = [1000, 700, 650, 610], 600, 5, binary(M)
+    c = Cache(sdv, rng, lens, [M] * 4, M, 1, D, 16, "i8")
+    q = rng.standard_normal((4, M, H, D)).astype(np.float32)
+
+    def at(b, j):
+        return int(c.table[b, j // 16]), j % 16
+
+    for b, L in enumerate(lens):
+        see = plain.seen_rows(L, M, parent, window, sinks)
+        for j in range(L - window - 30, L - window + 2):
+            if j >= sinks and not see[:, j].all():
+                c.vs[at(b, j)[0], :, at(b, j)[1]] = value
+        if b == 1:  # whole tiles of zeros behind the window's first
+            for j in range(L - window + 60, L - window + 200):
+                c.vs[at(b, j)[0], :, at(b, j)[1]] = 0.0
+        c.V[b] = c.rows(b, 0, L + M)[1]
+    out = run_attn(sdv, c, q, lens, [M] * 4, M, [parent] * 4, window, sinks)
+    for b, L in enumerate(lens):
+        see = plain.seen_rows(L, M, parent, window, sinks)
+        ref, tol = plain.attention(q[b], c.K[b], c.V[b], see)
+        j = torch.arange(L + M)
+        pg, r = c.table[b].cpu()[j // 16].long(), j % 16
+        code, scale = c.v.cpu()[pg, 0, r].double().numpy(), c.vs.cpu()[pg, 0, r].double().numpy()
+        for i in range(M):
+            left = 2.0 ** -38 * scale[see[i]].max() * np.abs(code[see[i]]).sum(0)
+            assert np.all(np.abs(out[b, i] - ref[i]) <= tol[i] + left), (b, i)
+
+
 @pytest.mark.parametrize("power", [-100, -60, -20, 20, 60, 100])
 @pytest.mark.parametrize("M,H,D,window", [(3, 1, 128, 0), (3, 4, 128, 0), (5, 10, 128, 300), (5, 30, 64, 300), (5, 2, 64, 70), (3, 4, 256, 300)])
 def test_scales_of_any_size(sdv, power, M, H, D, window):
