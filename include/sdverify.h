@@ -479,6 +479,101 @@ sd_status sd_pages_trim(int32_t *refs, int32_t n_pages, int32_t *table, int32_t 
 sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *table, int32_t width, int32_t B,
                            int32_t *remap, int32_t *n_live, void *workspace, size_t ws_bytes, sd_stream_t stream);
 
+/*
+ * Rotary positions (no counterpart on the pages, whose engines turn queries and keys inside their attention phases).
+ * A pair (a, b) of frequency f radians per position, at position p, becomes
+ *   (a cos(pf) - b sin(pf), a sin(pf) + b cos(pf)) * scale.
+ * The first rot elements of a head are pairs (i, i + rot/2), or with `interleaved` (2i, 2i + 1), the i-th of
+ * frequency inv_freq[i]; the others stay as they are.
+ *
+ * sd_rope: turns (device, 16-byte aligned) uint64 [rot/2], 2^64 times the turns (f / 2 pi) per position, modulo 2^64:
+ * the angle's fraction of a turn is position * turns modulo 2^64, which stays exact at any position (negative ones turn
+ * backwards).  rot is a multiple of 8, at most D.  scale multiplies what is turned (1 without a long-context rule).
+ * sd_rope_freqs (HOST): inv_freq [rot/2] and scale for frequencies base^(-2i/rot), rot even, and how they are
+ * stretched by `factor` >= 1 for contexts beyond the trained one:
+ *   SD_ROPE_PLAIN   not at all (factor and what follows are ignored);
+ *   SD_ROPE_LINEAR  f / factor;
+ *   SD_ROPE_NTK     the base times factor^(rot / (rot - 2)), so that the lowest frequency is divided by factor;
+ *   SD_ROPE_BANDS   with t = (original * f / 2 pi - low) / (high - low) held in [0, 1]: (1 - t) f / factor + t f (pairs that
+ *                   turn more than `high` times within `original` positions stay, less than `low` times are divided);
+ *   SD_ROPE_YARN    with d(r) = rot ln(original / (2 pi r)) / (2 ln base), first = max(0, floor d(high)), last =
+ *                   min(rot - 1, ceil d(low)) and t = (i - first) / (last - first) held in [0, 1]: t f / factor +
+ *                   (1 - t) f; scale = 0.1 ln(factor) + 1 (YaRN; usual: low 1, high 32).
+ *   BANDS and YARN need original > 0 and 0 < low < high.
+ * sd_rope_turns (HOST): the table of n frequencies (finite, at most 2^20 in magnitude), to be copied to the device.
+ *
+ * sd_rope_rows: x, out fp32, row i at i * stride (elements, multiples of 4, 16-byte aligned), its `heads` heads of D
+ * contiguous (D a multiple of 8, at most 1024); row i is turned to position pos[i] (device).  out may be x.
+ *
+ * sd_paged_append_rope: sd_paged_append of keys turned to their positions and of values as they are, and the turned
+ * queries beside it (8-bit rows are quantised after the turn).  Row i of sequence b stands at position lens[b] + depth(i),
+ * the depth of node i in the sequence's tree (parent int32 [B][M] as for sd_paged_attn, M <= 16; NULL: chains, depth i, any
+ * M); it is written to row lens[b] + i, so that a commit that moves an accepted path leaves every row at the place of its
+ * position.  q, q_out fp32 [row i of sequence b at b * seq_stride + i * row_stride], H heads of D contiguous, H any number
+ * (0: no queries); q_out may be q.  q, k_new and v_new may be columns of one fused projection.  Rows from n_new[b] on of
+ * q_out are left as they were.  Where a row's page is missing its query is turned all the same.
+ */
+typedef enum { SD_ROPE_PLAIN = 0, SD_ROPE_LINEAR = 1, SD_ROPE_NTK = 2, SD_ROPE_BANDS = 3, SD_ROPE_YARN = 4 } sd_rope_scaling;
+typedef struct {
+    const uint64_t *turns;
+    int32_t rot;
+    int32_t interleaved; /* 0 or 1 */
+    float scale;
+} sd_rope;
+sd_status sd_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double original, double low, double high,
+                        double *inv_freq, float *scale);
+sd_status sd_rope_turns(const double *inv_freq, int32_t n, uint64_t *turns);
+sd_status sd_rope_rows(const sd_rope *rope, const float *x, int64_t x_stride, const int32_t *pos, int32_t N, int32_t heads,
+                       int32_t D, float *out, int64_t out_stride, sd_stream_t stream);
+sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
+                               const int32_t *n_new, int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride,
+                               int64_t q_row_stride, const float *k_new, const float *v_new, int64_t seq_stride,
+                               int64_t row_stride, const int32_t *parent, const sd_rope *rope, float *q_out,
+                               int64_t out_seq_stride, int64_t out_row_stride, sd_stream_t stream);
+
+/*
+ * sd_paged_attn (full context) for a batch in which sequences share a long prefix, as sd_pages_fork leaves them: the
+ * pages that all of a group's sequences hold are read once for the group and not once per sequence.
+ * group int32 [B] (device): sequences with the same number, 0 .. B-1, are looked at together; -1: alone.  It is a hint
+ * about where to look: what is shared is what the tables say (of the group's sequences that have new rows: the leading slots
+ * that name the same page in all of them, and whose rows are committed in all, in whole 64-row tiles), so that a group
+ * that shares nothing, or a sequence that left its group, costs time and changes no result.  A group
+ * number outside [-1, B) counts as -1 and records SD_EDEVICE.
+ * Everything else is as in sd_paged_attn; the same call on the same inputs repeats bit for bit, and a sequence's
+ * last bits depend on its neighbours.
+ * workspace: sd_paged_attn_shared_workspace_bytes, zero-filled by the caller once; it serves every call of the same or a
+ * smaller B, M, H and D.
+ */
+size_t sd_paged_attn_shared_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D);
+sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
+                               const int32_t *n_new, const int32_t *group, int32_t B, int32_t M, int32_t H, const float *q,
+                               int64_t q_seq_stride, int64_t q_row_stride, const int32_t *parent, float *out,
+                               int64_t out_seq_stride, int64_t out_row_stride, void *workspace, size_t ws_bytes,
+                               sd_stream_t stream);
+
+/*
+ * One token for each of N rows of logits from given random numbers (the sampling knobs of "Inside OpenJet Engine", API
+ * section, for rows that are drawn without a draft: a drafter's own tokens, the first token of a conversation, a batch of
+ * samples; any top_k, and min-p).  logits fp32, row n at n * ld (any ld >= vocab).  Settings are one per row (device), each
+ * pointer NULL for "off" in all rows:
+ *   temperature fp32 >= 0 (NULL: 1; 0: the likeliest token), top_k int32 >= 0 (0 or >= vocab: off), top_p fp32 in (0, 1],
+ *   min_p fp32 in [0, 1]; u fp32 in [0, 1) (required).
+ * With m the row's largest logit, w_c = exp((l_c - m) / T), tokens in the order of larger l first (lower index
+ * among equals; -0 equals 0):
+ *   the first top_k of them; of these the shortest prefix whose sum of w reaches top_p times their sum; of these the ones
+ *   with l_c - m >= T ln(min_p);
+ * the token is the first in index order whose running sum of kept w exceeds u times their sum.  Weights are rounded to whole
+ * numbers of 2^-44 and added exactly, so a row's token is the same in any batch.  Minus infinity is a forbidden token and
+ * is never drawn, NaN counts as that; if plus infinity occurs, those tokens share everything.
+ * out_tokens int32 [N]; out_prob fp32 [N] (or NULL): the drawn token's probability among the kept; out_probs fp32 (or
+ * NULL), row n at n * ld_probs: all of them, 0 where not kept (q_probs of sd_accept_sample for a drafter that samples).
+ * A row with a setting out of range or without any token gets token -1, probability 0, and records SD_EDEVICE.
+ * 1 <= vocab <= 360448 (else SD_EUNSUPPORTED).  No workspace.
+ */
+sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, const float *u, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, int32_t *out_tokens, float *out_prob,
+                    float *out_probs, int64_t ld_probs, sd_stream_t stream);
+
 sd_status sd_shortlist_build(const void *head_blocks, int64_t vocab, int64_t hidden, void *copy_blocks, float *bound,
                              float *wnorm, sd_stream_t stream);
 size_t sd_shortlist_workspace_bytes(int64_t vocab, int64_t hidden);

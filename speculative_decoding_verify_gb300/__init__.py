@@ -75,6 +75,10 @@ class SdKvPages(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
 
 
+class SdRope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class SdError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {STATUS.get(code, code)} ({code})")
@@ -90,7 +94,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, I32, I64, U32, U64, F, SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int32, ctypes.c_int64,
                                            ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float, ctypes.c_size_t)
-        PG = ctypes.POINTER(SdKvPages)
+        PG, RP, F64 = ctypes.POINTER(SdKvPages), ctypes.POINTER(SdRope), ctypes.c_double
         sig = {
             "sd_status_string": ([I], ctypes.c_char_p),
             "sd_abi_version": ([], I),
@@ -122,6 +126,13 @@ def lib():
             "sd_pages_free": ([P, I32, P, I32, P, I32, I32, P, P, I32, P], I),
             "sd_pages_trim": ([P, I32, P, I32, P, I32, I32, I32, I32, P], I),
             "sd_pages_compact": ([PG, P, P, I32, I32, P, P, P, SZ, P], I),
+            "sd_rope_freqs": ([I32, F64, I32, F64, F64, F64, F64, P, ctypes.POINTER(F)], I),
+            "sd_rope_turns": ([P, I32, P], I),
+            "sd_rope_rows": ([RP, P, I64, P, I32, I32, I32, P, I64, P], I),
+            "sd_paged_append_rope": ([PG, P, I32, P, P, I32, I32, I32, P, I64, I64, P, P, I64, I64, P, RP, P, I64, I64, P], I),
+            "sd_paged_attn_shared_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+            "sd_paged_attn_shared": ([PG, P, I32, P, P, P, I32, I32, I32, P, I64, I64, P, P, I64, I64, P, SZ, P], I),
+            "sd_sample": ([P, I64, I64, I32, P, P, P, P, P, P, P, P, I64, P], I),
             "sd_shortlist_build": ([P, I64, I64, P, P, P, P], I),
             "sd_shortlist_workspace_bytes": ([I64, I64], SZ),
             "sd_head_shortlist": ([P, P, P, P, I64, I64, P, P, I32, P, P, P, SZ, P], I),
@@ -517,6 +528,132 @@ def pages_compact(pages: KvPages, refs: torch.Tensor, table: torch.Tensor, remap
                                   _here(remap, torch.int32, "remap", (pages.n_pages,), dev),
                                   _here(n_live, torch.int32, "n_live", (1,), dev), *_space(ws, dev), stream),
            "sd_pages_compact")
+
+
+# ---------------------------------------------------------------------------
+# many samples of one conversation: rotary positions, attention over a shared prefix, drawn tokens
+# ---------------------------------------------------------------------------
+
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+class Rope:
+    """Rotary positions of the first `rot` elements of a head: pairs (i, i + rot/2), or interleaved (2i, 2i + 1), of
+    frequencies base^(-2i/rot) stretched by `scaling` (plain, linear, ntk, bands, yarn; sd_rope_freqs), or of the given
+    inv_freq [rot/2] (then `scale` multiplies what is turned).  Holds its table on the current CUDA device."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "plain", factor: float = 1.0,
+                 original: float = 0.0, low: float = 0.0, high: float = 0.0, inv_freq=None, scale: float = 1.0):
+        if rot < 8 or rot % 8:
+            raise SdError(2, f"rope of {rot} elements: a multiple of 8 is wanted")
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling: expected one of {', '.join(ROPE_SCALINGS)}, got {scaling!r}")
+        n = rot // 2
+        freqs, turns, s = (ctypes.c_double * n)(), (ctypes.c_uint64 * n)(), ctypes.c_float(scale)
+        if inv_freq is None:
+            _check(lib().sd_rope_freqs(rot, base, ROPE_SCALINGS[scaling], factor, original, low, high, freqs, ctypes.byref(s)),
+                   "sd_rope_freqs")
+        else:
+            given = [float(f) for f in inv_freq]
+            if len(given) != n:
+                raise ValueError(f"inv_freq: expected {n} frequencies, got {len(given)}")
+            freqs[:] = given
+        _check(lib().sd_rope_turns(freqs, n, turns), "sd_rope_turns")
+        self.rot, self.interleaved, self.scale, self.inv_freq = rot, bool(interleaved), float(s.value), list(freqs)
+        self.turns = torch.frombuffer(bytearray(turns), dtype=torch.int64).cuda()
+        self.device_index = self.turns.get_device()
+        self.desc = SdRope(self.turns.data_ptr(), rot, int(self.interleaved), self.scale)
+        self._ref = ctypes.byref(self.desc)
+
+    def _arg(self, dev):
+        if self.device_index != dev:
+            raise ValueError("the rope's table is not on the current CUDA device")
+        return self._ref
+
+
+def rope_rows(x: torch.Tensor, pos: torch.Tensor, rope: Rope, out: torch.Tensor):
+    """x fp32 [N][heads][D] (heads contiguous) turned to positions pos int32 [N] -> out (which may be x)."""
+    dev, stream = _where()
+    N, heads, D = x.shape if x.dim() == 3 else (0, 0, 0)
+    shape = (1, N, heads, D)
+    xp, _, xs = _rows_of(x.unsqueeze(0), "x", shape, dev)
+    op, _, os_ = _rows_of(out.unsqueeze(0), "out", shape, dev)
+    _check(lib().sd_rope_rows(rope._arg(dev), xp, xs, _here(pos, torch.int32, "pos", (N,), dev), N, heads, D, op, os_, stream),
+           "sd_rope_rows")
+
+
+def paged_append_rope(q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor, pages: KvPages, table: torch.Tensor,
+                      lens: torch.Tensor, rope: Rope, q_out: torch.Tensor | None, n_new: torch.Tensor | None = None,
+                      parent: torch.Tensor | None = None):
+    """paged_append of keys turned to their positions, and q fp32 [B][M][H][D] turned into q_out (which may be q; None: no
+    queries); parent int32 [B][M]: a node stands at its depth (None: chains)."""
+    dev, stream = _where()
+    B, M = k_new.shape[:2]
+    w = table.shape[-1]
+    shape = (B, M, pages.H_kv, pages.D)
+    kp, sb, sm = _rows_of(k_new, "k_new", shape, dev)
+    vp, vb, vm = _rows_of(v_new, "v_new", shape, dev)
+    if (vb, vm) != (sb, sm):
+        raise ValueError("k_new and v_new: expected the same strides")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: expected both or neither")
+    H = 0 if q is None else q.shape[2]
+    qp, qb, qm, op, ob, om = None, 0, 0, None, 0, 0
+    if q is not None:
+        qp, qb, qm = _rows_of(q, "q", (B, M, H, pages.D), dev)
+        op, ob, om = _rows_of(q_out, "q_out", (B, M, H, pages.D), dev)
+    _check(lib().sd_paged_append_rope(pages._arg(dev), _here(table, torch.int32, "table", (B, w), dev), w,
+                                      _here(lens, torch.int32, "lens", (B,), dev),
+                                      _opt(n_new, torch.int32, "n_new", (B,), dev), B, M, H, qp, qb, qm, kp, vp, sb, sm,
+                                      _opt(parent, torch.int32, "parent", (B, M), dev), rope._arg(dev), op, ob, om, stream),
+           "sd_paged_append_rope")
+
+
+def paged_attn_shared_workspace_bytes(B: int, M: int, H: int, H_kv: int, D: int) -> int:
+    return int(lib().sd_paged_attn_shared_workspace_bytes(B, M, H, H_kv, D))
+
+
+def paged_attn_shared(q: torch.Tensor, pages: KvPages, table: torch.Tensor, lens: torch.Tensor, group: torch.Tensor,
+                      out: torch.Tensor, ws: torch.Tensor, n_new: torch.Tensor | None = None,
+                      parent: torch.Tensor | None = None):
+    """paged_attn in which the pages that all sequences of a group hold are read once for the group: group int32 [B],
+    equal numbers (0 .. B-1) for sequences that may share (-1: alone)."""
+    dev, stream = _where()
+    B, M, H = q.shape[:3]
+    w = table.shape[-1]
+    shape = (B, M, H, pages.D)
+    qp, qb, qm = _rows_of(q, "q", shape, dev)
+    op, ob, om = _rows_of(out, "out", shape, dev)
+    _check(lib().sd_paged_attn_shared(pages._arg(dev), _here(table, torch.int32, "table", (B, w), dev), w,
+                                      _here(lens, torch.int32, "lens", (B,), dev),
+                                      _opt(n_new, torch.int32, "n_new", (B,), dev),
+                                      _here(group, torch.int32, "group", (B,), dev), B, M, H, qp, qb, qm,
+                                      _opt(parent, torch.int32, "parent", (B, M), dev), op, ob, om,
+                                      *_space(ws, dev), stream), "sd_paged_attn_shared")
+
+
+def _wide_rows(t, name, N, V, dev):
+    """(address, row stride) of fp32 rows [N][V] whose elements are contiguous."""
+    if t.dtype is not torch.float32 or t.shape != (N, V) or (V > 1 and t.stride(1) != 1) or t.get_device() != dev:
+        raise ValueError(f"{name}: expected fp32 {(N, V)} with contiguous rows on the current CUDA device, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0) if N > 1 else V
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, tokens: torch.Tensor, temperature: torch.Tensor | None = None,
+           top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+           prob: torch.Tensor | None = None, probs: torch.Tensor | None = None):
+    """One token per row of logits fp32 [N][V] from random numbers u fp32 [N] -> tokens int32 [N]; temperature, top_p and
+    min_p fp32 [N], top_k int32 [N] (None: off); prob fp32 [N]: the token's probability; probs fp32 [N][V]: all of them."""
+    dev, stream = _where()
+    N, V = logits.shape
+    lp, ld = _wide_rows(logits, "logits", N, V, dev)
+    pp, ldp = _wide_rows(probs, "probs", N, V, dev) if probs is not None else (None, 0)
+    f32, i32 = torch.float32, torch.int32
+    _check(lib().sd_sample(lp, ld, V, N, _here(u, f32, "u", (N,), dev), _opt(temperature, f32, "temperature", (N,), dev),
+                           _opt(top_k, i32, "top_k", (N,), dev), _opt(top_p, f32, "top_p", (N,), dev),
+                           _opt(min_p, f32, "min_p", (N,), dev), _here(tokens, i32, "tokens", (N,), dev),
+                           _opt(prob, f32, "prob", (N,), dev), pp, ldp, stream), "sd_sample")
 
 
 def shortlist_build(head_blocks: torch.Tensor, vocab: int, hidden: int):

@@ -27,7 +27,7 @@ namespace sdv {
 // (Five warps a CTA put three of ten on one scheduler: above 168 registers one CTA runs per SM.  At D = 64 the 16-row
 // form is held to that, 162 -> 125 us for 16 sequences of 16000 bf16 rows; at D = 128 it would spill 60 registers and
 // take 20 % longer.)
-template <int T, int D, int NT>
+template <int T, int D, int NT, int MODE>
 __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
     paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
     pdl_wait();
     pdl_launch_dependents();
     Sched sc;
-    if (!make_sched<RPG, PA_THREADS>(a, prefix, ln, sc)) return;
+    if (!make_sched<RPG, PA_THREADS, MODE>(a, prefix, ln, sc)) return;
 
     if (warp == PA_CW) {
-        produce_tiles<T, D, RPG, 0, 1>(a, sc, &tmk, &tmv, ring, a.nst, full, empty, abort);
+        produce_tiles<T, D, RPG, 0, 1, MODE>(a, sc, &tmk, &tmv, ring, a.nst, full, empty, abort);
         return;
     }
 
@@ -78,9 +78,9 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
     int b = 0, slot = 0;
     uint32_t ph = 0;
     while (u < sc.u1) {
-        const Piece p = piece_at<RPG>(a, sc, u, b);
+        const Piece p = piece_at<RPG, MODE>(a, sc, u, b);
         b = p.b;
-        const int rows = p.n * a.g, total = p.len + p.n;
+        const int rows = p.n * a.g, total = MODE == PA_PREFIX ? p.len : p.len + p.n;
         // B fragments of query row g of each 8-row tile, in parts; fp16 parts of a row scaled by 2^(11-e) for
         // max |q| in [2^(e-1), 2^e), so that neither part is subnormal
         uint32_t qf[QSM ? 1 : NT][QSM ? 1 : KS][2][NP];
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
             const int tg = p.rg * RPG + nt * 8 + g;
             const bool real = tg < rows;
             const int i = real ? tg / a.g : 0, h = p.kh * a.g + (real ? tg % a.g : 0);
-            const float *qp = a.q + p.b * a.q_sb + i * a.q_sm + static_cast<int64_t>(h) * D;
+            const float *qp = q_row<MODE>(a, p.b, i) + static_cast<int64_t>(h) * D;
             float qv[KS][4];
             float mx = 0.0f;
 #pragma unroll
@@ -147,9 +147,12 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                 vis[nt][r] = 0;
                 low[nt][r] = INT32_MAX;
                 if (tr < rows) {
-                    int depth;
-                    vis[nt][r] = new_rows_seen(a, p.b, tr / a.g, p.len, depth);
-                    low[nt][r] = a.window > 0 ? p.len + depth - a.window + 1 : 0;
+                    low[nt][r] = 0;
+                    if constexpr (MODE != PA_PREFIX) {  // (a prefix is whole tiles of rows that all of its rows see)
+                        int depth;
+                        vis[nt][r] = new_rows_seen(a, p.b, tr / a.g, p.len, depth);
+                        if (a.window > 0) low[nt][r] = p.len + depth - a.window + 1;
+                    }
                 }
             }
         }
@@ -491,11 +494,14 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                     }
                     inv = lv == 0.0f ? 0.0f : 1.0f / lv;
                     if (!complete && tg < rows && (tid & 15) == 0) a.part_ml[pslot * RPG + tr] = make_float2(mx, lv);
+                    if constexpr (MODE != PA_ALL)
+                        if (complete && tg < rows && (tid & 15) == 0)
+                            put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
                 }
-                if (tg < rows && SD_INB(p.b < a.B && tg / a.g < a.M && p.kh < a.H_kv && (complete || (pslot + 1) * RPG <= a.part_rows),
+                if (tg < rows && SD_INB(p.b < a.B && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh < a.H_kv && (complete || (pslot + 1) * RPG <= a.part_rows),
                                         a.status, 117)) {  // site 117: rows of a piece
                     const int i = tg / a.g, h = p.kh * a.g + tg % a.g, d = 4 * (tid & 15);
-                    float *op = complete ? a.out + p.b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D
+                    float *op = complete ? out_row<MODE>(a, p.b, i, h, D)
                                          : a.part_o + (static_cast<int64_t>(pslot) * RPG + tr) * D;
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
             }
             named_bar_sync(1, 32 * PA_CW);
             if (*last) {
-                join_partials<RPG, D, 32 * PA_CW>(a, p, c0, c1, tid, sm_o, 1);
+                join_partials<RPG, D, 32 * PA_CW, MODE>(a, p, c0, c1, tid, sm_o, 1);
             }
         }
         u += p.t1 - p.t0;
@@ -542,10 +548,9 @@ static size_t pa_stage(int type, int D) {
 
 // Rows beside each other in one 8- or 16-row group; a persistent grid of two CTAs per SM, or one where their registers
 // or two stages of the ring each do not fit.
-static bool pa_plan(int type, int B, int M, int H, int H_kv, int D, PaPlan &p) {
+static bool pa_plan(int type, int B, int rows, int D, PaPlan &p) {
     const int sms = num_sms();
     if (sms < 1) return false;
-    const int rows = M * (H / H_kv);
     p.nt = rows > 8 ? 2 : 1;
     const int parts = type == SD_KV_BF16 ? 3 : 2;
     const size_t fixed = 1024 + static_cast<size_t>(PA_CW) * 8 * 68 * 4 + 2 * static_cast<size_t>(PA_CW) * 8 * p.nt * 4 +
@@ -577,7 +582,7 @@ static bool pa_wide(int rows, int D) { return rows > (D == 64 ? PA_WIDE_ROWS_64 
 
 // workspace: counters of the largest grid, then the partials: two per CTA, of 16 rows on two CTAs per SM or
 // of 128 rows on one
-static size_t pa_workspace(int D, size_t *off_ml, size_t *off_o) {
+size_t pa_workspace(int D, size_t *off_ml, size_t *off_o) {
     const size_t sms = num_sms() > 0 ? num_sms() : 0;
     if (!sms) return 0;
     const size_t rows = sms * 2 * 128;  // 4 x 16 rows per SM take less
@@ -608,39 +613,34 @@ static bool pages_map(CUtensorMap *tm, const sd_kv_pages *p, void *base) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int T, int D, int NT>
+template <int T, int D, int NT, int MODE>
 static cudaError_t pa_launch(const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
                              cudaStream_t s) {
-    const cudaError_t e = allow_max_dynamic_smem(paged_attn_kernel<T, D, NT>);
+    const cudaError_t e = allow_max_dynamic_smem(paged_attn_kernel<T, D, NT, MODE>);
     if (e != cudaSuccess) return e;
-    return launch(paged_attn_kernel<T, D, NT>, dim3(p.grid), dim3(PA_THREADS), p.smem, s, a, tmk, tmv);
+    return launch(paged_attn_kernel<T, D, NT, MODE>, dim3(p.grid), dim3(PA_THREADS), p.smem, s, a, tmk, tmv);
 }
-template <int T>
+template <int T, int MODE>
 static cudaError_t pa_launch_d(int D, const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk,
                                const CUtensorMap &tmv, cudaStream_t s) {
-    if (D == 256) return p.nt == 1 ? pa_launch<T, 256, 1>(p, a, tmk, tmv, s) : pa_launch<T, 256, 2>(p, a, tmk, tmv, s);
-    if (D == 128) return p.nt == 1 ? pa_launch<T, 128, 1>(p, a, tmk, tmv, s) : pa_launch<T, 128, 2>(p, a, tmk, tmv, s);
-    return p.nt == 1 ? pa_launch<T, 64, 1>(p, a, tmk, tmv, s) : pa_launch<T, 64, 2>(p, a, tmk, tmv, s);
+    if (D == 256)
+        return p.nt == 1 ? pa_launch<T, 256, 1, MODE>(p, a, tmk, tmv, s) : pa_launch<T, 256, 2, MODE>(p, a, tmk, tmv, s);
+    if (D == 128)
+        return p.nt == 1 ? pa_launch<T, 128, 1, MODE>(p, a, tmk, tmv, s) : pa_launch<T, 128, 2, MODE>(p, a, tmk, tmv, s);
+    return p.nt == 1 ? pa_launch<T, 64, 1, MODE>(p, a, tmk, tmv, s) : pa_launch<T, 64, 2, MODE>(p, a, tmk, tmv, s);
+}
+template <int MODE>
+static cudaError_t pa_launch_t(int type, int D, const PaPlan &p, const PagedArgs &a, const CUtensorMap &tmk,
+                               const CUtensorMap &tmv, cudaStream_t s) {
+    return type == SD_KV_F16    ? pa_launch_d<SD_KV_F16, MODE>(D, p, a, tmk, tmv, s)
+           : type == SD_KV_BF16 ? pa_launch_d<SD_KV_BF16, MODE>(D, p, a, tmk, tmv, s)
+                                : pa_launch_d<SD_KV_I8, MODE>(D, p, a, tmk, tmv, s);
 }
 
-}  // namespace sdv
-
-using namespace sdv;
-
-extern "C" {
-
-size_t sd_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D) {
-    if (B < 1 || B > PG_MAX_B || M < 1 || M > 16 || H_kv < 1 || H < H_kv || H % H_kv || (D != 64 && D != 128 && D != 256))
-        return 0;
-    return pa_workspace(D, nullptr, nullptr);
-}
-
-sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
-                        const int32_t *n_new, int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride,
-                        int64_t q_row_stride, const int32_t *parent, int32_t window, int32_t sinks, float *out,
-                        int64_t out_seq_stride, int64_t out_row_stride, void *workspace, size_t ws_bytes,
-                        sd_stream_t stream) {
-    SD_NVTX("sd_paged_attn");
+sd_status pa_call(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
+                  int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride, int64_t q_row_stride,
+                  const int32_t *parent, int32_t window, int32_t sinks, float *out, int64_t out_seq_stride,
+                  int64_t out_row_stride, void *workspace, size_t ws_bytes, PaCall &c) {
     const sd_status st = pages_check(pages);
     if (st != SD_OK) return st;
     const int H_kv = pages->H_kv, D = pages->D;
@@ -655,17 +655,18 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return SD_EINVAL;
     // positions are 32-bit
     if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 2 * PA_KT) return SD_EUNSUPPORTED;
-    PaPlan p;
     size_t off_ml, off_o;
     const size_t need = pa_workspace(D, &off_ml, &off_o);
-    if (!need || !pa_plan(pages->type, B, M, H, H_kv, D, p)) return SD_ECUDA;
+    if (!need) return SD_ECUDA;
     if (ws_bytes < need) return SD_EINVAL;
-    CUtensorMap tmk, tmv;
-    if (!pages_map(&tmk, pages, pages->k) || !pages_map(&tmv, pages, pages->v)) return SD_ECUDA;
+    if (!pages_map(&c.tmk, pages, pages->k) || !pages_map(&c.tmv, pages, pages->v)) return SD_ECUDA;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    PagedArgs a = {};
+    c.type = pages->type;
+    c.D = D;
+    PagedArgs &a = c.a;
+    a = {};
     a.q = q;
     a.out = out;
     a.table = table;
@@ -688,37 +689,91 @@ sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t 
     a.width = width;
     a.window = window;
     a.sinks = sinks;
-    a.nst = p.nst;
     a.qscale = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     a.counters = reinterpret_cast<int32_t *>(ws);
     a.part_rows = static_cast<int32_t>((need - off_o) / (static_cast<size_t>(D) * 4));
     a.part_ml = reinterpret_cast<float2 *>(ws + off_ml);
     a.part_o = reinterpret_cast<float *>(ws + off_o);
     a.status = status;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int rows = M * a.g;
-    if (pa_wide(rows, D)) {
-        const auto run = pages->type == SD_KV_F16 ? paged_wide_f16
-                         : pages->type == SD_KV_BF16 ? paged_wide_bf16
-                                                      : paged_wide_i8;
+    return SD_OK;
+}
+
+// the many-row kernel in any mode
+static cudaError_t pa_wide_run(PaMode mode, const PaCall &c, const PagedArgs &a, int rows, cudaStream_t s) {
+    const int grid = num_sms();
+    if (mode != PA_ALL) {
+        const auto run = c.type == SD_KV_F16 ? paged_shared_f16 : c.type == SD_KV_BF16 ? paged_shared_bf16 : paged_shared_i8;
+        return run(mode, a, c.tmk, c.tmv, c.D, rows, grid, s);
+    }
+    const auto run = c.type == SD_KV_F16 ? paged_wide_f16 : c.type == SD_KV_BF16 ? paged_wide_bf16 : paged_wide_i8;
+    return run(a, c.tmk, c.tmv, c.D, rows, grid, s);
+}
+
+sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s) {
+    PagedArgs a = c.a;
+    const int rows = a.M * a.g, B = a.B;
+    if (pa_wide(rows, c.D)) {
         const int part = B <= PA_WIDE_B ? B : (B + 1) / 2;
         static_assert(PG_MAX_B <= 2 * PA_WIDE_B, "two launches hold the most sequences");
         for (int b0 = 0; b0 < B; b0 += part) {
             a.B = B - b0 < part ? B - b0 : part;
-            a.table = table + static_cast<int64_t>(b0) * width;
-            a.lens = lens + b0;
-            a.n_new = n_new ? n_new + b0 : nullptr;
-            a.parent = parent ? parent + static_cast<int64_t>(b0) * M : nullptr;
-            a.q = q + b0 * q_seq_stride;
-            a.out = out + b0 * out_seq_stride;
-            if (run(a, tmk, tmv, D, rows, num_sms(), s) != cudaSuccess) return SD_ECUDA;
+            a.table = c.a.table + static_cast<int64_t>(b0) * a.width;
+            a.lens = c.a.lens + b0;
+            a.n_new = c.a.n_new ? c.a.n_new + b0 : nullptr;
+            a.parent = c.a.parent ? c.a.parent + static_cast<int64_t>(b0) * a.M : nullptr;
+            a.q = c.a.q + b0 * a.q_sb;
+            a.out = c.a.out + b0 * a.o_sb;
+            if (mode == PA_OWN) {
+                a.skip = c.a.skip + b0;
+                a.row_ml = c.a.row_ml + static_cast<int64_t>(b0) * a.M * a.H;
+            }
+            if (pa_wide_run(mode, c, a, rows, s) != cudaSuccess) return SD_ECUDA;
         }
         return SD_OK;
     }
-    const cudaError_t e = pages->type == SD_KV_F16    ? pa_launch_d<SD_KV_F16>(D, p, a, tmk, tmv, s)
-                          : pages->type == SD_KV_BF16 ? pa_launch_d<SD_KV_BF16>(D, p, a, tmk, tmv, s)
-                                                      : pa_launch_d<SD_KV_I8>(D, p, a, tmk, tmv, s);
+    PaPlan p;
+    if (!pa_plan(c.type, B, rows, c.D, p)) return SD_ECUDA;
+    a.nst = p.nst;
+    const cudaError_t e = mode == PA_ALL ? pa_launch_t<PA_ALL>(c.type, c.D, p, a, c.tmk, c.tmv, s)
+                                         : pa_launch_t<PA_OWN>(c.type, c.D, p, a, c.tmk, c.tmv, s);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
+}
+
+// A prefix has the query rows of at least two sequences: the tensor-memory kernel takes them but at D = 256.
+sd_status pa_prefix(const PaCall &c, int rows, cudaStream_t s) {
+    if (c.D <= 128) return pa_wide_run(PA_PREFIX, c, c.a, rows, s) == cudaSuccess ? SD_OK : SD_ECUDA;
+    PaPlan p;
+    PagedArgs a = c.a;
+    if (!pa_plan(c.type, a.B, 16, c.D, p)) return SD_ECUDA;
+    a.nst = p.nst;
+    const cudaError_t e = c.type == SD_KV_F16    ? pa_launch<SD_KV_F16, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s)
+                          : c.type == SD_KV_BF16 ? pa_launch<SD_KV_BF16, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s)
+                                                 : pa_launch<SD_KV_I8, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s);
+    return e == cudaSuccess ? SD_OK : SD_ECUDA;
+}
+
+}  // namespace sdv
+
+using namespace sdv;
+
+extern "C" {
+
+size_t sd_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D) {
+    if (B < 1 || B > PG_MAX_B || M < 1 || M > 16 || H_kv < 1 || H < H_kv || H % H_kv || (D != 64 && D != 128 && D != 256))
+        return 0;
+    return pa_workspace(D, nullptr, nullptr);
+}
+
+sd_status sd_paged_attn(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,
+                        const int32_t *n_new, int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride,
+                        int64_t q_row_stride, const int32_t *parent, int32_t window, int32_t sinks, float *out,
+                        int64_t out_seq_stride, int64_t out_row_stride, void *workspace, size_t ws_bytes,
+                        sd_stream_t stream) {
+    SD_NVTX("sd_paged_attn");
+    PaCall c;
+    const sd_status st = pa_call(pages, table, width, lens, n_new, B, M, H, q, q_seq_stride, q_row_stride, parent, window,
+                                 sinks, out, out_seq_stride, out_row_stride, workspace, ws_bytes, c);
+    return st == SD_OK ? pa_rows(c, PA_ALL, reinterpret_cast<cudaStream_t>(stream)) : st;
 }
 
 }  // extern "C"

@@ -13,6 +13,12 @@ constexpr float PA_NEG = -3.402823466e38f;  // running-max start: finite, below 
 constexpr float PA_PS = 16384.0f;  // fp16 weights are scaled by 2^14 (exact)
 constexpr uint64_t PA_WAIT_NS = 2000000000ull;
 
+// What a launch goes over: whole sequences (sd_paged_attn); or of a batch that shares prefixes (sd_paged_attn_shared) each
+// sequence's rows behind its group's prefix, or the groups' prefixes, where a "sequence" is a group's shared rows and its
+// new rows are those of all its members.  (The first is a mode of its own because the others' few instructions per piece
+// cost it 4 %: 515 against 535 us, 16 sequences of 20000-60000 8-bit rows.)
+enum PaMode { PA_ALL = 0, PA_OWN = 1, PA_PREFIX = 2 };
+
 struct PagedArgs {
     const float *q;  // row i of sequence b at b * q_sb + i * q_sm, heads contiguous
     float *out;
@@ -29,7 +35,34 @@ struct PagedArgs {
     int32_t *counters;    // [grid], zero between calls
     int32_t part_rows;    // rows of D floats that part_o holds (part_ml: as many pairs)
     int *status;
+    // PA_PREFIX: lens, n_new hold the groups' shared rows and numbers of new rows, first[v] where group v's begin in
+    // rows_of (sequence * M + row), leader[v] a sequence whose table names the group's pages; out [row of rows_of][H][D]
+    const int32_t *first, *leader, *rows_of;
+    const int32_t *skip;  // PA_OWN: [B] tiles of a sequence's shared prefix
+    float2 *row_ml;       // maximum and sum behind each row of out and head: PA_PREFIX [row of rows_of][H], PA_OWN [B * M][H]
 };
+
+// query and output row of new row i of sequence (or group) b
+template <int MODE>
+__device__ __forceinline__ const float *q_row(const PagedArgs &a, int b, int i) {
+    if constexpr (MODE == PA_PREFIX) {
+        const int at = a.rows_of[a.first[b] + i], sb = at / a.M;
+        return a.q + sb * a.q_sb + (at - sb * a.M) * a.q_sm;
+    } else {
+        return a.q + b * a.q_sb + i * a.q_sm;
+    }
+}
+template <int MODE>
+__device__ __forceinline__ float *out_row(const PagedArgs &a, int b, int i, int h, int D) {
+    if constexpr (MODE == PA_PREFIX) return a.out + (static_cast<int64_t>(a.first[b] + i) * a.H + h) * D;
+    else return a.out + b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D;
+}
+// the softmax statistics behind a finished row
+template <int MODE>
+__device__ __forceinline__ void put_ml(const PagedArgs &a, int b, int i, int h, float m, float l) {
+    if constexpr (MODE == PA_PREFIX) a.row_ml[static_cast<int64_t>(a.first[b] + i) * a.H + h] = make_float2(m, l);
+    if constexpr (MODE == PA_OWN) a.row_ml[(static_cast<int64_t>(b) * a.M + i) * a.H + h] = make_float2(m, l);
+}
 
 // the scales of 8-bit rows where there is no page
 static __device__ __align__(16) float pa_zeros[PA_KT];
@@ -156,6 +189,18 @@ __device__ __forceinline__ SeqTiles seq_tiles(int len, int n, int window, int si
     return s;
 }
 
+// the tiles of a launch's sequence (or group); skip: of its shared prefix (full context alone has one)
+template <int MODE>
+__device__ __forceinline__ SeqTiles tiles_of(const PagedArgs &a, int len, int n, int skip) {
+    if constexpr (MODE == PA_PREFIX) return {0, 0, len / PA_KT};  // whole tiles
+    SeqTiles s = seq_tiles(len, n, a.window, a.sinks);
+    if constexpr (MODE == PA_OWN) {
+        s.lo_tile += skip;
+        s.T -= skip;
+    }
+    return s;
+}
+
 // new rows that position i of a sequence sees: its path, cut by the window (the path's k-th node stands at depth k)
 __device__ __forceinline__ uint32_t new_rows_seen(const PagedArgs &a, int b, int i, int len, int &depth) {
     uint32_t path = 0;
@@ -195,20 +240,20 @@ struct Piece {
 
 struct Sched {
     const int64_t *prefix;  // [B + 1]: tiles of the sequences before
-    const int2 *ln;         // [B]: (len, n_new), n_new 0 where nothing is to be done
+    const int2 *ln;         // [B]: (len, n_new; PA_OWN: n_new + 32 * skipped tiles), n_new 0 where nothing is to be done
     int64_t u0, u1, W;
     int32_t G;              // CTAs that share the line
 };
 
-template <int RPG>
+template <int RPG, int MODE>
 __device__ __forceinline__ Piece piece_at(const PagedArgs &a, const Sched &s, int64_t u, int b) {
     Piece p;
     while (s.prefix[b + 1] <= u) ++b;
     p.b = b;
     const int2 ln = s.ln[b];
     p.len = ln.x;
-    p.n = ln.y;
-    p.st = seq_tiles(p.len, p.n, a.window, a.sinks);
+    p.n = MODE == PA_OWN ? ln.y & 31 : ln.y;
+    p.st = tiles_of<MODE>(a, p.len, p.n, MODE == PA_OWN ? ln.y >> 5 : 0);
     const int64_t rem = u - s.prefix[b];
     const int64_t run = rem / p.st.T;
     p.t0 = static_cast<int32_t>(rem - run * p.st.T);
@@ -223,19 +268,22 @@ __device__ __forceinline__ Piece piece_at(const PagedArgs &a, const Sched &s, in
 __device__ __forceinline__ int cta_of(const Sched &s, int64_t u) { return static_cast<int>(((u + 1) * s.G - 1) / s.W); }
 
 // The whole line of tiles and this CTA's share of it; false: the CTA has none.  All NTHR threads call it.
-template <int RPG, int NTHR>
+template <int RPG, int NTHR, int MODE>
 __device__ bool make_sched(const PagedArgs &a, int64_t *prefix, int2 *ln, Sched &sc) {
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     for (int b = tid; b < a.B; b += NTHR) {
         int len = a.lens[b], n = a.n_new ? a.n_new[b] : a.M;
-        if (len < 0 || n < 0 || n > a.M || static_cast<int64_t>(len) + n > static_cast<int64_t>(a.width) * a.P) {
-            set_status(a.status, SD_EDEVICE);
-            n = 0;
+        if constexpr (MODE != PA_PREFIX) {  // (the groups are made of sequences that pass this)
+            if (len < 0 || n < 0 || n > a.M || static_cast<int64_t>(len) + n > static_cast<int64_t>(a.width) * a.P) {
+                set_status(a.status, SD_EDEVICE);
+                n = 0;
+            }
         }
+        const int skip = MODE == PA_OWN && n > 0 ? a.skip[b] : 0;
         int64_t cost = 0;
         if (n > 0)
-            cost = static_cast<int64_t>(seq_tiles(len, n, a.window, a.sinks).T) * ((n * a.g + RPG - 1) / RPG) * a.H_kv;
-        ln[b] = make_int2(len, n);
+            cost = static_cast<int64_t>(tiles_of<MODE>(a, len, n, skip).T) * ((n * a.g + RPG - 1) / RPG) * a.H_kv;
+        ln[b] = make_int2(len, n + 32 * skip);
         prefix[b + 1] = cost;
     }
     if (tid == 0) prefix[0] = 0;
@@ -268,7 +316,7 @@ __device__ bool make_sched(const PagedArgs &a, int64_t *prefix, int2 *ln, Sched 
 // The producer warp's loop: the tiles of the CTA's pieces into the ring's stages, running ahead of whoever empties
 // them.  QS > 0: each piece's query rows come first, in QS stages of QR rows, each row D floats and 16 bytes apart (so
 // that threads of consecutive rows read them without bank conflicts).
-template <int T, int D, int RPG, int QS, int QR>
+template <int T, int D, int RPG, int QS, int QR, int MODE>
 __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtensorMap *tmk, const CUtensorMap *tmv,
                               uint8_t *ring, int nst, uint64_t *full, uint64_t *empty, volatile int *abort) {
     using LY = PaLayout<T, D>;
@@ -297,7 +345,7 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
         }
     };
     while (ok && u < sc.u1) {
-        const Piece p = piece_at<RPG>(a, sc, u, b);
+        const Piece p = piece_at<RPG, MODE>(a, sc, u, b);
         b = p.b;
         for (int s = 0; ok && s < QS; ++s) {
             ok = take();
@@ -311,19 +359,18 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
             __syncwarp();
             for (int i = lane; i < n; i += 32) {
                 const int tg = p.rg * RPG + r0 + i;
-                if (!SD_INB(p.b >= 0 && p.b < a.B && tg >= 0 && tg / a.g < a.M && p.kh >= 0 && p.kh < a.H_kv && slot < nst,
+                if (!SD_INB(p.b >= 0 && p.b < a.B && tg >= 0 && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh >= 0 && p.kh < a.H_kv && slot < nst,
                             a.status, 113))  // site 113: query row
                     continue;
                 bulk_g2s_l2keep(ring + static_cast<size_t>(slot) * LY::STAGE + i * (D * 4 + 16),
-                                a.q + p.b * a.q_sb + (tg / a.g) * a.q_sm +
-                                    static_cast<int64_t>(p.kh * a.g + tg % a.g) * D,
+                                q_row<MODE>(a, p.b, tg / a.g) + static_cast<int64_t>(p.kh * a.g + tg % a.g) * D,
                                 D * 4, &full[slot]);
             }
             taken();
         }
         if (!ok) break;
-        const int32_t *tab = a.table + static_cast<int64_t>(b) * a.width;
-        const int total = p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
+        const int32_t *tab = a.table + static_cast<int64_t>(MODE == PA_PREFIX ? a.leader[b] : b) * a.width;
+        const int total = MODE == PA_PREFIX ? p.len : p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
         // the pages of the piece's places in order, npt to a tile, 32 at a time and 32 more on their way: a table entry
         // fetched per tile would cost the tile its latency.  (A place without rows, or an entry that is no page, reads
         // as zeros.)
@@ -384,11 +431,12 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
 }
 
 // The partials of one run's CTAs c0 .. c1, joined in the order of their keys by the NTHR threads that call it (named
-// barrier `bar` among them).  A warp reads whole rows (a row of D = 64 half a warp), JC CTAs at a time: the weights of
+// barrier `bar` among them; l_unit: what their sums are in).  A warp reads whole rows (a row of D = 64 half a warp), JC CTAs at a time: the weights of
 // all rows come first, through shared memory (RPG * (JC + 2) floats), then every load of a pass is in flight at once.
 constexpr int JC = 8;
-template <int RPG, int D, int NTHR>
-__device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1, int tid, float *sm, int bar) {
+template <int RPG, int D, int NTHR, int MODE>
+__device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1, int tid, float *sm, int bar,
+                              float l_unit = 1.0f) {
     constexpr int LR = D / 4 < 32 ? D / 4 : 32, NV = D / 4 / LR;  // lanes of a row, 16-byte columns per lane
     constexpr int RT = NTHR / LR, NR = (RPG + RT - 1) / RT;       // rows at a time, rows per thread
     constexpr int XU = 16 / (NR * NV) > 0 ? (16 / (NR * NV) < JC ? 16 / (NR * NV) : JC) : 1;
@@ -407,6 +455,10 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
         }
         mx_of[tid] = mx;
         sum_of[tid] = lv == 0.0f ? 0.0f : 1.0f / lv;
+        if constexpr (MODE != PA_ALL) {
+            const int tg = p.rg * RPG + tid;
+            put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * l_unit);
+        }
     }
     const int r0 = tid / LR, col = tid % LR;
     float4 v[NR][NV];
@@ -415,7 +467,7 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
 #pragma unroll
         for (int k = 0; k < NV; ++k) v[i][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (!SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RPG <= a.part_rows && rows <= RPG &&
-                    (p.rg * RPG + rows - 1) / a.g < a.M,
+                    (p.rg * RPG + rows - 1) / a.g < (MODE == PA_PREFIX ? p.n : a.M),
                 a.status, 116))  // site 116: partials of a join, its output rows
         c1 = c0 - 1;
     for (int x0 = c0; x0 <= c1; x0 += JC) {
@@ -462,8 +514,7 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
         const int tr = r0 + i * RT, tg = p.rg * RPG + tr;
         if (tr < rows) {
             const float inv = sum_of[tr];
-            float4 *to = reinterpret_cast<float4 *>(a.out + p.b * a.o_sb + (tg / a.g) * a.o_sm +
-                                                    static_cast<int64_t>(p.kh * a.g + tg % a.g) * D) + col;
+            float4 *to = reinterpret_cast<float4 *>(out_row<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, D)) + col;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 to[k * LR] = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
@@ -472,6 +523,22 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
     named_bar_sync(bar, NTHR);
 }
 
+// A checked call of the attention over pages (sdv_paged_attn.cu): what its launches share.
+struct PaCall {
+    PagedArgs a;
+    CUtensorMap tmk, tmv;
+    int32_t type, D;
+};
+size_t pa_workspace(int D, size_t *off_ml, size_t *off_o);
+sd_status pa_call(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
+                  int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride, int64_t q_row_stride,
+                  const int32_t *parent, int32_t window, int32_t sinks, float *out, int64_t out_seq_stride,
+                  int64_t out_row_stride, void *workspace, size_t ws_bytes, PaCall &c);
+// the new rows of the sequences of c.a (PA_ALL or PA_OWN)
+sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s);
+// the prefixes of the groups of c.a (at most PG_MAX_B / 2), of at most `rows` query rows per KV head each
+sd_status pa_prefix(const PaCall &c, int rows, cudaStream_t s);
+
 // The many-row kernel (sdv_paged_wide.cuh): D = 64 or 128, `rows` the most query rows of a KV head, one CTA per SM.
 cudaError_t paged_wide_f16(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows,
                            int grid, cudaStream_t s);
@@ -479,5 +546,12 @@ cudaError_t paged_wide_bf16(const PagedArgs &a, const CUtensorMap &tmk, const CU
                             int grid, cudaStream_t s);
 cudaError_t paged_wide_i8(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows, int grid,
                           cudaStream_t s);
+// the same in the modes of shared prefixes
+cudaError_t paged_shared_f16(PaMode mode, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows,
+                             int grid, cudaStream_t s);
+cudaError_t paged_shared_bf16(PaMode mode, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows,
+                              int grid, cudaStream_t s);
+cudaError_t paged_shared_i8(PaMode mode, const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int D, int rows,
+                            int grid, cudaStream_t s);
 
 }  // namespace sdv

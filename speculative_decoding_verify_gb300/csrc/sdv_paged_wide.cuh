@@ -31,6 +31,7 @@ namespace sdv {
 constexpr int PW_NG = 2;       // softmax groups of four warps (the lane quarters of tensor memory)
 constexpr int PW_SOFT = 128 * PW_NG;
 constexpr float PW_UP = 14.0f; // weights are in units of 2^-14 throughout (their sum too): fp16 parts stay normal
+constexpr float PW_UNIT = 6.103515625e-05f;  // 2^-14
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -217,7 +218,7 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int R>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-template <int T, int D, int C>
+template <int T, int D, int C, int MODE>
 __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
     paged_wide_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
     pdl_wait();
     pdl_launch_dependents();
     Sched sc;
-    if (!make_sched<RP, W::THREADS>(a, prefix, ln, sc)) return;
+    if (!make_sched<RP, W::THREADS, MODE>(a, prefix, ln, sc)) return;
     if (warp == W::WARP_M) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tbase)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -286,9 +287,9 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
     if (warp >= W::WARP_P && warp < W::WARP_P + 4) regs_dec<W::REG_P>();
     if (warp == W::WARP_P) {
         if constexpr (W::I8)
-            produce_tiles<T, D, RP, W::QS, W::QR>(a, sc, &tmk, &tmv, raw, W::NRAW, raw_full, raw_empty, abort);
+            produce_tiles<T, D, RP, W::QS, W::QR, MODE>(a, sc, &tmk, &tmv, raw, W::NRAW, raw_full, raw_empty, abort);
         else
-            produce_tiles<T, D, RP, W::QS, W::QR>(a, sc, &tmk, &tmv, ops, W::NOP, op_full, op_empty, abort);
+            produce_tiles<T, D, RP, W::QS, W::QR, MODE>(a, sc, &tmk, &tmv, ops, W::NOP, op_full, op_empty, abort);
     } else if (warp == W::WARP_M) {
         // ---- the thread that issues the MMAs: tiles are numbered over the whole share
         if (elect_one()) {
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             uint32_t nqk = 0, npv = 0, np = 0;             // tiles and pieces so far
             bool ok = true;
             while (ok && u < sc.u1) {
-                const Piece p = piece_at<RP>(a, sc, u, b);
+                const Piece p = piece_at<RP, MODE>(a, sc, u, b);
                 b = p.b;
                 const int n = p.t1 - p.t0;
                 if (!wait(q_ready, np & 1u)) break;
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             uint32_t unit = 0x00800000u;
             for (; left > 0 || u < sc.u1; ++i, --left) {
                 if (left == 0) {  // the next piece: its queries' stages go back once they are read
-                    p = piece_at<RP>(a, sc, u, b);
+                    p = piece_at<RP, MODE>(a, sc, u, b);
                     b = p.b;
                     left = p.t1 - p.t0;
                     u += left;
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             return x;
         };
         while (u < sc.u1) {
-            const Piece p = piece_at<RP>(a, sc, u, b);
+            const Piece p = piece_at<RP, MODE>(a, sc, u, b);
             b = p.b;
             const int rows = p.n * a.g, tg = p.rg * RP + r;
             const bool real = tg < rows;
@@ -556,9 +557,12 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             uint32_t vis = 0;
             int low = INT32_MAX;
             if (real) {
-                int depth;
-                vis = new_rows_seen(a, p.b, tg / a.g, p.len, depth);
-                low = a.window > 0 ? p.len + depth - a.window + 1 : 0;
+                low = 0;
+                if constexpr (MODE != PA_PREFIX) {  // (a prefix is whole tiles of rows that all of its rows see)
+                    int depth;
+                    vis = new_rows_seen(a, p.b, tg / a.g, p.len, depth);
+                    if (a.window > 0) low = p.len + depth - a.window + 1;
+                }
             }
             const int full_lo = a.window > 0 ? p.len + p.n - a.window : 0, full_sink = a.window > 0 ? a.sinks : 0;
             // al: rescale of the outputs before the product still to be added; vunit: their unit (8-bit rows), a power of
@@ -821,6 +825,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             const float unit = W::I8 ? __uint_as_float(vunit) : 1.0f;
             const float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
+            if constexpr (MODE != PA_ALL)
+                if (complete && real && lg == 0 && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * PW_UNIT);
             // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared
             // memory: thread = 4 columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
             auto write_rows = [&](bool final, float fac) {
@@ -831,8 +837,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 for (int k = 0; k < NK; ++k) {
                     const int tr = wr + RW * k, y = p.rg * RP + tr;
                     to[k] = tr >= RP || y >= rows ? nullptr
-                            : final ? a.out + p.b * a.o_sb + (y / a.g) * a.o_sm +
-                                          static_cast<int64_t>(p.kh * a.g + y % a.g) * D + wc
+                            : final ? out_row<MODE>(a, p.b, y / a.g, p.kh * a.g + y % a.g, D) + wc
                                     : a.part_o + (static_cast<int64_t>(pslot) * RP + tr) * D + wc;
                 }
 #pragma unroll
@@ -846,7 +851,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     named_bar_sync(5, PW_SOFT);
 #pragma unroll
                     for (int k = 0; k < NK; ++k)
-                        if (to[k] && SD_INB(p.b < a.B && (p.rg * RP + wr + RW * k) / a.g < a.M && p.kh < a.H_kv &&
+                        if (to[k] && SD_INB(p.b < a.B && (p.rg * RP + wr + RW * k) / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh < a.H_kv &&
                                                 (final || (pslot + 1) * RP <= a.part_rows),
                                             a.status, 117)) {  // site 117: rows of a piece
                             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -888,7 +893,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 named_bar_sync(5, PW_SOFT);
                 if (*last) {
                     if constexpr (C > 1) {
-                        join_partials<RP, D, PW_SOFT>(a, p, c0, c1, tid, scratch, 5);
+                        join_partials<RP, D, PW_SOFT, MODE>(a, p, c0, c1, tid, scratch, 5, PW_UNIT);
                     } else {
                         // as join_partials: in the order of the keys, with a running maximum; two partials' loads in
                         // flight at once
@@ -925,6 +930,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         }
                         fac = jl == 0.0f ? 0.0f : 1.0f / jl;
                         rows_ready = true;
+                        if constexpr (MODE != PA_ALL)
+                            if (real && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, jm, jl * PW_UNIT);
                     }
                 }
             }
@@ -942,23 +949,23 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
     }
 }
 
-template <int T, int D, int C>
+template <int T, int D, int C, int MODE>
 cudaError_t wide_launch(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t s) {
     using W = WideLayout<T, D, C>;
     const size_t smem = W::fixed() + (static_cast<size_t>(a.B) + 1) * 8 + static_cast<size_t>(a.B) * 8;
-    const cudaError_t e = allow_max_dynamic_smem(paged_wide_kernel<T, D, C>);
+    const cudaError_t e = allow_max_dynamic_smem(paged_wide_kernel<T, D, C, MODE>);
     if (e != cudaSuccess) return e;
-    return launch(paged_wide_kernel<T, D, C>, dim3(grid), dim3(W::THREADS), smem, s, a, tmk, tmv);
+    return launch(paged_wide_kernel<T, D, C, MODE>, dim3(grid), dim3(W::THREADS), smem, s, a, tmk, tmv);
 }
-template <int T, int D>
+template <int T, int D, int MODE>
 cudaError_t wide_launch_c(const PagedArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int rows, int grid,
                           cudaStream_t s) {
-    if (rows <= 32) return wide_launch<T, D, 4>(a, tmk, tmv, grid, s);
+    if (rows <= 32) return wide_launch<T, D, 4, MODE>(a, tmk, tmv, grid, s);
     // (two lane groups for three bf16 parts make two passes of the product: 346 us against 264 us with one group, 64
     // rows, 16 sequences of 16000 rows)
     if constexpr (T != SD_KV_BF16)
-        if (rows <= 64) return wide_launch<T, D, 2>(a, tmk, tmv, grid, s);
-    return wide_launch<T, D, 1>(a, tmk, tmv, grid, s);
+        if (rows <= 64) return wide_launch<T, D, 2, MODE>(a, tmk, tmv, grid, s);
+    return wide_launch<T, D, 1, MODE>(a, tmk, tmv, grid, s);
 }
 
 }  // namespace sdv
