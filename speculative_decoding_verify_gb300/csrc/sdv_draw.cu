@@ -5,12 +5,16 @@
 // prefix of the order (larger logit first, lower index among equals), so each is a threshold in that order and the strictest
 // one counts; the token is the first in index order whose running sum of kept weights exceeds u times their total.
 //
-// A row is read from HBM once, by a cluster of CTAs that hold it in shared memory; what follows works there:
-//   the thresholds by histograms over the distance d = m - l (128 bins per octave first; bins with more than DR_LIST tokens
-//   are cut again, by the bits of d, then of l, then of the index), their bins added up over the cluster, each CTA a slice
-//   of them; the last few tokens are listed in every CTA and ranked by comparing all with all;
-//   the draw by one sum per thread over neighbouring tokens and a scan of those sums.
-// Bound by the exchanges over the cluster for few rows, by the passes over shared memory for many.
+// A row is read from HBM once, by a cluster of CTAs that hold it in shared memory; what follows works there.  A filter's
+// threshold is the token at a given count, or at a given sum of weights.  It is found by histograms over the distance d = m - l
+// (128 bins per octave first; a bin with more than DR_LIST tokens is cut again, by the bits of d, then of l, then of the
+// index): each CTA makes its own, one exchange later every CTA adds up the few bins that decide.  Counts are exact; a bin's
+// weights are 15-bit parts of its first token's, so the sum only says where to look: a pass over the tokens then takes the
+// exact sum of all before the bin and lists those in it, which are ranked by comparing all with all, and where the
+// threshold is not among them the search goes on at the next token before or behind.  That pass leaves each thread the sum
+// of its own neighbouring tokens, so the draw is a scan of those sums and a walk of one warp.
+// With top-k and a bin that ends under DR_LIST tokens the list holds all that may be kept, and everything is done on it.
+// Every exchange is one cluster barrier: three for a listed row, three or four for others, and one at each end.
 #include <cooperative_groups.h>
 
 #include "sdv_common.cuh"
@@ -20,12 +24,13 @@ namespace cg = cooperative_groups;
 namespace sdv {
 
 constexpr int DR_THREADS = 512, DR_WARPS = DR_THREADS / 32;
-constexpr int DR_BINS = 2048;
-constexpr int DR_LIST = 256;               // tokens that are ranked directly
+constexpr int DR_BITS = 10, DR_BINS = 1 << DR_BITS, DR_COARSE = 32;  // a coarse bin is 32 bins
+constexpr int DR_LIST = 256;      // tokens that are ranked directly
 constexpr int DR_MOST_CTAS = 8;
-constexpr int DR_CHUNK = 45056;            // most tokens of a CTA
-constexpr uint32_t DR_FIRST = 0x3b800000u;  // bits of 2^-8: where the first histogram's octaves start (16 of them)
-constexpr float DR_UNIT = 17592186044416.0f;  // 2^44
+constexpr int DR_CHUNK = 45056;   // most tokens of a CTA (88 a thread)
+// the first histogram: 8 octaves of d from 2^-3 on, by the bits of d
+constexpr uint32_t DR_FIRST = 0x3e000000u;
+constexpr int DR_SHIFT = 16;
 
 struct DrawArgs {
     const float *logits;
@@ -39,70 +44,97 @@ struct DrawArgs {
     int *status;
 };
 
-// order of logits as whole numbers
+// the order of logits as whole numbers, and back
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t b = __float_as_uint(x);
     return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float key_logit(uint32_t k) {
+    return __uint_as_float(k ^ (static_cast<uint32_t>(static_cast<int32_t>(~k) >> 31) | 0x80000000u));
+}
+// a token in the order: larger first
+__device__ __forceinline__ uint64_t place_of(float l, int idx) {
+    return static_cast<uint64_t>(order_key(l)) << 32 | (0xffffffffu - static_cast<uint32_t>(idx));
+}
+__device__ __forceinline__ int place_idx(uint64_t at) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(at)); }
 
-// counts and weights of a histogram's slice, or of everything before it
-struct Tally {
-    uint32_t n;
-    uint64_t w;
+// Which tokens a search has come down to: ranges of the bits of d, of the key from above, and of the index.
+struct Range {
+    uint32_t lo[3], hi[3];
 };
 
-// what a search gives all CTAs: the bin, what is before it and how many are in it
+// what a search of a histogram gives: the bin, the tokens before it and in it
 struct Found {
-    uint64_t before_w;
-    uint32_t before_n, bin, n;
+    uint32_t bin, before_n, n;
+    float before_m;  // about the weight before it, in units of 2^-15
+};
+
+// What a pass over the tokens tells of a CTA: the sums of all weights before the range and of the kept ones, and how many
+// tokens it listed.
+struct Passed {
+    uint64_t before, kept;
+    uint32_t n;
 };
 
 struct alignas(16) DrawShared {
-    uint32_t hist_n[DR_BINS], hist_lo[DR_BINS], hist_hi[DR_BINS];
-    uint64_t list_w[DR_LIST];
-    uint64_t list_at[DR_LIST];  // key and index in the order's terms
-    Tally total[2][DR_MOST_CTAS];  // of the first histogram and of the later ones
-    uint64_t warp_w[DR_WARPS + 1];
-    uint32_t warp_n[DR_WARPS + 1];
-    uint64_t sums[DR_MOST_CTAS];
-    float maxima[DR_MOST_CTAS];
-    float warp_max[DR_WARPS];
+    // ---- read or written by the cluster's other CTAs (what they write has two turns: a slow CTA still reads one)
+    uint32_t bin_n[2][DR_BINS], bin_m[2][DR_BINS];  // a level's histogram
+    uint2 coarse[2][DR_MOST_CTAS][DR_COARSE];       // every CTA's: tokens, weight (a float's bits)
+    uint64_t list[2][DR_LIST];                      // this CTA's tokens in a pass's range
+    Passed passed[2][DR_MOST_CTAS];                 // every CTA's
+    uint64_t sums[DR_MOST_CTAS];                    // every CTA's sum of all weights
+    float tops[DR_MOST_CTAS];                       // and largest logit
+    // ---- of this CTA alone
+    uint64_t at[DR_LIST], w[DR_LIST];  // the cluster's list
+    uint64_t cta_sum[DR_MOST_CTAS];
+    uint64_t part[DR_WARPS];
+    float warp_f[DR_WARPS];
     Found found;
     uint64_t thr, thr_sum;
-    uint32_t list_n;
-    float c_hi, c_lo;
-    uint32_t key_low;
-    int32_t k;
-    float p, u;
-    int bad;
+    double low_log;
+    float c_hi, c_lo, p, u, low;
+    uint32_t listed;
+    int32_t k, bad, owner;
 };
 
-// 2^x by its series in f ln 2 for x = round(x) + f: the terms behind the eighth power are under 2^-32
-__device__ __forceinline__ float exp2_parts(float xh, float xl) {
-    const float k = rintf(xh), f = (xh - k) + xl;
-    float p = 1.3215487e-6f;
-    p = fmaf(p, f, 1.5252734e-5f);
-    p = fmaf(p, f, 1.5403530e-4f);
-    p = fmaf(p, f, 1.3333558e-3f);
-    p = fmaf(p, f, 9.6181291e-3f);
-    p = fmaf(p, f, 5.5504109e-2f);
-    p = fmaf(p, f, 2.4022651e-1f);
-    p = fmaf(p, f, 6.9314718e-1f);
-    p = fmaf(p, f, 1.0f);
-    return p * __int_as_float((static_cast<int>(k) + 127) << 23);
+__device__ __forceinline__ float ex2_approx(float x) {  // 2^x to about 2^-22, 0 below the normal numbers
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// exp((l - m) / T): the difference and its product with log2(e) / T in two floats each, so that a far token's weight is as
-// good as a near one's; nothing below 2^-60
+// exp((l - m) / T): the difference and its product with c = log2(e) / T in two floats each, so that a far token's weight is
+// as good as a near one's; nothing below 2^-60
 __device__ __forceinline__ float weight_of(float l, float m, float c_hi, float c_lo) {
-    if (l == m) return 1.0f;
     const float s = l - m, xh = s * c_hi;
-    if (!(xh > -60.0f)) return 0.0f;
     const float bb = s - l, left = (l - (s - bb)) + (-m - bb);
     const float xl = fmaf(s, c_hi, -xh) + fmaf(s, c_lo, left * c_hi);
-    return exp2_parts(xh, xl);
+    const float e = ex2_approx(xh) * fmaf(xl, 0.693147182f, 1.0f);
+    return xh > -60.0f ? e : 0.0f;
 }
-__device__ __forceinline__ uint64_t units(float w) { return __float2ull_rn(w * DR_UNIT); }
+
+// Weights as whole numbers of 2^-44, summed in two words: adding 4 leaves the multiples of 2^-21 in the bits, adding
+// 1.5 * 2^-21 to the rest those of 2^-44 (under 2^22 of them, either sign).
+struct Units {
+    uint32_t hi, lo, n;
+    __device__ __forceinline__ void add(float e) {
+        const float t = e + 4.0f, r = (e - (t - 4.0f)) + 7.152557373046875e-07f;
+        hi += __float_as_uint(t);
+        lo += __float_as_uint(r);
+        ++n;
+    }
+    __device__ __forceinline__ uint64_t sum() const {  // of at most 512 weights
+        const uint32_t h = hi - n * 0x40800000u;
+        const int32_t l = static_cast<int32_t>(lo - n * 0x35400000u);
+        return (static_cast<uint64_t>(h) << 23) + static_cast<uint64_t>(static_cast<int64_t>(l));
+    }
+};
+__device__ __forceinline__ uint64_t units(float e) {
+    Units u = {0, 0, 0};
+    u.add(e);
+    return u.sum();
+}
+constexpr float DR_UNIT = 17592186044416.0f;  // 2^44
 
 // floor(f * x) for 0 <= f <= 1 (up: the least whole number not below f * x)
 template <bool UP>
@@ -116,229 +148,321 @@ __device__ __forceinline__ uint64_t whole_times(float f, uint64_t x) {
     return floor + (UP && rest ? 1 : 0);
 }
 
-// What one CTA of a row's cluster works with.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <class T>
+__device__ __forceinline__ T warp_sum(T v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <class T>
+__device__ __forceinline__ T warp_scan(T v) {  // inclusive
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+// the sum over the CTA, in every thread; `part` is free again behind the next barrier
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *part) {
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum((threadIdx.x & 31) < DR_WARPS ? part[threadIdx.x & 31] : uint64_t(0));
+}
+
+// What one CTA of a row's cluster of CS works with.
+template <int CS>
 struct Draw {
     const DrawArgs &a;
     DrawShared &sh;
-    float *x;       // this CTA's logits
-    Tally *first, *later;  // this CTA's slice of the first histogram and of a later one
-    int rank, ctas, lo, n;  // tokens [lo, lo + n) of the row
-    float m;
-};
+    const float *x;    // this CTA's logits, minus infinity up to a multiple of four
+    int rank, lo, n;   // tokens [lo, lo + n) of the row
+    float m, c_hi, c_lo;
+    int level, turn;   // histograms and passes so far
 
-// Which tokens a search still goes through: ranges of the bits of d, of the key from above, and of the index.
-struct Range {
-    uint32_t lo[3], hi[3];
-};
-__device__ __forceinline__ uint32_t value_of(int phase, float l, float m, int idx) {
-    if (phase == 0) return __float_as_uint(l == m ? 0.0f : m - l);
-    return phase == 1 ? ~order_key(l) : static_cast<uint32_t>(idx);
-}
-__device__ __forceinline__ bool in_range(const Range &r, float l, float m, int idx) {
-    const uint32_t d = value_of(0, l, m, idx), k = value_of(1, l, m, idx), i = static_cast<uint32_t>(idx);
-    return d >= r.lo[0] && d <= r.hi[0] && k >= r.lo[1] && k <= r.hi[1] && i >= r.lo[2] && i <= r.hi[2];
-}
-
-// The row's histogram over the values of one phase (first: of all tokens over the octaves of d), added up over the
-// cluster: each CTA is left with its slice in `slice`, and every CTA with all slices' totals.
-__device__ void histogram(const Draw &w, bool first, int phase, const Range &r, int shift, bool mass, Tally *slice) {
-    DrawShared &sh = w.sh;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < DR_BINS; i += DR_THREADS) sh.hist_n[i] = sh.hist_lo[i] = sh.hist_hi[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < w.n; i += DR_THREADS) {
-        const float l = w.x[i];
-        uint32_t bin;
-        if (first) {
-            const uint32_t d = value_of(0, l, w.m, 0);
-            bin = d < DR_FIRST ? 0u : min((d - DR_FIRST) >> 16, static_cast<uint32_t>(DR_BINS - 1));
-        } else {
-            if (!in_range(r, l, w.m, w.lo + i)) continue;
-            bin = (value_of(phase, l, w.m, w.lo + i) - r.lo[phase]) >> shift;
-        }
-        if (!SD_INB(bin < DR_BINS, w.a.status, 123)) continue;  // site 123: bin
-        atomicAdd(&sh.hist_n[bin], 1u);
-        if (mass) {  // a 64-bit sum in two words, by the carry of the lower one
-            const uint64_t u = units(weight_of(l, w.m, sh.c_hi, sh.c_lo));
-            const uint32_t low = static_cast<uint32_t>(u);
-            uint32_t high = static_cast<uint32_t>(u >> 32);
-            if (low) high += atomicAdd(&sh.hist_lo[bin], low) > ~low;
-            if (high) atomicAdd(&sh.hist_hi[bin], high);
-        }
+    template <class T>
+    __device__ __forceinline__ T *of(T *mine, int c) const {
+        return cg::this_cluster().map_shared_rank(mine, c);
     }
-    cluster.sync();
-    const int bins = DR_BINS / w.ctas;  // of a slice
-    Tally sum = {0, 0};
-    for (int i = tid; i < bins; i += DR_THREADS) {
-        Tally t = {0, 0};
-        const int bin = w.rank * bins + i;
-#pragma unroll 1
-        for (int c = 0; c < w.ctas; ++c) {
-            t.n += *cluster.map_shared_rank(&sh.hist_n[bin], c);
-            if (mass) {
-                t.w += *cluster.map_shared_rank(&sh.hist_lo[bin], c);
-                t.w += static_cast<uint64_t>(*cluster.map_shared_rank(&sh.hist_hi[bin], c)) << 32;
+
+    // bits of d, key from above, or index
+    __device__ __forceinline__ uint32_t value(int phase, float l, int idx) const {
+        if (phase == 0) return __float_as_uint(fabsf(l - m));
+        return phase == 1 ? ~order_key(l) : static_cast<uint32_t>(idx);
+    }
+    // -1: before the range, 0: in it, 1: behind
+    __device__ __forceinline__ int side(const Range &r, float l, int idx) const {
+        const uint32_t d = value(0, l, idx);
+        if (d < r.lo[0]) return -1;
+        if (d > r.hi[0]) return 1;
+        const uint32_t k = value(1, l, idx), i = static_cast<uint32_t>(idx);
+        if (k < r.lo[1]) return -1;
+        if (k > r.hi[1]) return 1;
+        return i < r.lo[2] ? -1 : i > r.hi[2] ? 1 : 0;
+    }
+    // where a bin of a level begins, as a distance
+    __device__ __forceinline__ float edge(bool first, int phase, const Range &r, int shift, uint32_t bin) const {
+        if (first) return bin == 0 ? 0.0f : __uint_as_float(DR_FIRST + (bin << DR_SHIFT));
+        return __uint_as_float(phase == 0 ? r.lo[0] + (bin << shift) : r.lo[0]);
+    }
+
+    // A level: the tokens of the range (first: all) counted and weighed by bins.  Ends with the exchange.
+    template <bool FIRST, bool MASS>
+    __device__ void histogram(int phase, const Range &r, int shift, bool total) {
+        const int tid = static_cast<int>(threadIdx.x), b = level & 1;
+        for (int i = tid; i < DR_BINS; i += DR_THREADS) sh.bin_n[b][i] = sh.bin_m[b][i] = 0;
+        __syncthreads();
+        Units all = {0, 0, 0};
+        for (int i = 4 * tid; i < n; i += 4 * DR_THREADS) {
+            const float4 v = *reinterpret_cast<const float4 *>(x + i);
+            const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t bin;
+                float from = 0.0f;
+                if constexpr (FIRST) {
+                    const int32_t d = static_cast<int32_t>(value(0, l[j], 0));
+                    bin = static_cast<uint32_t>(min(max((d - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT, 0), DR_BINS - 1));
+                    if constexpr (MASS)
+                        from = __uint_as_float(min(static_cast<uint32_t>(d) & (0xffffffffu << DR_SHIFT),
+                                                   DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT)));
+                    if (MASS && bin == 0) from = 0.0f;
+                } else {
+                    if (side(r, l[j], lo + i + j) != 0) continue;
+                    bin = (value(phase, l[j], lo + i + j) - r.lo[phase]) >> shift;
+                    if constexpr (MASS) from = edge(false, phase, r, shift, bin);
+                }
+                if (!SD_INB(bin < DR_BINS && i + 3 < a.chunk, a.status, 123)) continue;  // site 123: bin
+                atomicAdd(&sh.bin_n[b][bin], 1u);
+                if constexpr (MASS) {  // its weight as a part of the bin's first, in units of 2^-15
+                    const float part = ex2_approx((from - fabsf(l[j] - m)) * c_hi);
+                    atomicAdd(&sh.bin_m[b][bin], __float_as_uint(part + 256.0f) - 0x43800000u);
+                    if (FIRST && total) all.add(weight_of(l[j], m, c_hi, c_lo));
+                }
             }
         }
-        slice[i] = t;
-        sum.n += t.n;
-        sum.w += t.w;
-    }
+        if (FIRST && MASS && total) {
+            const uint64_t s = block_sum(all.sum(), sh.part);
+            if (tid < CS) *of(&sh.sums[rank], tid) = s;
+        }
+        __syncthreads();
+        // 16 threads per coarse bin
+        {
+            uint32_t cn = 0;
+            float cm = 0.0f;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        sum.n += __shfl_xor_sync(0xffffffffu, sum.n, o);
-        sum.w += __shfl_xor_sync(0xffffffffu, sum.w, o);
-    }
-    if (lane == 0) {
-        sh.warp_n[warp] = sum.n;
-        sh.warp_w[warp] = sum.w;
-    }
-    __syncthreads();
-    if (tid < w.ctas) {
-        Tally t = {0, 0};
-        for (int i = 0; i < DR_WARPS; ++i) {
-            t.n += sh.warp_n[i];
-            t.w += sh.warp_w[i];
-        }
-        *cluster.map_shared_rank(&sh.total[first ? 0 : 1][w.rank], tid) = t;
-    }
-    cluster.sync();
-}
-
-// The bin of the token that brings the count (or, by_mass, the weight) to `target`, and what is before that bin.
-__device__ Found locate(const Draw &w, bool first, bool by_mass, uint64_t target) {
-    DrawShared &sh = w.sh;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    const Tally *slice = first ? w.first : w.later;
-    const int bins = DR_BINS / w.ctas, per = (bins + DR_THREADS - 1) / DR_THREADS, b0 = tid * per, b1 = min(bins, b0 + per);
-    Tally mine = {0, 0};
-    for (int i = b0; i < b1; ++i) {
-        mine.n += slice[i].n;
-        mine.w += slice[i].w;
-    }
-    Tally inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t yn = __shfl_up_sync(0xffffffffu, inc.n, o);
-        const uint64_t yw = __shfl_up_sync(0xffffffffu, inc.w, o);
-        if (lane >= o) {
-            inc.n += yn;
-            inc.w += yw;
-        }
-    }
-    __syncthreads();
-    if (lane == 31) {
-        sh.warp_n[warp] = inc.n;
-        sh.warp_w[warp] = inc.w;
-    }
-    __syncthreads();
-    Tally at = {inc.n - mine.n, inc.w - mine.w};
-    for (int i = 0; i < warp; ++i) {
-        at.n += sh.warp_n[i];
-        at.w += sh.warp_w[i];
-    }
-    for (int c = 0; c < w.rank; ++c) {
-        at.n += sh.total[first ? 0 : 1][c].n;
-        at.w += sh.total[first ? 0 : 1][c].w;
-    }
-    for (int i = b0; i < b1; ++i) {
-        const Tally t = slice[i];
-        const uint64_t before = by_mass ? at.w : at.n, here = by_mass ? t.w : t.n;
-        if (before < target && target <= before + here) {
-            const Found f = {at.w, at.n, static_cast<uint32_t>(w.rank * bins + i), t.n};
-            for (int c = 0; c < w.ctas; ++c) *cluster.map_shared_rank(&sh.found, c) = f;
-        }
-        at.n += t.n;
-        at.w += t.w;
-    }
-    cluster.sync();
-    return sh.found;
-}
-
-// The token at which the count reaches `target` (by_mass: at which the weight does), as (key, ~index) in one number, and
-// the weight of all up to it.  The first histogram is there already.
-__device__ void select(const Draw &w, bool by_mass, uint64_t target, bool mass, uint64_t &thr, uint64_t &thr_sum) {
-    DrawShared &sh = w.sh;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int tid = static_cast<int>(threadIdx.x);
-    Range r;
-    for (int i = 0; i < 3; ++i) {
-        r.lo[i] = 0;
-        r.hi[i] = i == 2 ? static_cast<uint32_t>(w.a.V - 1) : 0xffffffffu;
-    }
-    Found f = locate(w, true, by_mass, target);
-    uint64_t before_w = f.before_w, before_n = f.before_n;
-    if (f.bin > 0) r.lo[0] = DR_FIRST + (f.bin << 16);
-    if (f.bin < DR_BINS - 1) r.hi[0] = DR_FIRST + ((f.bin + 1) << 16) - 1;
-    int phase = 0;
-    while (f.n > DR_LIST) {
-        while (phase < 2 && r.lo[phase] == r.hi[phase]) ++phase;
-        const uint32_t width = r.hi[phase] - r.lo[phase];
-        const int shift = max(0, 32 - __clz(width) - 11);
-        histogram(w, false, phase, r, shift, mass, w.later);
-        f = locate(w, false, by_mass, target - (by_mass ? before_w : before_n));
-        before_w += f.before_w;
-        before_n += f.before_n;
-        const uint32_t at = r.lo[phase] + (f.bin << shift);
-        r.lo[phase] = at;
-        r.hi[phase] = min(r.hi[phase], at + ((1u << shift) - 1u));
-    }
-    // the few that are left, in every CTA
-    uint32_t *counter = cluster.map_shared_rank(&sh.list_n, 0);
-    for (int i = tid; i < w.n; i += DR_THREADS) {
-        const float l = w.x[i];
-        if (!in_range(r, l, w.m, w.lo + i)) continue;
-        const uint32_t slot = atomicAdd(counter, 1u);
-        if (slot >= DR_LIST || !SD_INB(slot < DR_LIST, w.a.status, 124)) continue;  // site 124: listed token
-        const uint64_t at = static_cast<uint64_t>(order_key(l)) << 32 | (0xffffffffu - static_cast<uint32_t>(w.lo + i));
-        const uint64_t u = mass ? units(weight_of(l, w.m, sh.c_hi, sh.c_lo)) : 0;
-        for (int c = 0; c < w.ctas; ++c) {
-            *cluster.map_shared_rank(&sh.list_at[slot], c) = at;
-            *cluster.map_shared_rank(&sh.list_w[slot], c) = u;
-        }
-    }
-    cluster.sync();
-    const int n = static_cast<int>(min(f.n, static_cast<uint32_t>(DR_LIST)));
-    if (tid < n) {
-        const uint64_t at = sh.list_at[tid], u = sh.list_w[tid];
-        uint64_t bw = before_w, bn = before_n;
-        for (int j = 0; j < n; ++j)
-            if (sh.list_at[j] > at) {
-                bw += sh.list_w[j];
-                ++bn;
+            for (int j = 0; j < DR_BINS / DR_THREADS; ++j) {
+                const uint32_t bin = DR_BINS / DR_THREADS * tid + j;
+                cn += sh.bin_n[b][bin];
+                if constexpr (MASS)
+                    cm += static_cast<float>(sh.bin_m[b][bin]) * ex2_approx(-c_hi * edge(FIRST, phase, r, shift, bin));
             }
-        if (by_mass ? bw < target && target <= bw + u : bn + 1 == target) {
-            sh.thr = at;
-            sh.thr_sum = bw + u;
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) {
+                cn += __shfl_xor_sync(0xffffffffu, cn, o);
+                cm += __shfl_xor_sync(0xffffffffu, cm, o);
+            }
+            if ((tid & 15) < CS) *of(&sh.coarse[b][rank][tid >> 4], tid & 15) = make_uint2(cn, __float_as_uint(cm));
         }
+        cluster_arrive();
+        cluster_wait();
+        ++level;
     }
-    if (tid == 0 && w.rank == 0) sh.list_n = 0;  // (the next list comes behind another exchange)
-    __syncthreads();
-    thr = sh.thr;
-    thr_sum = sh.thr_sum;
-}
 
+    // The bin of the last level with the token that brings the count (by_mass: about the weight) to `target`, from the
+    // CTAs' 32 coarse bins and the 32 bins of one of them.  Every CTA finds the same.
+    __device__ Found locate(bool first, int phase, const Range &r, int shift, bool by_mass, uint32_t target_n, float target_m) {
+        const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, b = (level - 1) & 1;
+        if (tid < 32) {
+            uint32_t cn = 0;
+            float cm = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CS; ++c) {
+                const uint2 y = sh.coarse[b][c][lane];
+                cn += y.x;
+                cm += __uint_as_float(y.y);
+            }
+            const uint32_t in = warp_scan(cn);
+            const float im = warp_scan(cm);
+            // (rounded sums may fall short of their own total: the last bin that has tokens, then)
+            const uint32_t there = __ballot_sync(0xffffffffu, cn > 0);
+            const uint32_t at = __ballot_sync(0xffffffffu, cn > 0 && (by_mass ? im >= target_m : in >= target_n));
+            const int q = at ? __ffs(at) - 1 : 31 - __clz(there);
+            const uint32_t bn = __shfl_sync(0xffffffffu, in - cn, q);
+            const float bm = __shfl_sync(0xffffffffu, im - cm, q);
+            const int bin = 32 * q + lane;
+            uint32_t fn = 0;
+            uint64_t fm = 0;
+#pragma unroll
+            for (int c = 0; c < CS; ++c) {
+                fn += *of(&sh.bin_n[b][bin], c);
+                fm += *of(&sh.bin_m[b][bin], c);
+            }
+            const float mf = static_cast<float>(fm) * ex2_approx(-c_hi * edge(first, phase, r, shift, bin));
+            const uint32_t sn = bn + warp_scan(fn);
+            const float sm = bm + warp_scan(mf);
+            const uint32_t hits = __ballot_sync(0xffffffffu, fn > 0 && (by_mass ? sm >= target_m : sn >= target_n));
+            const uint32_t some = __ballot_sync(0xffffffffu, fn > 0);
+            if (lane == (hits ? __ffs(hits) - 1 : 31 - __clz(some))) sh.found = {static_cast<uint32_t>(bin), sn - fn, fn, sm - mf};
+        }
+        __syncthreads();
+        const Found f = sh.found;
+        __syncthreads();
+        return f;
+    }
+
+    // From a bin of the first level to a range of at most DR_LIST tokens, which has the token at the count (by_mass: about
+    // the weight) `target`; f: the tokens before the range and in it.
+    template <bool MASS>
+    __device__ Range narrow(Found &f, bool by_mass, uint32_t target_n, float target_m) {
+        Range r = whole();
+        if (f.bin > 0) r.lo[0] = DR_FIRST + (f.bin << DR_SHIFT);
+        if (f.bin < DR_BINS - 1) r.hi[0] = DR_FIRST + ((f.bin + 1) << DR_SHIFT) - 1;
+        int phase = 0;
+        while (f.n > DR_LIST) {
+            while (phase < 2 && r.lo[phase] == r.hi[phase]) ++phase;
+            const int shift = max(0, 32 - __clz(r.hi[phase] - r.lo[phase]) - DR_BITS);
+            histogram<false, MASS>(phase, r, shift, false);
+            const Found g = locate(false, phase, r, shift, by_mass, target_n - f.before_n, target_m - f.before_m);
+            f = {g.bin, f.before_n + g.before_n, g.n, f.before_m + g.before_m};
+            const uint32_t at = r.lo[phase] + (g.bin << shift);
+            r.lo[phase] = at;
+            r.hi[phase] = min(r.hi[phase], at + ((1u << shift) - 1u));
+        }
+        return r;
+    }
+    __device__ Range whole() const {
+        Range r;
+        for (int i = 0; i < 3; ++i) {
+            r.lo[i] = 0;
+            r.hi[i] = i == 2 ? static_cast<uint32_t>(a.V - 1) : 0xffffffffu;
+        }
+        return r;
+    }
+
+    // A thread's tokens in the passes and the draw: neighbours, an odd number (no bank conflicts).
+    __device__ __forceinline__ int per() const { return ((n + DR_THREADS - 1) / DR_THREADS) | 1; }
+
+    // A pass over the tokens (RANGED; else all count as before): the sum of all weights before the range in every CTA, of
+    // those from `low` on each CTA's in sh.cta_sum and this thread's as the result, and the range's tokens in sh.at, sh.w (listed
+    // of them, the places of the others behind the order's end).
+    template <bool RANGED>
+    __device__ uint64_t pass(const Range &r, float low, uint64_t &before) {
+        const int tid = static_cast<int>(threadIdx.x), q = turn++ & 1;
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        const int i0 = min(n, tid * per()), i1 = min(n, i0 + per());
+        Units all = {0, 0, 0}, kept = {0, 0, 0};
+#pragma unroll 4
+        for (int i = i0; i < i1; ++i) {
+            const float l = x[i];
+            const int s = RANGED ? side(r, l, lo + i) : -1;
+            if (s < 0) {
+                const float e = weight_of(l, m, c_hi, c_lo);
+                all.add(e);
+                if (l >= low) kept.add(e);
+            } else if (s == 0) {
+                const uint32_t slot = atomicAdd(&sh.listed, 1u);
+                if (slot < DR_LIST && SD_INB(slot < DR_LIST, a.status, 124)) sh.list[q][slot] = place_of(l, lo + i);  // site 124: listed token
+            }
+        }
+        const uint64_t mine = kept.sum();
+        const uint64_t b = block_sum(all.sum(), sh.part), k = block_sum(mine, sh.part);
+        if (tid < CS) *of(&sh.passed[q][rank], tid) = Passed{b, k, min(sh.listed, static_cast<uint32_t>(DR_LIST))};
+        cluster_arrive();
+        cluster_wait();
+        before = 0;
+        if (tid < CS) sh.cta_sum[tid] = sh.passed[q][tid].kept;
+        uint32_t from = 0;
+        const uint64_t *src = nullptr;
+#pragma unroll
+        for (int c = 0; c < CS; ++c) {
+            const uint32_t nc = sh.passed[q][c].n;
+            before += sh.passed[q][c].before;
+            if (RANGED && tid >= static_cast<int>(from) && tid < static_cast<int>(from + nc)) src = of(&sh.list[q][tid - from], c);
+            from += nc;
+        }
+        if (RANGED && tid < DR_LIST) {
+            const uint64_t p = src ? *src : 0;
+            sh.at[tid] = p;
+            sh.w[tid] = src ? units(weight_of(key_logit(static_cast<uint32_t>(p >> 32)), m, c_hi, c_lo)) : 0;
+        }
+        __syncthreads();
+        listed = RANGED ? static_cast<int>(min(from, static_cast<uint32_t>(DR_LIST))) : 0;
+        return mine;
+    }
+
+    // The rank of this thread's listed token: weight and number of those before it (in the list, and as many more).
+    __device__ __forceinline__ void ranks(uint64_t before_w, uint32_t before_n) {
+        const int tid = static_cast<int>(threadIdx.x);
+        rank_w = before_w;
+        rank_n = before_n;
+        if (tid >= listed) return;
+        const uint64_t at = sh.at[tid];
+#pragma unroll 8
+        for (int j = 0; j < listed; ++j)
+            if (sh.at[j] > at) {
+                rank_w += sh.w[j];
+                ++rank_n;
+            }
+    }
+    // The listed token at which the count (by_mass: the weight) reaches `target` becomes the threshold; false: not listed.
+    __device__ bool pick(bool by_mass, uint64_t target) {
+        const int tid = static_cast<int>(threadIdx.x);
+        bool hit = false;
+        if (tid < listed) {
+            hit = by_mass ? rank_w < target && target <= rank_w + sh.w[tid] : rank_n + 1 == target;
+            if (hit) {
+                sh.thr = sh.at[tid];
+                sh.thr_sum = rank_w + sh.w[tid];
+            }
+        }
+        return __syncthreads_or(hit) != 0;
+    }
+    int listed;
+    uint64_t rank_w;
+    uint32_t rank_n;
+};
+
+template <int CS>
 __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     DrawShared &sh = *reinterpret_cast<DrawShared *>(smem_raw);
-    cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-    Tally *slices = reinterpret_cast<Tally *>(smem_raw + sizeof(DrawShared));
-    float *x = reinterpret_cast<float *>(slices + 2 * (DR_BINS / ctas));
+    float *x = reinterpret_cast<float *>(smem_raw + sizeof(DrawShared));
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / ctas;
+    const int64_t row = blockIdx.x / CS;
+    const int rank = static_cast<int>(blockIdx.x % CS);  // (the clusters are made of neighbours)
     const int lo = min(a.V, rank * a.chunk), n = min(a.V, lo + a.chunk) - lo;
     const float *from = a.logits + row * a.ld + lo;
 
+    cluster_arrive();  // that this CTA runs, and may be written to
     pdl_wait();
     pdl_launch_dependents();
+    if (tid == 0) {  // the row's settings
+        const float T = a.temperature ? a.temperature[row] : 1.0f, p = a.top_p ? a.top_p[row] : 1.0f;
+        const float low = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
+        const int k = a.top_k ? a.top_k[row] : 0;
+        sh.bad = !(T >= 0.0f && T < INFINITY) || !(p > 0.0f && p <= 1.0f) || !(low >= 0.0f && low <= 1.0f) ||
+                 !(u >= 0.0f && u < 1.0f) || k < 0;
+        // (held under 10^36: temperatures below 2^-119 count as that)
+        const double c = T > 0.0f ? fmin(1.4426950408889634 / static_cast<double>(T), 1e36) : 1.4426950408889634;
+        sh.c_hi = static_cast<float>(c);
+        sh.c_lo = static_cast<float>(c - static_cast<double>(sh.c_hi));
+        sh.k = T == 0.0f ? 1 : k >= a.V ? 0 : k;
+        sh.p = p;
+        sh.u = u;
+        sh.low_log = low > 0.0f && T > 0.0f ? static_cast<double>(T) * log(static_cast<double>(low)) : -INFINITY;
+    }
     // ---- the row's tokens of this CTA; a NaN counts as minus infinity, -0 as 0
     float top = -INFINITY;
-    auto clean = [](float v) { return v != v ? -INFINITY : v + 0.0f; };
-    const bool wide = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
-    const int n4 = wide ? n / 4 : 0;
+    auto clean = [](float v) { return fmaxf(v, -INFINITY) + 0.0f; };
+    const int n4 = (reinterpret_cast<uintptr_t>(from) & 15) == 0 ? n / 4 : 0;
     constexpr int FLY = 8;
     for (int i = tid; i < n4; i += FLY * DR_THREADS) {
         float4 v[FLY];
@@ -362,128 +486,189 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
         for (int j = 0; j < FLY; ++j)
             if (i + j * DR_THREADS < n && SD_INB(i + j * DR_THREADS < a.chunk, a.status, 125)) {
                 x[i + j * DR_THREADS] = clean(v[j]);
-                top = fmaxf(top, x[i + j * DR_THREADS]);
+                top = fmaxf(top, clean(v[j]));
             }
     }
+    if (tid < ((n + 3) / 4 * 4 - n)) x[n + tid] = -INFINITY;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sh.warp_max[warp] = top;
-    if (tid == 0) sh.list_n = 0;
+    if (lane == 0) sh.warp_f[warp] = top;
     __syncthreads();
-    if (tid < ctas)
-        for (int i = 0; i < DR_WARPS; ++i) top = fmaxf(top, sh.warp_max[i]);
-    cluster.sync();  // every CTA of the cluster runs before another writes to its shared memory
-    if (tid < ctas) *cluster.map_shared_rank(&sh.maxima[rank], tid) = top;
-    cluster.sync();
+    cluster_wait();
+    if (tid < CS) {
+        for (int i = 0; i < DR_WARPS; ++i) top = fmaxf(top, sh.warp_f[i]);
+        *cg::this_cluster().map_shared_rank(&sh.tops[rank], tid) = top;
+    }
+    cluster_arrive();
+    cluster_wait();
     float m = -INFINITY;
-    for (int c = 0; c < ctas; ++c) m = fmaxf(m, sh.maxima[c]);
+#pragma unroll
+    for (int c = 0; c < CS; ++c) m = fmaxf(m, sh.tops[c]);
+    const bool bad = sh.bad || m == -INFINITY;
+    if (m == INFINITY) {  // those tokens share everything
+        for (int i = tid; i < n; i += DR_THREADS) x[i] = x[i] == INFINITY ? 0.0f : -INFINITY;
+        m = 0.0f;
+    }
+    // the lowest logit that min-p keeps; minus infinity never is
+    if (tid == 0) sh.low = fmaxf(__double2float_ru(static_cast<double>(m) + sh.low_log), -3.402823466e38f) + 0.0f;
+    __syncthreads();
 
-    // ---- the row's settings
-    if (tid == 0) {
-        const float T = a.temperature ? a.temperature[row] : 1.0f, p = a.top_p ? a.top_p[row] : 1.0f;
-        const float low = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
-        const int k = a.top_k ? a.top_k[row] : 0;
-        sh.bad = !(T >= 0.0f && T < INFINITY) || !(p > 0.0f && p <= 1.0f) || !(low >= 0.0f && low <= 1.0f) ||
-                 !(u >= 0.0f && u < 1.0f) || k < 0 || m == -INFINITY;
-        const double c = T > 0.0f ? 1.4426950408889634 / static_cast<double>(T) : 1.4426950408889634;
-        sh.c_hi = static_cast<float>(c);
-        sh.c_lo = sh.c_hi < INFINITY ? static_cast<float>(c - static_cast<double>(sh.c_hi)) : 0.0f;
-        sh.k = T == 0.0f ? 1 : k >= a.V ? 0 : k;
-        sh.p = p;
-        sh.u = u;
-        // the lowest logit that min-p keeps; minus infinity never is
-        sh.key_low = order_key(-INFINITY) + 1;
-        if (low > 0.0f && T > 0.0f && m < INFINITY) {
-            const float at = __double2float_ru(static_cast<double>(m) + static_cast<double>(T) * log(static_cast<double>(low)));
-            sh.key_low = max(sh.key_low, order_key(at + 0.0f));
-        }
-        if (sh.bad && rank == 0) {
+    float inv = 0.0f;
+    uint64_t thr = ~uint64_t(0);
+    const float c_hi = sh.c_hi, c_lo = sh.c_lo;
+    if (bad) {
+        if (tid == 0 && rank == 0) {
             set_status(a.status, SD_EDEVICE);
             a.tokens[row] = -1;
             if (a.prob) a.prob[row] = 0.0f;
         }
-    }
-    __syncthreads();
-    const float c_hi = sh.c_hi, c_lo = sh.c_lo;
-    const bool bad = sh.bad != 0;
-    float inv = 0.0f;
-    if (!bad) {
-        const Draw w = {a, sh, x, slices, slices + DR_BINS / ctas, rank, ctas, lo, n, m};
-        // ---- the thresholds
-        uint64_t thr = static_cast<uint64_t>(sh.key_low) << 32;
-        const int k = sh.k;
-        const float p = sh.p;
-        if (k > 0 || p < 1.0f) {
-            const bool mass = p < 1.0f;
-            histogram(w, true, 0, Range{}, 0, mass, w.first);
-            uint64_t total = 0, at;
-            for (int c = 0; c < ctas; ++c) total += sh.total[0][c].w;
-            if (k > 0) {
-                select(w, false, static_cast<uint64_t>(k), mass, at, total);
-                thr = max(thr, at);
-            }
-            if (p < 1.0f) {
-                uint64_t sum;
-                select(w, true, whole_times<true>(p, total), mass, at, sum);
-                thr = max(thr, at);
+    } else {
+        Draw<CS> w = {a, sh, x, rank, lo, n, m, c_hi, c_lo, 0, 0};
+        const float p = sh.p, low = sh.low;
+        const uint32_t k = static_cast<uint32_t>(sh.k);
+        const float per_unit = 1.0f / 536870912.0f;  // 2^-29: of weights' units into those of the bins
+        uint64_t mine, before, target = 0;
+        thr = static_cast<uint64_t>(order_key(low)) << 32;
+        bool nucleus = p < 1.0f;  // top-p still to be done
+        Found f;
+        Range r = w.whole();
+        if (k > 0) {
+            w.template histogram<true, false>(0, r, DR_SHIFT, false);
+            f = w.locate(true, 0, r, DR_SHIFT, false, k, 0.0f);
+            const bool all = f.before_n + f.n <= DR_LIST;  // the list holds all that may be kept
+            r = all ? w.whole() : w.template narrow<false>(f, false, k, 0.0f);
+            if (all && f.bin < DR_BINS - 1) r.hi[0] = DR_FIRST + ((f.bin + 1) << DR_SHIFT) - 1;
+            mine = w.template pass<true>(r, low, before);
+            w.ranks(before, all ? 0 : f.before_n);
+            w.pick(false, k);
+            thr = max(thr, sh.thr);
+            target = whole_times<true>(p, sh.thr_sum);
+            if (all && nucleus) {
+                __syncthreads();
+                w.pick(true, target);
+                thr = max(thr, sh.thr);
+                nucleus = false;
             }
         }
-        // ---- the kept tokens' weights, over their logits; a thread sums neighbours (an odd number: no bank conflicts)
-        const int per = ((n + DR_THREADS - 1) / DR_THREADS) | 1, i0 = min(n, tid * per), i1 = min(n, i0 + per);
-        uint64_t mine = 0;
-        for (int i = i0; i < i1; ++i) {
-            const float l = x[i];
-            const uint64_t at = static_cast<uint64_t>(order_key(l)) << 32 | (0xffffffffu - static_cast<uint32_t>(lo + i));
-            const float e = at >= thr ? weight_of(l, m, c_hi, c_lo) : 0.0f;
-            x[i] = e;
-            mine += units(e);
-        }
-        uint64_t inc = mine;
+        if (nucleus) {
+            r = w.whole();
+            w.template histogram<true, true>(0, r, DR_SHIFT, k == 0);
+            if (k == 0) {
+                uint64_t total = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+                for (int c = 0; c < CS; ++c) total += sh.sums[c];
+                target = whole_times<true>(p, total);
+            }
+            const float about = static_cast<float>(target) * per_unit;
+            f = w.locate(true, 0, r, DR_SHIFT, true, 0, about);
+            r = w.template narrow<true>(f, true, 0, about);
+            for (;;) {
+                mine = w.template pass<true>(r, low, before);
+                w.ranks(before, f.before_n);
+                if (w.pick(true, target)) break;
+                // the threshold is before the range or behind it: on with the next token there, by counts
+                const uint32_t next = target <= before ? f.before_n : f.before_n + f.n + 1;
+                if (next < 1 || next > static_cast<uint32_t>(a.V)) break;  // (never: the weights of all reach the target)
+                r = w.whole();
+                w.template histogram<true, false>(0, r, DR_SHIFT, false);
+                f = w.locate(true, 0, r, DR_SHIFT, false, next, 0.0f);
+                r = w.template narrow<false>(f, false, next, 0.0f);
+            }
+            thr = max(thr, sh.thr);
+        } else if (k == 0) {
+            mine = w.template pass<false>(r, low, before);
+        }
+        // ---- the draw: the listed tokens that are kept join their CTAs' sums
+        // (what the listed tokens add to the threads' sums: where the histograms were, which nobody reads any more)
+        uint64_t *extra = reinterpret_cast<uint64_t *>(sh.bin_n);
+        static_assert(sizeof(sh.bin_n) >= DR_THREADS * 8, "a sum per thread");
+        __syncthreads();
+        extra[tid] = 0;
+        const uint64_t at = tid < w.listed ? sh.at[tid] : 0;
+        const bool kept = tid < w.listed && at >= thr;
+        __syncthreads();
+        if (kept) {
+            const int idx = place_idx(at);
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sh.cta_sum[CS == 1 ? 0 : idx / a.chunk]), sh.w[tid]);
+            if (idx >= lo && idx < lo + n)
+                atomicAdd(reinterpret_cast<unsigned long long *>(&extra[(idx - lo) / w.per()]), sh.w[tid]);
         }
         __syncthreads();
-        if (lane == 31) sh.warp_w[warp] = inc;
-        __syncthreads();
-        uint64_t at = inc - mine, all = 0;
-        for (int i = 0; i < DR_WARPS; ++i) {
-            if (i < warp) at += sh.warp_w[i];
-            all += sh.warp_w[i];
+        uint64_t total = 0, base = 0;
+#pragma unroll
+        for (int c = 0; c < CS; ++c) {
+            if (c == rank) base = total;
+            total += sh.cta_sum[c];
         }
-        if (tid < ctas) *cluster.map_shared_rank(&sh.sums[rank], tid) = all;
-        cluster.sync();
-        uint64_t total = 0;
-        for (int c = 0; c < ctas; ++c) {
-            if (c < rank) at += sh.sums[c];
-            total += sh.sums[c];
-        }
-        // ---- the draw
         const uint64_t want = whole_times<false>(sh.u, total);  // (under the total: u < 1)
         inv = DR_UNIT / static_cast<float>(total);
-        if (at <= want && want < at + mine) {
-            int i = i0;
-            for (; i < i1; ++i) {
-                at += units(x[i]);
-                if (at > want) break;
+        if (base <= want && want < base + sh.cta_sum[rank]) {
+            mine += extra[tid];
+            const uint64_t inc = warp_scan(mine);
+            if (lane == 31) sh.part[warp] = inc;
+            __syncthreads();
+            const uint64_t pw = warp_scan(lane < DR_WARPS ? sh.part[lane] : uint64_t(0));
+            uint64_t start = base + inc - mine;
+            const uint64_t ahead = __shfl_sync(0xffffffffu, pw, max(warp - 1, 0));
+            if (warp > 0) start += ahead;
+            // the warp of the thread whose tokens the draw falls on goes through them
+            const uint32_t who = __ballot_sync(0xffffffffu, start <= want && want < start + mine);
+            if (who) {
+                const int owner = __ffs(who) - 1, i0 = min(n, (32 * warp + owner) * w.per()), i1 = min(n, i0 + w.per());
+                uint64_t run = __shfl_sync(0xffffffffu, start, owner);
+                for (int i = i0 + lane; i - lane < i1; i += 32) {
+                    float e = 0.0f;
+                    if (i < i1 && place_of(x[i], lo + i) >= thr) e = weight_of(x[i], m, c_hi, c_lo);
+                    const uint64_t here = run + warp_scan(units(e));
+                    const uint32_t over = __ballot_sync(0xffffffffu, here > want);
+                    if (over) {
+                        if (lane == __ffs(over) - 1) {
+                            a.tokens[row] = lo + i;
+                            if (a.prob) a.prob[row] = e * inv;
+                        }
+                        break;
+                    }
+                    run = __shfl_sync(0xffffffffu, here, 31);
+                }
             }
-            a.tokens[row] = lo + i;
-            if (a.prob) a.prob[row] = x[i] * inv;
         }
     }
     if (a.probs) {
-        __syncthreads();
         float *to = a.probs + row * a.ldp + lo;
+        const float tl = key_logit(static_cast<uint32_t>(thr >> 32));
+        const int ti = place_idx(thr);  // (the last index where all of that logit are kept)
+        auto prob = [&](int i) {
+            const float l = x[i];
+            const bool in = !bad && (l > tl || (l == tl && (lo + i <= ti || ti < 0)));
+            return in ? weight_of(l, m, c_hi, c_lo) * inv : 0.0f;
+        };
         const int m4 = (reinterpret_cast<uintptr_t>(to) & 15) == 0 ? n / 4 : 0;
-        for (int i = tid; i < m4; i += DR_THREADS) {
-            const float4 e = reinterpret_cast<const float4 *>(x)[i];
-            __stcs(reinterpret_cast<float4 *>(to) + i,
-                   bad ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(e.x * inv, e.y * inv, e.z * inv, e.w * inv));
-        }
-        for (int i = 4 * m4 + tid; i < n; i += DR_THREADS) to[i] = bad ? 0.0f : x[i] * inv;
+        for (int i = tid; i < m4; i += DR_THREADS)
+            __stcs(reinterpret_cast<float4 *>(to) + i, make_float4(prob(4 * i), prob(4 * i + 1), prob(4 * i + 2), prob(4 * i + 3)));
+        for (int i = 4 * m4 + tid; i < n; i += DR_THREADS) to[i] = prob(i);
     }
-    cluster.sync();  // no CTA leaves while another may read its shared memory
+    cluster_arrive();  // no CTA leaves while another may read its shared memory
+    cluster_wait();
+}
+
+template <int CS>
+static cudaError_t sample_launch(const DrawArgs &a, int N, cudaStream_t s) {
+    const cudaError_t e = allow_max_dynamic_smem(sample_kernel<CS>);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(N) * CS);
+    cfg.blockDim = dim3(DR_THREADS);
+    cfg.dynamicSmemBytes = sizeof(DrawShared) + static_cast<size_t>(a.chunk) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CS;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, sample_kernel<CS>, a);
 }
 
 }  // namespace sdv
@@ -519,22 +704,12 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     a.probs = out_probs;
     a.ldp = ld_probs;
     a.status = status;
-    if (allow_max_dynamic_smem(sample_kernel) != cudaSuccess) return SD_ECUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(N) * ctas);
-    cfg.blockDim = dim3(DR_THREADS);
-    cfg.dynamicSmemBytes = sizeof(DrawShared) + 2 * static_cast<size_t>(DR_BINS / ctas) * sizeof(Tally) +
-                           static_cast<size_t>(a.chunk) * 4;
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel, a) == cudaSuccess ? SD_OK : SD_ECUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = ctas == 1   ? sample_launch<1>(a, N, s)
+                          : ctas == 2 ? sample_launch<2>(a, N, s)
+                          : ctas == 4 ? sample_launch<4>(a, N, s)
+                                      : sample_launch<8>(a, N, s);
+    return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
 }  // extern "C"

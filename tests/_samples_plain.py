@@ -46,9 +46,9 @@ def turn(x, pos, freq, scale, interleaved):
     return y, tol
 
 
-# A weight is off by at most 8 u of itself (its exponent is held in two floats; eight fused steps of the series, of which the
-# last one and the scaling round at the result's size: 4 u; twice that to be sure) and by half a unit of 2^-44; a sum of
-# weights by as much.
+# A weight is off by at most 8 u of itself (the exponent is held in two floats, whose second adds under 2^-44 of it; ex2.approx is
+# good to 2^-22 = 4 u, the factor for the second float and the product round once each, u; twice that u for what the second
+# float's own terms round) and by half a unit of 2^-44; a sum of weights by as much.
 WEIGHT = 8 * U
 UNIT = 2.0 ** -45
 
