@@ -17,6 +17,8 @@
 // Every exchange is one cluster barrier: three for a listed row, three or four for others, and one at each end.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "sdv_common.cuh"
 
 namespace cg = cooperative_groups;
@@ -63,27 +65,27 @@ struct Range {
     uint32_t lo[3], hi[3];
 };
 
-// what a search of a histogram gives: the bin, the tokens before it and in it
+// what a histogram says of the bin that was looked for: the tokens before it and in it (a search by counts), or about the
+// weight before it and the least number of tokens that its weight takes (a search by weights)
 struct Found {
     uint32_t bin, before_n, n;
-    float before_m;  // about the weight before it, in units of 2^-15
+    float before_m, target_m;  // in units of 2^-15
 };
 
-// What a pass over the tokens tells of a CTA: the sums of all weights before the range and of the kept ones, and how many
-// tokens it listed.
+// What a pass over the tokens tells of a CTA: the sums of all weights, of those before the range and of the kept ones, and
+// how many tokens are in the range.
 struct Passed {
-    uint64_t before, kept;
+    uint64_t all, before, kept;
     uint32_t n;
 };
 
 struct alignas(16) DrawShared {
     // ---- read or written by the cluster's other CTAs (what they write has two turns: a slow CTA still reads one)
-    uint32_t bin_n[2][DR_BINS], bin_m[2][DR_BINS];  // a level's histogram
-    uint2 coarse[2][DR_MOST_CTAS][DR_COARSE];       // every CTA's: tokens, weight (a float's bits)
-    uint64_t list[2][DR_LIST];                      // this CTA's tokens in a pass's range
-    Passed passed[2][DR_MOST_CTAS];                 // every CTA's
-    uint64_t sums[DR_MOST_CTAS];                    // every CTA's sum of all weights
-    float tops[DR_MOST_CTAS];                       // and largest logit
+    uint32_t bins[2][DR_BINS];                   // a level's histogram: tokens, or weights in units of 2^-15
+    uint32_t coarse[2][DR_MOST_CTAS][DR_COARSE];  // every CTA's: tokens, or weights (floats' bits)
+    uint64_t list[2][DR_LIST];                   // this CTA's tokens in a pass's range
+    Passed passed[2][DR_MOST_CTAS];              // every CTA's
+    float tops[DR_MOST_CTAS];                    // every CTA's largest logit
     // ---- of this CTA alone
     uint64_t at[DR_LIST], w[DR_LIST];  // the cluster's list
     uint64_t cta_sum[DR_MOST_CTAS];
@@ -103,36 +105,44 @@ __device__ __forceinline__ float ex2_approx(float x) {  // 2^x to about 2^-22, 0
     return y;
 }
 
-// exp((l - m) / T): the difference and its product with c = log2(e) / T in two floats each, so that a far token's weight is
-// as good as a near one's; nothing below 2^-60
+// exp((l - m) / T) of two tokens: the difference and its product with c = log2(e) / T in two floats each, so that a far
+// token's weight is as good as a near one's; nothing below 2^-60
+__device__ __forceinline__ float2 weights_of(float2 l, float m, float c_hi, float c_lo) {
+    const float2 one = make_float2(-1.0f, -1.0f), c = make_float2(c_hi, c_hi);
+    const float2 s = fadd2_rn(l, make_float2(-m, -m)), bb = ffma2_rn(l, one, s);
+    const float2 left = fadd2_rn(ffma2_rn(ffma2_rn(bb, one, s), one, l), ffma2_rn(bb, one, make_float2(-m, -m)));
+    const float2 down = fmul2_rn(s, make_float2(-c_hi, -c_hi));
+    const float2 xl = ffma2_rn(left, c, ffma2_rn(s, make_float2(c_lo, c_lo), ffma2_rn(s, c, down)));
+    const float2 g = ffma2_rn(xl, make_float2(0.693147182f, 0.693147182f), make_float2(1.0f, 1.0f));
+    const float2 e = fmul2_rn(make_float2(ex2_approx(-down.x), ex2_approx(-down.y)), g);
+    return make_float2(down.x < 60.0f ? e.x : 0.0f, down.y < 60.0f ? e.y : 0.0f);
+}
 __device__ __forceinline__ float weight_of(float l, float m, float c_hi, float c_lo) {
-    const float s = l - m, xh = s * c_hi;
-    const float bb = s - l, left = (l - (s - bb)) + (-m - bb);
-    const float xl = fmaf(s, c_hi, -xh) + fmaf(s, c_lo, left * c_hi);
-    const float e = ex2_approx(xh) * fmaf(xl, 0.693147182f, 1.0f);
-    return xh > -60.0f ? e : 0.0f;
+    return weights_of(make_float2(l, l), m, c_hi, c_lo).x;
 }
 
 // Weights as whole numbers of 2^-44, summed in two words: adding 4 leaves the multiples of 2^-21 in the bits, adding
-// 1.5 * 2^-21 to the rest those of 2^-44 (under 2^22 of them, either sign).
+// 1.5 * 2^-21 to the rest those of 2^-44 (under 2^22 of them, either sign).  What is added twice per weight comes off at
+// the end.
 struct Units {
-    uint32_t hi, lo, n;
-    __device__ __forceinline__ void add(float e) {
-        const float t = e + 4.0f, r = (e - (t - 4.0f)) + 7.152557373046875e-07f;
-        hi += __float_as_uint(t);
-        lo += __float_as_uint(r);
-        ++n;
+    uint32_t hi, lo;
+    __device__ __forceinline__ void add(float2 e) {
+        const float2 t = fadd2_rn(e, make_float2(4.0f, 4.0f));
+        const float2 r = ffma2_rn(fadd2_rn(t, make_float2(-4.0f, -4.0f)), make_float2(-1.0f, -1.0f), e);
+        const float2 q = fadd2_rn(r, make_float2(7.152557373046875e-07f, 7.152557373046875e-07f));
+        hi += __float_as_uint(t.x) + __float_as_uint(t.y);
+        lo += __float_as_uint(q.x) + __float_as_uint(q.y);
     }
-    __device__ __forceinline__ uint64_t sum() const {  // of at most 512 weights
+    __device__ __forceinline__ uint64_t sum(uint32_t n) const {  // n weights were added, at most 512
         const uint32_t h = hi - n * 0x40800000u;
         const int32_t l = static_cast<int32_t>(lo - n * 0x35400000u);
         return (static_cast<uint64_t>(h) << 23) + static_cast<uint64_t>(static_cast<int64_t>(l));
     }
 };
 __device__ __forceinline__ uint64_t units(float e) {
-    Units u = {0, 0, 0};
-    u.add(e);
-    return u.sum();
+    Units u = {0, 0};
+    u.add(make_float2(e, 0.0f));
+    return u.sum(2);
 }
 constexpr float DR_UNIT = 17592186044416.0f;  // 2^44
 
@@ -176,6 +186,13 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *part) {
     return warp_sum((threadIdx.x & 31) < DR_WARPS ? part[threadIdx.x & 31] : uint64_t(0));
 }
 
+// A search for a threshold so far: the range, the phase that cuts it next, and what the last histogram said.
+struct Search {
+    Range r;
+    int phase;
+    Found f;
+};
+
 // What one CTA of a row's cluster of CS works with.
 template <int CS>
 struct Draw {
@@ -196,9 +213,8 @@ struct Draw {
         if (phase == 0) return __float_as_uint(fabsf(l - m));
         return phase == 1 ? ~order_key(l) : static_cast<uint32_t>(idx);
     }
-    // -1: before the range, 0: in it, 1: behind
-    __device__ __forceinline__ int side(const Range &r, float l, int idx) const {
-        const uint32_t d = value(0, l, idx);
+    // -1: before the range, 0: in it, 1: behind (d: the bits of its distance)
+    __device__ __forceinline__ int side(const Range &r, uint32_t d, float l, int idx) const {
         if (d < r.lo[0]) return -1;
         if (d > r.hi[0]) return 1;
         const uint32_t k = value(1, l, idx), i = static_cast<uint32_t>(idx);
@@ -212,104 +228,100 @@ struct Draw {
         return __uint_as_float(phase == 0 ? r.lo[0] + (bin << shift) : r.lo[0]);
     }
 
-    // A level: the tokens of the range (first: all) counted and weighed by bins.  Ends with the exchange.
+    // A level: the tokens of the range (FIRST: all) counted, or weighed, by bins.  Ends with the exchange.
     template <bool FIRST, bool MASS>
-    __device__ void histogram(int phase, const Range &r, int shift, bool total) {
+    __device__ void histogram(int phase, const Range &r, int shift) {
         const int tid = static_cast<int>(threadIdx.x), b = level & 1;
-        for (int i = tid; i < DR_BINS; i += DR_THREADS) sh.bin_n[b][i] = sh.bin_m[b][i] = 0;
+        uint32_t *bins = sh.bins[b];
+        for (int i = tid; i < DR_BINS; i += DR_THREADS) bins[i] = 0;
         __syncthreads();
-        Units all = {0, 0, 0};
         for (int i = 4 * tid; i < n; i += 4 * DR_THREADS) {
             const float4 v = *reinterpret_cast<const float4 *>(x + i);
             const float l[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                const uint32_t d = value(0, l[j], 0);
                 uint32_t bin;
                 float from = 0.0f;
                 if constexpr (FIRST) {
-                    const int32_t d = static_cast<int32_t>(value(0, l[j], 0));
-                    bin = static_cast<uint32_t>(min(max((d - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT, 0), DR_BINS - 1));
-                    if constexpr (MASS)
-                        from = __uint_as_float(min(static_cast<uint32_t>(d) & (0xffffffffu << DR_SHIFT),
-                                                   DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT)));
-                    if (MASS && bin == 0) from = 0.0f;
+                    const int32_t y = (static_cast<int32_t>(d) - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT;
+                    bin = static_cast<uint32_t>(min(max(y, 0), DR_BINS - 1));
+                    if constexpr (MASS) {
+                        from = __uint_as_float(min(d & (0xffffffffu << DR_SHIFT), DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT)));
+                        if (y <= 0) from = 0.0f;
+                    }
                 } else {
-                    if (side(r, l[j], lo + i + j) != 0) continue;
+                    if (d < r.lo[0] || d > r.hi[0] || side(r, d, l[j], lo + i + j) != 0) continue;
                     bin = (value(phase, l[j], lo + i + j) - r.lo[phase]) >> shift;
                     if constexpr (MASS) from = edge(false, phase, r, shift, bin);
                 }
                 if (!SD_INB(bin < DR_BINS && i + 3 < a.chunk, a.status, 123)) continue;  // site 123: bin
-                atomicAdd(&sh.bin_n[b][bin], 1u);
-                if constexpr (MASS) {  // its weight as a part of the bin's first, in units of 2^-15
-                    const float part = ex2_approx((from - fabsf(l[j] - m)) * c_hi);
-                    atomicAdd(&sh.bin_m[b][bin], __float_as_uint(part + 256.0f) - 0x43800000u);
-                    if (FIRST && total) all.add(weight_of(l[j], m, c_hi, c_lo));
+                if constexpr (MASS) {  // its weight as a part of the bin's first
+                    const float part = ex2_approx((from - __uint_as_float(d)) * c_hi);
+                    atomicAdd(&bins[bin], __float_as_uint(part + 256.0f) - 0x43800000u);
+                } else {
+                    atomicAdd(&bins[bin], 1u);
                 }
             }
         }
-        if (FIRST && MASS && total) {
-            const uint64_t s = block_sum(all.sum(), sh.part);
-            if (tid < CS) *of(&sh.sums[rank], tid) = s;
-        }
         __syncthreads();
-        // 16 threads per coarse bin
-        {
+        {  // 16 threads per coarse bin; every CTA gets them
             uint32_t cn = 0;
             float cm = 0.0f;
 #pragma unroll
             for (int j = 0; j < DR_BINS / DR_THREADS; ++j) {
                 const uint32_t bin = DR_BINS / DR_THREADS * tid + j;
-                cn += sh.bin_n[b][bin];
-                if constexpr (MASS)
-                    cm += static_cast<float>(sh.bin_m[b][bin]) * ex2_approx(-c_hi * edge(FIRST, phase, r, shift, bin));
+                if constexpr (MASS) cm += static_cast<float>(bins[bin]) * ex2_approx(-c_hi * edge(FIRST, phase, r, shift, bin));
+                else cn += bins[bin];
             }
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) {
-                cn += __shfl_xor_sync(0xffffffffu, cn, o);
-                cm += __shfl_xor_sync(0xffffffffu, cm, o);
+                if constexpr (MASS) cm += __shfl_xor_sync(0xffffffffu, cm, o);
+                else cn += __shfl_xor_sync(0xffffffffu, cn, o);
             }
-            if ((tid & 15) < CS) *of(&sh.coarse[b][rank][tid >> 4], tid & 15) = make_uint2(cn, __float_as_uint(cm));
+            if ((tid & 15) < CS) *of(&sh.coarse[b][rank][tid >> 4], tid & 15) = MASS ? __float_as_uint(cm) : cn;
         }
         cluster_arrive();
         cluster_wait();
         ++level;
     }
 
-    // The bin of the last level with the token that brings the count (by_mass: about the weight) to `target`, from the
-    // CTAs' 32 coarse bins and the 32 bins of one of them.  Every CTA finds the same.
-    __device__ Found locate(bool first, int phase, const Range &r, int shift, bool by_mass, uint32_t target_n, float target_m) {
+    // The bin of the last level with the token that brings the count (MASS: about the weight; a share of the whole level's
+    // where target_m is under 0) to the target, from the CTAs' 32 coarse bins and the 32 bins of one of them.  Every CTA
+    // finds the same.
+    template <bool MASS>
+    __device__ Found locate(bool first, int phase, const Range &r, int shift, uint32_t target_n, float target_m) {
         const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, b = (level - 1) & 1;
         if (tid < 32) {
-            uint32_t cn = 0;
-            float cm = 0.0f;
+            using Sum = typename std::conditional<MASS, float, uint32_t>::type;
+            Sum cs = 0;
 #pragma unroll
             for (int c = 0; c < CS; ++c) {
-                const uint2 y = sh.coarse[b][c][lane];
-                cn += y.x;
-                cm += __uint_as_float(y.y);
+                const uint32_t y = sh.coarse[b][c][lane];
+                if constexpr (MASS) cs += __uint_as_float(y);
+                else cs += y;
             }
-            const uint32_t in = warp_scan(cn);
-            const float im = warp_scan(cm);
-            // (rounded sums may fall short of their own total: the last bin that has tokens, then)
-            const uint32_t there = __ballot_sync(0xffffffffu, cn > 0);
-            const uint32_t at = __ballot_sync(0xffffffffu, cn > 0 && (by_mass ? im >= target_m : in >= target_n));
-            const int q = at ? __ffs(at) - 1 : 31 - __clz(there);
-            const uint32_t bn = __shfl_sync(0xffffffffu, in - cn, q);
-            const float bm = __shfl_sync(0xffffffffu, im - cm, q);
+            const Sum in = warp_scan(cs);
+            Sum target;
+            if constexpr (MASS) target = target_m < 0.0f ? -target_m * __shfl_sync(0xffffffffu, in, 31) : target_m;
+            else target = target_n;
+            // (rounded sums may fall short of their own total: the last bin that has any, then)
+            const uint32_t there = __ballot_sync(0xffffffffu, cs > 0), at = __ballot_sync(0xffffffffu, cs > 0 && in >= target);
+            const int q = at ? __ffs(at) - 1 : there ? 31 - __clz(there) : 0;
+            const Sum before = __shfl_sync(0xffffffffu, in - cs, q);
             const int bin = 32 * q + lane;
-            uint32_t fn = 0;
-            uint64_t fm = 0;
+            uint64_t raw = 0;
 #pragma unroll
-            for (int c = 0; c < CS; ++c) {
-                fn += *of(&sh.bin_n[b][bin], c);
-                fm += *of(&sh.bin_m[b][bin], c);
+            for (int c = 0; c < CS; ++c) raw += *of(&sh.bins[b][bin], c);
+            Sum fs;
+            if constexpr (MASS) fs = static_cast<float>(raw) * ex2_approx(-c_hi * edge(first, phase, r, shift, bin));
+            else fs = static_cast<uint32_t>(raw);
+            const Sum upto = before + warp_scan(fs);
+            const uint32_t some = __ballot_sync(0xffffffffu, fs > 0), hits = __ballot_sync(0xffffffffu, fs > 0 && upto >= target);
+            if (lane == (hits ? __ffs(hits) - 1 : some ? 31 - __clz(some) : 0)) {
+                if constexpr (MASS) sh.found = {static_cast<uint32_t>(bin), 0, static_cast<uint32_t>(raw >> 15), upto - fs, target};
+                else sh.found = {static_cast<uint32_t>(bin), upto - fs, fs, 0.0f, 0.0f};
             }
-            const float mf = static_cast<float>(fm) * ex2_approx(-c_hi * edge(first, phase, r, shift, bin));
-            const uint32_t sn = bn + warp_scan(fn);
-            const float sm = bm + warp_scan(mf);
-            const uint32_t hits = __ballot_sync(0xffffffffu, fn > 0 && (by_mass ? sm >= target_m : sn >= target_n));
-            const uint32_t some = __ballot_sync(0xffffffffu, fn > 0);
-            if (lane == (hits ? __ffs(hits) - 1 : 31 - __clz(some))) sh.found = {static_cast<uint32_t>(bin), sn - fn, fn, sm - mf};
         }
         __syncthreads();
         const Found f = sh.found;
@@ -317,26 +329,6 @@ struct Draw {
         return f;
     }
 
-    // From a bin of the first level to a range of at most DR_LIST tokens, which has the token at the count (by_mass: about
-    // the weight) `target`; f: the tokens before the range and in it.
-    template <bool MASS>
-    __device__ Range narrow(Found &f, bool by_mass, uint32_t target_n, float target_m) {
-        Range r = whole();
-        if (f.bin > 0) r.lo[0] = DR_FIRST + (f.bin << DR_SHIFT);
-        if (f.bin < DR_BINS - 1) r.hi[0] = DR_FIRST + ((f.bin + 1) << DR_SHIFT) - 1;
-        int phase = 0;
-        while (f.n > DR_LIST) {
-            while (phase < 2 && r.lo[phase] == r.hi[phase]) ++phase;
-            const int shift = max(0, 32 - __clz(r.hi[phase] - r.lo[phase]) - DR_BITS);
-            histogram<false, MASS>(phase, r, shift, false);
-            const Found g = locate(false, phase, r, shift, by_mass, target_n - f.before_n, target_m - f.before_m);
-            f = {g.bin, f.before_n + g.before_n, g.n, f.before_m + g.before_m};
-            const uint32_t at = r.lo[phase] + (g.bin << shift);
-            r.lo[phase] = at;
-            r.hi[phase] = min(r.hi[phase], at + ((1u << shift) - 1u));
-        }
-        return r;
-    }
     __device__ Range whole() const {
         Range r;
         for (int i = 0; i < 3; ++i) {
@@ -345,57 +337,123 @@ struct Draw {
         }
         return r;
     }
+    // the first level and its bin's range
+    template <bool MASS>
+    __device__ Search start(uint32_t target_n, float target_m) {
+        Search q = {whole(), 0, {}};
+        histogram<true, MASS>(0, q.r, DR_SHIFT);
+        q.f = locate<MASS>(true, 0, q.r, DR_SHIFT, target_n, target_m);
+        if (q.f.bin > 0) q.r.lo[0] = DR_FIRST + (q.f.bin << DR_SHIFT);
+        if (q.f.bin < DR_BINS - 1) q.r.hi[0] = DR_FIRST + ((q.f.bin + 1) << DR_SHIFT) - 1;
+        return q;
+    }
+    // one level more
+    template <bool MASS>
+    __device__ void refine(Search &q, uint32_t target_n, float target_m) {
+        while (q.phase < 2 && q.r.lo[q.phase] == q.r.hi[q.phase]) ++q.phase;
+        const int phase = q.phase, shift = max(0, 32 - __clz(q.r.hi[phase] - q.r.lo[phase]) - DR_BITS);
+        histogram<false, MASS>(phase, q.r, shift);
+        const Found g = locate<MASS>(false, phase, q.r, shift, target_n - q.f.before_n, fmaxf(target_m - q.f.before_m, 0.0f));
+        q.f = {g.bin, q.f.before_n + g.before_n, g.n, q.f.before_m + g.before_m, target_m};
+        const uint32_t at = q.r.lo[phase] + (g.bin << shift);
+        q.r.hi[phase] = min(q.r.hi[phase], at + ((1u << shift) - 1u));
+        q.r.lo[phase] = at;
+    }
+    // by counts, to a range of at most DR_LIST tokens
+    __device__ Search search_count(uint32_t target) {
+        Search q = start<false>(target, 0.0f);
+        while (q.f.n > DR_LIST) refine<false>(q, target, 0.0f);
+        return q;
+    }
 
     // A thread's tokens in the passes and the draw: neighbours, an odd number (no bank conflicts).
     __device__ __forceinline__ int per() const { return ((n + DR_THREADS - 1) / DR_THREADS) | 1; }
 
-    // A pass over the tokens (RANGED; else all count as before): the sum of all weights before the range in every CTA, of
-    // those from `low` on each CTA's in sh.cta_sum and this thread's as the result, and the range's tokens in sh.at, sh.w (listed
-    // of them, the places of the others behind the order's end).
-    template <bool RANGED>
-    __device__ uint64_t pass(const Range &r, float low, uint64_t &before) {
-        const int tid = static_cast<int>(threadIdx.x), q = turn++ & 1;
+    // A pass over the tokens: the sum of the weights before the range (not RANGED: of logits from `low` on) in every CTA, and
+    // with TOTAL of all; of the kept ones (those before; with LOW only from `low` on) each CTA's in sh.cta_sum and this
+    // thread's as the result; the range's tokens in sh.at, sh.w (`listed` of them), false in `fits` if they are too many.
+    template <bool RANGED, bool TOTAL, bool LOW>
+    __device__ uint64_t pass(const Range &r, float low, uint64_t &before, uint64_t &all) {
+        const int tid = static_cast<int>(threadIdx.x), t = turn++ & 1;
         if (tid == 0) sh.listed = 0;
         __syncthreads();
         const int i0 = min(n, tid * per()), i1 = min(n, i0 + per());
-        Units all = {0, 0, 0}, kept = {0, 0, 0};
-#pragma unroll 4
-        for (int i = i0; i < i1; ++i) {
-            const float l = x[i];
-            const int s = RANGED ? side(r, l, lo + i) : -1;
-            if (s < 0) {
-                const float e = weight_of(l, m, c_hi, c_lo);
-                all.add(e);
-                if (l >= low) kept.add(e);
-            } else if (s == 0) {
-                const uint32_t slot = atomicAdd(&sh.listed, 1u);
-                if (slot < DR_LIST && SD_INB(slot < DR_LIST, a.status, 124)) sh.list[q][slot] = place_of(l, lo + i);  // site 124: listed token
+        Units sa = {0, 0}, sb = {0, 0}, sk = {0, 0};
+        uint32_t added = 0;
+#pragma unroll 2
+        for (int i = i0; i < i1; i += 2) {  // (a last token alone is joined by one of no weight)
+            const bool two = i + 1 < i1;
+            const float2 l = make_float2(x[i], two ? x[i + 1] : -INFINITY);
+            bool b0, b1;
+            if constexpr (RANGED) {
+                const uint32_t d0 = value(0, l.x, 0), d1 = value(0, l.y, 0);
+                int s0 = d0 < r.lo[0] ? -1 : 1, s1 = d1 < r.lo[0] ? -1 : 1;
+                if (d0 >= r.lo[0] && d0 <= r.hi[0]) s0 = side(r, d0, l.x, lo + i);
+                if (d1 >= r.lo[0] && d1 <= r.hi[0] && two) s1 = side(r, d1, l.y, lo + i + 1);
+                if (s0 == 0) list(t, l.x, lo + i);
+                if (s1 == 0) list(t, l.y, lo + i + 1);
+                b0 = s0 < 0;
+                b1 = s1 < 0;
+            } else {
+                b0 = l.x >= low;
+                b1 = l.y >= low;
             }
+            if (!TOTAL && !(b0 || b1)) continue;
+            const float2 e = weights_of(l, m, c_hi, c_lo);
+            const float2 eb = make_float2(b0 ? e.x : 0.0f, b1 ? e.y : 0.0f);
+            if constexpr (TOTAL) sa.add(e);
+            sb.add(eb);
+            if constexpr (LOW) sk.add(make_float2(l.x >= low ? eb.x : 0.0f, l.y >= low ? eb.y : 0.0f));
+            added += 2;
         }
-        const uint64_t mine = kept.sum();
-        const uint64_t b = block_sum(all.sum(), sh.part), k = block_sum(mine, sh.part);
-        if (tid < CS) *of(&sh.passed[q][rank], tid) = Passed{b, k, min(sh.listed, static_cast<uint32_t>(DR_LIST))};
+        const uint64_t mb = sb.sum(added), mine = LOW ? sk.sum(added) : mb;
+        Passed p;
+        p.all = TOTAL ? block_sum(sa.sum(added), sh.part) : 0;
+        p.before = block_sum(mb, sh.part);
+        p.kept = LOW ? block_sum(mine, sh.part) : p.before;
+        p.n = sh.listed;
+        if (tid < CS) *of(&sh.passed[t][rank], tid) = p;
         cluster_arrive();
         cluster_wait();
-        before = 0;
-        if (tid < CS) sh.cta_sum[tid] = sh.passed[q][tid].kept;
+        before = all = 0;
+        if (tid < CS) sh.cta_sum[tid] = sh.passed[t][tid].kept;
         uint32_t from = 0;
         const uint64_t *src = nullptr;
 #pragma unroll
         for (int c = 0; c < CS; ++c) {
-            const uint32_t nc = sh.passed[q][c].n;
-            before += sh.passed[q][c].before;
-            if (RANGED && tid >= static_cast<int>(from) && tid < static_cast<int>(from + nc)) src = of(&sh.list[q][tid - from], c);
+            const uint32_t nc = sh.passed[t][c].n;
+            before += sh.passed[t][c].before;
+            if (TOTAL) all += sh.passed[t][c].all;
+            if (RANGED && static_cast<uint32_t>(tid) >= from && static_cast<uint32_t>(tid) - from < nc && tid < DR_LIST)
+                src = of(&sh.list[t][tid - from], c);
             from += nc;
         }
+        fits = from <= DR_LIST;
+        listed = fits ? static_cast<int>(from) : 0;
         if (RANGED && tid < DR_LIST) {
-            const uint64_t p = src ? *src : 0;
-            sh.at[tid] = p;
-            sh.w[tid] = src ? units(weight_of(key_logit(static_cast<uint32_t>(p >> 32)), m, c_hi, c_lo)) : 0;
+            const uint64_t at = src && fits ? *src : 0;
+            sh.at[tid] = at;
+            sh.w[tid] = src && fits ? units(weight_of(key_logit(static_cast<uint32_t>(at >> 32)), m, c_hi, c_lo)) : 0;
         }
         __syncthreads();
-        listed = RANGED ? static_cast<int>(min(from, static_cast<uint32_t>(DR_LIST))) : 0;
         return mine;
+    }
+    __device__ __forceinline__ void list(int t, float l, int idx) {
+        const uint32_t slot = atomicAdd(&sh.listed, 1u);
+        if (slot < DR_LIST && SD_INB(slot < DR_LIST, a.status, 124)) sh.list[t][slot] = place_of(l, idx);  // site 124: listed token
+    }
+    // how many tokens are before a range, in every CTA
+    __device__ uint32_t count_before(const Range &r) {
+        const int tid = static_cast<int>(threadIdx.x), t = turn++ & 1;
+        uint64_t mine = 0;
+        for (int i = tid; i < n; i += DR_THREADS) mine += side(r, value(0, x[i], 0), x[i], lo + i) < 0 ? 1 : 0;
+        const Passed p = {0, block_sum(mine, sh.part), 0, 0};
+        if (tid < CS) *of(&sh.passed[t][rank], tid) = p;
+        cluster_arrive();
+        cluster_wait();
+        uint32_t sum = 0;
+        for (int c = 0; c < CS; ++c) sum += static_cast<uint32_t>(sh.passed[t][c].before);
+        return sum;
     }
 
     // The rank of this thread's listed token: weight and number of those before it (in the list, and as many more).
@@ -426,6 +484,7 @@ struct Draw {
         return __syncthreads_or(hit) != 0;
     }
     int listed;
+    bool fits;
     uint64_t rank_w;
     uint32_t rank_n;
 };
@@ -525,63 +584,73 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
     } else {
         Draw<CS> w = {a, sh, x, rank, lo, n, m, c_hi, c_lo, 0, 0};
         const float p = sh.p, low = sh.low;
-        const uint32_t k = static_cast<uint32_t>(sh.k);
-        const float per_unit = 1.0f / 536870912.0f;  // 2^-29: of weights' units into those of the bins
-        uint64_t mine, before, target = 0;
+        const uint32_t k = static_cast<uint32_t>(sh.k), low_d = __float_as_uint(fabsf(low - m));
+        const bool has_low = low > -3.402823466e38f;
+        uint64_t mine = 0, before, all = 0, target = 0;
         thr = static_cast<uint64_t>(order_key(low)) << 32;
         bool nucleus = p < 1.0f;  // top-p still to be done
-        Found f;
-        Range r = w.whole();
+        const Range none = w.whole();
         if (k > 0) {
-            w.template histogram<true, false>(0, r, DR_SHIFT, false);
-            f = w.locate(true, 0, r, DR_SHIFT, false, k, 0.0f);
-            const bool all = f.before_n + f.n <= DR_LIST;  // the list holds all that may be kept
-            r = all ? w.whole() : w.template narrow<false>(f, false, k, 0.0f);
-            if (all && f.bin < DR_BINS - 1) r.hi[0] = DR_FIRST + ((f.bin + 1) << DR_SHIFT) - 1;
-            mine = w.template pass<true>(r, low, before);
-            w.ranks(before, all ? 0 : f.before_n);
+            Search q = w.template start<false>(k, 0.0f);
+            const bool few = q.f.before_n + q.f.n <= DR_LIST;  // the list holds all that may be kept
+            if (few) {
+                q.r.lo[0] = 0;
+                q.f.before_n = 0;
+            }
+            while (!few && q.f.n > DR_LIST) w.template refine<false>(q, k, 0.0f);
+            mine = has_low && low_d <= q.r.hi[0] ? w.template pass<true, false, true>(q.r, low, before, all)
+                                                 : w.template pass<true, false, false>(q.r, low, before, all);
+            w.ranks(before, q.f.before_n);
             w.pick(false, k);
             thr = max(thr, sh.thr);
             target = whole_times<true>(p, sh.thr_sum);
-            if (all && nucleus) {
+            if (few && nucleus) {
                 __syncthreads();
                 w.pick(true, target);
                 thr = max(thr, sh.thr);
                 nucleus = false;
             }
+        } else if (!nucleus || has_low) {
+            // no order is needed where min-p alone keeps no more than top-p would
+            mine = nucleus ? w.template pass<false, true, false>(none, low, before, all)
+                           : w.template pass<false, false, false>(none, low, before, all);
+            if (nucleus) {
+                target = whole_times<true>(p, all);
+                nucleus = before > target;
+            }
         }
         if (nucleus) {
-            r = w.whole();
-            w.template histogram<true, true>(0, r, DR_SHIFT, k == 0);
-            if (k == 0) {
-                uint64_t total = 0;
-#pragma unroll
-                for (int c = 0; c < CS; ++c) total += sh.sums[c];
-                target = whole_times<true>(p, total);
-            }
-            const float about = static_cast<float>(target) * per_unit;
-            f = w.locate(true, 0, r, DR_SHIFT, true, 0, about);
-            r = w.template narrow<true>(f, true, 0, about);
-            for (;;) {
-                mine = w.template pass<true>(r, low, before);
-                w.ranks(before, f.before_n);
-                if (w.pick(true, target)) break;
-                // the threshold is before the range or behind it: on with the next token there, by counts
-                const uint32_t next = target <= before ? f.before_n : f.before_n + f.n + 1;
-                if (next < 1 || next > static_cast<uint32_t>(a.V)) break;  // (never: the weights of all reach the target)
-                r = w.whole();
-                w.template histogram<true, false>(0, r, DR_SHIFT, false);
-                f = w.locate(true, 0, r, DR_SHIFT, false, next, 0.0f);
-                r = w.template narrow<false>(f, false, next, 0.0f);
+            const bool known = target != 0;  // else the histogram's own sum says about where to look
+            const float per_unit = 1.0f / 536870912.0f;  // 2^-29: of weights' units into the bins'
+            Search q = w.template start<true>(0, known ? static_cast<float>(target) * per_unit : -p);
+            const float about = q.f.target_m;
+            while (q.f.n > DR_LIST - 32) w.template refine<true>(q, 0, about);
+            bool found = false;
+            for (int turn = 0; !found; ++turn) {
+                const bool cut = has_low && low_d <= q.r.hi[0];
+                if (known || turn > 0)
+                    mine = cut ? w.template pass<true, false, true>(q.r, low, before, all)
+                               : w.template pass<true, false, false>(q.r, low, before, all);
+                else mine = w.template pass<true, true, false>(q.r, low, before, all);
+                if (!known && turn == 0) target = whole_times<true>(p, all);
+                if (!w.fits) {
+                    w.template refine<true>(q, 0, static_cast<float>(target) * per_unit);
+                    continue;
+                }
+                w.ranks(before, 0);
+                found = w.pick(true, target);
+                if (!found) {  // the threshold is before the range or behind it: on with the next token there, by counts
+                    const uint32_t next = w.count_before(q.r) + (target <= before ? 0 : w.listed + 1);
+                    if (next < 1 || next > static_cast<uint32_t>(a.V)) break;  // (never: the weights of all reach the target)
+                    q = w.search_count(next);
+                }
             }
             thr = max(thr, sh.thr);
-        } else if (k == 0) {
-            mine = w.template pass<false>(r, low, before);
         }
         // ---- the draw: the listed tokens that are kept join their CTAs' sums
         // (what the listed tokens add to the threads' sums: where the histograms were, which nobody reads any more)
-        uint64_t *extra = reinterpret_cast<uint64_t *>(sh.bin_n);
-        static_assert(sizeof(sh.bin_n) >= DR_THREADS * 8, "a sum per thread");
+        uint64_t *extra = reinterpret_cast<uint64_t *>(sh.bins);
+        static_assert(sizeof(sh.bins) >= DR_THREADS * 8, "a sum per thread");
         __syncthreads();
         extra[tid] = 0;
         const uint64_t at = tid < w.listed ? sh.at[tid] : 0;
