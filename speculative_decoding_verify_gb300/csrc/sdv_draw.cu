@@ -5,16 +5,19 @@
 // prefix of the order (larger logit first, lower index among equals), so each is a threshold in that order and the strictest
 // one counts; the token is the first in index order whose running sum of kept weights exceeds u times their total.
 //
-// A row is read from HBM once, by a cluster of CTAs that hold it in shared memory; what follows works there.  A filter's
-// threshold is the token at a given count, or at a given sum of weights.  It is found by histograms over the distance d = m - l
-// (128 bins per octave first; a bin with more than DR_LIST tokens is cut again, by the bits of d, then of l, then of the
-// index): each CTA makes its own, one exchange later every CTA adds up the few bins that decide.  Counts are exact; a bin's
-// weights are 15-bit parts of its first token's, so the sum only says where to look: a pass over the tokens then takes the
-// exact sum of all before the bin and lists those in it, which are ranked by comparing all with all, and where the
-// threshold is not among them the search goes on at the next token before or behind.  That pass leaves each thread the sum
-// of its own neighbouring tokens, so the draw is a scan of those sums and a walk of one warp.
-// With top-k and a bin that ends under DR_LIST tokens the list holds all that may be kept, and everything is done on it.
-// Every exchange is one cluster barrier: three for a listed row, three or four for others, and one at each end.
+// A row is read from HBM once, by a cluster of CTAs that hold it in shared memory; what follows works there.  A warp has a
+// run of neighbouring tokens, a lane four of each 128 of them; a lane whose largest logit is out of a pass's reach
+// leaves its tokens out.  A filter's threshold is the token at a given count, or at a given sum of weights:
+//   a small top-k looks at the lanes' largest logits first: no more tokens than about k are as large as the k-th of those.
+//   They are listed in every CTA and ranked by comparing all with all, and everything else is done on the list;
+//   otherwise histograms over the distance d = m - l (128 bins per octave first; a bin with more than DR_LIST tokens
+//   is cut again, by the bits of d, then of l, then of the index): each CTA makes its own, one exchange later every CTA adds
+//   up the few bins that decide.  Counts are exact; a bin's weights are 15-bit parts of its first token's, so their sum only
+//   says where to look: a pass over the tokens then takes the exact sum of all before the bin and lists those in
+//   it, and where the threshold is not among them the search goes on at the next token before or behind.
+// A pass leaves the sum of each warp's kept tokens, so the draw is a search among those and a walk of one warp over its run.
+// Every exchange is one cluster barrier: two for a row without top-k or top-p, three with a small top-k, four with top-p of a
+// flat row, and one at each end.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -30,6 +33,7 @@ constexpr int DR_BITS = 10, DR_BINS = 1 << DR_BITS, DR_COARSE = 32;  // a coarse
 constexpr int DR_LIST = 256;      // tokens that are ranked directly
 constexpr int DR_MOST_CTAS = 8;
 constexpr int DR_CHUNK = 45056;   // most tokens of a CTA (88 a thread)
+constexpr int DR_SMALL_K = 192;   // top-k for which about as many tokens are worth listing
 // the first histogram: 8 octaves of d from 2^-3 on, by the bits of d
 constexpr uint32_t DR_FIRST = 0x3e000000u;
 constexpr int DR_SHIFT = 16;
@@ -89,7 +93,7 @@ struct alignas(16) DrawShared {
     // ---- of this CTA alone
     uint64_t at[DR_LIST], w[DR_LIST];  // the cluster's list
     uint64_t cta_sum[DR_MOST_CTAS];
-    uint64_t part[DR_WARPS];
+    uint64_t part[3][DR_WARPS];  // the warps' sums: of all, of those before, of the kept ones
     float warp_f[DR_WARPS];
     Found found;
     uint64_t thr, thr_sum;
@@ -177,15 +181,6 @@ __device__ __forceinline__ T warp_scan(T v) {  // inclusive
     }
     return v;
 }
-// the sum over the CTA, in every thread; `part` is free again behind the next barrier
-__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *part) {
-    v = warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return warp_sum((threadIdx.x & 31) < DR_WARPS ? part[threadIdx.x & 31] : uint64_t(0));
-}
-
 // A search for a threshold so far: the range, the phase that cuts it next, and what the last histogram said.
 struct Search {
     Range r;
@@ -200,7 +195,8 @@ struct Draw {
     DrawShared &sh;
     const float *x;    // this CTA's logits, minus infinity up to a multiple of four
     int rank, lo, n;   // tokens [lo, lo + n) of the row
-    float m, c_hi, c_lo;
+    int w0, w1;        // of these, this warp's
+    float m, top, c_hi, c_lo;  // the row's largest logit, this thread's
     int level, turn;   // histograms and passes so far
 
     template <class T>
@@ -235,7 +231,9 @@ struct Draw {
         uint32_t *bins = sh.bins[b];
         for (int i = tid; i < DR_BINS; i += DR_THREADS) bins[i] = 0;
         __syncthreads();
-        for (int i = 4 * tid; i < n; i += 4 * DR_THREADS) {
+        const bool reach = FIRST || value(0, top, 0) <= r.hi[0];
+#pragma unroll 2
+        for (int i = w0 + 4 * (tid & 31); reach && i < w1; i += 128) {
             const float4 v = *reinterpret_cast<const float4 *>(x + i);
             const float l[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -244,11 +242,10 @@ struct Draw {
                 uint32_t bin;
                 float from = 0.0f;
                 if constexpr (FIRST) {
-                    const int32_t y = (static_cast<int32_t>(d) - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT;
-                    bin = static_cast<uint32_t>(min(max(y, 0), DR_BINS - 1));
+                    bin = first_bin(d);
                     if constexpr (MASS) {
                         from = __uint_as_float(min(d & (0xffffffffu << DR_SHIFT), DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT)));
-                        if (y <= 0) from = 0.0f;
+                        if (bin == 0) from = 0.0f;
                     }
                 } else {
                     if (d < r.lo[0] || d > r.hi[0] || side(r, d, l[j], lo + i + j) != 0) continue;
@@ -264,23 +261,40 @@ struct Draw {
                 }
             }
         }
+        share<FIRST, MASS>(phase, r, shift);
+    }
+    // The first level over the threads' largest logits alone: as many different tokens.
+    __device__ void histogram_of_tops() {
+        const int tid = static_cast<int>(threadIdx.x);
+        uint32_t *bins = sh.bins[level & 1];
+        for (int i = tid; i < DR_BINS; i += DR_THREADS) bins[i] = 0;
         __syncthreads();
-        {  // 16 threads per coarse bin; every CTA gets them
-            uint32_t cn = 0;
-            float cm = 0.0f;
+        atomicAdd(&bins[first_bin(value(0, top, 0))], 1u);
+        share<true, false>(0, whole(), DR_SHIFT);
+    }
+    __device__ __forceinline__ static uint32_t first_bin(uint32_t d) {
+        return static_cast<uint32_t>(min(max((static_cast<int32_t>(d) - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT, 0), DR_BINS - 1));
+    }
+    // 16 threads per coarse bin; every CTA gets them
+    template <bool FIRST, bool MASS>
+    __device__ void share(int phase, const Range &r, int shift) {
+        const int tid = static_cast<int>(threadIdx.x), b = level & 1;
+        const uint32_t *bins = sh.bins[b];
+        __syncthreads();
+        uint32_t cn = 0;
+        float cm = 0.0f;
 #pragma unroll
-            for (int j = 0; j < DR_BINS / DR_THREADS; ++j) {
-                const uint32_t bin = DR_BINS / DR_THREADS * tid + j;
-                if constexpr (MASS) cm += static_cast<float>(bins[bin]) * ex2_approx(-c_hi * edge(FIRST, phase, r, shift, bin));
-                else cn += bins[bin];
-            }
-#pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) {
-                if constexpr (MASS) cm += __shfl_xor_sync(0xffffffffu, cm, o);
-                else cn += __shfl_xor_sync(0xffffffffu, cn, o);
-            }
-            if ((tid & 15) < CS) *of(&sh.coarse[b][rank][tid >> 4], tid & 15) = MASS ? __float_as_uint(cm) : cn;
+        for (int j = 0; j < DR_BINS / DR_THREADS; ++j) {
+            const uint32_t bin = DR_BINS / DR_THREADS * tid + j;
+            if constexpr (MASS) cm += static_cast<float>(bins[bin]) * ex2_approx(-c_hi * edge(FIRST, phase, r, shift, bin));
+            else cn += bins[bin];
         }
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) {
+            if constexpr (MASS) cm += __shfl_xor_sync(0xffffffffu, cm, o);
+            else cn += __shfl_xor_sync(0xffffffffu, cn, o);
+        }
+        if ((tid & 15) < CS) *of(&sh.coarse[b][rank][tid >> 4], tid & 15) = MASS ? __float_as_uint(cm) : cn;
         cluster_arrive();
         cluster_wait();
         ++level;
@@ -344,8 +358,11 @@ struct Draw {
         histogram<true, MASS>(0, q.r, DR_SHIFT);
         q.f = locate<MASS>(true, 0, q.r, DR_SHIFT, target_n, target_m);
         if (q.f.bin > 0) q.r.lo[0] = DR_FIRST + (q.f.bin << DR_SHIFT);
-        if (q.f.bin < DR_BINS - 1) q.r.hi[0] = DR_FIRST + ((q.f.bin + 1) << DR_SHIFT) - 1;
+        q.r.hi[0] = bin_end(q.f.bin);
         return q;
+    }
+    __device__ __forceinline__ static uint32_t bin_end(uint32_t bin) {
+        return bin < DR_BINS - 1 ? DR_FIRST + ((bin + 1) << DR_SHIFT) - 1 : 0xffffffffu;
     }
     // one level more
     template <bool MASS>
@@ -366,55 +383,79 @@ struct Draw {
         return q;
     }
 
-    // A thread's tokens in the passes and the draw: neighbours, an odd number (no bank conflicts).
-    __device__ __forceinline__ int per() const { return ((n + DR_THREADS - 1) / DR_THREADS) | 1; }
-
     // A pass over the tokens: the sum of the weights before the range (not RANGED: of logits from `low` on) in every CTA, and
-    // with TOTAL of all; of the kept ones (those before; with LOW only from `low` on) each CTA's in sh.cta_sum and this
-    // thread's as the result; the range's tokens in sh.at, sh.w (`listed` of them), false in `fits` if they are too many.
+    // with TOTAL of all; of the kept ones (those before; with LOW only from `low` on) each warp's in sh.part[2] and each
+    // CTA's in sh.cta_sum; the range's tokens in sh.at, sh.w (`listed` of them), false in `fits` if they are too many.
     template <bool RANGED, bool TOTAL, bool LOW>
-    __device__ uint64_t pass(const Range &r, float low, uint64_t &before, uint64_t &all) {
-        const int tid = static_cast<int>(threadIdx.x), t = turn++ & 1;
+    __device__ void pass(const Range &r, float low, uint64_t &before, uint64_t &all) {
+        const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, t = turn++ & 1;
         if (tid == 0) sh.listed = 0;
         __syncthreads();
-        const int i0 = min(n, tid * per()), i1 = min(n, i0 + per());
         Units sa = {0, 0}, sb = {0, 0}, sk = {0, 0};
         uint32_t added = 0;
+        const bool reach = TOTAL || (RANGED ? value(0, top, 0) <= r.hi[0] : top >= low);
 #pragma unroll 2
-        for (int i = i0; i < i1; i += 2) {  // (a last token alone is joined by one of no weight)
-            const bool two = i + 1 < i1;
-            const float2 l = make_float2(x[i], two ? x[i + 1] : -INFINITY);
-            bool b0, b1;
-            if constexpr (RANGED) {
-                const uint32_t d0 = value(0, l.x, 0), d1 = value(0, l.y, 0);
-                int s0 = d0 < r.lo[0] ? -1 : 1, s1 = d1 < r.lo[0] ? -1 : 1;
-                if (d0 >= r.lo[0] && d0 <= r.hi[0]) s0 = side(r, d0, l.x, lo + i);
-                if (d1 >= r.lo[0] && d1 <= r.hi[0] && two) s1 = side(r, d1, l.y, lo + i + 1);
-                if (s0 == 0) list(t, l.x, lo + i);
-                if (s1 == 0) list(t, l.y, lo + i + 1);
-                b0 = s0 < 0;
-                b1 = s1 < 0;
-            } else {
-                b0 = l.x >= low;
-                b1 = l.y >= low;
+        for (int i = w0 + 4 * lane; reach && i < w1; i += 128) {
+            const float4 v = *reinterpret_cast<const float4 *>(x + i);  // (behind the row's end: minus infinity)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 l = h ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+                const int at = i + 2 * h;
+                bool b0, b1;
+                if constexpr (RANGED) {
+                    const uint32_t d0 = value(0, l.x, 0), d1 = value(0, l.y, 0);
+                    b0 = d0 < r.lo[0];
+                    b1 = d1 < r.lo[0];
+                    if (!b0 && d0 <= r.hi[0]) b0 = list(r, t, d0, l.x, lo + at);
+                    if (!b1 && d1 <= r.hi[0]) b1 = list(r, t, d1, l.y, lo + at + 1);
+                } else {
+                    b0 = l.x >= low;
+                    b1 = l.y >= low;
+                }
+                if (!TOTAL && !(b0 || b1)) continue;
+                const float2 e = weights_of(l, m, c_hi, c_lo);
+                const float2 eb = make_float2(b0 ? e.x : 0.0f, b1 ? e.y : 0.0f);
+                if constexpr (TOTAL) sa.add(e);
+                sb.add(eb);
+                if constexpr (LOW) sk.add(make_float2(l.x >= low ? eb.x : 0.0f, l.y >= low ? eb.y : 0.0f));
+                added += 2;
             }
-            if (!TOTAL && !(b0 || b1)) continue;
-            const float2 e = weights_of(l, m, c_hi, c_lo);
-            const float2 eb = make_float2(b0 ? e.x : 0.0f, b1 ? e.y : 0.0f);
-            if constexpr (TOTAL) sa.add(e);
-            sb.add(eb);
-            if constexpr (LOW) sk.add(make_float2(l.x >= low ? eb.x : 0.0f, l.y >= low ? eb.y : 0.0f));
-            added += 2;
         }
-        const uint64_t mb = sb.sum(added), mine = LOW ? sk.sum(added) : mb;
-        Passed p;
-        p.all = TOTAL ? block_sum(sa.sum(added), sh.part) : 0;
-        p.before = block_sum(mb, sh.part);
-        p.kept = LOW ? block_sum(mine, sh.part) : p.before;
-        p.n = sh.listed;
-        if (tid < CS) *of(&sh.passed[t][rank], tid) = p;
+        tell<TOTAL, LOW>(t, TOTAL ? sa.sum(added) : 0, sb.sum(added), LOW ? sk.sum(added) : 0);
+        hear<RANGED>(t, before, all);
+    }
+    // a listed token goes into the list; whether it is before the range
+    __device__ __forceinline__ bool list(const Range &r, int t, uint32_t d, float l, int idx) {
+        const int s = side(r, d, l, idx);
+        if (s == 0) put(t, l, idx);
+        return s < 0;
+    }
+    // the CTA's sums and list to all CTAs
+    template <bool TOTAL, bool LOW>
+    __device__ __forceinline__ void tell(int t, uint64_t sa, uint64_t sb, uint64_t sk) {
+        const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+        if (TOTAL) sa = warp_sum(sa);
+        sb = warp_sum(sb);
+        sk = LOW ? warp_sum(sk) : sb;
+        if (lane == 0) {
+            sh.part[0][warp] = sa;
+            sh.part[1][warp] = sb;
+            sh.part[2][warp] = sk;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            Passed p = {0, 0, 0, sh.listed};
+            if (TOTAL) p.all = warp_sum(lane < DR_WARPS ? sh.part[0][lane] : uint64_t(0));
+            p.before = warp_sum(lane < DR_WARPS ? sh.part[1][lane] : uint64_t(0));
+            p.kept = LOW ? warp_sum(lane < DR_WARPS ? sh.part[2][lane] : uint64_t(0)) : p.before;
+            if (lane < CS) *of(&sh.passed[t][rank], lane) = p;
+        }
         cluster_arrive();
         cluster_wait();
+    }
+    template <bool LISTED>
+    __device__ __forceinline__ void hear(int t, uint64_t &before, uint64_t &all) {
+        const int tid = static_cast<int>(threadIdx.x);
         before = all = 0;
         if (tid < CS) sh.cta_sum[tid] = sh.passed[t][tid].kept;
         uint32_t from = 0;
@@ -423,22 +464,42 @@ struct Draw {
         for (int c = 0; c < CS; ++c) {
             const uint32_t nc = sh.passed[t][c].n;
             before += sh.passed[t][c].before;
-            if (TOTAL) all += sh.passed[t][c].all;
-            if (RANGED && static_cast<uint32_t>(tid) >= from && static_cast<uint32_t>(tid) - from < nc && tid < DR_LIST)
+            all += sh.passed[t][c].all;
+            if (LISTED && static_cast<uint32_t>(tid) >= from && static_cast<uint32_t>(tid) - from < nc && tid < DR_LIST)
                 src = of(&sh.list[t][tid - from], c);
             from += nc;
         }
         fits = from <= DR_LIST;
-        listed = fits ? static_cast<int>(from) : 0;
-        if (RANGED && tid < DR_LIST) {
+        listed = LISTED && fits ? static_cast<int>(from) : 0;
+        if (LISTED && tid < DR_LIST) {
             const uint64_t at = src && fits ? *src : 0;
             sh.at[tid] = at;
             sh.w[tid] = src && fits ? units(weight_of(key_logit(static_cast<uint32_t>(at >> 32)), m, c_hi, c_lo)) : 0;
         }
         __syncthreads();
-        return mine;
     }
-    __device__ __forceinline__ void list(int t, float l, int idx) {
+    // The tokens whose distance has at most the bits d_end, listed.
+    __device__ void gather(uint32_t d_end) {
+        const int tid = static_cast<int>(threadIdx.x), t = turn++ & 1;
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        if (value(0, top, 0) <= d_end)
+            for (int i = w0 + 4 * (tid & 31); i < w1; i += 128) {
+                const float4 v = *reinterpret_cast<const float4 *>(x + i);
+                const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (value(0, l[j], 0) <= d_end && i + j < n) put(t, l[j], lo + i + j);
+            }
+        __syncthreads();
+        if (tid < DR_WARPS) sh.part[2][tid] = 0;
+        if (tid < CS) *of(&sh.passed[t][rank], tid) = Passed{0, 0, 0, sh.listed};
+        cluster_arrive();
+        cluster_wait();
+        uint64_t before, all;
+        hear<true>(t, before, all);
+    }
+    __device__ __forceinline__ void put(int t, float l, int idx) {
         const uint32_t slot = atomicAdd(&sh.listed, 1u);
         if (slot < DR_LIST && SD_INB(slot < DR_LIST, a.status, 124)) sh.list[t][slot] = place_of(l, idx);  // site 124: listed token
     }
@@ -447,10 +508,7 @@ struct Draw {
         const int tid = static_cast<int>(threadIdx.x), t = turn++ & 1;
         uint64_t mine = 0;
         for (int i = tid; i < n; i += DR_THREADS) mine += side(r, value(0, x[i], 0), x[i], lo + i) < 0 ? 1 : 0;
-        const Passed p = {0, block_sum(mine, sh.part), 0, 0};
-        if (tid < CS) *of(&sh.passed[t][rank], tid) = p;
-        cluster_arrive();
-        cluster_wait();
+        tell<false, false>(t, 0, mine, 0);
         uint32_t sum = 0;
         for (int c = 0; c < CS; ++c) sum += static_cast<uint32_t>(sh.passed[t][c].before);
         return sum;
@@ -518,37 +576,37 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
         sh.u = u;
         sh.low_log = low > 0.0f && T > 0.0f ? static_cast<double>(T) * log(static_cast<double>(low)) : -INFINITY;
     }
-    // ---- the row's tokens of this CTA; a NaN counts as minus infinity, -0 as 0
-    float top = -INFINITY;
+    // ---- the row's tokens of this CTA; a NaN counts as minus infinity, -0 as 0, and minus infinity fills up the last four
+    const int run = (n + 4 * DR_WARPS - 1) / (4 * DR_WARPS) * 4, w0 = min(n, warp * run), w1 = min(n, w0 + run);
+    float mine = -INFINITY;
     auto clean = [](float v) { return fmaxf(v, -INFINITY) + 0.0f; };
-    const int n4 = (reinterpret_cast<uintptr_t>(from) & 15) == 0 ? n / 4 : 0;
-    constexpr int FLY = 8;
-    for (int i = tid; i < n4; i += FLY * DR_THREADS) {
+    const bool wide = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
+    constexpr int FLY = 5;
+    for (int i0 = w0 + 4 * lane; i0 < w1; i0 += FLY * 128) {
         float4 v[FLY];
 #pragma unroll
-        for (int j = 0; j < FLY; ++j)
-            if (i + j * DR_THREADS < n4) v[j] = __ldcs(reinterpret_cast<const float4 *>(from) + i + j * DR_THREADS);
+        for (int j = 0; j < FLY; ++j) {
+            const int i = i0 + 128 * j;
+            if (wide && i + 4 <= w1) {
+                v[j] = __ldcs(reinterpret_cast<const float4 *>(from + i));
+            } else if (i < w1) {
+                v[j].x = __ldcs(from + i);
+                v[j].y = i + 1 < w1 ? __ldcs(from + i + 1) : -INFINITY;
+                v[j].z = i + 2 < w1 ? __ldcs(from + i + 2) : -INFINITY;
+                v[j].w = i + 3 < w1 ? __ldcs(from + i + 3) : -INFINITY;
+            }
+        }
 #pragma unroll
-        for (int j = 0; j < FLY; ++j)
-            if (i + j * DR_THREADS < n4 && SD_INB(4 * (i + j * DR_THREADS) + 4 <= a.chunk, a.status, 125)) {  // site 125: logits
+        for (int j = 0; j < FLY; ++j) {
+            const int i = i0 + 128 * j;
+            if (i < w1 && SD_INB(i + 4 <= a.chunk, a.status, 125)) {  // site 125: logits
                 const float4 c = make_float4(clean(v[j].x), clean(v[j].y), clean(v[j].z), clean(v[j].w));
-                reinterpret_cast<float4 *>(x)[i + j * DR_THREADS] = c;
-                top = fmaxf(top, fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)));
+                *reinterpret_cast<float4 *>(x + i) = c;
+                mine = fmaxf(mine, fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)));
             }
+        }
     }
-    for (int i = 4 * n4 + tid; i < n; i += FLY * DR_THREADS) {
-        float v[FLY];
-#pragma unroll
-        for (int j = 0; j < FLY; ++j)
-            if (i + j * DR_THREADS < n) v[j] = __ldcs(from + i + j * DR_THREADS);
-#pragma unroll
-        for (int j = 0; j < FLY; ++j)
-            if (i + j * DR_THREADS < n && SD_INB(i + j * DR_THREADS < a.chunk, a.status, 125)) {
-                x[i + j * DR_THREADS] = clean(v[j]);
-                top = fmaxf(top, clean(v[j]));
-            }
-    }
-    if (tid < ((n + 3) / 4 * 4 - n)) x[n + tid] = -INFINITY;
+    float top = mine;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) sh.warp_f[warp] = top;
@@ -566,6 +624,7 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
     const bool bad = sh.bad || m == -INFINITY;
     if (m == INFINITY) {  // those tokens share everything
         for (int i = tid; i < n; i += DR_THREADS) x[i] = x[i] == INFINITY ? 0.0f : -INFINITY;
+        mine = mine == INFINITY ? 0.0f : -INFINITY;
         m = 0.0f;
     }
     // the lowest logit that min-p keeps; minus infinity never is
@@ -582,25 +641,28 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             if (a.prob) a.prob[row] = 0.0f;
         }
     } else {
-        Draw<CS> w = {a, sh, x, rank, lo, n, m, c_hi, c_lo, 0, 0};
+        Draw<CS> w = {a, sh, x, rank, lo, n, w0, w1, m, mine, c_hi, c_lo, 0, 0};
         const float p = sh.p, low = sh.low;
         const uint32_t k = static_cast<uint32_t>(sh.k), low_d = __float_as_uint(fabsf(low - m));
         const bool has_low = low > -3.402823466e38f;
-        uint64_t mine = 0, before, all = 0, target = 0;
+        uint64_t before, all = 0, target = 0;
         thr = static_cast<uint64_t>(order_key(low)) << 32;
         bool nucleus = p < 1.0f;  // top-p still to be done
         const Range none = w.whole();
         if (k > 0) {
-            Search q = w.template start<false>(k, 0.0f);
-            const bool few = q.f.before_n + q.f.n <= DR_LIST;  // the list holds all that may be kept
+            bool few = k <= DR_SMALL_K;
             if (few) {
-                q.r.lo[0] = 0;
-                q.f.before_n = 0;
+                w.histogram_of_tops();
+                w.gather(Draw<CS>::bin_end(w.template locate<false>(true, 0, none, DR_SHIFT, k, 0.0f).bin));
+                few = w.fits;
+                w.ranks(0, 0);
             }
-            while (!few && q.f.n > DR_LIST) w.template refine<false>(q, k, 0.0f);
-            mine = has_low && low_d <= q.r.hi[0] ? w.template pass<true, false, true>(q.r, low, before, all)
-                                                 : w.template pass<true, false, false>(q.r, low, before, all);
-            w.ranks(before, q.f.before_n);
+            if (!few) {
+                const Search q = w.search_count(k);
+                if (has_low && low_d <= q.r.hi[0]) w.template pass<true, false, true>(q.r, low, before, all);
+                else w.template pass<true, false, false>(q.r, low, before, all);
+                w.ranks(before, q.f.before_n);
+            }
             w.pick(false, k);
             thr = max(thr, sh.thr);
             target = whole_times<true>(p, sh.thr_sum);
@@ -612,8 +674,8 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             }
         } else if (!nucleus || has_low) {
             // no order is needed where min-p alone keeps no more than top-p would
-            mine = nucleus ? w.template pass<false, true, false>(none, low, before, all)
-                           : w.template pass<false, false, false>(none, low, before, all);
+            if (nucleus) w.template pass<false, true, false>(none, low, before, all);
+            else w.template pass<false, false, false>(none, low, before, all);
             if (nucleus) {
                 target = whole_times<true>(p, all);
                 nucleus = before > target;
@@ -628,10 +690,9 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             bool found = false;
             for (int turn = 0; !found; ++turn) {
                 const bool cut = has_low && low_d <= q.r.hi[0];
-                if (known || turn > 0)
-                    mine = cut ? w.template pass<true, false, true>(q.r, low, before, all)
-                               : w.template pass<true, false, false>(q.r, low, before, all);
-                else mine = w.template pass<true, true, false>(q.r, low, before, all);
+                if (!known && turn == 0) w.template pass<true, true, false>(q.r, low, before, all);
+                else if (cut) w.template pass<true, false, true>(q.r, low, before, all);
+                else w.template pass<true, false, false>(q.r, low, before, all);
                 if (!known && turn == 0) target = whole_times<true>(p, all);
                 if (!w.fits) {
                     w.template refine<true>(q, 0, static_cast<float>(target) * per_unit);
@@ -648,19 +709,13 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             thr = max(thr, sh.thr);
         }
         // ---- the draw: the listed tokens that are kept join their CTAs' sums
-        // (what the listed tokens add to the threads' sums: where the histograms were, which nobody reads any more)
-        uint64_t *extra = reinterpret_cast<uint64_t *>(sh.bins);
-        static_assert(sizeof(sh.bins) >= DR_THREADS * 8, "a sum per thread");
         __syncthreads();
-        extra[tid] = 0;
         const uint64_t at = tid < w.listed ? sh.at[tid] : 0;
-        const bool kept = tid < w.listed && at >= thr;
-        __syncthreads();
-        if (kept) {
+        if (tid < w.listed && at >= thr) {
             const int idx = place_idx(at);
             atomicAdd(reinterpret_cast<unsigned long long *>(&sh.cta_sum[CS == 1 ? 0 : idx / a.chunk]), sh.w[tid]);
             if (idx >= lo && idx < lo + n)
-                atomicAdd(reinterpret_cast<unsigned long long *>(&extra[(idx - lo) / w.per()]), sh.w[tid]);
+                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.part[2][(idx - lo) / run]), sh.w[tid]);
         }
         __syncthreads();
         uint64_t total = 0, base = 0;
@@ -672,32 +727,36 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
         const uint64_t want = whole_times<false>(sh.u, total);  // (under the total: u < 1)
         inv = DR_UNIT / static_cast<float>(total);
         if (base <= want && want < base + sh.cta_sum[rank]) {
-            mine += extra[tid];
-            const uint64_t inc = warp_scan(mine);
-            if (lane == 31) sh.part[warp] = inc;
-            __syncthreads();
-            const uint64_t pw = warp_scan(lane < DR_WARPS ? sh.part[lane] : uint64_t(0));
-            uint64_t start = base + inc - mine;
-            const uint64_t ahead = __shfl_sync(0xffffffffu, pw, max(warp - 1, 0));
-            if (warp > 0) start += ahead;
-            // the warp of the thread whose tokens the draw falls on goes through them
-            const uint32_t who = __ballot_sync(0xffffffffu, start <= want && want < start + mine);
-            if (who) {
-                const int owner = __ffs(who) - 1, i0 = min(n, (32 * warp + owner) * w.per()), i1 = min(n, i0 + w.per());
-                uint64_t run = __shfl_sync(0xffffffffu, start, owner);
-                for (int i = i0 + lane; i - lane < i1; i += 32) {
-                    float e = 0.0f;
-                    if (i < i1 && place_of(x[i], lo + i) >= thr) e = weight_of(x[i], m, c_hi, c_lo);
-                    const uint64_t here = run + warp_scan(units(e));
+            const uint64_t own = lane < DR_WARPS ? sh.part[2][lane] : 0, upto = base + warp_scan(own);
+            uint64_t done = __shfl_sync(0xffffffffu, upto - own, warp);
+            if (done <= want && want < __shfl_sync(0xffffffffu, upto, warp)) {  // the draw falls on this warp's run
+                for (int i0 = w0; i0 < w1; i0 += 128) {
+                    const int i = i0 + 4 * lane;
+                    float e[4];
+                    uint64_t s = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e[j] = i + j < w1 && place_of(x[i + j], lo + i + j) >= thr ? weight_of(x[i + j], m, c_hi, c_lo) : 0.0f;
+                        s += units(e[j]);
+                    }
+                    const uint64_t here = done + warp_scan(s);
                     const uint32_t over = __ballot_sync(0xffffffffu, here > want);
                     if (over) {
                         if (lane == __ffs(over) - 1) {
-                            a.tokens[row] = lo + i;
-                            if (a.prob) a.prob[row] = e * inv;
+                            uint64_t y = here - s;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint64_t z = y + units(e[j]);
+                                if (y <= want && want < z) {
+                                    a.tokens[row] = lo + i + j;
+                                    if (a.prob) a.prob[row] = e[j] * inv;
+                                }
+                                y = z;
+                            }
                         }
                         break;
                     }
-                    run = __shfl_sync(0xffffffffu, here, 31);
+                    done = __shfl_sync(0xffffffffu, here, 31);
                 }
             }
         }
