@@ -15,7 +15,7 @@
 //   up the few bins that decide.  Counts are exact; a bin's weights are 15-bit parts of its first token's, so their sum only
 //   says where to look: a pass over the tokens then takes the exact sum of all before the bin and lists those in
 //   it, and where the threshold is not among them the search goes on at the next token before or behind.
-// A pass leaves the sum of each warp's kept tokens, so the draw is a search among those and a walk of one warp over its run.
+// A pass leaves the sum of each warp's kept tokens, so the draw is a search among those and a scan of one run.
 // Every exchange is one cluster barrier: two for a row without top-k or top-p, three with a small top-k, four with top-p of a
 // flat row, and one at each end.
 #include <cooperative_groups.h>
@@ -98,7 +98,7 @@ struct alignas(16) DrawShared {
     Found found;
     uint64_t thr, thr_sum;
     double low_log;
-    float c_hi, c_lo, p, u, low;
+    float c_hi, c_lo, p, u;
     uint32_t listed;
     int32_t k, bad, owner;
 };
@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
         m = 0.0f;
     }
     // the lowest logit that min-p keeps; minus infinity never is
-    if (tid == 0) sh.low = fmaxf(__double2float_ru(static_cast<double>(m) + sh.low_log), -3.402823466e38f) + 0.0f;
+    float low = -3.402823466e38f;
+    if (sh.low_log > -INFINITY) low = fmaxf(__double2float_ru(static_cast<double>(m) + sh.low_log), low) + 0.0f;
     __syncthreads();
 
     float inv = 0.0f;
@@ -642,15 +643,16 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
         }
     } else {
         Draw<CS> w = {a, sh, x, rank, lo, n, w0, w1, m, mine, c_hi, c_lo, 0, 0};
-        const float p = sh.p, low = sh.low;
+        const float p = sh.p;
         const uint32_t k = static_cast<uint32_t>(sh.k), low_d = __float_as_uint(fabsf(low - m));
         const bool has_low = low > -3.402823466e38f;
         uint64_t before, all = 0, target = 0;
         thr = static_cast<uint64_t>(order_key(low)) << 32;
         bool nucleus = p < 1.0f;  // top-p still to be done
+        bool few = false;         // the list holds all that may be kept
         const Range none = w.whole();
         if (k > 0) {
-            bool few = k <= DR_SMALL_K;
+            few = k <= DR_SMALL_K;
             if (few) {
                 w.histogram_of_tops();
                 w.gather(Draw<CS>::bin_end(w.template locate<false>(true, 0, none, DR_SHIFT, k, 0.0f).bin));
@@ -665,7 +667,7 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             }
             w.pick(false, k);
             thr = max(thr, sh.thr);
-            target = whole_times<true>(p, sh.thr_sum);
+            if (nucleus) target = whole_times<true>(p, sh.thr_sum);
             if (few && nucleus) {
                 __syncthreads();
                 w.pick(true, target);
@@ -708,55 +710,81 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             }
             thr = max(thr, sh.thr);
         }
-        // ---- the draw: the listed tokens that are kept join their CTAs' sums
         __syncthreads();
         const uint64_t at = tid < w.listed ? sh.at[tid] : 0;
-        if (tid < w.listed && at >= thr) {
-            const int idx = place_idx(at);
-            atomicAdd(reinterpret_cast<unsigned long long *>(&sh.cta_sum[CS == 1 ? 0 : idx / a.chunk]), sh.w[tid]);
-            if (idx >= lo && idx < lo + n)
-                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.part[2][(idx - lo) / run]), sh.w[tid]);
-        }
-        __syncthreads();
-        uint64_t total = 0, base = 0;
+        const bool kept = tid < w.listed && at >= thr;
+        if (few) {
+            // ---- the draw from a list: each kept token's running sum in index order (the first CTA draws; where all
+            // probabilities are wanted each needs the total)
+            if (rank == 0 || a.probs) {
+                if (tid < w.listed && !kept) sh.w[tid] = 0;
+                __syncthreads();
+                uint64_t total = 0, upto = 0;
+#pragma unroll 8
+                for (int j = 0; j < w.listed; ++j) {
+                    const uint64_t y = sh.w[j];
+                    total += y;
+                    // (a lower index is a larger second half of the place)
+                    upto += static_cast<uint32_t>(sh.at[j]) >= static_cast<uint32_t>(at) ? y : 0;
+                }
+                inv = DR_UNIT / static_cast<float>(total);
+                const uint64_t want = whole_times<false>(sh.u, total);  // (under the total: u < 1)
+                if (rank == 0 && kept && want < upto && upto - sh.w[tid] <= want) {
+                    a.tokens[row] = place_idx(at);
+                    if (a.prob) a.prob[row] = weight_of(key_logit(static_cast<uint32_t>(at >> 32)), m, c_hi, c_lo) * inv;
+                }
+            }
+        } else {
+            // ---- the draw: the listed tokens that are kept join their CTAs' and warps' sums
+            if (kept) {
+                const int idx = place_idx(at);
+                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.cta_sum[CS == 1 ? 0 : idx / a.chunk]), sh.w[tid]);
+                if (idx >= lo && idx < lo + n)
+                    atomicAdd(reinterpret_cast<unsigned long long *>(&sh.part[2][(idx - lo) / run]), sh.w[tid]);
+            }
+            __syncthreads();
+            uint64_t total = 0, base = 0;
 #pragma unroll
-        for (int c = 0; c < CS; ++c) {
-            if (c == rank) base = total;
-            total += sh.cta_sum[c];
-        }
-        const uint64_t want = whole_times<false>(sh.u, total);  // (under the total: u < 1)
-        inv = DR_UNIT / static_cast<float>(total);
-        if (base <= want && want < base + sh.cta_sum[rank]) {
-            const uint64_t own = lane < DR_WARPS ? sh.part[2][lane] : 0, upto = base + warp_scan(own);
-            uint64_t done = __shfl_sync(0xffffffffu, upto - own, warp);
-            if (done <= want && want < __shfl_sync(0xffffffffu, upto, warp)) {  // the draw falls on this warp's run
-                for (int i0 = w0; i0 < w1; i0 += 128) {
-                    const int i = i0 + 4 * lane;
+            for (int c = 0; c < CS; ++c) {
+                if (c == rank) base = total;
+                total += sh.cta_sum[c];
+            }
+            const uint64_t want = whole_times<false>(sh.u, total);
+            inv = DR_UNIT / static_cast<float>(total);
+            if (base <= want && want < base + sh.cta_sum[rank]) {
+                // the warp whose run it falls on; the CTA's threads take four of its tokens each
+                const uint64_t own = lane < DR_WARPS ? sh.part[2][lane] : 0, upto = base + warp_scan(own);
+                const int q = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
+                uint64_t done = __shfl_sync(0xffffffffu, upto - own, q);
+                const int r0 = min(n, q * run), r1 = min(n, r0 + run);
+                for (int i0 = r0; i0 < r1; i0 += 4 * DR_THREADS) {
+                    const int i = i0 + 4 * tid;
                     float e[4];
                     uint64_t s = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        e[j] = i + j < w1 && place_of(x[i + j], lo + i + j) >= thr ? weight_of(x[i + j], m, c_hi, c_lo) : 0.0f;
+                        e[j] = i + j < r1 && place_of(x[i + j], lo + i + j) >= thr ? weight_of(x[i + j], m, c_hi, c_lo) : 0.0f;
                         s += units(e[j]);
                     }
-                    const uint64_t here = done + warp_scan(s);
-                    const uint32_t over = __ballot_sync(0xffffffffu, here > want);
-                    if (over) {
-                        if (lane == __ffs(over) - 1) {
-                            uint64_t y = here - s;
+                    const uint64_t inc = warp_scan(s);
+                    __syncthreads();
+                    if (lane == 31) sh.part[0][warp] = inc;
+                    __syncthreads();
+                    const uint64_t pw = warp_scan(lane < DR_WARPS ? sh.part[0][lane] : uint64_t(0));
+                    const uint64_t ahead = __shfl_sync(0xffffffffu, pw, max(warp - 1, 0));
+                    uint64_t y = done + inc - s + (warp > 0 ? ahead : 0);
+                    if (y <= want && want < y + s) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint64_t z = y + units(e[j]);
-                                if (y <= want && want < z) {
-                                    a.tokens[row] = lo + i + j;
-                                    if (a.prob) a.prob[row] = e[j] * inv;
-                                }
-                                y = z;
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t z = y + units(e[j]);
+                            if (y <= want && want < z) {
+                                a.tokens[row] = lo + i + j;
+                                if (a.prob) a.prob[row] = e[j] * inv;
                             }
+                            y = z;
                         }
-                        break;
                     }
-                    done = __shfl_sync(0xffffffffu, here, 31);
+                    done += __shfl_sync(0xffffffffu, pw, DR_WARPS - 1);
                 }
             }
         }
