@@ -12,7 +12,7 @@
 //   They are listed in every CTA and ranked by comparing all with all, and everything else is done on the list;
 //   otherwise histograms over the distance d = m - l (128 bins per octave first; a bin with more than DR_LIST tokens
 //   is cut again, by the bits of d, then of l, then of the index): each CTA makes its own, one exchange later every CTA adds
-//   up the few bins that decide.  Counts are exact; a bin's weights are 15-bit parts of its first token's, so their sum only
+//   up the few bins that decide.  Counts are exact; a bin's weights are 13- to 15-bit parts of its first token's, so their sum only
 //   says where to look: a pass over the tokens then takes the exact sum of all before the bin and lists those in
 //   it, and where the threshold is not among them the search goes on at the next token before or behind.
 // A pass leaves the sum of each warp's kept tokens, so the draw is a search among those and a scan of one run.
@@ -32,7 +32,7 @@ constexpr int DR_THREADS = 512, DR_WARPS = DR_THREADS / 32;
 constexpr int DR_BITS = 10, DR_BINS = 1 << DR_BITS, DR_COARSE = 32;  // a coarse bin is 32 bins
 constexpr int DR_LIST = 256;      // tokens that are ranked directly
 constexpr int DR_MOST_CTAS = 8;
-constexpr int DR_CHUNK = 45056;   // most tokens of a CTA (88 a thread)
+constexpr int DR_VOCAB = 360448;  // most tokens of a row
 constexpr int DR_SMALL_K = 192;   // top-k for which about as many tokens are worth listing
 // the first histogram: 8 octaves of d from 2^-3 on, by the bits of d
 constexpr uint32_t DR_FIRST = 0x3e000000u;
@@ -73,7 +73,7 @@ struct Range {
 // weight before it and the least number of tokens that its weight takes (a search by weights)
 struct Found {
     uint32_t bin, before_n, n;
-    float before_m, target_m;  // in units of 2^-15
+    float before_m, target_m;  // in units of 2^-MASS
 };
 
 // What a pass over the tokens tells of a CTA: the sums of all weights, of those before the range and of the kept ones, and
@@ -85,7 +85,7 @@ struct Passed {
 
 struct alignas(16) DrawShared {
     // ---- read or written by the cluster's other CTAs (what they write has two turns: a slow CTA still reads one)
-    uint32_t bins[2][DR_BINS];                   // a level's histogram: tokens, or weights in units of 2^-15
+    uint32_t bins[2][DR_BINS];                   // a level's histogram: tokens, or parts of weights
     uint32_t coarse[2][DR_MOST_CTAS][DR_COARSE];  // every CTA's: tokens, or weights (floats' bits)
     uint64_t list[2][DR_LIST];                   // this CTA's tokens in a pass's range
     Passed passed[2][DR_MOST_CTAS];              // every CTA's
@@ -128,6 +128,7 @@ __device__ __forceinline__ float weight_of(float l, float m, float c_hi, float c
 // Weights as whole numbers of 2^-44, summed in two words: adding 4 leaves the multiples of 2^-21 in the bits, adding
 // 1.5 * 2^-21 to the rest those of 2^-44 (under 2^22 of them, either sign).  What is added twice per weight comes off at
 // the end.
+constexpr uint32_t DR_ADDS = 511;  // (the second word's sum stays under 2^31)
 struct Units {
     uint32_t hi, lo;
     __device__ __forceinline__ void add(float2 e) {
@@ -137,7 +138,7 @@ struct Units {
         hi += __float_as_uint(t.x) + __float_as_uint(t.y);
         lo += __float_as_uint(q.x) + __float_as_uint(q.y);
     }
-    __device__ __forceinline__ uint64_t sum(uint32_t n) const {  // n weights were added, at most 512
+    __device__ __forceinline__ uint64_t sum(uint32_t n) const {  // n weights were added, at most DR_ADDS
         const uint32_t h = hi - n * 0x40800000u;
         const int32_t l = static_cast<int32_t>(lo - n * 0x35400000u);
         return (static_cast<uint64_t>(h) << 23) + static_cast<uint64_t>(static_cast<int64_t>(l));
@@ -188,20 +189,78 @@ struct Search {
     Found f;
 };
 
-// What one CTA of a row's cluster of CS works with.
-template <int CS>
+// a logit as it counts: a NaN as minus infinity, -0 as 0; in a row with plus infinities those share everything
+__device__ __forceinline__ float clean(float v) { return fmaxf(v, -INFINITY) + 0.0f; }
+__device__ __forceinline__ float clean_of(float v, bool infinite) {
+    return infinite ? (v == INFINITY ? 0.0f : -INFINITY) : clean(v);
+}
+
+// Four logits of a CTA from i (a multiple of four) on, minus infinity from `end` on.
+__device__ __forceinline__ float4 four_of(const float *from, bool wide, int i, int end) {
+    if (wide && i + 4 <= end) return __ldg(reinterpret_cast<const float4 *>(from + i));
+    float4 v;
+    v.x = i < end ? __ldg(from + i) : -INFINITY;
+    v.y = i + 1 < end ? __ldg(from + i + 1) : -INFINITY;
+    v.z = i + 2 < end ? __ldg(from + i + 2) : -INFINITY;
+    v.w = i + 3 < end ? __ldg(from + i + 3) : -INFINITY;
+    return v;
+}
+
+// What one CTA of a row's cluster of CS works with.  HELD: its logits are in shared memory, cleaned; else they are read
+// again.
+template <int CS, bool HELD>
 struct Draw {
     const DrawArgs &a;
     DrawShared &sh;
-    const float *x;    // this CTA's logits, minus infinity up to a multiple of four
+    const float *x;       // this CTA's logits (HELD: minus infinity up to a multiple of four)
+    bool wide, infinite;  // not HELD: 16-byte loads; plus infinities
     int rank, lo, n;   // tokens [lo, lo + n) of the row
     int w0, w1;        // of these, this warp's
     float m, top, c_hi, c_lo;  // the row's largest logit, this thread's
     int level, turn;   // histograms and passes so far
 
+    // a token's weight in a histogram: a part of its bin's first token's, in units of 2^-MASS (no CTA's sum passes 32 bits)
+    static constexpr int MASS_BITS = CS == 1 ? 13 : CS == 2 ? 14 : 15;
+    static_assert(static_cast<uint64_t>((DR_VOCAB + CS - 1) / CS + 3) << MASS_BITS < 1ull << 32, "a bin's sum");
+    static constexpr float MASS_ONE = static_cast<float>(1 << (23 - MASS_BITS));  // adding it leaves the units in the bits
+    static constexpr float PER_UNIT = static_cast<float>(1 << MASS_BITS) / 17592186044416.0f;  // of weights' units into these
+
     template <class T>
     __device__ __forceinline__ T *of(T *mine, int c) const {
         return cg::this_cluster().map_shared_rank(mine, c);
+    }
+
+    __device__ __forceinline__ float4 four(int i) const {
+        if constexpr (HELD) return *reinterpret_cast<const float4 *>(x + i);
+        const float4 v = four_of(x, wide, i, n);
+        return make_float4(clean_of(v.x, infinite), clean_of(v.y, infinite), clean_of(v.z, infinite), clean_of(v.w, infinite));
+    }
+
+    // f(i, four logits from i on) for this lane's tokens.  Those that are read again come four loads at a time (a load that may
+    // be cut short would wait for the one before: two branches write the same registers)
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+        const int at = w0 + 4 * (static_cast<int>(threadIdx.x) & 31);
+        if constexpr (HELD) {
+#pragma unroll 2
+            for (int i = at; i < w1; i += 128) f(i, *reinterpret_cast<const float4 *>(x + i));
+        } else {
+            constexpr int BATCH = 4;
+            for (int i0 = at; i0 < w1; i0 += 128 * BATCH) {
+                if (wide && i0 + 128 * (BATCH - 1) + 4 <= w1) {
+                    float4 v[BATCH];
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) v[j] = __ldg(reinterpret_cast<const float4 *>(x + i0 + 128 * j));
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j)
+                        f(i0 + 128 * j, make_float4(clean_of(v[j].x, infinite), clean_of(v[j].y, infinite),
+                                                    clean_of(v[j].z, infinite), clean_of(v[j].w, infinite)));
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < BATCH && i0 + 128 * j < w1; ++j) f(i0 + 128 * j, four(i0 + 128 * j));
+                }
+            }
+        }
     }
 
     // bits of d, key from above, or index
@@ -231,36 +290,34 @@ struct Draw {
         uint32_t *bins = sh.bins[b];
         for (int i = tid; i < DR_BINS; i += DR_THREADS) bins[i] = 0;
         __syncthreads();
-        const bool reach = FIRST || value(0, top, 0) <= r.hi[0];
-#pragma unroll 2
-        for (int i = w0 + 4 * (tid & 31); reach && i < w1; i += 128) {
-            const float4 v = *reinterpret_cast<const float4 *>(x + i);
-            const float l[4] = {v.x, v.y, v.z, v.w};
+        if (FIRST || value(0, top, 0) <= r.hi[0])
+            each([&](int i, float4 v) {
+                const float l[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t d = value(0, l[j], 0);
-                uint32_t bin;
-                float from = 0.0f;
-                if constexpr (FIRST) {
-                    bin = first_bin(d);
-                    if constexpr (MASS) {
-                        from = __uint_as_float(min(d & (0xffffffffu << DR_SHIFT), DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT)));
-                        if (bin == 0) from = 0.0f;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t d = value(0, l[j], 0);
+                    uint32_t bin;
+                    float from = 0.0f;
+                    if constexpr (FIRST) {
+                        bin = first_bin(d);
+                        if constexpr (MASS) {
+                            from = __uint_as_float(min(d & (0xffffffffu << DR_SHIFT), DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT)));
+                            if (bin == 0) from = 0.0f;
+                        }
+                    } else {
+                        if (d < r.lo[0] || d > r.hi[0] || side(r, d, l[j], lo + i + j) != 0) continue;
+                        bin = (value(phase, l[j], lo + i + j) - r.lo[phase]) >> shift;
+                        if constexpr (MASS) from = edge(false, phase, r, shift, bin);
                     }
-                } else {
-                    if (d < r.lo[0] || d > r.hi[0] || side(r, d, l[j], lo + i + j) != 0) continue;
-                    bin = (value(phase, l[j], lo + i + j) - r.lo[phase]) >> shift;
-                    if constexpr (MASS) from = edge(false, phase, r, shift, bin);
+                    if (!SD_INB(bin < DR_BINS && i + 3 < a.chunk, a.status, 123)) continue;  // site 123: bin
+                    if constexpr (MASS) {  // its weight as a part of the bin's first
+                        const float part = ex2_approx((from - __uint_as_float(d)) * c_hi);
+                        atomicAdd(&bins[bin], __float_as_uint(part + MASS_ONE) - __float_as_uint(MASS_ONE));
+                    } else {
+                        atomicAdd(&bins[bin], 1u);
+                    }
                 }
-                if (!SD_INB(bin < DR_BINS && i + 3 < a.chunk, a.status, 123)) continue;  // site 123: bin
-                if constexpr (MASS) {  // its weight as a part of the bin's first
-                    const float part = ex2_approx((from - __uint_as_float(d)) * c_hi);
-                    atomicAdd(&bins[bin], __float_as_uint(part + 256.0f) - 0x43800000u);
-                } else {
-                    atomicAdd(&bins[bin], 1u);
-                }
-            }
-        }
+            });
         share<FIRST, MASS>(phase, r, shift);
     }
     // The first level over the threads' largest logits alone: as many different tokens.
@@ -333,7 +390,7 @@ struct Draw {
             const Sum upto = before + warp_scan(fs);
             const uint32_t some = __ballot_sync(0xffffffffu, fs > 0), hits = __ballot_sync(0xffffffffu, fs > 0 && upto >= target);
             if (lane == (hits ? __ffs(hits) - 1 : some ? 31 - __clz(some) : 0)) {
-                if constexpr (MASS) sh.found = {static_cast<uint32_t>(bin), 0, static_cast<uint32_t>(raw >> 15), upto - fs, target};
+                if constexpr (MASS) sh.found = {static_cast<uint32_t>(bin), 0, static_cast<uint32_t>(raw >> MASS_BITS), upto - fs, target};
                 else sh.found = {static_cast<uint32_t>(bin), upto - fs, fs, 0.0f, 0.0f};
             }
         }
@@ -388,40 +445,49 @@ struct Draw {
     // CTA's in sh.cta_sum; the range's tokens in sh.at, sh.w (`listed` of them), false in `fits` if they are too many.
     template <bool RANGED, bool TOTAL, bool LOW>
     __device__ void pass(const Range &r, float low, uint64_t &before, uint64_t &all) {
-        const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, t = turn++ & 1;
+        const int tid = static_cast<int>(threadIdx.x), t = turn++ & 1;
         if (tid == 0) sh.listed = 0;
         __syncthreads();
+        uint64_t sum_a = 0, sum_b = 0, sum_k = 0;
+        const bool reach = TOTAL || (RANGED ? value(0, top, 0) <= r.hi[0] : top >= low);
         Units sa = {0, 0}, sb = {0, 0}, sk = {0, 0};
         uint32_t added = 0;
-        const bool reach = TOTAL || (RANGED ? value(0, top, 0) <= r.hi[0] : top >= low);
-#pragma unroll 2
-        for (int i = w0 + 4 * lane; reach && i < w1; i += 128) {
-            const float4 v = *reinterpret_cast<const float4 *>(x + i);  // (behind the row's end: minus infinity)
+        auto fold = [&]() {
+            if (TOTAL) sum_a += sa.sum(added);
+            sum_b += sb.sum(added);
+            if (LOW) sum_k += sk.sum(added);
+            sa = sb = sk = {0, 0};
+            added = 0;
+        };
+        if (reach)
+            each([&](int i, float4 v) {  // (behind the row's end: minus infinity)
+                if (added > DR_ADDS - 4) fold();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float2 l = h ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
-                const int at = i + 2 * h;
-                bool b0, b1;
-                if constexpr (RANGED) {
-                    const uint32_t d0 = value(0, l.x, 0), d1 = value(0, l.y, 0);
-                    b0 = d0 < r.lo[0];
-                    b1 = d1 < r.lo[0];
-                    if (!b0 && d0 <= r.hi[0]) b0 = list(r, t, d0, l.x, lo + at);
-                    if (!b1 && d1 <= r.hi[0]) b1 = list(r, t, d1, l.y, lo + at + 1);
-                } else {
-                    b0 = l.x >= low;
-                    b1 = l.y >= low;
+                for (int h = 0; h < 2; ++h) {
+                    const float2 l = h ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+                    const int at = i + 2 * h;
+                    bool b0, b1;
+                    if constexpr (RANGED) {
+                        const uint32_t d0 = value(0, l.x, 0), d1 = value(0, l.y, 0);
+                        b0 = d0 < r.lo[0];
+                        b1 = d1 < r.lo[0];
+                        if (!b0 && d0 <= r.hi[0]) b0 = list(r, t, d0, l.x, lo + at);
+                        if (!b1 && d1 <= r.hi[0]) b1 = list(r, t, d1, l.y, lo + at + 1);
+                    } else {
+                        b0 = l.x >= low;
+                        b1 = l.y >= low;
+                    }
+                    if (!TOTAL && !(b0 || b1)) continue;
+                    const float2 e = weights_of(l, m, c_hi, c_lo);
+                    const float2 eb = make_float2(b0 ? e.x : 0.0f, b1 ? e.y : 0.0f);
+                    if constexpr (TOTAL) sa.add(e);
+                    sb.add(eb);
+                    if constexpr (LOW) sk.add(make_float2(l.x >= low ? eb.x : 0.0f, l.y >= low ? eb.y : 0.0f));
+                    added += 2;
                 }
-                if (!TOTAL && !(b0 || b1)) continue;
-                const float2 e = weights_of(l, m, c_hi, c_lo);
-                const float2 eb = make_float2(b0 ? e.x : 0.0f, b1 ? e.y : 0.0f);
-                if constexpr (TOTAL) sa.add(e);
-                sb.add(eb);
-                if constexpr (LOW) sk.add(make_float2(l.x >= low ? eb.x : 0.0f, l.y >= low ? eb.y : 0.0f));
-                added += 2;
-            }
-        }
-        tell<TOTAL, LOW>(t, TOTAL ? sa.sum(added) : 0, sb.sum(added), LOW ? sk.sum(added) : 0);
+            });
+        fold();
+        tell<TOTAL, LOW>(t, sum_a, sum_b, sum_k);
         hear<RANGED>(t, before, all);
     }
     // a listed token goes into the list; whether it is before the range
@@ -484,13 +550,12 @@ struct Draw {
         if (tid == 0) sh.listed = 0;
         __syncthreads();
         if (value(0, top, 0) <= d_end)
-            for (int i = w0 + 4 * (tid & 31); i < w1; i += 128) {
-                const float4 v = *reinterpret_cast<const float4 *>(x + i);
+            each([&](int i, float4 v) {
                 const float l[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (value(0, l[j], 0) <= d_end && i + j < n) put(t, l[j], lo + i + j);
-            }
+            });
         __syncthreads();
         if (tid < DR_WARPS) sh.part[2][tid] = 0;
         if (tid < CS) *of(&sh.passed[t][rank], tid) = Passed{0, 0, 0, sh.listed};
@@ -505,9 +570,13 @@ struct Draw {
     }
     // how many tokens are before a range, in every CTA
     __device__ uint32_t count_before(const Range &r) {
-        const int tid = static_cast<int>(threadIdx.x), t = turn++ & 1;
+        const int t = turn++ & 1;
         uint64_t mine = 0;
-        for (int i = tid; i < n; i += DR_THREADS) mine += side(r, value(0, x[i], 0), x[i], lo + i) < 0 ? 1 : 0;
+        each([&](int i, float4 v) {
+            const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mine += side(r, value(0, l[j], 0), l[j], lo + i + j) < 0 ? 1 : 0;
+        });
         tell<false, false>(t, 0, mine, 0);
         uint32_t sum = 0;
         for (int c = 0; c < CS; ++c) sum += static_cast<uint32_t>(sh.passed[t][c].before);
@@ -547,11 +616,11 @@ struct Draw {
     uint32_t rank_n;
 };
 
-template <int CS>
-__global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
+template <int CS, bool HELD>
+__global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     DrawShared &sh = *reinterpret_cast<DrawShared *>(smem_raw);
-    float *x = reinterpret_cast<float *>(smem_raw + sizeof(DrawShared));
+    float *held = reinterpret_cast<float *>(smem_raw + sizeof(DrawShared));
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / CS;
     const int rank = static_cast<int>(blockIdx.x % CS);  // (the clusters are made of neighbours)
@@ -579,31 +648,25 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
     // ---- the row's tokens of this CTA; a NaN counts as minus infinity, -0 as 0, and minus infinity fills up the last four
     const int run = (n + 4 * DR_WARPS - 1) / (4 * DR_WARPS) * 4, w0 = min(n, warp * run), w1 = min(n, w0 + run);
     float mine = -INFINITY;
-    auto clean = [](float v) { return fmaxf(v, -INFINITY) + 0.0f; };
     const bool wide = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
-    constexpr int FLY = 5;
+    auto take = [&](int i, float4 v) {
+        if (!SD_INB(i + 4 <= a.chunk, a.status, 125)) return;  // site 125: logits
+        const float4 c = make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+        if constexpr (HELD) *reinterpret_cast<float4 *>(held + i) = c;
+        mine = fmaxf(mine, fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)));
+    };
+    constexpr int FLY = HELD ? 5 : 8;
+    const int whole = wide ? w0 + (w1 - w0) / 4 * 4 : w0;
     for (int i0 = w0 + 4 * lane; i0 < w1; i0 += FLY * 128) {
         float4 v[FLY];
 #pragma unroll
-        for (int j = 0; j < FLY; ++j) {
-            const int i = i0 + 128 * j;
-            if (wide && i + 4 <= w1) {
-                v[j] = __ldcs(reinterpret_cast<const float4 *>(from + i));
-            } else if (i < w1) {
-                v[j].x = __ldcs(from + i);
-                v[j].y = i + 1 < w1 ? __ldcs(from + i + 1) : -INFINITY;
-                v[j].z = i + 2 < w1 ? __ldcs(from + i + 2) : -INFINITY;
-                v[j].w = i + 3 < w1 ? __ldcs(from + i + 3) : -INFINITY;
-            }
-        }
+        for (int j = 0; j < FLY; ++j)
+            if (i0 + 128 * j < whole) v[j] = __ldg(reinterpret_cast<const float4 *>(from + i0 + 128 * j));
 #pragma unroll
         for (int j = 0; j < FLY; ++j) {
             const int i = i0 + 128 * j;
-            if (i < w1 && SD_INB(i + 4 <= a.chunk, a.status, 125)) {  // site 125: logits
-                const float4 c = make_float4(clean(v[j].x), clean(v[j].y), clean(v[j].z), clean(v[j].w));
-                *reinterpret_cast<float4 *>(x + i) = c;
-                mine = fmaxf(mine, fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)));
-            }
+            if (i < whole) take(i, v[j]);
+            else if (i < w1) take(i, four_of(from, false, i, w1));
         }
     }
     float top = mine;
@@ -622,8 +685,10 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
 #pragma unroll
     for (int c = 0; c < CS; ++c) m = fmaxf(m, sh.tops[c]);
     const bool bad = sh.bad || m == -INFINITY;
-    if (m == INFINITY) {  // those tokens share everything
-        for (int i = tid; i < n; i += DR_THREADS) x[i] = x[i] == INFINITY ? 0.0f : -INFINITY;
+    const bool infinite = m == INFINITY;
+    if (infinite) {
+        if constexpr (HELD)
+            for (int i = tid; i < n; i += DR_THREADS) held[i] = clean_of(held[i], true);
         mine = mine == INFINITY ? 0.0f : -INFINITY;
         m = 0.0f;
     }
@@ -642,7 +707,7 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             if (a.prob) a.prob[row] = 0.0f;
         }
     } else {
-        Draw<CS> w = {a, sh, x, rank, lo, n, w0, w1, m, mine, c_hi, c_lo, 0, 0};
+        Draw<CS, HELD> w = {a, sh, HELD ? held : from, wide, infinite, rank, lo, n, w0, w1, m, mine, c_hi, c_lo, 0, 0};
         const float p = sh.p;
         const uint32_t k = static_cast<uint32_t>(sh.k), low_d = __float_as_uint(fabsf(low - m));
         const bool has_low = low > -3.402823466e38f;
@@ -655,7 +720,7 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
             few = k <= DR_SMALL_K;
             if (few) {
                 w.histogram_of_tops();
-                w.gather(Draw<CS>::bin_end(w.template locate<false>(true, 0, none, DR_SHIFT, k, 0.0f).bin));
+                w.gather(Draw<CS, HELD>::bin_end(w.template locate<false>(true, 0, none, DR_SHIFT, k, 0.0f).bin));
                 few = w.fits;
                 w.ranks(0, 0);
             }
@@ -685,7 +750,7 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
         }
         if (nucleus) {
             const bool known = target != 0;  // else the histogram's own sum says about where to look
-            const float per_unit = 1.0f / 536870912.0f;  // 2^-29: of weights' units into the bins'
+            const float per_unit = Draw<CS, HELD>::PER_UNIT;
             Search q = w.template start<true>(0, known ? static_cast<float>(target) * per_unit : -p);
             const float about = q.f.target_m;
             while (q.f.n > DR_LIST - 32) w.template refine<true>(q, 0, about);
@@ -759,12 +824,16 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
                 const int r0 = min(n, q * run), r1 = min(n, r0 + run);
                 for (int i0 = r0; i0 < r1; i0 += 4 * DR_THREADS) {
                     const int i = i0 + 4 * tid;
-                    float e[4];
+                    float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                     uint64_t s = 0;
+                    if (i < r1) {
+                        const float4 v = w.four(i);
+                        const float l[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        e[j] = i + j < r1 && place_of(x[i + j], lo + i + j) >= thr ? weight_of(x[i + j], m, c_hi, c_lo) : 0.0f;
-                        s += units(e[j]);
+                        for (int j = 0; j < 4; ++j) {
+                            if (i + j < r1 && place_of(l[j], lo + i + j) >= thr) e[j] = weight_of(l[j], m, c_hi, c_lo);
+                            s += units(e[j]);
+                        }
                     }
                     const uint64_t inc = warp_scan(s);
                     __syncthreads();
@@ -793,28 +862,37 @@ __global__ void __launch_bounds__(DR_THREADS) sample_kernel(const DrawArgs a) {
         float *to = a.probs + row * a.ldp + lo;
         const float tl = key_logit(static_cast<uint32_t>(thr >> 32));
         const int ti = place_idx(thr);  // (the last index where all of that logit are kept)
-        auto prob = [&](int i) {
-            const float l = x[i];
+        auto prob = [&](float l, int i) {
             const bool in = !bad && (l > tl || (l == tl && (lo + i <= ti || ti < 0)));
             return in ? weight_of(l, m, c_hi, c_lo) * inv : 0.0f;
         };
-        const int m4 = (reinterpret_cast<uintptr_t>(to) & 15) == 0 ? n / 4 : 0;
-        for (int i = tid; i < m4; i += DR_THREADS)
-            __stcs(reinterpret_cast<float4 *>(to) + i, make_float4(prob(4 * i), prob(4 * i + 1), prob(4 * i + 2), prob(4 * i + 3)));
-        for (int i = 4 * m4 + tid; i < n; i += DR_THREADS) to[i] = prob(i);
+        const bool wide_to = (reinterpret_cast<uintptr_t>(to) & 15) == 0;
+        const Draw<CS, HELD> w = {a, sh, HELD ? held : from, wide, infinite, rank, lo, n};
+        for (int i = 4 * tid; i < n; i += 4 * DR_THREADS) {
+            const float4 v = w.four(i);
+            const float4 e = make_float4(prob(v.x, i), prob(v.y, i + 1), prob(v.z, i + 2), prob(v.w, i + 3));
+            if (wide_to && i + 4 <= n) {
+                __stcs(reinterpret_cast<float4 *>(to + i), e);
+            } else {
+                to[i] = e.x;
+                if (i + 1 < n) to[i + 1] = e.y;
+                if (i + 2 < n) to[i + 2] = e.z;
+                if (i + 3 < n) to[i + 3] = e.w;
+            }
+        }
     }
     cluster_arrive();  // no CTA leaves while another may read its shared memory
     cluster_wait();
 }
 
-template <int CS>
+template <int CS, bool HELD>
 static cudaError_t sample_launch(const DrawArgs &a, int N, cudaStream_t s) {
-    const cudaError_t e = allow_max_dynamic_smem(sample_kernel<CS>);
+    const cudaError_t e = allow_max_dynamic_smem(sample_kernel<CS, HELD>);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(N) * CS);
     cfg.blockDim = dim3(DR_THREADS);
-    cfg.dynamicSmemBytes = sizeof(DrawShared) + static_cast<size_t>(a.chunk) * 4;
+    cfg.dynamicSmemBytes = sizeof(DrawShared) + (HELD ? static_cast<size_t>(a.chunk) * 4 : 0);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -824,7 +902,7 @@ static cudaError_t sample_launch(const DrawArgs &a, int N, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<CS>, a);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<CS, HELD>, a);
 }
 
 }  // namespace sdv
@@ -840,11 +918,17 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     if (!logits || !u || !out_tokens || N < 1 || vocab < 1) return SD_EINVAL;
     if (ld < vocab || (out_probs && ld_probs < vocab)) return SD_EINVAL;
     if (!aligned(logits, 4) || (out_probs && !aligned(out_probs, 4))) return SD_EINVAL;
-    if (vocab > static_cast<int64_t>(DR_MOST_CTAS) * DR_CHUNK || N > INT32_MAX / DR_MOST_CTAS) return SD_EUNSUPPORTED;
+    if (vocab > DR_VOCAB || N > INT32_MAX / DR_MOST_CTAS) return SD_EUNSUPPORTED;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
+    // As many CTAs per row as the GPU holds at once beside the other rows', two per SM; two at least where top-p may have to
+    // order a flat row (95 us for one CTA); no more than the row has 1024 tokens for.  256 rows of 151936 tokens by
+    // 1 / 2 / 4 / 8 CTAs: top-k of 50 54 / 59 / 74 / 103 us, each row with its own settings 132 / 99 / 96 / 119 us; 64 rows,
+    // top-k 29 / 20 / 18 / 26 us.
+    const int slots = 2 * num_sms(), least = top_p ? 2 : 1;
     int ctas = DR_MOST_CTAS;
-    while (ctas > 1 && vocab <= static_cast<int64_t>(ctas) * 1024) ctas /= 2;
+    while (ctas > 1 && (vocab <= static_cast<int64_t>(ctas) * 1024 || (ctas > least && static_cast<int64_t>(N) * ctas > slots)))
+        ctas /= 2;
     DrawArgs a = {};
     a.logits = logits;
     a.ld = ld;
@@ -861,10 +945,14 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     a.ldp = ld_probs;
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = ctas == 1   ? sample_launch<1>(a, N, s)
-                          : ctas == 2 ? sample_launch<2>(a, N, s)
-                          : ctas == 4 ? sample_launch<4>(a, N, s)
-                                      : sample_launch<8>(a, N, s);
+    // (two CTAs of an SM hold their logits in its shared memory where they fit)
+    const bool held = (sizeof(DrawShared) + static_cast<size_t>(a.chunk) * 4 + 1024) * 2 <= 228 * 1024;
+    auto run = [&](auto h) {
+        constexpr bool H = decltype(h)::value;
+        return ctas == 1 ? sample_launch<1, H>(a, N, s) : ctas == 2 ? sample_launch<2, H>(a, N, s)
+               : ctas == 4 ? sample_launch<4, H>(a, N, s) : sample_launch<8, H>(a, N, s);
+    };
+    const cudaError_t e = held ? run(std::true_type()) : run(std::false_type());
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
