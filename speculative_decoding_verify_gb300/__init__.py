@@ -143,6 +143,7 @@ def lib():
             "sd_set_pdl": ([I], None),
             "sd_debug_block_dots": ([I, P, I64, I64, P, I32, P, P], I),
             "sd_debug_silu_mul_requant": ([P, P, I32, I64, P, P, P], I),
+            "sd_debug_share_from": ([I64], None),
             "sd_debug_cexp": ([P, I64, P, P], I),
             "sd_debug_philox": ([U64, I64, I64, P, P], I),
             "sd_debug_wait_timeout": ([I64, P], I),
@@ -772,6 +773,11 @@ def debug_silu_mul_requant(g: torch.Tensor, u: torch.Tensor):
     s = torch.empty((M, F // 32), dtype=torch.float32, device=g.device)
     _check(lib().sd_debug_silu_mul_requant(_p(g), _p(u), M, F, _p(q), _p(s), _stream()), "sd_debug_silu_mul_requant")
     return q, s
+
+
+def debug_share_from(tiles: int):
+    """Tiles that paged_attn_shared has to be able to leave out before it shares (3000 by default)."""
+    lib().sd_debug_share_from(tiles)
 
 
 def debug_cexp(x: torch.Tensor) -> torch.Tensor:

@@ -58,13 +58,18 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
         *abort = 0;
         fence_barrier_init();
     }
-    pdl_wait();
+    // (PA_OWN: as in paged_wide_kernel)
+    if (MODE != PA_OWN || !a.beside) pdl_wait();
     pdl_launch_dependents();
     Sched sc;
-    if (!make_sched<RPG, PA_THREADS, MODE>(a, prefix, ln, sc)) return;
+    if (!make_sched<RPG, PA_THREADS, MODE>(a, prefix, ln, sc)) {
+        if constexpr (MODE == PA_OWN) pdl_wait();
+        return;
+    }
 
     if (warp == PA_CW) {
         produce_tiles<T, D, RPG, 0, 1, MODE>(a, sc, &tmk, &tmv, ring, a.nst, full, empty, abort);
+        if constexpr (MODE == PA_OWN) pdl_wait();
         return;
     }
 
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                 ph ^= 1u;
             }
         }
-        if (bar_any(1, 32 * PA_CW, !ok)) return;  // every consumer warp leaves together
+        if (bar_any(1, 32 * PA_CW, !ok)) break;  // every consumer warp leaves together
         // ---- join the warps' states and write the piece: rows that are whole go out, others become partials
         const bool complete = p.t0 == 0 && p.t1 == p.st.T;
         const int pslot = 2 * static_cast<int>(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
@@ -470,7 +475,9 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                 }
             }
             const int r = tid >> 4, tr = nt * 8 + r, tg = p.rg * RPG + tr;
-            float f[PA_CW], mx = PA_NEG, lv = 0.0f, inv = 0.0f;
+            const bool joins = MODE == PA_OWN && complete && p.st.lo_tile > 0;
+            float f[PA_CW], mx = PA_NEG, lv = 0.0f, inv = 0.0f, of_prefix = 0.0f;
+            if (joins) pdl_wait();
 #pragma unroll
             for (int cc = 0; cc < D / 64; ++cc) {  // 64 columns at a time
                 float *ow = sm_o + warp * 8 * SD;
@@ -494,9 +501,13 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                     }
                     inv = lv == 0.0f ? 0.0f : 1.0f / lv;
                     if (!complete && tg < rows && (tid & 15) == 0) a.part_ml[pslot * RPG + tr] = make_float2(mx, lv);
-                    if constexpr (MODE != PA_ALL)
-                        if (complete && tg < rows && (tid & 15) == 0)
-                            put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
+                    if constexpr (MODE == PA_PREFIX)
+                        if (complete && tg < rows && (tid & 15) == 0) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
+                    if (joins && tg < rows) {
+                        const float2 y = with_prefix(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
+                        inv = y.x;
+                        of_prefix = y.y;
+                    }
                 }
                 if (tg < rows && SD_INB(p.b < a.B && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh < a.H_kv && (complete || (pslot + 1) * RPG <= a.part_rows),
                                         a.status, 117)) {  // site 117: rows of a piece
@@ -513,6 +524,11 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                         v.w = fmaf(x.w, f[w], v.w);
                     }
                     if (complete) v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    if (joins) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(prefix_row(a, p.b, i, h, D) + 64 * cc + d));
+                        v = make_float4(fmaf(y.x, of_prefix, v.x), fmaf(y.y, of_prefix, v.y), fmaf(y.z, of_prefix, v.z),
+                                        fmaf(y.w, of_prefix, v.w));
+                    }
                     *reinterpret_cast<float4 *>(op + 64 * cc + d) = v;
                 }
                 named_bar_sync(1, 32 * PA_CW);
@@ -530,11 +546,13 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
             }
             named_bar_sync(1, 32 * PA_CW);
             if (*last) {
+                if (MODE == PA_OWN && p.st.lo_tile > 0) pdl_wait();
                 join_partials<RPG, D, 32 * PA_CW, MODE>(a, p, c0, c1, tid, sm_o, 1);
             }
         }
         u += p.t1 - p.t0;
     }
+    if constexpr (MODE == PA_OWN) pdl_wait();
 }
 
 struct PaPlan {
@@ -582,11 +600,12 @@ static bool pa_wide(int rows, int D) { return rows > (D == 64 ? PA_WIDE_ROWS_64 
 
 // workspace: counters of the largest grid, then the partials: two per CTA, of 16 rows on two CTAs per SM or
 // of 128 rows on one
+size_t pa_counters() { return (static_cast<size_t>(num_sms()) * 2 * 4 + 255) / 256 * 256; }
 size_t pa_workspace(int D, size_t *off_ml, size_t *off_o) {
     const size_t sms = num_sms() > 0 ? num_sms() : 0;
     if (!sms) return 0;
     const size_t rows = sms * 2 * 128;  // 4 x 16 rows per SM take less
-    const size_t ml = (2 * sms * 4 + 255) / 256 * 256, o = ml + (rows * 8 + 255) / 256 * 256;
+    const size_t ml = pa_counters(), o = ml + (rows * 8 + 255) / 256 * 256;
     if (off_ml) *off_ml = ml;
     if (off_o) *off_o = o;
     return o + rows * static_cast<size_t>(D) * 4;
@@ -725,7 +744,8 @@ sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s) {
             a.out = c.a.out + b0 * a.o_sb;
             if (mode == PA_OWN) {
                 a.skip = c.a.skip + b0;
-                a.row_ml = c.a.row_ml + static_cast<int64_t>(b0) * a.M * a.H;
+                a.start = c.a.start + b0;
+                a.beside = b0 == 0;
             }
             if (pa_wide_run(mode, c, a, rows, s) != cudaSuccess) return SD_ECUDA;
         }
@@ -734,6 +754,7 @@ sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s) {
     PaPlan p;
     if (!pa_plan(c.type, B, rows, c.D, p)) return SD_ECUDA;
     a.nst = p.nst;
+    a.beside = 1;
     const cudaError_t e = mode == PA_ALL ? pa_launch_t<PA_ALL>(c.type, c.D, p, a, c.tmk, c.tmv, s)
                                          : pa_launch_t<PA_OWN>(c.type, c.D, p, a, c.tmk, c.tmv, s);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;

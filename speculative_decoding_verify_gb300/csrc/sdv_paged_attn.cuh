@@ -38,8 +38,12 @@ struct PagedArgs {
     // PA_PREFIX: lens, n_new hold the groups' shared rows and numbers of new rows, first[v] where group v's begin in
     // rows_of (sequence * M + row), leader[v] a sequence whose table names the group's pages; out [row of rows_of][H][D]
     const int32_t *first, *leader, *rows_of;
-    const int32_t *skip;  // PA_OWN: [B] tiles of a sequence's shared prefix
-    float2 *row_ml;       // maximum and sum behind each row of out and head: PA_PREFIX [row of rows_of][H], PA_OWN [B * M][H]
+    // what the prefixes' rows came to: maximum and sum [row of rows_of][H] and, in out of PA_PREFIX, normalised outputs
+    // [row of rows_of][H][D]
+    float2 *pre_ml;
+    const float *pre_o;
+    const int32_t *skip, *start;  // PA_OWN: [B] tiles of a sequence's prefix, and where its rows are in rows_of
+    int32_t beside;               // PA_OWN: 1 where the launch before is the prefixes' (and not another of its own)
 };
 
 // query and output row of new row i of sequence (or group) b
@@ -57,11 +61,20 @@ __device__ __forceinline__ float *out_row(const PagedArgs &a, int b, int i, int 
     if constexpr (MODE == PA_PREFIX) return a.out + (static_cast<int64_t>(a.first[b] + i) * a.H + h) * D;
     else return a.out + b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D;
 }
-// the softmax statistics behind a finished row
-template <int MODE>
+// the softmax statistics behind a finished row of a prefix
 __device__ __forceinline__ void put_ml(const PagedArgs &a, int b, int i, int h, float m, float l) {
-    if constexpr (MODE == PA_PREFIX) a.row_ml[static_cast<int64_t>(a.first[b] + i) * a.H + h] = make_float2(m, l);
-    if constexpr (MODE == PA_OWN) a.row_ml[(static_cast<int64_t>(b) * a.M + i) * a.H + h] = make_float2(m, l);
+    a.pre_ml[static_cast<int64_t>(a.first[b] + i) * a.H + h] = make_float2(m, l);
+}
+// A row's own keys came to maximum m, sum l and outputs o, its prefix to (m', l', o' / l'): the whole softmax is
+//   (2^(m - n) o + 2^(m' - n) l' (o' / l')) / (2^(m - n) l + 2^(m' - n) l'),  n = max(m, m').
+// Returns the factors of o and of the prefix's outputs.
+__device__ __forceinline__ float2 with_prefix(const PagedArgs &a, int b, int i, int h, float m, float l) {
+    const float2 p = __ldcg(&a.pre_ml[static_cast<int64_t>(a.start[b] + i) * a.H + h]);
+    const float n = fmaxf(m, p.x), w = exp2f(m - n), wp = p.y * exp2f(p.x - n), inv = 1.0f / fmaf(l, w, wp);
+    return make_float2(w * inv, wp * inv);
+}
+__device__ __forceinline__ const float *prefix_row(const PagedArgs &a, int b, int i, int h, int D) {
+    return a.pre_o + (static_cast<int64_t>(a.start[b] + i) * a.H + h) * D;
 }
 
 // the scales of 8-bit rows where there is no page
@@ -455,9 +468,12 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
         }
         mx_of[tid] = mx;
         sum_of[tid] = lv == 0.0f ? 0.0f : 1.0f / lv;
-        if constexpr (MODE != PA_ALL) {
-            const int tg = p.rg * RPG + tid;
-            put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * l_unit);
+        const int tg = p.rg * RPG + tid;
+        if constexpr (MODE == PA_PREFIX) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * l_unit);
+        if (MODE == PA_OWN && p.st.lo_tile > 0) {
+            const float2 f = with_prefix(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * l_unit);
+            sum_of[tid] = f.x * l_unit;
+            weight[tid] = f.y;
         }
     }
     const int r0 = tid / LR, col = tid % LR;
@@ -466,6 +482,12 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
     for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int k = 0; k < NV; ++k) v[i][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float of_prefix[NR] = {};
+    if (MODE == PA_OWN && p.st.lo_tile > 0) {
+        named_bar_sync(bar, NTHR);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) of_prefix[i] = r0 + i * RT < rows ? weight[r0 + i * RT] : 0.0f;
+    }
     if (!SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RPG <= a.part_rows && rows <= RPG &&
                     (p.rg * RPG + rows - 1) / a.g < (MODE == PA_PREFIX ? p.n : a.M),
                 a.status, 116))  // site 116: partials of a join, its output rows
@@ -516,8 +538,16 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
             const float inv = sum_of[tr];
             float4 *to = reinterpret_cast<float4 *>(out_row<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, D)) + col;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                to[k * LR] = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
+            for (int k = 0; k < NV; ++k) {
+                float4 x = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
+                if (MODE == PA_OWN && p.st.lo_tile > 0) {
+                    const float *from = prefix_row(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, D);
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(from) + col + k * LR);
+                    const float f = of_prefix[i];
+                    x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+                }
+                to[k * LR] = x;
+            }
         }
     }
     named_bar_sync(bar, NTHR);
@@ -530,6 +560,7 @@ struct PaCall {
     int32_t type, D;
 };
 size_t pa_workspace(int D, size_t *off_ml, size_t *off_o);
+size_t pa_counters();  // bytes of counters at its start
 sd_status pa_call(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
                   int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride, int64_t q_row_stride,
                   const int32_t *parent, int32_t window, int32_t sinks, float *out, int64_t out_seq_stride,

@@ -265,10 +265,15 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         for (int i = 0; i < 6; ++i) badw[i] = 0;
         fence_barrier_init();
     }
-    pdl_wait();
+    // (PA_OWN starts beside the prefixes' launch, whose CTAs have all seen what was before it, and waits for it where it reads
+    // their outputs, and ahead of its end)
+    if (MODE != PA_OWN || !a.beside) pdl_wait();
     pdl_launch_dependents();
     Sched sc;
-    if (!make_sched<RP, W::THREADS, MODE>(a, prefix, ln, sc)) return;
+    if (!make_sched<RP, W::THREADS, MODE>(a, prefix, ln, sc)) {
+        if constexpr (MODE == PA_OWN) pdl_wait();
+        return;
+    }
     if (warp == W::WARP_M) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tbase)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -823,10 +828,23 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 lv = fmaf(x, ex2(sm_m[j * RP + r] - mx), lv);
             }
             const float unit = W::I8 ? __uint_as_float(vunit) : 1.0f;
-            const float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
+            float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
+            // a finished row that has a prefix: the factor of the prefix's outputs for the threads that write it
+            const bool joins = MODE == PA_OWN && p.st.lo_tile > 0;
+            float *of_prefix = sm_m + PW_SOFT;
+            auto join_prefix = [&](float rm, float rl) {
+                const float2 y = real ? with_prefix(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, rm, rl * PW_UNIT) : make_float2(0.0f, 0.0f);
+                if (lg == 0 && grp == 0) of_prefix[r] = y.y;
+                return y.x * PW_UNIT;
+            };
+            if constexpr (MODE == PA_OWN)
+                if (joins) {
+                    pdl_wait();
+                    if (complete) f = ex2(m - mx) * unit * join_prefix(mx, lv);
+                }
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
-            if constexpr (MODE != PA_ALL)
-                if (complete && real && lg == 0 && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * PW_UNIT);
+            if constexpr (MODE == PA_PREFIX)
+                if (complete && real && lg == 0 && grp == 0) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * PW_UNIT);
             // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared
             // memory: thread = 4 columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
             auto write_rows = [&](bool final, float fac) {
@@ -860,6 +878,13 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                                 const float4 x = *reinterpret_cast<const float4 *>(
                                     scratch + (wg * 128 + j * RP + wr + RW * k) * 20 + 4 * (tid & 3));
                                 v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+                            }
+                            if (joins && final) {
+                                const int y = p.rg * RP + wr + RW * k;
+                                const float g = of_prefix[wr + RW * k];
+                                const float4 x = __ldcg(reinterpret_cast<const float4 *>(
+                                    prefix_row(a, p.b, y / a.g, p.kh * a.g + y % a.g, D) + wc + d));
+                                v = make_float4(fmaf(x.x, g, v.x), fmaf(x.y, g, v.y), fmaf(x.z, g, v.z), fmaf(x.w, g, v.w));
                             }
                             *reinterpret_cast<float4 *>(to[k] + d) = v;
                         }
@@ -930,8 +955,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         }
                         fac = jl == 0.0f ? 0.0f : 1.0f / jl;
                         rows_ready = true;
-                        if constexpr (MODE != PA_ALL)
-                            if (real && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, jm, jl * PW_UNIT);
+                        if constexpr (MODE == PA_PREFIX)
+                            if (real && grp == 0) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, jm, jl * PW_UNIT);
+                        if constexpr (MODE == PA_OWN)
+                            if (joins) fac = join_prefix(jm, jl);
                     }
                 }
             }
@@ -941,6 +968,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         }
     }
     // ---- every role is done
+    if constexpr (MODE == PA_OWN) pdl_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == W::WARP_M) {

@@ -21,7 +21,9 @@ def sdv():
     b.build()
     import speculative_decoding_verify_gb300 as m
     m.lib()
-    return m
+    m.debug_share_from(1)  # small groups too
+    yield m
+    m.debug_share_from(3000)
 
 
 def share(c, groups):
@@ -110,6 +112,17 @@ def test_trees(sdv, dtype, M):
 def test_long_prefixes_cut_between_ctas(sdv, dtype):
     lens = [20000, 20100, 20037, 50]
     check(sdv, 1, lens, [1, 2, 3, 3], {(0, 1, 2): 1240}, 3, 4, 1, 128, 16, dtype)
+
+
+@pytest.mark.parametrize("rows", [63, 64, 65])
+def test_the_least_that_is_shared(sdv, rows):
+    """Around the number of tiles from which on a prefix is computed once: 3 other members of 2 heads by 5 tiles."""
+    try:
+        for tiles in (29, 30, 31, 1 << 30):
+            sdv.debug_share_from(tiles)
+            check(sdv, rows, [256 + rows] * 4, [2] * 4, {(0, 1, 2, 3): (256 + rows) // 8}, 2, 4, 2, 64, 8, "f16")
+    finally:
+        sdv.debug_share_from(1)
 
 
 def test_prefixes_that_differ_in_size_by_far(sdv):
