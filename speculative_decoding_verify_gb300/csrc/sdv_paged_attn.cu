@@ -28,7 +28,7 @@ namespace sdv {
 // form is held to that, 162 -> 125 us for 16 sequences of 16000 bf16 rows; at D = 128 it would spill 60 registers and
 // take 20 % longer.)
 template <int T, int D, int NT, int MODE>
-__global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
+__global__ void __launch_bounds__(PA_THREADS, D == 64 || (MODE == PA_OWN && D == 128 && NT == 1) ? 2 : 0)
     paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
     using LY = PaLayout<T, D>;
@@ -85,6 +85,10 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
     while (u < sc.u1) {
         const Piece p = piece_at<RPG, MODE>(a, sc, u, b);
         b = p.b;
+        if (MODE == PA_OWN && p.t1 <= p.t0) {
+            u = p.next;
+            continue;
+        }
         const int rows = p.n * a.g, total = MODE == PA_PREFIX ? p.len : p.len + p.n;
         // B fragments of query row g of each 8-row tile, in parts; fp16 parts of a row scaled by 2^(11-e) for
         // max |q| in [2^(e-1), 2^e), so that neither part is subnormal
@@ -475,9 +479,7 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                 }
             }
             const int r = tid >> 4, tr = nt * 8 + r, tg = p.rg * RPG + tr;
-            const bool joins = MODE == PA_OWN && complete && p.st.lo_tile > 0;
-            float f[PA_CW], mx = PA_NEG, lv = 0.0f, inv = 0.0f, of_prefix = 0.0f;
-            if (joins) pdl_wait();
+            float f[PA_CW], mx = PA_NEG, lv = 0.0f, inv = 0.0f;
 #pragma unroll
             for (int cc = 0; cc < D / 64; ++cc) {  // 64 columns at a time
                 float *ow = sm_o + warp * 8 * SD;
@@ -501,13 +503,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                     }
                     inv = lv == 0.0f ? 0.0f : 1.0f / lv;
                     if (!complete && tg < rows && (tid & 15) == 0) a.part_ml[pslot * RPG + tr] = make_float2(mx, lv);
-                    if constexpr (MODE == PA_PREFIX)
-                        if (complete && tg < rows && (tid & 15) == 0) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
-                    if (joins && tg < rows) {
-                        const float2 y = with_prefix(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
-                        inv = y.x;
-                        of_prefix = y.y;
-                    }
+                    if constexpr (MODE != PA_ALL)
+                        if (complete && tg < rows && (tid & 15) == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
                 }
                 if (tg < rows && SD_INB(p.b < a.B && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh < a.H_kv && (complete || (pslot + 1) * RPG <= a.part_rows),
                                         a.status, 117)) {  // site 117: rows of a piece
@@ -524,17 +521,12 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
                         v.w = fmaf(x.w, f[w], v.w);
                     }
                     if (complete) v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                    if (joins) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(prefix_row(a, p.b, i, h, D) + 64 * cc + d));
-                        v = make_float4(fmaf(y.x, of_prefix, v.x), fmaf(y.y, of_prefix, v.y), fmaf(y.z, of_prefix, v.z),
-                                        fmaf(y.w, of_prefix, v.w));
-                    }
                     *reinterpret_cast<float4 *>(op + 64 * cc + d) = v;
                 }
                 named_bar_sync(1, 32 * PA_CW);
             }
         }
-        if (!complete) {
+        if (MODE != PA_PREFIX && !complete) {
             // the last of the run's CTAs to come here joins their partials, in the order of their keys
             const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
             __threadfence();
@@ -546,11 +538,10 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 ? 2 : 0)
             }
             named_bar_sync(1, 32 * PA_CW);
             if (*last) {
-                if (MODE == PA_OWN && p.st.lo_tile > 0) pdl_wait();
                 join_partials<RPG, D, 32 * PA_CW, MODE>(a, p, c0, c1, tid, sm_o, 1);
             }
         }
-        u += p.t1 - p.t0;
+        u = behind<MODE>(p, u);
     }
     if constexpr (MODE == PA_OWN) pdl_wait();
 }
@@ -728,49 +719,78 @@ static cudaError_t pa_wide_run(PaMode mode, const PaCall &c, const PagedArgs &a,
     return run(a, c.tmk, c.tmv, c.D, rows, grid, s);
 }
 
-sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s) {
-    PagedArgs a = c.a;
-    const int rows = a.M * a.g, B = a.B;
-    if (pa_wide(rows, c.D)) {
-        const int part = B <= PA_WIDE_B ? B : (B + 1) / 2;
-        static_assert(PG_MAX_B <= 2 * PA_WIDE_B, "two launches hold the most sequences");
-        for (int b0 = 0; b0 < B; b0 += part) {
-            a.B = B - b0 < part ? B - b0 : part;
-            a.table = c.a.table + static_cast<int64_t>(b0) * a.width;
-            a.lens = c.a.lens + b0;
-            a.n_new = c.a.n_new ? c.a.n_new + b0 : nullptr;
-            a.parent = c.a.parent ? c.a.parent + static_cast<int64_t>(b0) * a.M : nullptr;
-            a.q = c.a.q + b0 * a.q_sb;
-            a.out = c.a.out + b0 * a.o_sb;
-            if (mode == PA_OWN) {
-                a.skip = c.a.skip + b0;
-                a.start = c.a.start + b0;
-                a.beside = b0 == 0;
-            }
-            if (pa_wide_run(mode, c, a, rows, s) != cudaSuccess) return SD_ECUDA;
-        }
-        return SD_OK;
-    }
+// Tiles behind a prefix up to which the kernel of few rows takes a sequence whatever its query rows are: it holds more runs at
+// a time, each with less ahead of its first tile.
+constexpr int PA_SHORT = 8;
+
+static sd_status pa_narrow_run(PaMode mode, const PaCall &c, const PagedArgs &from, cudaStream_t s) {
     PaPlan p;
-    if (!pa_plan(c.type, B, rows, c.D, p)) return SD_ECUDA;
+    PagedArgs a = from;
+    // (short runs: 8 rows of D <= 128 at a time, two CTAs per SM, hide more of each other's latency than 16)
+    const int rows = mode == PA_PREFIX ? 16 : mode == PA_OWN && c.D <= 128 && a.own_max == PA_SHORT ? 8 : a.M * a.g;
+    if (!pa_plan(c.type, a.B, rows, c.D, p)) return SD_ECUDA;
     a.nst = p.nst;
-    a.beside = 1;
-    const cudaError_t e = mode == PA_ALL ? pa_launch_t<PA_ALL>(c.type, c.D, p, a, c.tmk, c.tmv, s)
-                                         : pa_launch_t<PA_OWN>(c.type, c.D, p, a, c.tmk, c.tmv, s);
+    cudaError_t e;
+    if (mode == PA_PREFIX)
+        e = c.type == SD_KV_F16    ? pa_launch<SD_KV_F16, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s)
+            : c.type == SD_KV_BF16 ? pa_launch<SD_KV_BF16, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s)
+                                   : pa_launch<SD_KV_I8, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s);
+    else
+        e = mode == PA_ALL ? pa_launch_t<PA_ALL>(c.type, c.D, p, a, c.tmk, c.tmv, s)
+                           : pa_launch_t<PA_OWN>(c.type, c.D, p, a, c.tmk, c.tmv, s);
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
-// A prefix has the query rows of at least two sequences: the tensor-memory kernel takes them but at D = 256.
-sd_status pa_prefix(const PaCall &c, int rows, cudaStream_t s) {
-    if (c.D <= 128) return pa_wide_run(PA_PREFIX, c, c.a, rows, s) == cudaSuccess ? SD_OK : SD_ECUDA;
-    PaPlan p;
+sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s) {
     PagedArgs a = c.a;
-    if (!pa_plan(c.type, a.B, 16, c.D, p)) return SD_ECUDA;
-    a.nst = p.nst;
-    const cudaError_t e = c.type == SD_KV_F16    ? pa_launch<SD_KV_F16, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s)
-                          : c.type == SD_KV_BF16 ? pa_launch<SD_KV_BF16, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s)
-                                                 : pa_launch<SD_KV_I8, 256, 2, PA_PREFIX>(p, a, c.tmk, c.tmv, s);
-    return e == cudaSuccess ? SD_OK : SD_ECUDA;
+    const int rows = a.M * a.g, B = a.B;
+    a.own_min = 0;
+    a.own_max = INT32_MAX;
+    a.beside = 1;
+    if (!pa_wide(rows, c.D)) return pa_narrow_run(mode, c, a, s);
+    if (mode == PA_OWN) {
+        a.own_max = PA_SHORT;
+        const sd_status st = pa_narrow_run(mode, c, a, s);
+        if (st != SD_OK) return st;
+        a.own_min = PA_SHORT + 1;
+        a.own_max = INT32_MAX;
+        a.beside = 0;
+    }
+    const int part = B <= PA_WIDE_B ? B : (B + 1) / 2;
+    static_assert(PG_MAX_B <= 2 * PA_WIDE_B, "two launches hold the most sequences");
+    for (int b0 = 0; b0 < B; b0 += part) {
+        a.B = B - b0 < part ? B - b0 : part;
+        a.table = c.a.table + static_cast<int64_t>(b0) * a.width;
+        a.lens = c.a.lens + b0;
+        a.n_new = c.a.n_new ? c.a.n_new + b0 : nullptr;
+        a.parent = c.a.parent ? c.a.parent + static_cast<int64_t>(b0) * a.M : nullptr;
+        a.q = c.a.q + b0 * a.q_sb;
+        a.out = c.a.out + b0 * a.o_sb;
+        if (mode == PA_OWN) {
+            a.skip = c.a.skip + b0;
+            a.row_ml = c.a.row_ml + static_cast<int64_t>(b0) * a.M * a.H;
+        }
+        if (pa_wide_run(mode, c, a, rows, s) != cudaSuccess) return SD_ECUDA;
+    }
+    return SD_OK;
+}
+
+// A prefix has the query rows of at least two sequences: the tensor-memory kernel takes them but at D = 256.
+PrefixLayout pa_prefix_layout(const PaCall &c, int rows) {
+    PrefixLayout l;
+    PaPlan p = {};
+    if (c.D > 128) {
+        (void)pa_plan(c.type, 1, 16, c.D, p);
+        return {16, p.grid, 1.0f};
+    }
+    l.rp = rows <= 32 ? 32 : rows <= 64 && c.type != SD_KV_BF16 ? 64 : 128;
+    l.grid = num_sms();
+    l.unit = 6.103515625e-05f;  // (the many-row kernel's weights are in units of 2^-14)
+    return l;
+}
+sd_status pa_prefix(const PaCall &c, int rows, cudaStream_t s) {
+    if (c.D > 128) return pa_narrow_run(PA_PREFIX, c, c.a, s);
+    return pa_wide_run(PA_PREFIX, c, c.a, rows, s) == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
 }  // namespace sdv

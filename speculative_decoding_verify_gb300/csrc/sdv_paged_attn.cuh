@@ -38,12 +38,12 @@ struct PagedArgs {
     // PA_PREFIX: lens, n_new hold the groups' shared rows and numbers of new rows, first[v] where group v's begin in
     // rows_of (sequence * M + row), leader[v] a sequence whose table names the group's pages; out [row of rows_of][H][D]
     const int32_t *first, *leader, *rows_of;
-    // what the prefixes' rows came to: maximum and sum [row of rows_of][H] and, in out of PA_PREFIX, normalised outputs
-    // [row of rows_of][H][D]
-    float2 *pre_ml;
-    const float *pre_o;
-    const int32_t *skip, *start;  // PA_OWN: [B] tiles of a sequence's prefix, and where its rows are in rows_of
-    int32_t beside;               // PA_OWN: 1 where the launch before is the prefixes' (and not another of its own)
+    // maximum and sum behind each row of out and head: PA_PREFIX [row of rows_of][H] (of runs inside one CTA; those that are cut
+    // stay as partials), PA_OWN [B * M][H]
+    float2 *row_ml;
+    const int32_t *skip;          // PA_OWN: [B] tiles of a sequence's prefix
+    int32_t beside;               // PA_OWN: 1 where nothing but the prefixes' launch may still run
+    int32_t own_min, own_max;     // PA_OWN: the sequences of so many tiles behind their prefix
 };
 
 // query and output row of new row i of sequence (or group) b
@@ -61,20 +61,11 @@ __device__ __forceinline__ float *out_row(const PagedArgs &a, int b, int i, int 
     if constexpr (MODE == PA_PREFIX) return a.out + (static_cast<int64_t>(a.first[b] + i) * a.H + h) * D;
     else return a.out + b * a.o_sb + i * a.o_sm + static_cast<int64_t>(h) * D;
 }
-// the softmax statistics behind a finished row of a prefix
+// the softmax statistics behind a finished row
+template <int MODE>
 __device__ __forceinline__ void put_ml(const PagedArgs &a, int b, int i, int h, float m, float l) {
-    a.pre_ml[static_cast<int64_t>(a.first[b] + i) * a.H + h] = make_float2(m, l);
-}
-// A row's own keys came to maximum m, sum l and outputs o, its prefix to (m', l', o' / l'): the whole softmax is
-//   (2^(m - n) o + 2^(m' - n) l' (o' / l')) / (2^(m - n) l + 2^(m' - n) l'),  n = max(m, m').
-// Returns the factors of o and of the prefix's outputs.
-__device__ __forceinline__ float2 with_prefix(const PagedArgs &a, int b, int i, int h, float m, float l) {
-    const float2 p = __ldcg(&a.pre_ml[static_cast<int64_t>(a.start[b] + i) * a.H + h]);
-    const float n = fmaxf(m, p.x), w = exp2f(m - n), wp = p.y * exp2f(p.x - n), inv = 1.0f / fmaf(l, w, wp);
-    return make_float2(w * inv, wp * inv);
-}
-__device__ __forceinline__ const float *prefix_row(const PagedArgs &a, int b, int i, int h, int D) {
-    return a.pre_o + (static_cast<int64_t>(a.start[b] + i) * a.H + h) * D;
+    if constexpr (MODE == PA_PREFIX) a.row_ml[static_cast<int64_t>(a.first[b] + i) * a.H + h] = make_float2(m, l);
+    if constexpr (MODE == PA_OWN) a.row_ml[(static_cast<int64_t>(b) * a.M + i) * a.H + h] = make_float2(m, l);
 }
 
 // the scales of 8-bit rows where there is no page
@@ -249,7 +240,13 @@ struct Piece {
     int32_t b, kh, rg, t0, t1, len, n;
     SeqTiles st;
     int64_t run0;  // the run's first tile in the whole line
+    int64_t next;  // PA_OWN: where the CTA's next piece begins
 };
+// PA_OWN: what a run costs beside its tiles, in tiles.  The line has as many places ahead of the run's own, so that a CTA
+// gets fewer short runs than long ones' tiles.
+constexpr int PA_RUN = 3;
+// and the tiles up to which it is one CTA's: a short run that is cut costs its CTAs a partial, a fence and a join each
+constexpr int PA_WHOLE = 12;
 
 struct Sched {
     const int64_t *prefix;  // [B + 1]: tiles of the sequences before
@@ -268,15 +265,32 @@ __device__ __forceinline__ Piece piece_at(const PagedArgs &a, const Sched &s, in
     p.n = MODE == PA_OWN ? ln.y & 31 : ln.y;
     p.st = tiles_of<MODE>(a, p.len, p.n, MODE == PA_OWN ? ln.y >> 5 : 0);
     const int64_t rem = u - s.prefix[b];
-    const int64_t run = rem / p.st.T;
-    p.t0 = static_cast<int32_t>(rem - run * p.st.T);
-    p.run0 = u - p.t0;
     const int RG = (p.n * a.g + RPG - 1) / RPG;
-    p.kh = static_cast<int32_t>(run / RG);
-    p.rg = static_cast<int32_t>(run - static_cast<int64_t>(p.kh) * RG);
-    const int64_t left = s.u1 - u;
-    p.t1 = left < p.st.T - p.t0 ? p.t0 + static_cast<int32_t>(left) : p.st.T;
+    if constexpr (MODE == PA_OWN) {
+        const int all = p.st.T + PA_RUN;
+        const int64_t run = rem / all;
+        const int at = static_cast<int>(rem - run * all);
+        p.run0 = u - at + PA_RUN;
+        p.kh = static_cast<int32_t>(run / RG);
+        p.rg = static_cast<int32_t>(run - static_cast<int64_t>(p.kh) * RG);
+        p.next = min(s.u1, u - at + all);
+        p.t0 = max(0, at - PA_RUN);
+        p.t1 = static_cast<int32_t>(p.next - (u - at)) - PA_RUN;  // (no tiles where it is not above t0)
+    } else {
+        const int64_t run = rem / p.st.T;
+        p.t0 = static_cast<int32_t>(rem - run * p.st.T);
+        p.run0 = u - p.t0;
+        p.kh = static_cast<int32_t>(run / RG);
+        p.rg = static_cast<int32_t>(run - static_cast<int64_t>(p.kh) * RG);
+        const int64_t left = s.u1 - u;
+        p.t1 = left < p.st.T - p.t0 ? p.t0 + static_cast<int32_t>(left) : p.st.T;
+    }
     return p;
+}
+// the place behind a piece
+template <int MODE>
+__device__ __forceinline__ int64_t behind(const Piece &p, int64_t u) {
+    return MODE == PA_OWN ? p.next : u + (p.t1 - p.t0);
 }
 __device__ __forceinline__ int cta_of(const Sched &s, int64_t u) { return static_cast<int>(((u + 1) * s.G - 1) / s.W); }
 
@@ -294,8 +308,11 @@ __device__ bool make_sched(const PagedArgs &a, int64_t *prefix, int2 *ln, Sched 
         }
         const int skip = MODE == PA_OWN && n > 0 ? a.skip[b] : 0;
         int64_t cost = 0;
-        if (n > 0)
-            cost = static_cast<int64_t>(tiles_of<MODE>(a, len, n, skip).T) * ((n * a.g + RPG - 1) / RPG) * a.H_kv;
+        if (n > 0) {
+            const int tiles = tiles_of<MODE>(a, len, n, skip).T;
+            if (MODE == PA_OWN && (tiles < a.own_min || tiles > a.own_max)) n = 0;
+            else cost = static_cast<int64_t>(tiles + (MODE == PA_OWN ? PA_RUN : 0)) * ((n * a.g + RPG - 1) / RPG) * a.H_kv;
+        }
         ln[b] = make_int2(len, n + 32 * skip);
         prefix[b + 1] = cost;
     }
@@ -323,6 +340,23 @@ __device__ bool make_sched(const PagedArgs &a, int64_t *prefix, int2 *ln, Sched 
     if (static_cast<int64_t>(blockIdx.x) >= sc.W) return false;
     sc.u0 = static_cast<int64_t>(blockIdx.x) * sc.W / sc.G;
     sc.u1 = static_cast<int64_t>(blockIdx.x + 1) * sc.W / sc.G;
+    if constexpr (MODE == PA_OWN) {
+        // an end inside a short run moves to its start, which leaves the ends inside the others, and so cta_of there, as they are
+        auto whole = [&](int64_t u) {
+            if (u >= sc.W) return u;
+            int lo = 0, hi = a.B - 1;
+            while (lo < hi) {  // the sequence of u
+                const int mid = (lo + hi) / 2;
+                if (prefix[mid + 1] <= u) lo = mid + 1;
+                else hi = mid;
+            }
+            const int T = tiles_of<MODE>(a, ln[lo].x, ln[lo].y & 31, ln[lo].y >> 5).T;
+            return T <= PA_WHOLE ? u - (u - prefix[lo]) % (T + PA_RUN) : u;
+        };
+        sc.u0 = whole(sc.u0);
+        sc.u1 = whole(sc.u1);
+        return sc.u0 < sc.u1;
+    }
     return true;
 }
 
@@ -360,6 +394,10 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
     while (ok && u < sc.u1) {
         const Piece p = piece_at<RPG, MODE>(a, sc, u, b);
         b = p.b;
+        if (MODE == PA_OWN && p.t1 <= p.t0) {
+            u = p.next;
+            continue;
+        }
         for (int s = 0; ok && s < QS; ++s) {
             ok = take();
             if (!ok) break;
@@ -434,7 +472,7 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
             }
             taken();
         }
-        u += p.t1 - p.t0;
+        u = behind<MODE>(p, u);
     }
     if (!ok && lane == 0) {  // never leave with copies in flight
         for (int i = max(0, issued - nst); i < issued; ++i)
@@ -468,12 +506,9 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
         }
         mx_of[tid] = mx;
         sum_of[tid] = lv == 0.0f ? 0.0f : 1.0f / lv;
-        const int tg = p.rg * RPG + tid;
-        if constexpr (MODE == PA_PREFIX) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * l_unit);
-        if (MODE == PA_OWN && p.st.lo_tile > 0) {
-            const float2 f = with_prefix(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * l_unit);
-            sum_of[tid] = f.x * l_unit;
-            weight[tid] = f.y;
+        if constexpr (MODE == PA_OWN) {
+            const int tg = p.rg * RPG + tid;
+            put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * l_unit);
         }
     }
     const int r0 = tid / LR, col = tid % LR;
@@ -482,12 +517,6 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
     for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int k = 0; k < NV; ++k) v[i][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float of_prefix[NR] = {};
-    if (MODE == PA_OWN && p.st.lo_tile > 0) {
-        named_bar_sync(bar, NTHR);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) of_prefix[i] = r0 + i * RT < rows ? weight[r0 + i * RT] : 0.0f;
-    }
     if (!SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RPG <= a.part_rows && rows <= RPG &&
                     (p.rg * RPG + rows - 1) / a.g < (MODE == PA_PREFIX ? p.n : a.M),
                 a.status, 116))  // site 116: partials of a join, its output rows
@@ -538,16 +567,8 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
             const float inv = sum_of[tr];
             float4 *to = reinterpret_cast<float4 *>(out_row<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, D)) + col;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                float4 x = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
-                if (MODE == PA_OWN && p.st.lo_tile > 0) {
-                    const float *from = prefix_row(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, D);
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(from) + col + k * LR);
-                    const float f = of_prefix[i];
-                    x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
-                }
-                to[k * LR] = x;
-            }
+            for (int k = 0; k < NV; ++k)
+                to[k * LR] = make_float4(v[i][k].x * inv, v[i][k].y * inv, v[i][k].z * inv, v[i][k].w * inv);
         }
     }
     named_bar_sync(bar, NTHR);
@@ -567,7 +588,13 @@ sd_status pa_call(const sd_kv_pages *pages, const int32_t *table, int32_t width,
                   int64_t out_row_stride, void *workspace, size_t ws_bytes, PaCall &c);
 // the new rows of the sequences of c.a (PA_ALL or PA_OWN)
 sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s);
-// the prefixes of the groups of c.a (at most PG_MAX_B / 2), of at most `rows` query rows per KV head each
+// the prefixes of the groups of c.a (at most PG_MAX_B / 2), of at most `rows` query rows per KV head each, and how their
+// partials are left: rows of one, the CTAs that share the line of tiles, and what the sums and outputs are in
+struct PrefixLayout {
+    int32_t rp, grid;
+    float unit;
+};
+PrefixLayout pa_prefix_layout(const PaCall &c, int rows);
 sd_status pa_prefix(const PaCall &c, int rows, cudaStream_t s);
 
 // The many-row kernel (sdv_paged_wide.cuh): D = 64 or 128, `rows` the most query rows of a KV head, one CTA per SM.

@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         for (int i = 0; i < 6; ++i) badw[i] = 0;
         fence_barrier_init();
     }
-    // (PA_OWN starts beside the prefixes' launch, whose CTAs have all seen what was before it, and waits for it where it reads
-    // their outputs, and ahead of its end)
+    // (PA_OWN starts beside the prefixes' launch, whose CTAs have all seen what was before it; it waits for it ahead of its
+    // end alone, so that what comes next finds both done)
     if (MODE != PA_OWN || !a.beside) pdl_wait();
     pdl_launch_dependents();
     Sched sc;
@@ -312,6 +312,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 const Piece p = piece_at<RP, MODE>(a, sc, u, b);
                 b = p.b;
                 const int n = p.t1 - p.t0;
+                if (MODE == PA_OWN && n <= 0) {
+                    u = p.next;
+                    continue;
+                }
                 if (!wait(q_ready, np & 1u)) break;
                 ++np;
                 if constexpr (!W::I8)
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     // the scores of tile i + 2 go where the weights of tile i are; MMAs of one thread execute in order
                     if (i + 2 < n) ok = scores();
                 }
-                u += n;
+                u = behind<MODE>(p, u);
             }
             tc_commit(done);  // no MMA is left when the tensor memory goes
             (void)mbar_wait_bounded(done, 0, PA_WAIT_NS);
@@ -397,7 +401,15 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     p = piece_at<RP, MODE>(a, sc, u, b);
                     b = p.b;
                     left = p.t1 - p.t0;
-                    u += left;
+                    u = behind<MODE>(p, u);
+                    if constexpr (MODE == PA_OWN) {
+                        for (; left <= 0 && u < sc.u1; u = p.next) {
+                            p = piece_at<RP, MODE>(a, sc, u, b);
+                            b = p.b;
+                            left = p.t1 - p.t0;
+                        }
+                        if (left <= 0) break;
+                    }
                     unit = 0x00800000u;
                     if (!mbar_wait_bounded(q_ready, np++ & 1u, PA_WAIT_NS, abort)) {
                         set_status(a.status, SD_ETIMEOUT);
@@ -502,6 +514,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         while (u < sc.u1) {
             const Piece p = piece_at<RP, MODE>(a, sc, u, b);
             b = p.b;
+            if (MODE == PA_OWN && p.t1 <= p.t0) {
+                u = p.next;
+                continue;
+            }
             const int rows = p.n * a.g, tg = p.rg * RP + r;
             const bool real = tg < rows;
             float2 o[W::DO / 2];
@@ -828,23 +844,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                 lv = fmaf(x, ex2(sm_m[j * RP + r] - mx), lv);
             }
             const float unit = W::I8 ? __uint_as_float(vunit) : 1.0f;
-            float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
-            // a finished row that has a prefix: the factor of the prefix's outputs for the threads that write it
-            const bool joins = MODE == PA_OWN && p.st.lo_tile > 0;
-            float *of_prefix = sm_m + PW_SOFT;
-            auto join_prefix = [&](float rm, float rl) {
-                const float2 y = real ? with_prefix(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, rm, rl * PW_UNIT) : make_float2(0.0f, 0.0f);
-                if (lg == 0 && grp == 0) of_prefix[r] = y.y;
-                return y.x * PW_UNIT;
-            };
-            if constexpr (MODE == PA_OWN)
-                if (joins) {
-                    pdl_wait();
-                    if (complete) f = ex2(m - mx) * unit * join_prefix(mx, lv);
-                }
+            const float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
-            if constexpr (MODE == PA_PREFIX)
-                if (complete && real && lg == 0 && grp == 0) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * PW_UNIT);
+            if constexpr (MODE != PA_ALL)
+                if (complete && real && lg == 0 && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * PW_UNIT);
             // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared
             // memory: thread = 4 columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
             auto write_rows = [&](bool final, float fac) {
@@ -879,13 +882,6 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                                     scratch + (wg * 128 + j * RP + wr + RW * k) * 20 + 4 * (tid & 3));
                                 v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
                             }
-                            if (joins && final) {
-                                const int y = p.rg * RP + wr + RW * k;
-                                const float g = of_prefix[wr + RW * k];
-                                const float4 x = __ldcg(reinterpret_cast<const float4 *>(
-                                    prefix_row(a, p.b, y / a.g, p.kh * a.g + y % a.g, D) + wc + d));
-                                v = make_float4(fmaf(x.x, g, v.x), fmaf(x.y, g, v.y), fmaf(x.z, g, v.z), fmaf(x.w, g, v.w));
-                            }
                             *reinterpret_cast<float4 *>(to[k] + d) = v;
                         }
                     named_bar_sync(5, PW_SOFT);
@@ -897,7 +893,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             float4 *lanes = reinterpret_cast<float4 *>(a.part_o) + grp * (W::DO / 4) * 128 + lt;
             bool rows_ready = complete;
             float fac = f;
-            if constexpr (C > 1) {
+            if constexpr (C > 1 || MODE == PA_PREFIX) {
                 write_rows(complete, f);
             } else if (!complete) {
 #pragma unroll
@@ -905,7 +901,7 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     lanes[static_cast<int64_t>(pslot) * (RP * D / 4) + d * 128] =
                         make_float4(o[2 * d].x * unit, o[2 * d].y * unit, o[2 * d + 1].x * unit, o[2 * d + 1].y * unit);
             }
-            if (!complete) {
+            if (MODE != PA_PREFIX && !complete) {
                 const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
                 __threadfence();
                 named_bar_sync(5, PW_SOFT);
@@ -955,16 +951,14 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                         }
                         fac = jl == 0.0f ? 0.0f : 1.0f / jl;
                         rows_ready = true;
-                        if constexpr (MODE == PA_PREFIX)
-                            if (real && grp == 0) put_ml(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, jm, jl * PW_UNIT);
                         if constexpr (MODE == PA_OWN)
-                            if (joins) fac = join_prefix(jm, jl);
+                            if (real && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, jm, jl * PW_UNIT);
                     }
                 }
             }
-            if constexpr (C == 1)
+            if constexpr (C == 1 && MODE != PA_PREFIX)
                 if (rows_ready) write_rows(true, fac);
-            u += p.t1 - p.t0;
+            u = behind<MODE>(p, u);
         }
     }
     // ---- every role is done

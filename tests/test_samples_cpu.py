@@ -175,7 +175,7 @@ def test_python_refuses(sdv):
         sdv.sample(x, torch.zeros(2), torch.zeros(2, dtype=torch.int32))
 
 
-@pytest.mark.parametrize("name,sites", [("sdv_rope.cu", {119, 120, 121, 122}), ("sdv_draw.cu", {123, 124, 125}), ("sdv_paged_shared.cu", {126, 127, 128})])
+@pytest.mark.parametrize("name,sites", [("sdv_rope.cu", {119, 120, 121, 122}), ("sdv_draw.cu", {123, 124, 125}), ("sdv_paged_shared.cu", {126, 127, 128, 129})])
 def test_the_bounds_checked_build_checks_these_kernels(sdv, name, sites):
     import os
     import re
