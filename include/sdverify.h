@@ -539,7 +539,7 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
  * that name the same page in all of them, and whose rows are committed in all, in whole 64-row tiles), so that a group
  * that shares nothing, or a sequence that left its group, changes no result.  Where too little is shared for a launch of its
  * own to pay (about 3000 64-row tiles per KV head and member, one member of each group not counted), each sequence reads
- * all of its rows, and a batch whose tables cannot hold that much is not looked at.  A group number outside [-1, B) counts as
+ * all of its rows, and a batch whose tables cannot hold twice that much is not looked at.  A group number outside [-1, B) counts as
  * -1, and records SD_EDEVICE in a batch that is looked at.
  * Everything else is as in sd_paged_attn; the same call on the same inputs repeats bit for bit, and a sequence's
  * last bits depend on its neighbours.
@@ -791,7 +791,7 @@ sd_status sd_debug_block_dots(int qtype, const void *w, int64_t n_out, int64_t k
 /* The matmul's SiLU*mul requantisation applied to given g, u fp32 [M][F]. */
 sd_status sd_debug_silu_mul_requant(const float *g, const float *u, int32_t M, int64_t F, int8_t *q, float *scales,
                                     sd_stream_t stream);
-/* Tiles that sd_paged_attn_shared has to be able to leave out before it shares (at least 1; 3000 by default). */
+/* Tiles that sd_paged_attn_shared has to be able to leave out before it looks and shares (0: its own numbers, 6000 and 3000). */
 void sd_debug_share_from(int64_t tiles);
 /* The canonical exponential on n values. */
 sd_status sd_debug_cexp(const float *x, int64_t n, float *y, sd_stream_t stream);

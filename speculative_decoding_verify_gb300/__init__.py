@@ -572,13 +572,23 @@ class Rope:
         return self._ref
 
 
+def _lines_of(t, name, shape, D, dev):
+    """(address, row stride) of fp32 rows [N][heads][D] whose heads are contiguous."""
+    st = t.stride()
+    if t.dtype is not torch.float32 or t.shape != shape or len(st) != 3 or st[2] != 1 or (st[1] != D and shape[1] > 1) \
+            or t.get_device() != dev:
+        raise ValueError(f"{name}: expected fp32 [N][heads][D] {tuple(shape)} with contiguous heads on the current CUDA device, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * D
+
+
 def rope_rows(x: torch.Tensor, pos: torch.Tensor, rope: Rope, out: torch.Tensor):
     """x fp32 [N][heads][D] (heads contiguous) turned to positions pos int32 [N] -> out (which may be x)."""
     dev, stream = _where()
-    N, heads, D = x.shape if x.dim() == 3 else (0, 0, 0)
-    shape = (1, N, heads, D)
-    xp, _, xs = _rows_of(x.unsqueeze(0), "x", shape, dev)
-    op, _, os_ = _rows_of(out.unsqueeze(0), "out", shape, dev)
+    shape = x.shape
+    N, heads, D = shape if len(shape) == 3 else (0, 0, 0)
+    xp, xs = _lines_of(x, "x", shape, D, dev)
+    op, os_ = _lines_of(out, "out", shape, D, dev)
     _check(lib().sd_rope_rows(rope._arg(dev), xp, xs, _here(pos, torch.int32, "pos", (N,), dev), N, heads, D, op, os_, stream),
            "sd_rope_rows")
 
@@ -776,7 +786,7 @@ def debug_silu_mul_requant(g: torch.Tensor, u: torch.Tensor):
 
 
 def debug_share_from(tiles: int):
-    """Tiles that paged_attn_shared has to be able to leave out before it shares (3000 by default)."""
+    """Tiles that paged_attn_shared has to be able to leave out before it looks and shares (0: its own numbers)."""
     lib().sd_debug_share_from(tiles)
 
 

@@ -197,12 +197,12 @@ __device__ __forceinline__ float clean_of(float v, bool infinite) {
 
 // Four logits of a CTA from i (a multiple of four) on, minus infinity from `end` on.
 __device__ __forceinline__ float4 four_of(const float *from, bool wide, int i, int end) {
-    if (wide && i + 4 <= end) return __ldg(reinterpret_cast<const float4 *>(from + i));
+    if (wide && i + 4 <= end) return *reinterpret_cast<const float4 *>(from + i);
     float4 v;
-    v.x = i < end ? __ldg(from + i) : -INFINITY;
-    v.y = i + 1 < end ? __ldg(from + i + 1) : -INFINITY;
-    v.z = i + 2 < end ? __ldg(from + i + 2) : -INFINITY;
-    v.w = i + 3 < end ? __ldg(from + i + 3) : -INFINITY;
+    v.x = i < end ? from[i] : -INFINITY;
+    v.y = i + 1 < end ? from[i + 1] : -INFINITY;
+    v.z = i + 2 < end ? from[i + 2] : -INFINITY;
+    v.w = i + 3 < end ? from[i + 3] : -INFINITY;
     return v;
 }
 
@@ -250,7 +250,7 @@ struct Draw {
                 if (wide && i0 + 128 * (BATCH - 1) + 4 <= w1) {
                     float4 v[BATCH];
 #pragma unroll
-                    for (int j = 0; j < BATCH; ++j) v[j] = __ldg(reinterpret_cast<const float4 *>(x + i0 + 128 * j));
+                    for (int j = 0; j < BATCH; ++j) v[j] = *reinterpret_cast<const float4 *>(x + i0 + 128 * j);
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j)
                         f(i0 + 128 * j, make_float4(clean_of(v[j].x, infinite), clean_of(v[j].y, infinite),
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
         float4 v[FLY];
 #pragma unroll
         for (int j = 0; j < FLY; ++j)
-            if (i0 + 128 * j < whole) v[j] = __ldg(reinterpret_cast<const float4 *>(from + i0 + 128 * j));
+            if (i0 + 128 * j < whole) v[j] = *reinterpret_cast<const float4 *>(from + i0 + 128 * j);
 #pragma unroll
         for (int j = 0; j < FLY; ++j) {
             const int i = i0 + 128 * j;

@@ -16,9 +16,11 @@
 namespace sdv {
 
 constexpr int SP_THREADS = 256;
-// Tiles of keys (per KV head and member) that have to be left out for the prefixes' launch to pay: it costs about as long as
-// 3000 of them.  (A test may set another number.)
-static int64_t g_worth = 3000;
+// Tiles of keys (per KV head and member) that have to be left out for the prefixes' launch to pay: it and the join cost about
+// as long as 3000 of them.  Where the tables cannot hold SP_LOOK of them, which the plan costs too, nobody looks.  (A test
+// may set another number for both.)
+constexpr int64_t SP_WORTH = 3000, SP_LOOK = 6000;
+static int64_t g_share_from = 0;
 
 // The plan, in the workspace.
 struct SharedPlan {
@@ -255,15 +257,16 @@ struct JoinArgs {
 // A warp per query row and head: with (m, l, o) the maximum, the sum and the outputs (weights' sum times the average row) of
 // each part, n the largest m,
 //   out = sum 2^(m - n) o / sum 2^(m - n) l.
-// The parts' statistics are a lane's each, 32 at a time; then their outputs, 8 loads in flight.
+// The parts' statistics are a lane's each, 32 at a time; the outputs of the first few are on their way beside them.
 template <int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const JoinArgs a) {
+__global__ void __launch_bounds__(256, 4) shared_join_kernel(const JoinArgs a) {
     constexpr int NV = D / 128 > 0 ? D / 128 : 1;  // 16-byte columns of a lane (D = 64: half a warp has one)
+    constexpr int FLY = 4 / NV;                    // parts whose outputs are on their way
     pdl_wait();
     pdl_launch_dependents();
     const int lane = static_cast<int>(threadIdx.x) & 31;
     const bool on = lane < D / 4;
-    const int64_t items = static_cast<int64_t>(__ldg(&a.pl.head[1])) * a.H, W = *a.pl.line;
+    const int64_t items = static_cast<int64_t>(__ldcg(&a.pl.head[1])) * a.H, W = *a.pl.line;
     const int64_t G = min(static_cast<int64_t>(a.lay.grid), W);
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += static_cast<int64_t>(gridDim.x) * 8) {
         const int x = static_cast<int>(it / a.H), h = static_cast<int>(it - static_cast<int64_t>(x) * a.H);
@@ -294,6 +297,16 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const JoinArgs a) {
             return n == 1 ? reinterpret_cast<const float4 *>(a.prefix_o) + it * (D / 4) + c4
                           : reinterpret_cast<const float4 *>(a.part_o) + (slot_of(p) * a.lay.rp + r) * (D / 4) + c4;
         };
+        // (the first outputs are on their way beside the statistics)
+        float4 t[FLY][NV];
+        auto load = [&](int p0) {
+#pragma unroll
+            for (int q = 0; q < FLY; ++q)
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    t[q][k] = on && p0 + q < n ? __ldcg(outs(p0 + q, lane + 32 * k)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        };
+        load(0);
         float m = own.x;
         for (int p = lane; p < n; p += 32) m = fmaxf(m, stats(p).x);
 #pragma unroll
@@ -307,15 +320,10 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const JoinArgs a) {
             const float e = exp2f(z.x - m), f = e * z.z;
             sum = fmaf(z.y, e, sum);
             const int np = min(32, n - p0);
-            for (int q0 = 0; q0 < np; q0 += 8) {
-                float4 t[8][NV];
+            for (int q0 = 0; q0 < np; q0 += FLY) {
+                if (p0 + q0 > 0) load(p0 + q0);
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-#pragma unroll
-                    for (int k = 0; k < NV; ++k)
-                        t[q][k] = on && q0 + q < np ? *outs(p0 + q0 + q, lane + 32 * k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < FLY; ++q) {
                     const float g = __shfl_sync(0xffffffffu, f, (q0 + q) & 31);
                     if (q0 + q < np)
 #pragma unroll
@@ -340,7 +348,7 @@ using namespace sdv;
 
 extern "C" {
 
-void sd_debug_share_from(int64_t tiles) { g_worth = tiles < 1 ? 1 : tiles > (1 << 20) ? (1 << 20) : tiles; }
+void sd_debug_share_from(int64_t tiles) { g_share_from = tiles < 0 ? 0 : tiles > (1 << 20) ? (1 << 20) : tiles; }
 
 size_t sd_paged_attn_shared_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D) {
     if (!sd_paged_attn_workspace_bytes(B, M, H, H_kv, D)) return 0;
@@ -364,11 +372,11 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // the most tiles that could be left out
     const int64_t most = static_cast<int64_t>(B - 1) * (static_cast<int64_t>(width) * c.a.P / PA_KT) * c.a.H_kv;
-    if (most < g_worth) return pa_rows(c, PA_ALL, s);
+    if (most < (g_share_from ? g_share_from : SP_LOOK)) return pa_rows(c, PA_ALL, s);
     const int rows = B * M * c.a.g;
     const PrefixLayout lay = pa_prefix_layout(c, rows);
     if (launch(shared_plan_kernel, dim3(B), dim3(SP_THREADS), 0, s, w.p, table, width, lens, n_new, group, B, M, c.a.P, c.a.H_kv,
-               c.a.g, lay.rp, c.a.n_pages, g_worth, c.a.status) != cudaSuccess)
+               c.a.g, lay.rp, c.a.n_pages, g_share_from ? g_share_from : SP_WORTH, c.a.status) != cudaSuccess)
         return SD_ECUDA;
     PaCall g = c;
     size_t off_ml, off_o;

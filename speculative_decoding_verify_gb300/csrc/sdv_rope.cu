@@ -38,8 +38,8 @@ __device__ __forceinline__ Turn turn_of(const RopeArgs &r, int l, int64_t pos) {
         t.s[j] = 0.0f;
     }
     if (on) {
-        const ulonglong2 f0 = __ldg(reinterpret_cast<const ulonglong2 *>(r.turns) + 2 * l);
-        const ulonglong2 f1 = __ldg(reinterpret_cast<const ulonglong2 *>(r.turns) + 2 * l + 1);
+        const ulonglong2 f0 = reinterpret_cast<const ulonglong2 *>(r.turns)[2 * l];
+        const ulonglong2 f1 = reinterpret_cast<const ulonglong2 *>(r.turns)[2 * l + 1];
         const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(RP_THREADS) rope_rows_kernel(RopeArgs r, const
                 if (hj < h1 && SD_INB(n < N && hj < heads && at.x + 4 <= D && at.y + 4 <= D, status, 119)) {
                     if (on) turn_lane(a[j], b[j], t, r.interleaved != 0);
                     float *p = out + n * os + static_cast<int64_t>(hj) * D;
-                    *reinterpret_cast<float4 *>(p + at.x) = a[j];
-                    *reinterpret_cast<float4 *>(p + at.y) = b[j];
+                    __stcs(reinterpret_cast<float4 *>(p + at.x), a[j]);
+                    __stcs(reinterpret_cast<float4 *>(p + at.y), b[j]);
                 }
             }
         }
@@ -267,10 +267,9 @@ static int heads_per_block(int64_t rows, int heads, int slots) {
     const int64_t full = rows * ((heads + RP_HEADS * slots - 1) / (RP_HEADS * slots));
     return full >= 2 * num_sms() ? RP_HEADS * slots : slots;
 }
-static int rope_grid(int64_t items) {
-    const int64_t most = static_cast<int64_t>(num_sms()) * 16;
-    return static_cast<int>(items < most ? items : most);
-}
+// A block per item: as many as the GPU starts by itself beside each other (a grid that stays, 16 blocks per SM, took 118 us
+// for 16384 rows of 40 heads and 148 us for 8 prompts of 2048 rows, this 97 and 131).
+static int rope_grid(int64_t items) { return static_cast<int>(items < INT32_MAX ? items : INT32_MAX); }
 
 static sd_status rope_check(const sd_rope *r, int D) {
     if (!r || !r->turns || !aligned(r->turns, 16)) return SD_EINVAL;

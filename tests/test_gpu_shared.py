@@ -23,7 +23,7 @@ def sdv():
     m.lib()
     m.debug_share_from(1)  # small groups too
     yield m
-    m.debug_share_from(3000)
+    m.debug_share_from(0)
 
 
 def share(c, groups):
