@@ -7,9 +7,10 @@
 // radians off at a position of a million; fp64 would run on a pipe that is a 64th as wide).  It is rounded to fp32 as a
 // signed half turn, where sincospif takes it.
 //
-// A lane holds the same 8 elements (4 pairs) of every head, so that its 4 sines and cosines, formed once, serve all heads
-// it goes through: LR = D / 8 lanes a head, RP_HEADS heads a lane with all their loads in flight.  Bound by HBM for
-// many rows, by the launch and one chain of loads for few.
+// A block takes one row's heads, RP_HEADS a lane with all their loads in flight, LR = D / 8 lanes a head: a lane has the same
+// 8 elements (4 pairs) of each, and the block's threads form the row's sines and cosines once, a pair each, into shared
+// memory (by every lane for itself they were half of the instructions: 16384 rows of 8 + 8 + 8 heads into 8-bit rows 97 -> 69
+// us).  Bound by HBM for many rows, by the launch and one chain of loads for few.
 #include <math.h>
 
 #include "sdv_paged.cuh"
@@ -25,32 +26,27 @@ struct RopeArgs {
     float scale;
 };
 
-// sines and cosines of lane l's four pairs at a position; a lane that is not turned keeps (0, 1)
+// sines and cosines of a row's pairs, times the factor; ends with a barrier
+struct Turns {
+    float c[512], s[512];
+};
+__device__ __forceinline__ void turns_of(const RopeArgs &r, int64_t pos, Turns &t) {
+    for (int p = static_cast<int>(threadIdx.x); p < r.rot / 2; p += RP_THREADS) {
+        const int64_t part = static_cast<int64_t>(r.turns[p] * static_cast<uint64_t>(pos));  // of 2^64, signed
+        float s, c;
+        sincospif(__ll2float_rn(part) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+        t.c[p] = c * r.scale;
+        t.s[p] = s * r.scale;
+    }
+    __syncthreads();
+}
+// lane l's four pairs
 struct Turn {
     float c[4], s[4];
 };
-__device__ __forceinline__ Turn turn_of(const RopeArgs &r, int l, int64_t pos) {
-    Turn t;
-    const bool on = l < r.rot / 8;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        t.c[j] = 1.0f;
-        t.s[j] = 0.0f;
-    }
-    if (on) {
-        const ulonglong2 f0 = reinterpret_cast<const ulonglong2 *>(r.turns)[2 * l];
-        const ulonglong2 f1 = reinterpret_cast<const ulonglong2 *>(r.turns)[2 * l + 1];
-        const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t part = static_cast<int64_t>(f[j] * static_cast<uint64_t>(pos));  // of 2^64, signed
-            float s, c;
-            sincospif(__ll2float_rn(part) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
-            t.c[j] = c * r.scale;
-            t.s[j] = s * r.scale;
-        }
-    }
-    return t;
+__device__ __forceinline__ Turn turn_of(const Turns &t, int l) {
+    const float4 c = reinterpret_cast<const float4 *>(t.c)[l], s = reinterpret_cast<const float4 *>(t.s)[l];
+    return {{c.x, c.y, c.z, c.w}, {s.x, s.y, s.z, s.w}};
 }
 
 // where lane l's two groups of four elements stand in a head: the halves of its pairs, or 8 in a row
@@ -77,42 +73,41 @@ __device__ __forceinline__ void turn_lane(float4 &x, float4 &y, const Turn &t, b
     }
 }
 
-// Rows: a block takes `per` heads of one row, LR lanes a head; the threads behind the last whole head of the block wait.
+// Rows: block (n, y) takes the y-th `per` heads of row n; the threads behind the last whole head of a block only help with the
+// sines.
 __global__ void __launch_bounds__(RP_THREADS) rope_rows_kernel(RopeArgs r, const float *x, int64_t xs, const int32_t *pos,
                                                                int32_t N, int32_t heads, int32_t LR, int32_t per,
                                                                float *out, int64_t os, int *status) {
+    __shared__ __align__(16) Turns turns;
     pdl_wait();
     pdl_launch_dependents();
     const int slots = RP_THREADS / LR, slot = static_cast<int>(threadIdx.x) / LR, l = static_cast<int>(threadIdx.x) % LR;
-    if (slot >= slots) return;
-    const int chunks = (heads + per - 1) / per, D = 8 * LR;
+    const int64_t n = blockIdx.x;
+    const int h0 = static_cast<int>(blockIdx.y) * per + slot, h1 = min(heads, static_cast<int>(blockIdx.y + 1) * per), D = 8 * LR;
     const int2 at = lane_at(r, l);
+    const bool work = slot < slots;
+    float4 a[RP_HEADS], b[RP_HEADS];
+#pragma unroll
+    for (int j = 0; j < RP_HEADS; ++j) {
+        const int hj = h0 + j * slots;
+        if (work && hj < h1 && SD_INB(n < N && hj < heads && at.x + 4 <= D && at.y + 4 <= D, status, 119)) {  // site 119: row
+            const float *p = x + n * xs + static_cast<int64_t>(hj) * D;
+            a[j] = __ldcs(reinterpret_cast<const float4 *>(p + at.x));
+            b[j] = __ldcs(reinterpret_cast<const float4 *>(p + at.y));
+        }
+    }
+    turns_of(r, pos[n], turns);
     const bool on = l < r.rot / 8;
-    for (int64_t it = blockIdx.x; it < static_cast<int64_t>(N) * chunks; it += gridDim.x) {
-        const int64_t n = it / chunks;
-        const int h0 = static_cast<int>(it - n * chunks) * per, h1 = min(heads, h0 + per);
-        const Turn t = turn_of(r, l, pos[n]);
-        for (int h = h0 + slot; h < h1; h += RP_HEADS * slots) {
-            float4 a[RP_HEADS], b[RP_HEADS];
+    Turn t = {};
+    if (on) t = turn_of(turns, l);
 #pragma unroll
-            for (int j = 0; j < RP_HEADS; ++j) {
-                const int hj = h + j * slots;
-                if (hj < h1 && SD_INB(n < N && hj < heads && at.x + 4 <= D && at.y + 4 <= D, status, 119)) {  // site 119: row
-                    const float *p = x + n * xs + static_cast<int64_t>(hj) * D;
-                    a[j] = __ldcs(reinterpret_cast<const float4 *>(p + at.x));
-                    b[j] = __ldcs(reinterpret_cast<const float4 *>(p + at.y));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < RP_HEADS; ++j) {
-                const int hj = h + j * slots;
-                if (hj < h1 && SD_INB(n < N && hj < heads && at.x + 4 <= D && at.y + 4 <= D, status, 119)) {
-                    if (on) turn_lane(a[j], b[j], t, r.interleaved != 0);
-                    float *p = out + n * os + static_cast<int64_t>(hj) * D;
-                    __stcs(reinterpret_cast<float4 *>(p + at.x), a[j]);
-                    __stcs(reinterpret_cast<float4 *>(p + at.y), b[j]);
-                }
-            }
+    for (int j = 0; j < RP_HEADS; ++j) {
+        const int hj = h0 + j * slots;
+        if (work && hj < h1 && SD_INB(n < N && hj < heads && at.x + 4 <= D && at.y + 4 <= D, status, 119)) {
+            if (on) turn_lane(a[j], b[j], t, r.interleaved != 0);
+            float *p = out + n * os + static_cast<int64_t>(hj) * D;
+            __stcs(reinterpret_cast<float4 *>(p + at.x), a[j]);
+            __stcs(reinterpret_cast<float4 *>(p + at.y), b[j]);
         }
     }
 }
@@ -142,120 +137,125 @@ __device__ __forceinline__ uint2 pack4(float4 x) {
     }
     return w;
 }
-// 4 codes of a row whose scale is d (0 codes where d is 0, NaN or infinite), as sd_paged_append makes them
-__device__ __forceinline__ uint32_t codes4(float4 x, float d) {
-    uint32_t w = 0;
-    if (d > 0.0f && d < INFINITY) {
-        const float f[4] = {x.x, x.y, x.z, x.w};
+// 4 codes of a row whose scale is d (0 codes where d is 0, NaN or infinite; inv: its rounded inverse), as sd_paged_append
+// makes them: the nearest whole numbers to the rounded quotients x / d, halves away from 0.  x times inv is within
+// 127 * 4 * 2^-24 < 2^-15 of that quotient and not above 127 + 2^-15, so the whole number is in the low bits of the product
+// plus 1.5 * 2^23, and only where it is as near as 2^-10 to a half are the divisions themselves made.
+__device__ __forceinline__ uint32_t codes4(float4 x, float d, float inv) {
+    if (!(d > 0.0f && d < INFINITY)) return 0;
+    const float f[4] = {x.x, x.y, x.z, x.w};
+    uint32_t b[4];
+    float off = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float q = __fmul_rn(f[i], inv), t = __fadd_rn(q, 12582912.0f);
+        b[i] = __float_as_uint(t);
+        off = fmaxf(off, fabsf(__fsub_rn(q, __fsub_rn(t, 12582912.0f))));
+    }
+    if (!(off < 0.4990234375f && d > 1e-37f)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            int v = static_cast<int>(roundf(__fdiv_rn(f[i], d)));
-            v = v > 127 ? 127 : (v < -127 ? -127 : v);
-            w |= (static_cast<uint32_t>(v) & 255u) << (8 * i);
+            const int v = static_cast<int>(roundf(__fdiv_rn(f[i], d)));
+            b[i] = static_cast<uint32_t>(v > 127 ? 127 : v < -127 ? -127 : v);
         }
     }
-    return w;
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 __device__ __forceinline__ uint32_t magnitude4(float4 x) {  // by its bits: an infinity above every number, a NaN above that
     return max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
                max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w))));
 }
 
-// A block takes `per` of the H + 2 H_kv heads [Q | K | V] of one new row.
+// Block (y, z) takes the z-th `per` of the H + 2 H_kv heads [Q | K | V] of new row y.
 template <int T, int D>
 __global__ void __launch_bounds__(RP_THREADS) paged_append_rope_kernel(const AppendRopeArgs a) {
     constexpr int LR = D / 8, SLOTS = RP_THREADS / LR;
+    __shared__ __align__(16) Turns turns;
     pdl_wait();
     pdl_launch_dependents();
     const int slot = static_cast<int>(threadIdx.x) / LR, l = static_cast<int>(threadIdx.x) % LR, lane = threadIdx.x & 31;
-    const int HK = a.pv.H_kv, heads = a.H + 2 * HK, chunks = (heads + a.per - 1) / a.per;
+    const int HK = a.pv.H_kv, heads = a.H + 2 * HK;
+    const int h0 = static_cast<int>(blockIdx.y) * a.per + slot, h1 = min(heads, static_cast<int>(blockIdx.y + 1) * a.per);
+    const int b = static_cast<int>(blockIdx.x) / a.M, i = static_cast<int>(blockIdx.x) - b * a.M;
+    const int n = a.n_new ? a.n_new[b] : a.M, len = a.lens[b];
+    // a tree's parents, one a lane
+    const int par = a.parent && lane < a.M ? a.parent[static_cast<int64_t>(b) * a.M + lane] : lane - 1;
+    if (n < 0 || n > a.M || len < 0 || static_cast<int64_t>(len) + n > static_cast<int64_t>(a.width) * a.pv.P) {
+        set_status(a.status, SD_EDEVICE);
+        return;
+    }
+    if (i >= n) return;
     const int2 at = lane_at(a.r, l);
-    const bool turned = l < a.r.rot / 8;
-    for (int64_t it = blockIdx.x; it < static_cast<int64_t>(a.B) * a.M * chunks; it += gridDim.x) {
-        const int64_t y = it / chunks;
-        const int h0 = static_cast<int>(it - y * chunks) * a.per, h1 = min(heads, h0 + a.per);
-        const int b = static_cast<int>(y / a.M), i = static_cast<int>(y - static_cast<int64_t>(b) * a.M);
-        const int n = a.n_new ? a.n_new[b] : a.M, len = a.lens[b];
-        // a tree's parents, one a lane
-        const int par = a.parent && lane < a.M ? a.parent[static_cast<int64_t>(b) * a.M + lane] : lane - 1;
-        if (n < 0 || n > a.M || len < 0 || static_cast<int64_t>(len) + n > static_cast<int64_t>(a.width) * a.pv.P) {
+    float4 x[RP_HEADS], z[RP_HEADS];
+#pragma unroll
+    for (int j = 0; j < RP_HEADS; ++j) {
+        const int hj = h0 + j * SLOTS;
+        if (hj < h1 && SD_INB(b < a.B && i < a.M && hj < heads && at.y + 4 <= D, a.status, 120)) {  // site 120: new row
+            const float *p = hj < a.H ? a.q + b * a.q_sb + i * a.q_sm + static_cast<int64_t>(hj) * D
+                             : hj < a.H + HK ? a.k_new + b * a.sb + i * a.sm + static_cast<int64_t>(hj - a.H) * D
+                                             : a.v_new + b * a.sb + i * a.sm + static_cast<int64_t>(hj - a.H - HK) * D;
+            const int2 w = hj < a.H + HK ? at : make_int2(8 * l, 8 * l + 4);
+            x[j] = __ldcs(reinterpret_cast<const float4 *>(p + w.x));
+            z[j] = __ldcs(reinterpret_cast<const float4 *>(p + w.y));
+        }
+    }
+    const int place = len + i, sl = place / a.pv.P, row = place - sl * a.pv.P;
+    int page = -1;
+    if (static_cast<int>(blockIdx.y + 1) * a.per > a.H) {  // the block has heads of K or V
+        page = a.table[static_cast<int64_t>(b) * a.width + sl];
+        if (page < 0 || page >= a.pv.n_pages) {
             set_status(a.status, SD_EDEVICE);
-            continue;
+            page = -1;
         }
-        if (i >= n) continue;
-        int depth = i;
-        if (a.parent) {  // M <= 16
-            int x = i;
-            depth = 0;
-            for (;; ++depth) {
-                const int up = __shfl_sync(0xffffffffu, par, x);
-                if (up >= x) set_status(a.status, SD_EDEVICE);  // parents come before their children
-                if (up < 0 || up >= x) break;
-                x = up;
-            }
+    }
+    int depth = i;
+    if (a.parent) {  // M <= 16
+        int up = i;
+        depth = 0;
+        for (;; ++depth) {
+            const int y = __shfl_sync(0xffffffffu, par, up);
+            if (y >= up) set_status(a.status, SD_EDEVICE);  // parents come before their children
+            if (y < 0 || y >= up) break;
+            up = y;
         }
-        const int place = len + i, sl = place / a.pv.P, row = place - sl * a.pv.P;
-        int page = -1;
-        if (h1 > a.H) {  // the block has heads of K or V
-            page = a.table[static_cast<int64_t>(b) * a.width + sl];
-            if (page < 0 || page >= a.pv.n_pages) {
-                set_status(a.status, SD_EDEVICE);
-                page = -1;
-            }
-        }
-        const Turn t = turn_of(a.r, l, static_cast<int64_t>(len) + depth);
-        const int64_t into = page * a.pv.ps + row * a.pv.rs;
-        for (int h = h0 + slot; h - slot < h1; h += RP_HEADS * SLOTS) {  // (the same turns in all lanes of a warp)
-            float4 x[RP_HEADS], z[RP_HEADS];
+    }
+    turns_of(a.r, static_cast<int64_t>(len) + depth, turns);
+    const bool turned = l < a.r.rot / 8;
+    Turn t = {};
+    if (turned) t = turn_of(turns, l);
+    const int64_t into = page * a.pv.ps + row * a.pv.rs;
 #pragma unroll
-            for (int j = 0; j < RP_HEADS; ++j) {
-                const int hj = h + j * SLOTS;
-                x[j] = z[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (hj < h1 && SD_INB(b < a.B && i < a.M && hj < heads && at.y + 4 <= D, a.status, 120)) {  // site 120: new row
-                    const float *p = hj < a.H ? a.q + b * a.q_sb + i * a.q_sm + static_cast<int64_t>(hj) * D
-                                     : hj < a.H + HK ? a.k_new + b * a.sb + i * a.sm + static_cast<int64_t>(hj - a.H) * D
-                                                     : a.v_new + b * a.sb + i * a.sm + static_cast<int64_t>(hj - a.H - HK) * D;
-                    const int2 w = hj < a.H + HK ? at : make_int2(8 * l, 8 * l + 4);
-                    x[j] = __ldcs(reinterpret_cast<const float4 *>(p + w.x));
-                    z[j] = __ldcs(reinterpret_cast<const float4 *>(p + w.y));
-                }
-            }
+    for (int j = 0; j < RP_HEADS; ++j) {
+        const int hj = h0 + j * SLOTS;
+        const bool isv = hj >= a.H + HK;
+        if (hj >= h1) continue;
+        if (turned && !isv) turn_lane(x[j], z[j], t, a.r.interleaved != 0);
+        if (hj < a.H) {
+            if (!SD_INB(b < a.B && i < n && at.y + 4 <= D, a.status, 121)) continue;  // site 121: turned query
+            float *p = a.q_out + b * a.o_sb + i * a.o_sm + static_cast<int64_t>(hj) * D;
+            *reinterpret_cast<float4 *>(p + at.x) = x[j];
+            *reinterpret_cast<float4 *>(p + at.y) = z[j];
+        } else if (page >= 0) {
+            const int hk = hj - a.H - (isv ? HK : 0);
+            if (!SD_INB(hk >= 0 && hk < HK && sl < a.width && row >= 0 && row < a.pv.P && page < a.pv.n_pages, a.status,
+                        122))  // site 122: row in its page
+                continue;
+            const int64_t dst = into + hk * a.pv.hs;
+            const int2 w = isv ? make_int2(8 * l, 8 * l + 4) : at;
+            if constexpr (T == SD_KV_I8) {  // the largest magnitude of the row, over its lanes
+                uint32_t top = max(magnitude4(x[j]), magnitude4(z[j]));
+                const unsigned mask = LR == 32 ? 0xffffffffu : ((1u << (LR & 31)) - 1u) << (lane / LR * LR);
 #pragma unroll
-            for (int j = 0; j < RP_HEADS; ++j) {
-                const int hj = h + j * SLOTS;
-                const bool isv = hj >= a.H + HK;
-                if (turned && !isv) turn_lane(x[j], z[j], t, a.r.interleaved != 0);
-                float d = 0.0f;
-                if constexpr (T == SD_KV_I8) {  // the largest magnitude of the row, over its lanes
-                    uint32_t top = max(magnitude4(x[j]), magnitude4(z[j]));
-#pragma unroll
-                    for (int o = LR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    d = __fdiv_rn(__uint_as_float(top), 127.0f);
-                }
-                if (hj >= h1) continue;
-                if (hj < a.H) {
-                    if (!SD_INB(b < a.B && i < n && at.y + 4 <= D, a.status, 121)) continue;  // site 121: turned query
-                    float *p = a.q_out + b * a.o_sb + i * a.o_sm + static_cast<int64_t>(hj) * D;
-                    *reinterpret_cast<float4 *>(p + at.x) = x[j];
-                    *reinterpret_cast<float4 *>(p + at.y) = z[j];
-                } else if (page >= 0) {
-                    const int hk = hj - a.H - (isv ? HK : 0);
-                    if (!SD_INB(hk >= 0 && hk < HK && sl < a.width && row >= 0 && row < a.pv.P && page < a.pv.n_pages, a.status,
-                                122))  // site 122: row in its page
-                        continue;
-                    const int64_t dst = into + hk * a.pv.hs;
-                    const int2 w = isv ? make_int2(8 * l, 8 * l + 4) : at;
-                    if constexpr (T == SD_KV_I8) {
-                        int8_t *to = static_cast<int8_t *>(isv ? a.v : a.k) + dst;
-                        *reinterpret_cast<uint32_t *>(to + w.x) = codes4(x[j], d);
-                        *reinterpret_cast<uint32_t *>(to + w.y) = codes4(z[j], d);
-                        if (l == 0) (isv ? a.v_scale : a.k_scale)[(static_cast<int64_t>(page) * HK + hk) * a.pv.P + row] = d;
-                    } else {
-                        uint16_t *to = static_cast<uint16_t *>(isv ? a.v : a.k) + dst;
-                        *reinterpret_cast<uint2 *>(to + w.x) = pack4<T>(x[j]);
-                        *reinterpret_cast<uint2 *>(to + w.y) = pack4<T>(z[j]);
-                    }
-                }
+                for (int o = LR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+                const float d = __fdiv_rn(__uint_as_float(top), 127.0f), inv = __frcp_rn(d);
+                int8_t *to = static_cast<int8_t *>(isv ? a.v : a.k) + dst;
+                *reinterpret_cast<uint32_t *>(to + w.x) = codes4(x[j], d, inv);
+                *reinterpret_cast<uint32_t *>(to + w.y) = codes4(z[j], d, inv);
+                if (l == 0) (isv ? a.v_scale : a.k_scale)[(static_cast<int64_t>(page) * HK + hk) * a.pv.P + row] = d;
+            } else {
+                uint16_t *to = static_cast<uint16_t *>(isv ? a.v : a.k) + dst;
+                *reinterpret_cast<uint2 *>(to + w.x) = pack4<T>(x[j]);
+                *reinterpret_cast<uint2 *>(to + w.y) = pack4<T>(z[j]);
             }
         }
     }
@@ -263,14 +263,12 @@ __global__ void __launch_bounds__(RP_THREADS) paged_append_rope_kernel(const App
 
 // Heads of a block's turn: all RP_HEADS of its lanes' where there are blocks enough for every SM all the same, one
 // otherwise (the launch and the loads' latency are all there is).
+// (A block per row and turn: a grid that stays, 16 blocks per SM, took 118 us for 16384 rows of 40 heads and 148 us for 8
+// prompts of 2048 rows, this 97 and 131.)
 static int heads_per_block(int64_t rows, int heads, int slots) {
     const int64_t full = rows * ((heads + RP_HEADS * slots - 1) / (RP_HEADS * slots));
     return full >= 2 * num_sms() ? RP_HEADS * slots : slots;
 }
-// A block per item: as many as the GPU starts by itself beside each other (a grid that stays, 16 blocks per SM, took 118 us
-// for 16384 rows of 40 heads and 148 us for 8 prompts of 2048 rows, this 97 and 131).
-static int rope_grid(int64_t items) { return static_cast<int>(items < INT32_MAX ? items : INT32_MAX); }
-
 static sd_status rope_check(const sd_rope *r, int D) {
     if (!r || !r->turns || !aligned(r->turns, 16)) return SD_EINVAL;
     if (r->rot < 2 || r->rot > D || (r->interleaved != 0 && r->interleaved != 1) || !isfinite(r->scale)) return SD_EINVAL;
@@ -278,10 +276,10 @@ static sd_status rope_check(const sd_rope *r, int D) {
 }
 
 template <int T>
-static cudaError_t append_rope_launch(int D, const AppendRopeArgs &a, int grid, cudaStream_t s) {
-    if (D == 64) return launch(paged_append_rope_kernel<T, 64>, dim3(grid), dim3(RP_THREADS), 0, s, a);
-    if (D == 128) return launch(paged_append_rope_kernel<T, 128>, dim3(grid), dim3(RP_THREADS), 0, s, a);
-    return launch(paged_append_rope_kernel<T, 256>, dim3(grid), dim3(RP_THREADS), 0, s, a);
+static cudaError_t append_rope_launch(int D, const AppendRopeArgs &a, dim3 grid, cudaStream_t s) {
+    if (D == 64) return launch(paged_append_rope_kernel<T, 64>, grid, dim3(RP_THREADS), 0, s, a);
+    if (D == 128) return launch(paged_append_rope_kernel<T, 128>, grid, dim3(RP_THREADS), 0, s, a);
+    return launch(paged_append_rope_kernel<T, 256>, grid, dim3(RP_THREADS), 0, s, a);
 }
 
 }  // namespace sdv
@@ -350,9 +348,9 @@ sd_status sd_rope_rows(const sd_rope *rope, const float *x, int64_t x_stride, co
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     const int LR = D / 8, per = heads_per_block(N, heads, RP_THREADS / LR);
-    const int64_t items = static_cast<int64_t>(N) * ((heads + per - 1) / per);
+    if ((heads + per - 1) / per > 65535) return SD_EUNSUPPORTED;
     const RopeArgs r = {rope->turns, rope->rot, rope->interleaved, rope->scale};
-    return launch(rope_rows_kernel, dim3(rope_grid(items)), dim3(RP_THREADS), 0, reinterpret_cast<cudaStream_t>(stream), r, x,
+    return launch(rope_rows_kernel, dim3(N, (heads + per - 1) / per), dim3(RP_THREADS), 0, reinterpret_cast<cudaStream_t>(stream), r, x,
                   x_stride, pos, N, heads, static_cast<int32_t>(LR), static_cast<int32_t>(per), out, out_stride,
                   status) == cudaSuccess
                ? SD_OK
@@ -412,7 +410,9 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
     a.sm = row_stride;
     a.r = {rope->turns, rope->rot, rope->interleaved, rope->scale};
     a.status = status;
-    const int grid = rope_grid(rows * ((heads + a.per - 1) / a.per));
+    const int turns = (heads + a.per - 1) / a.per;
+    if (rows > INT32_MAX || turns > 65535) return SD_EUNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(rows), turns);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = pages->type == SD_KV_F16    ? append_rope_launch<SD_KV_F16>(pages->D, a, grid, s)
                           : pages->type == SD_KV_BF16 ? append_rope_launch<SD_KV_BF16>(pages->D, a, grid, s)
