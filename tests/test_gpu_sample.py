@@ -93,6 +93,55 @@ def test_whole_vocabularies(sdv, V):
         check(sdv, logits(rng, N, V, kind), rng.random(N).astype(np.float32) * 0.999, [T] * N, [k] * N, [p] * N, [low] * N)
 
 
+@pytest.mark.parametrize("N,V", [(320, 151936), (320, 151937), (160, 100001), (70, 151937), (70, 360448)])
+def test_many_rows_of_whole_vocabularies(sdv, N, V):
+    """Rows that share the GPU with so many others that one, two or four CTAs read them again and again: the same tokens and
+    probabilities as alone, and right."""
+    rng = np.random.default_rng(N)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(N)
+    l = torch.randn(N, V, generator=gen, device="cuda") * 2
+    l[1::4] = torch.round(l[1::4] * 4) / 4
+    l[2::8] = -float("inf")
+    l[2::8, 77:1000] = 0.25
+    l[3, 5] = l[3, 9] = float("inf")
+    l[5] = float("nan")
+    l[5, 11] = -1.0
+    u = rng.random(N).astype(np.float32) * 0.999
+    T = (0.5 + rng.random(N)).astype(np.float32)
+    k = rng.choice([0, 0, 1, 30, 300, 5000], N).astype(np.int32)
+    p = rng.choice([1.0, 0.9, 0.3], N).astype(np.float32)
+    low = rng.choice([0.0, 0.0, 0.02], N).astype(np.float32)
+    for with_p in (True, False):
+        args = (T, k, p if with_p else None, low)
+        tokens, prob, _ = run(sdv, l, u, *args, probs=False)
+        status_ok()
+        for n in list(range(12)) + [N - 1]:
+            alone, prob1, q = run(sdv, l[n:n + 1], u[n:n + 1], *(x[n:n + 1] if x is not None else None for x in args))
+            assert alone[0] == tokens[n] and prob1[0] == prob[n]
+            plain.check_row(host(l[n]), float(u[n]), float(T[n]), int(k[n]), float(p[n]) if with_p else 1.0, float(low[n]), int(tokens[n]),
+                            float(prob[n]), q[0].astype(np.float64))
+    status_ok()
+
+
+@pytest.mark.parametrize("V,N", [(1000, 64), (30000, 64), (30000, 2000)])
+def test_nuclei_that_end_at_a_border(sdv, V, N):
+    """Levels of equal logits, and top-p within some roundings of the sum down to a level's end: the histogram's sums alone do not
+    tell on which side of it the nucleus ends."""
+    rng = np.random.default_rng(V)
+    l, p = np.zeros((N, V), np.float32), np.zeros(N, np.float32)
+    for n in range(N):
+        cut = np.sort(rng.choice(np.arange(1, V), 4, replace=False))
+        level = -np.cumsum(rng.choice([0.01, 0.3, 1.0, 2.5], 5)).astype(np.float32)
+        l[n] = rng.permutation(level[np.searchsorted(cut, np.arange(V), side="right")])
+        w = np.exp(np.sort(l[n].astype(np.float64))[::-1] - l[n].max())
+        share = np.cumsum(w)[cut[rng.integers(4)] - 1] / w.sum()
+        p[n] = np.float32(share) + np.float32(rng.integers(-3, 4)) * np.spacing(np.float32(share))
+    check(sdv, l, rng.random(N).astype(np.float32) * 0.999, p=np.minimum(p, 1))
+    if N < 100:
+        check(sdv, l, rng.random(N).astype(np.float32) * 0.999, p=np.minimum(p, 1), k=[V - 1] * N, probs=False)
+
+
 def test_ties_go_to_the_lower_index(sdv):
     l = np.array([[1, 3, 3, 2, 3, 3, 0, 3.0]] * 8, np.float32)
     u = np.arange(8) / 8 + 1 / 16
@@ -223,6 +272,25 @@ def test_captured_and_on_another_stream(sdv):
             for n in range(4):
                 plain.check_row(host(l)[n], float(u[n]), 1.0, 30, 1.0, 0.0, int(tokens[n]), float(prob[n]), None)
     status_ok()
+
+
+def test_two_streams_at_once(sdv):
+    rng = np.random.default_rng(12)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    l = [cuda(logits(rng, 20, 60000, "plain")) for _ in range(2)]
+    u = [cuda(rng.random(20).astype(np.float32) * 0.999) for _ in range(2)]
+    p = torch.full((20,), 0.9, device="cuda")
+    out = [(torch.zeros(20, dtype=torch.int32, device="cuda"), torch.zeros(20, device="cuda")) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, x, y, o in zip(streams, l, u, out):
+            with torch.cuda.stream(s):
+                sdv.sample(x, y, o[0], top_p=p, prob=o[1])
+    torch.cuda.synchronize()
+    status_ok()
+    for x, y, o in zip(l, u, out):
+        for n in range(20):
+            plain.check_row(host(x)[n], float(y[n]), 1.0, 0, float(np.float32(0.9)), 0.0, int(o[0][n]), float(o[1][n]), None)
 
 
 def test_a_drafter_that_samples(sdv):

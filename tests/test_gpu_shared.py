@@ -255,6 +255,28 @@ def test_columns_of_wider_rows(sdv):
     assert torch.all(to[:, :, 0] == 123.0) and torch.all(to[:, :, 5:] == 123.0)
 
 
+def test_two_streams_at_once(sdv):
+    """Calls beside each other, each with its own workspace."""
+    rng = np.random.default_rng(11)
+    sets = []
+    for D in (128, 64):
+        lens, news = [640, 700, 650, 30], [2, 2, 1, 2]
+        c = Cache(sdv, rng, lens, news, 2, 2, D, 16, "f16")
+        share(c, {(0, 1, 2): 40})
+        q = rng.standard_normal((4, 2, 8, D)).astype(np.float32)
+        sets.append((c, q, lens, news, torch.cuda.Stream(), sdv.workspace(sdv.paged_attn_shared_workspace_bytes(4, 2, 8, 2, D))))
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for _ in range(10):
+        for i, (c, q, lens, news, s, ws) in enumerate(sets):
+            with torch.cuda.stream(s):
+                outs[i] = run(sdv, c, q, lens, news, [0] * 4, 2, ws=ws)
+    torch.cuda.synchronize()
+    status_ok()
+    for out, (c, q, lens, news, _, _) in zip(outs, sets):
+        compare(out, c, q, lens, news)
+
+
 def test_parallel_sampling(sdv):
     """One prompt forked into six samples: reserve, rotary append, shared attention, a head, drawn tokens and commit, as one
     captured graph replayed for 40 steps; every step's rows, outputs and tokens against plain forms, the prompt's pages still
