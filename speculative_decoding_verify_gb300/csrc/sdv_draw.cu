@@ -13,8 +13,9 @@
 //   otherwise histograms over the distance d = m - l (128 bins per octave first; a bin with more than DR_LIST tokens
 //   is cut again, by the bits of d, then of l, then of the index): each CTA makes its own, one exchange later every CTA adds
 //   up the few bins that decide.  Counts are exact; a bin's weights are 13- to 15-bit parts of its first token's, so their sum only
-//   says where to look: a pass over the tokens then takes the exact sum of all before the bin and lists those in
-//   it, and where the threshold is not among them the search goes on at the next token before or behind.
+//   says where to look (about a token off in a flat row): a pass over the tokens then takes the exact sum of all before the
+//   bin and lists those in it and beside it, and where the threshold is not among them the search goes on at the next token
+//   before or behind.
 // A pass leaves the sum of each warp's kept tokens, so the draw is a search among those and a scan of one run.
 // Every exchange is one cluster barrier: two for a row without top-k or top-p, three with a small top-k, four with top-p of a
 // flat row, and one at each end.
@@ -33,6 +34,8 @@ constexpr int DR_BITS = 10, DR_BINS = 1 << DR_BITS, DR_COARSE = 32;  // a coarse
 constexpr int DR_LIST = 256;      // tokens that are ranked directly
 constexpr int DR_MOST_CTAS = 8;
 constexpr int DR_VOCAB = 360448;  // most tokens of a row
+constexpr int DR_ORDER = 4096;    // most rows that are put in order
+constexpr uint32_t DR_BESIDE = 100;  // tokens on either side of a threshold that are listed with it
 constexpr int DR_SMALL_K = 192;   // top-k for which about as many tokens are worth listing
 // the first histogram: 8 octaves of d from 2^-3 on, by the bits of d
 constexpr uint32_t DR_FIRST = 0x3e000000u;
@@ -47,6 +50,7 @@ struct DrawArgs {
     int32_t *tokens;
     float *prob, *probs;
     int64_t ldp;
+    int32_t N, order;  // order: the rows that take longest come first
     int *status;
 };
 
@@ -69,10 +73,11 @@ struct Range {
     uint32_t lo[3], hi[3];
 };
 
-// what a histogram says of the bin that was looked for: the tokens before it and in it (a search by counts), or about the
-// weight before it and the least number of tokens that its weight takes (a search by weights)
+// what a histogram says of the bin that was looked for: the tokens before it and in it (a search by counts); or about the
+// weight before it and the least number of tokens that its weight takes (a search by weights, where bins beside it come along
+// as long as the tokens stay few: the sums are a little off)
 struct Found {
-    uint32_t bin, before_n, n;
+    uint32_t bin, last, before_n, n;
     float before_m, target_m;  // in units of 2^-MASS
 };
 
@@ -99,6 +104,7 @@ struct alignas(16) DrawShared {
     uint64_t thr, thr_sum;
     double low_log;
     float c_hi, c_lo, p, u;
+    uint32_t heavy[DR_ORDER / 32];
     uint32_t listed;
     int32_t k, bad, owner;
 };
@@ -358,7 +364,7 @@ struct Draw {
     }
 
     // The bin of the last level with the token that brings the count (MASS: about the weight; a share of the whole level's
-    // where target_m is under 0) to the target, from the CTAs' 32 coarse bins and the 32 bins of one of them.  Every CTA
+    // where target_m is under 0) to the target, from the CTAs' 32 coarse bins and the bins of three of them.  Every CTA
     // finds the same.
     template <bool MASS>
     __device__ Found locate(bool first, int phase, const Range &r, int shift, uint32_t target_n, float target_m) {
@@ -379,19 +385,70 @@ struct Draw {
             // (rounded sums may fall short of their own total: the last bin that has any, then)
             const uint32_t there = __ballot_sync(0xffffffffu, cs > 0), at = __ballot_sync(0xffffffffu, cs > 0 && in >= target);
             const int q = at ? __ffs(at) - 1 : there ? 31 - __clz(there) : 0;
-            const Sum before = __shfl_sync(0xffffffffu, in - cs, q);
-            const int bin = 32 * q + lane;
-            uint64_t raw = 0;
+            // that coarse bin's and its neighbours' bins, three a lane
+            const int g0 = min(max(q - 1, 0), DR_COARSE - 3), bin0 = 32 * g0 + 3 * lane;
+            uint64_t raw[3] = {0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < CS; ++c) raw += *of(&sh.bins[b][bin], c);
-            Sum fs;
-            if constexpr (MASS) fs = static_cast<float>(raw) * ex2_approx(-c_hi * edge(first, phase, r, shift, bin));
-            else fs = static_cast<uint32_t>(raw);
-            const Sum upto = before + warp_scan(fs);
-            const uint32_t some = __ballot_sync(0xffffffffu, fs > 0), hits = __ballot_sync(0xffffffffu, fs > 0 && upto >= target);
-            if (lane == (hits ? __ffs(hits) - 1 : some ? 31 - __clz(some) : 0)) {
-                if constexpr (MASS) sh.found = {static_cast<uint32_t>(bin), 0, static_cast<uint32_t>(raw >> MASS_BITS), upto - fs, target};
-                else sh.found = {static_cast<uint32_t>(bin), upto - fs, fs, 0.0f, 0.0f};
+            for (int c = 0; c < CS; ++c)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) raw[i] += *of(&sh.bins[b][bin0 + i], c);
+            Sum f[3], upto[3], mine = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                if constexpr (MASS) f[i] = static_cast<float>(raw[i]) * ex2_approx(-c_hi * edge(first, phase, r, shift, bin0 + i));
+                else f[i] = static_cast<uint32_t>(raw[i]);
+                mine += f[i];
+                upto[i] = mine;
+            }
+            const Sum ahead = __shfl_sync(0xffffffffu, in - cs, g0) + (warp_scan(mine) - mine);
+            int hit = INT_MAX, some = -1;
+#pragma unroll
+            for (int i = 2; i >= 0; --i) {
+                upto[i] += ahead;
+                if (f[i] > 0 && upto[i] >= target) hit = 3 * lane + i;
+                if (f[i] > 0) some = max(some, 3 * lane + i);
+            }
+            hit = __reduce_min_sync(0xffffffffu, hit);
+            some = __reduce_max_sync(0xffffffffu, some);
+            const int who = hit != INT_MAX ? hit : max(some, 0);
+            // value x[i] of bin k of the 96
+            auto of_bin = [&](auto (&x)[3], int k) { return __shfl_sync(0xffffffffu, k % 3 == 0 ? x[0] : k % 3 == 1 ? x[1] : x[2], k / 3); };
+            int lo = who, hi = who;
+            uint32_t n[3], sum[3], all = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                n[i] = static_cast<uint32_t>(MASS ? raw[i] >> MASS_BITS : raw[i]);
+                all += n[i];
+                sum[i] = all;
+            }
+            const uint32_t n_ahead = warp_scan(all) - all;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) sum[i] += n_ahead;
+            if constexpr (MASS) {
+                const uint32_t who_sum = of_bin(sum, who), who_n = of_bin(n, who);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int k = 3 * lane + i;
+                    if (k < who && who_sum - sum[i] + n[i] <= DR_BESIDE) lo = min(lo, k);
+                    if (k > who && sum[i] - who_sum + who_n <= DR_BESIDE) hi = max(hi, k);
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+            }
+            const uint32_t inside = of_bin(sum, hi) - (of_bin(sum, lo) - of_bin(n, lo));
+            const Sum before = of_bin(upto, lo) - of_bin(f, lo);
+            if (lane == 0) {
+                sh.found.bin = 32 * g0 + lo;
+                sh.found.last = 32 * g0 + hi;
+                sh.found.n = inside;
+                if constexpr (MASS) {
+                    sh.found.before_n = 0;
+                    sh.found.before_m = before;
+                    sh.found.target_m = target;
+                } else {
+                    sh.found.before_n = before;
+                    sh.found.before_m = sh.found.target_m = 0.0f;
+                }
             }
         }
         __syncthreads();
@@ -415,7 +472,7 @@ struct Draw {
         histogram<true, MASS>(0, q.r, DR_SHIFT);
         q.f = locate<MASS>(true, 0, q.r, DR_SHIFT, target_n, target_m);
         if (q.f.bin > 0) q.r.lo[0] = DR_FIRST + (q.f.bin << DR_SHIFT);
-        q.r.hi[0] = bin_end(q.f.bin);
+        q.r.hi[0] = bin_end(q.f.last);
         return q;
     }
     __device__ __forceinline__ static uint32_t bin_end(uint32_t bin) {
@@ -428,10 +485,9 @@ struct Draw {
         const int phase = q.phase, shift = max(0, 32 - __clz(q.r.hi[phase] - q.r.lo[phase]) - DR_BITS);
         histogram<false, MASS>(phase, q.r, shift);
         const Found g = locate<MASS>(false, phase, q.r, shift, target_n - q.f.before_n, fmaxf(target_m - q.f.before_m, 0.0f));
-        q.f = {g.bin, q.f.before_n + g.before_n, g.n, q.f.before_m + g.before_m, target_m};
-        const uint32_t at = q.r.lo[phase] + (g.bin << shift);
-        q.r.hi[phase] = min(q.r.hi[phase], at + ((1u << shift) - 1u));
-        q.r.lo[phase] = at;
+        q.f = {g.bin, g.last, q.f.before_n + g.before_n, g.n, q.f.before_m + g.before_m, target_m};
+        q.r.hi[phase] = min(q.r.hi[phase], q.r.lo[phase] + (g.last << shift) + ((1u << shift) - 1u));
+        q.r.lo[phase] += g.bin << shift;
     }
     // by counts, to a range of at most DR_LIST tokens
     __device__ Search search_count(uint32_t target) {
@@ -616,20 +672,67 @@ struct Draw {
     uint32_t rank_n;
 };
 
+// The row of a cluster where there are more than the GPU holds at once: first those that may have to be ordered by weight,
+// then the others (a late one of the first kind is several times as long behind the rest: 96 -> 86 us for 256 rows with
+// settings of their own).
+__device__ __forceinline__ int row_in_order(const DrawArgs &a, DrawShared &sh, int q) {
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+    for (int r = tid; r < DR_ORDER; r += DR_THREADS) {
+        bool heavy = false;
+        if (r < a.N) {
+            const int k = a.top_k ? a.top_k[r] : 0;
+            heavy = a.top_p[r] < 1.0f && (k == 0 || k > DR_SMALL_K) && !(a.temperature && a.temperature[r] == 0.0f);
+        }
+        const uint32_t word = __ballot_sync(0xffffffffu, heavy);
+        if (lane == 0) sh.heavy[r >> 5] = word;
+    }
+    __syncthreads();
+    constexpr int PER = DR_ORDER / 32 / 32;  // words of a lane
+    uint32_t w[PER], first = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) first += __popc(sh.heavy[PER * lane + i]);
+    first = warp_sum(first);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int r0 = 32 * (PER * lane + i);
+        const uint32_t there = r0 >= a.N ? 0u : a.N - r0 >= 32 ? 0xffffffffu : (1u << (a.N - r0)) - 1u;
+        w[i] = (q < static_cast<int>(first) ? sh.heavy[PER * lane + i] : ~sh.heavy[PER * lane + i]) & there;
+        sum += __popc(w[i]);
+    }
+    uint32_t rank = q < static_cast<int>(first) ? q : q - first;
+    const uint32_t upto = warp_scan(sum);
+    int row = 0;
+    if (rank < upto && rank >= upto - sum) {
+        rank -= upto - sum;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const uint32_t n = __popc(w[i]);
+            if (rank < n) {
+                row = 32 * (PER * lane + i) + static_cast<int>(__fns(w[i], 0, static_cast<int>(rank) + 1));
+                rank = 0xffffffffu;
+            } else if (rank != 0xffffffffu) {
+                rank -= n;
+            }
+        }
+    }
+    return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(row)));
+}
+
 template <int CS, bool HELD>
 __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     DrawShared &sh = *reinterpret_cast<DrawShared *>(smem_raw);
     float *held = reinterpret_cast<float *>(smem_raw + sizeof(DrawShared));
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / CS;
+    int64_t row = blockIdx.x / CS;
     const int rank = static_cast<int>(blockIdx.x % CS);  // (the clusters are made of neighbours)
     const int lo = min(a.V, rank * a.chunk), n = min(a.V, lo + a.chunk) - lo;
-    const float *from = a.logits + row * a.ld + lo;
 
     cluster_arrive();  // that this CTA runs, and may be written to
     pdl_wait();
     pdl_launch_dependents();
+    if (a.order) row = row_in_order(a, sh, static_cast<int>(row));
+    const float *from = a.logits + row * a.ld + lo;
     if (tid == 0) {  // the row's settings
         const float T = a.temperature ? a.temperature[row] : 1.0f, p = a.top_p ? a.top_p[row] : 1.0f;
         const float low = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
@@ -923,7 +1026,7 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     if (!status) return SD_ECUDA;
     // As many CTAs per row as the GPU holds at once beside the other rows', two per SM; two at least where top-p may have to
     // order a flat row (95 us for one CTA); no more than the row has 1024 tokens for.  256 rows of 151936 tokens by
-    // 1 / 2 / 4 / 8 CTAs: top-k of 50 54 / 59 / 74 / 103 us, each row with its own settings 132 / 99 / 96 / 119 us; 64 rows,
+    // 1 / 2 / 4 / 8 CTAs: top-k of 50 54 / 59 / 74 / 103 us, each row with its own settings 132 / 86 / 86 / 116 us; 64 rows,
     // top-k 29 / 20 / 18 / 26 us.
     const int slots = 2 * num_sms(), least = top_p ? 2 : 1;
     int ctas = DR_MOST_CTAS;
@@ -943,6 +1046,8 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     a.prob = out_prob;
     a.probs = out_probs;
     a.ldp = ld_probs;
+    a.N = N;
+    a.order = top_p && static_cast<int64_t>(N) * ctas > slots && N <= DR_ORDER;
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // (two CTAs of an SM hold their logits in its shared memory where they fit)
