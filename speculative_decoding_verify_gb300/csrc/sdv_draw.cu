@@ -15,7 +15,7 @@
 //   up the few bins that decide.  Counts are exact; a bin's weights are 13- to 15-bit parts of its first token's, so their sum only
 //   says where to look (about a token off in a flat row): a pass over the tokens then takes the exact sum of all before the
 //   bin and lists those in it and beside it, and where the threshold is not among them the search goes on at the next token
-//   before or behind.
+//   before or behind, then by halves.
 // A pass leaves the sum of each warp's kept tokens, so the draw is a search among those and a scan of one run.
 // Every exchange is one cluster barrier: two for a row without top-k or top-p, three with a small top-k, four with top-p of a
 // flat row, and one at each end.
@@ -106,7 +106,9 @@ struct alignas(16) DrawShared {
     float c_hi, c_lo, p, u;
     uint32_t heavy[DR_ORDER / 32];
     uint32_t listed;
-    int32_t k, bad, owner;
+    uint32_t after, upto;  // top-p's threshold is among tokens after+1 .. upto of the order
+    bool walked;           // and a search by counts has been made for it
+    int32_t k, bad;
 };
 
 __device__ __forceinline__ float ex2_approx(float x) {  // 2^x to about 2^-22, 0 below the normal numbers
@@ -852,6 +854,11 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
             }
         }
         if (nucleus) {
+            if (tid == 0) {
+                sh.after = 0;
+                sh.upto = static_cast<uint32_t>(a.V);
+                sh.walked = false;
+            }
             const bool known = target != 0;  // else the histogram's own sum says about where to look
             const float per_unit = Draw<CS, HELD>::PER_UNIT;
             Search q = w.template start<true>(0, known ? static_cast<float>(target) * per_unit : -p);
@@ -870,10 +877,21 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
                 }
                 w.ranks(before, 0);
                 found = w.pick(true, target);
-                if (!found) {  // the threshold is before the range or behind it: on with the next token there, by counts
-                    const uint32_t next = w.count_before(q.r) + (target <= before ? 0 : w.listed + 1);
-                    if (next < 1 || next > static_cast<uint32_t>(a.V)) break;  // (never: the weights of all reach the target)
-                    q = w.search_count(next);
+                if (!found) {
+                    // the threshold is before the range or behind it, among tokens after+1 .. upto: the next token there,
+                    // by counts (the sums are mostly a token off), then the middle (where a temperature is so low that a
+                    // bin's weights differ by more than its parts' bits, they may be off by most of the row)
+                    const uint32_t ahead = w.count_before(q.r);
+                    const bool back = target <= before, again = sh.walked;
+                    const uint32_t after = back ? sh.after : ahead + w.listed, upto = back ? ahead : sh.upto;
+                    __syncthreads();
+                    if (tid == 0) {
+                        sh.after = after;
+                        sh.upto = upto;
+                        sh.walked = true;
+                    }
+                    if (after >= upto) break;  // (never: the weights of all reach the target)
+                    q = w.search_count(again ? after + (upto - after + 1) / 2 : back ? upto : after + 1);
                 }
             }
             thr = max(thr, sh.thr);
@@ -1022,6 +1040,7 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     if (ld < vocab || (out_probs && ld_probs < vocab)) return SD_EINVAL;
     if (!aligned(logits, 4) || (out_probs && !aligned(out_probs, 4))) return SD_EINVAL;
     if (vocab > DR_VOCAB || N > INT32_MAX / DR_MOST_CTAS) return SD_EUNSUPPORTED;
+    if (out_probs == logits) return SD_EINVAL;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     // As many CTAs per row as the GPU holds at once beside the other rows', two per SM; two at least where top-p may have to

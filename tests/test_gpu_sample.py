@@ -142,6 +142,30 @@ def test_nuclei_that_end_at_a_border(sdv, V, N):
         check(sdv, l, rng.random(N).astype(np.float32) * 0.999, p=np.minimum(p, 1), k=[V - 1] * N, probs=False)
 
 
+@pytest.mark.parametrize("N", [6, 160])
+def test_low_temperatures(sdv, N):
+    """A token and, 9.5 to 13 temperatures behind it, all others: at such a temperature that distance is within one of the first
+    histogram's bins, where the others' parts are rounded away, although together they weigh as much or more."""
+    rng = np.random.default_rng(N)
+    V, T = 151936, np.float32([1e-3, 3e-4, 1e-6, 5e-3, 1e-2, 1e-3])[np.arange(N) % 6]
+    far = np.float32([9.5, 10.6, 11.3, 12.0, 10.6, 13.0])[np.arange(N) % 6]
+    l = -T[:, None] * (far[:, None] + 0.2 * rng.random((N, V)))
+    top = rng.integers(V, size=N)
+    l[np.arange(N), top] = 0.0
+    l = l.astype(np.float32)
+    u = rng.random(N).astype(np.float32) * 0.999
+    for p in (0.3, 0.5, 0.8, 0.999):
+        for k, low in ((0, 0.0), (100000, 0.0), (0, 1e-5)):
+            tokens, prob, _ = run(sdv, l, u, T, [k] * N, [p] * N, [low] * N, probs=False)
+            status_ok()
+            for n in range(6):
+                tok1, prob1, q = run(sdv, l[n:n + 1], u[n:n + 1], T[n:n + 1], [k], [p], [low])
+                assert tok1[0] == tokens[n] and prob1[0] == prob[n]
+                plain.check_row(l[n], float(u[n]), float(T[n]), k, float(np.float32(p)), float(np.float32(low)), int(tokens[n]), float(prob[n]),
+                                q[0].astype(np.float64))
+    status_ok()
+
+
 def test_ties_go_to_the_lower_index(sdv):
     l = np.array([[1, 3, 3, 2, 3, 3, 0, 3.0]] * 8, np.float32)
     u = np.arange(8) / 8 + 1 / 16
