@@ -503,14 +503,15 @@ sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
  * sd_rope_turns (HOST): the table of n frequencies (finite, at most 2^20 in magnitude), to be copied to the device.
  *
  * sd_rope_rows: x, out fp32, row i at i * stride (elements, multiples of 4, 16-byte aligned), its `heads` heads of D
- * contiguous (D a multiple of 8, at most 1024); row i is turned to position pos[i] (device).  out may be x.
+ * contiguous (D a multiple of 8, at most 1024); row i is turned to position pos[i] (device).  out may be x (with the same
+ * stride), and must not overlap it otherwise.
  *
  * sd_paged_append_rope: sd_paged_append of keys turned to their positions and of values as they are, and the turned
  * queries beside it (8-bit rows are quantised after the turn).  Row i of sequence b stands at position lens[b] + depth(i),
  * the depth of node i in the sequence's tree (parent int32 [B][M] as for sd_paged_attn, M <= 16; NULL: chains, depth i, any
  * M); it is written to row lens[b] + i, so that a commit that moves an accepted path leaves every row at the place of its
  * position.  q, q_out fp32 [row i of sequence b at b * seq_stride + i * row_stride], H heads of D contiguous, H any number
- * (0: no queries); q_out may be q.  q, k_new and v_new may be columns of one fused projection.  Rows from n_new[b] on of
+ * (0: no queries); q_out may be q (with the same strides), and must not overlap the inputs otherwise.  q, k_new and v_new may be columns of one fused projection.  Rows from n_new[b] on of
  * q_out are left as they were.  Where a row's page is missing its query is turned all the same.
  */
 typedef enum { SD_ROPE_PLAIN = 0, SD_ROPE_LINEAR = 1, SD_ROPE_NTK = 2, SD_ROPE_BANDS = 3, SD_ROPE_YARN = 4 } sd_rope_scaling;
@@ -542,7 +543,7 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
  * all of its rows, and a batch whose tables cannot hold twice that much is not looked at.  A group number outside [-1, B) counts as
  * -1, and records SD_EDEVICE in a batch that is looked at.
  * Everything else is as in sd_paged_attn; the same call on the same inputs repeats bit for bit, and a sequence's
- * last bits depend on its neighbours.
+ * last bits depend on its neighbours.  out must not overlap q (out == q: SD_EINVAL).
  * workspace: sd_paged_attn_shared_workspace_bytes, zero-filled by the caller once; it serves every call of the same or a
  * smaller B, M, H and D.
  */
@@ -570,7 +571,8 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
  * out_tokens int32 [N]; out_prob fp32 [N] (or NULL): the drawn token's probability among the kept; out_probs fp32 (or
  * NULL), row n at n * ld_probs: all of them, 0 where not kept (q_probs of sd_accept_sample for a drafter that samples).
  * A row with a setting out of range or without any token gets token -1, probability 0, and records SD_EDEVICE.
- * 1 <= vocab <= 360448 (else SD_EUNSUPPORTED).  No workspace.
+ * out_probs must not overlap the logits (out_probs == logits: SD_EINVAL); a difference l_c - m beyond fp32's range weighs
+ * nothing.  1 <= vocab <= 360448 (else SD_EUNSUPPORTED).  No workspace.
  */
 sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, const float *u, const float *temperature,
                     const int32_t *top_k, const float *top_p, const float *min_p, int32_t *out_tokens, float *out_prob,

@@ -362,7 +362,7 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
                                sd_stream_t stream) {
     SD_NVTX("sd_paged_attn_shared");
     const size_t ahead = 256;
-    if (!group || !workspace || !aligned(workspace, 256) || ws_bytes < ahead) return SD_EINVAL;
+    if (!group || !workspace || !aligned(workspace, 256) || ws_bytes < ahead || (out && out == q)) return SD_EINVAL;
     PaCall c;
     const sd_status st = pa_call(pages, table, width, lens, n_new, B, M, H, q, q_seq_stride, q_row_stride, parent, 0, 0, out,
                                  out_seq_stride, out_row_stride, static_cast<uint8_t *>(workspace) + ahead, ws_bytes - ahead, c);

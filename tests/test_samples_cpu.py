@@ -125,7 +125,7 @@ def test_rope_calls_refuse(sdv):
 
 
 def shared(sdv, p, **kw):
-    d = dict(table=A, width=4, lens=A, n_new=None, group=A, B=2, M=5, H=8, q=A, q_sb=5 * 1024, q_sm=1024, parent=None, out=A, o_sb=5 * 1024,
+    d = dict(table=A, width=4, lens=A, n_new=None, group=A, B=2, M=5, H=8, q=A, q_sb=5 * 1024, q_sm=1024, parent=None, out=2 * A, o_sb=5 * 1024,
              o_sm=1024, ws=A, nb=1 << 40)
     d.update(kw)
     return sdv.lib().sd_paged_attn_shared(p, *d.values(), None)
@@ -155,6 +155,11 @@ def test_sample_refuses(sdv):
                          (dict(V=0), EINVAL), (dict(ld=4999), EINVAL), (dict(probs=A, ldp=4999), EINVAL), (dict(probs=A + 2, ldp=5000), EINVAL),
                          (dict(V=360449, ld=1 << 20), EUNSUPPORTED), (dict(N=1 << 30), EUNSUPPORTED)]:
         assert draw(sdv, **change) == code, change
+
+
+def test_outputs_in_the_inputs_place_are_refused(sdv):
+    assert shared(sdv, pages(sdv), q=A, out=A) == EINVAL
+    assert draw(sdv, logits=A, probs=A, ldp=5000) == EINVAL
 
 
 def test_python_refuses(sdv):
