@@ -30,16 +30,16 @@ namespace cg = cooperative_groups;
 namespace sdv {
 
 constexpr int DR_THREADS = 512, DR_WARPS = DR_THREADS / 32;
-constexpr int DR_BITS = 10, DR_BINS = 1 << DR_BITS, DR_COARSE = 32;  // a coarse bin is 32 bins
+// Bins of a histogram, 32 to a coarse one: 1024 beside a row that is held in shared memory; 4096 for one that is read again,
+// where a bin of the first level mostly has few enough tokens to be listed (a level more is a pass more).
+constexpr int bits_of(bool held) { return held ? 10 : 12; }
 constexpr int DR_LIST = 256;      // tokens that are ranked directly
 constexpr int DR_MOST_CTAS = 8;
 constexpr int DR_VOCAB = 360448;  // most tokens of a row
 constexpr int DR_ORDER = 4096;    // most rows that are put in order
 constexpr uint32_t DR_BESIDE = 100;  // tokens on either side of a threshold that are listed with it
 constexpr int DR_SMALL_K = 192;   // top-k for which about as many tokens are worth listing
-// the first histogram: 8 octaves of d from 2^-3 on, by the bits of d
-constexpr uint32_t DR_FIRST = 0x3e000000u;
-constexpr int DR_SHIFT = 16;
+constexpr uint32_t DR_FIRST = 0x3e000000u;  // the first histogram: 8 octaves of d from 2^-3 on, by the bits of d
 
 struct DrawArgs {
     const float *logits;
@@ -54,9 +54,9 @@ struct DrawArgs {
     int *status;
 };
 
-// the order of logits as whole numbers, and back
+// the order of logits as whole numbers (-0 as 0), and back
 __device__ __forceinline__ uint32_t order_key(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.0f);
     return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
@@ -74,8 +74,8 @@ struct Range {
 };
 
 // what a histogram says of the bin that was looked for: the tokens before it and in it (a search by counts); or about the
-// weight before it and the least number of tokens that its weight takes (a search by weights, where bins beside it come along
-// as long as the tokens stay few: the sums are a little off)
+// weight before it and the least number of tokens that the bins' weights take (a search by weights, where bins beside it come
+// along as long as the tokens stay few: the sums are a little off)
 struct Found {
     uint32_t bin, last, before_n, n;
     float before_m, target_m;  // in units of 2^-MASS
@@ -88,10 +88,11 @@ struct Passed {
     uint32_t n;
 };
 
+template <bool HELD>
 struct alignas(16) DrawShared {
     // ---- read or written by the cluster's other CTAs (what they write has two turns: a slow CTA still reads one)
-    uint32_t bins[2][DR_BINS];                   // a level's histogram: tokens, or parts of weights
-    uint32_t coarse[2][DR_MOST_CTAS][DR_COARSE];  // every CTA's: tokens, or weights (floats' bits)
+    uint32_t bins[2][1 << bits_of(HELD)];                     // a level's histogram: tokens, or parts of weights
+    uint32_t coarse[2][DR_MOST_CTAS][1 << (bits_of(HELD) - 5)];  // every CTA's: tokens, or weights (floats' bits)
     uint64_t list[2][DR_LIST];                   // this CTA's tokens in a pass's range
     Passed passed[2][DR_MOST_CTAS];              // every CTA's
     float tops[DR_MOST_CTAS];                    // every CTA's largest logit
@@ -190,6 +191,11 @@ __device__ __forceinline__ T warp_scan(T v) {  // inclusive
     }
     return v;
 }
+template <class T>
+__device__ __forceinline__ T before_me(T v) {  // the sum of the lanes before
+    const T y = __shfl_up_sync(0xffffffffu, warp_scan(v), 1);
+    return (threadIdx.x & 31) ? y : T(0);
+}
 // A search for a threshold so far: the range, the phase that cuts it next, and what the last histogram said.
 struct Search {
     Range r;
@@ -197,10 +203,13 @@ struct Search {
     Found f;
 };
 
-// a logit as it counts: a NaN as minus infinity, -0 as 0; in a row with plus infinities those share everything
-__device__ __forceinline__ float clean(float v) { return fmaxf(v, -INFINITY) + 0.0f; }
-__device__ __forceinline__ float clean_of(float v, bool infinite) {
-    return infinite ? (v == INFINITY ? 0.0f : -INFINITY) : clean(v);
+// a logit as it counts: a NaN as minus infinity; in a row with plus infinities those share everything
+__device__ __forceinline__ float clean(float v) { return fmaxf(v, -INFINITY); }
+__device__ __forceinline__ float4 clean_of(float4 v, bool infinite) {
+    if (infinite)
+        return make_float4(v.x == INFINITY ? 0.0f : -INFINITY, v.y == INFINITY ? 0.0f : -INFINITY,
+                           v.z == INFINITY ? 0.0f : -INFINITY, v.w == INFINITY ? 0.0f : -INFINITY);
+    return make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
 }
 
 // Four logits of a CTA from i (a multiple of four) on, minus infinity from `end` on.
@@ -219,7 +228,7 @@ __device__ __forceinline__ float4 four_of(const float *from, bool wide, int i, i
 template <int CS, bool HELD>
 struct Draw {
     const DrawArgs &a;
-    DrawShared &sh;
+    DrawShared<HELD> &sh;
     const float *x;       // this CTA's logits (HELD: minus infinity up to a multiple of four)
     bool wide, infinite;  // not HELD: 16-byte loads; plus infinities
     int rank, lo, n;   // tokens [lo, lo + n) of the row
@@ -227,6 +236,7 @@ struct Draw {
     float m, top, c_hi, c_lo;  // the row's largest logit, this thread's
     int level, turn;   // histograms and passes so far
 
+    static constexpr int DR_BITS = bits_of(HELD), DR_BINS = 1 << DR_BITS, DR_COARSE = DR_BINS / 32, DR_SHIFT = 26 - DR_BITS;
     // a token's weight in a histogram: a part of its bin's first token's, in units of 2^-MASS (no CTA's sum passes 32 bits)
     static constexpr int MASS_BITS = CS == 1 ? 13 : CS == 2 ? 14 : 15;
     static_assert(static_cast<uint64_t>((DR_VOCAB + CS - 1) / CS + 3) << MASS_BITS < 1ull << 32, "a bin's sum");
@@ -240,8 +250,7 @@ struct Draw {
 
     __device__ __forceinline__ float4 four(int i) const {
         if constexpr (HELD) return *reinterpret_cast<const float4 *>(x + i);
-        const float4 v = four_of(x, wide, i, n);
-        return make_float4(clean_of(v.x, infinite), clean_of(v.y, infinite), clean_of(v.z, infinite), clean_of(v.w, infinite));
+        return clean_of(four_of(x, wide, i, n), infinite);
     }
 
     // f(i, four logits from i on) for this lane's tokens.  Those that are read again come four loads at a time (a load that may
@@ -260,9 +269,7 @@ struct Draw {
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) v[j] = *reinterpret_cast<const float4 *>(x + i0 + 128 * j);
 #pragma unroll
-                    for (int j = 0; j < BATCH; ++j)
-                        f(i0 + 128 * j, make_float4(clean_of(v[j].x, infinite), clean_of(v[j].y, infinite),
-                                                    clean_of(v[j].z, infinite), clean_of(v[j].w, infinite)));
+                    for (int j = 0; j < BATCH; ++j) f(i0 + 128 * j, clean_of(v[j], infinite));
                 } else {
 #pragma unroll 1
                     for (int j = 0; j < BATCH && i0 + 128 * j < w1; ++j) f(i0 + 128 * j, four(i0 + 128 * j));
@@ -340,53 +347,71 @@ struct Draw {
     __device__ __forceinline__ static uint32_t first_bin(uint32_t d) {
         return static_cast<uint32_t>(min(max((static_cast<int32_t>(d) - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT, 0), DR_BINS - 1));
     }
-    // 16 threads per coarse bin; every CTA gets them
+    // The coarse bins; every CTA gets them.
     template <bool FIRST, bool MASS>
     __device__ void share(int phase, const Range &r, int shift) {
         const int tid = static_cast<int>(threadIdx.x), b = level & 1;
+        constexpr int OWN = DR_BINS / DR_THREADS, TEAM = 32 / OWN;  // bins of a thread, threads of a coarse bin
         const uint32_t *bins = sh.bins[b];
         __syncthreads();
         uint32_t cn = 0;
         float cm = 0.0f;
 #pragma unroll
-        for (int j = 0; j < DR_BINS / DR_THREADS; ++j) {
-            const uint32_t bin = DR_BINS / DR_THREADS * tid + j;
+        for (int j = 0; j < OWN; ++j) {
+            const uint32_t bin = OWN * tid + j;
             if constexpr (MASS) cm += static_cast<float>(bins[bin]) * ex2_approx(-c_hi * edge(FIRST, phase, r, shift, bin));
             else cn += bins[bin];
         }
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) {
+        for (int o = TEAM / 2; o >= 1; o >>= 1) {
             if constexpr (MASS) cm += __shfl_xor_sync(0xffffffffu, cm, o);
             else cn += __shfl_xor_sync(0xffffffffu, cn, o);
         }
-        if ((tid & 15) < CS) *of(&sh.coarse[b][rank][tid >> 4], tid & 15) = MASS ? __float_as_uint(cm) : cn;
+#pragma unroll
+        for (int c = tid % TEAM; c < CS; c += TEAM) *of(&sh.coarse[b][rank][tid / TEAM], c) = MASS ? __float_as_uint(cm) : cn;
         cluster_arrive();
         cluster_wait();
         ++level;
     }
 
     // The bin of the last level with the token that brings the count (MASS: about the weight; a share of the whole level's
-    // where target_m is under 0) to the target, from the CTAs' 32 coarse bins and the bins of three of them.  Every CTA
+    // where target_m is under 0) to the target, from the CTAs' coarse bins and the bins of three of them.  Every CTA
     // finds the same.
     template <bool MASS>
     __device__ Found locate(bool first, int phase, const Range &r, int shift, uint32_t target_n, float target_m) {
         const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, b = (level - 1) & 1;
         if (tid < 32) {
             using Sum = typename std::conditional<MASS, float, uint32_t>::type;
-            Sum cs = 0;
+            // NC coarse bins a lane: each one's sum, and that of all before it
+            constexpr int NC = DR_COARSE / 32;
+            Sum cs[NC], pre[NC], sum_c = 0;
 #pragma unroll
-            for (int c = 0; c < CS; ++c) {
-                const uint32_t y = sh.coarse[b][c][lane];
-                if constexpr (MASS) cs += __uint_as_float(y);
-                else cs += y;
+            for (int i = 0; i < NC; ++i) {
+                cs[i] = 0;
+#pragma unroll
+                for (int c = 0; c < CS; ++c) {
+                    const uint32_t y = sh.coarse[b][c][NC * lane + i];
+                    if constexpr (MASS) cs[i] += __uint_as_float(y);
+                    else cs[i] += y;
+                }
+                pre[i] = sum_c;
+                sum_c += cs[i];
             }
-            const Sum in = warp_scan(cs);
+            const Sum pre_c = before_me(sum_c);
             Sum target;
-            if constexpr (MASS) target = target_m < 0.0f ? -target_m * __shfl_sync(0xffffffffu, in, 31) : target_m;
+            if constexpr (MASS) target = target_m < 0.0f ? -target_m * __shfl_sync(0xffffffffu, pre_c + sum_c, 31) : target_m;
             else target = target_n;
             // (rounded sums may fall short of their own total: the last bin that has any, then)
-            const uint32_t there = __ballot_sync(0xffffffffu, cs > 0), at = __ballot_sync(0xffffffffu, cs > 0 && in >= target);
-            const int q = at ? __ffs(at) - 1 : there ? 31 - __clz(there) : 0;
+            int at = INT_MAX, there = 0;
+#pragma unroll
+            for (int i = NC - 1; i >= 0; --i) {
+                pre[i] += pre_c;
+                if (cs[i] > 0 && pre[i] + cs[i] >= target) at = NC * lane + i;
+                if (cs[i] > 0) there = max(there, NC * lane + i);
+            }
+            at = __reduce_min_sync(0xffffffffu, at);
+            there = __reduce_max_sync(0xffffffffu, there);
+            const int q = at != INT_MAX ? at : there;
             // that coarse bin's and its neighbours' bins, three a lane
             const int g0 = min(max(q - 1, 0), DR_COARSE - 3), bin0 = 32 * g0 + 3 * lane;
             uint64_t raw[3] = {0, 0, 0};
@@ -402,7 +427,11 @@ struct Draw {
                 mine += f[i];
                 upto[i] = mine;
             }
-            const Sum ahead = __shfl_sync(0xffffffffu, in - cs, g0) + (warp_scan(mine) - mine);
+            Sum pre_g = pre[0];
+#pragma unroll
+            for (int i = 1; i < NC; ++i)
+                if (g0 % NC == i) pre_g = pre[i];
+            const Sum ahead = __shfl_sync(0xffffffffu, pre_g, g0 / NC) + before_me(mine);
             int hit = INT_MAX, some = -1;
 #pragma unroll
             for (int i = 2; i >= 0; --i) {
@@ -419,7 +448,7 @@ struct Draw {
             uint32_t n[3], sum[3], all = 0;
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                n[i] = static_cast<uint32_t>(MASS ? raw[i] >> MASS_BITS : raw[i]);
+                n[i] = static_cast<uint32_t>(MASS ? (raw[i] + ((1u << MASS_BITS) - 1)) >> MASS_BITS : raw[i]);
                 all += n[i];
                 sum[i] = all;
             }
@@ -677,7 +706,7 @@ struct Draw {
 // The row of a cluster where there are more than the GPU holds at once: first those that may have to be ordered by weight,
 // then the others (a late one of the first kind is several times as long behind the rest: 96 -> 86 us for 256 rows with
 // settings of their own).
-__device__ __forceinline__ int row_in_order(const DrawArgs &a, DrawShared &sh, int q) {
+__device__ __forceinline__ int row_in_order(const DrawArgs &a, uint32_t *heavies, int q) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
     for (int r = tid; r < DR_ORDER; r += DR_THREADS) {
         bool heavy = false;
@@ -686,19 +715,19 @@ __device__ __forceinline__ int row_in_order(const DrawArgs &a, DrawShared &sh, i
             heavy = a.top_p[r] < 1.0f && (k == 0 || k > DR_SMALL_K) && !(a.temperature && a.temperature[r] == 0.0f);
         }
         const uint32_t word = __ballot_sync(0xffffffffu, heavy);
-        if (lane == 0) sh.heavy[r >> 5] = word;
+        if (lane == 0) heavies[r >> 5] = word;
     }
     __syncthreads();
     constexpr int PER = DR_ORDER / 32 / 32;  // words of a lane
     uint32_t w[PER], first = 0, sum = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) first += __popc(sh.heavy[PER * lane + i]);
+    for (int i = 0; i < PER; ++i) first += __popc(heavies[PER * lane + i]);
     first = warp_sum(first);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int r0 = 32 * (PER * lane + i);
         const uint32_t there = r0 >= a.N ? 0u : a.N - r0 >= 32 ? 0xffffffffu : (1u << (a.N - r0)) - 1u;
-        w[i] = (q < static_cast<int>(first) ? sh.heavy[PER * lane + i] : ~sh.heavy[PER * lane + i]) & there;
+        w[i] = (q < static_cast<int>(first) ? heavies[PER * lane + i] : ~heavies[PER * lane + i]) & there;
         sum += __popc(w[i]);
     }
     uint32_t rank = q < static_cast<int>(first) ? q : q - first;
@@ -723,8 +752,8 @@ __device__ __forceinline__ int row_in_order(const DrawArgs &a, DrawShared &sh, i
 template <int CS, bool HELD>
 __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    DrawShared &sh = *reinterpret_cast<DrawShared *>(smem_raw);
-    float *held = reinterpret_cast<float *>(smem_raw + sizeof(DrawShared));
+    DrawShared<HELD> &sh = *reinterpret_cast<DrawShared<HELD> *>(smem_raw);
+    float *held = reinterpret_cast<float *>(smem_raw + sizeof(DrawShared<HELD>));
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     int64_t row = blockIdx.x / CS;
     const int rank = static_cast<int>(blockIdx.x % CS);  // (the clusters are made of neighbours)
@@ -733,7 +762,7 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
     cluster_arrive();  // that this CTA runs, and may be written to
     pdl_wait();
     pdl_launch_dependents();
-    if (a.order) row = row_in_order(a, sh, static_cast<int>(row));
+    if (a.order) row = row_in_order(a, sh.heavy, static_cast<int>(row));
     const float *from = a.logits + row * a.ld + lo;
     if (tid == 0) {  // the row's settings
         const float T = a.temperature ? a.temperature[row] : 1.0f, p = a.top_p ? a.top_p[row] : 1.0f;
@@ -750,7 +779,7 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
         sh.u = u;
         sh.low_log = low > 0.0f && T > 0.0f ? static_cast<double>(T) * log(static_cast<double>(low)) : -INFINITY;
     }
-    // ---- the row's tokens of this CTA; a NaN counts as minus infinity, -0 as 0, and minus infinity fills up the last four
+    // ---- the row's tokens of this CTA; a NaN counts as minus infinity, and minus infinity fills up the last four
     const int run = (n + 4 * DR_WARPS - 1) / (4 * DR_WARPS) * 4, w0 = min(n, warp * run), w1 = min(n, w0 + run);
     float mine = -INFINITY;
     const bool wide = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
@@ -793,7 +822,7 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
     const bool infinite = m == INFINITY;
     if (infinite) {
         if constexpr (HELD)
-            for (int i = tid; i < n; i += DR_THREADS) held[i] = clean_of(held[i], true);
+            for (int i = tid; i < n; i += DR_THREADS) held[i] = held[i] == INFINITY ? 0.0f : -INFINITY;
         mine = mine == INFINITY ? 0.0f : -INFINITY;
         m = 0.0f;
     }
@@ -825,7 +854,7 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
             few = k <= DR_SMALL_K;
             if (few) {
                 w.histogram_of_tops();
-                w.gather(Draw<CS, HELD>::bin_end(w.template locate<false>(true, 0, none, DR_SHIFT, k, 0.0f).bin));
+                w.gather(Draw<CS, HELD>::bin_end(w.template locate<false>(true, 0, none, Draw<CS, HELD>::DR_SHIFT, k, 0.0f).bin));
                 few = w.fits;
                 w.ranks(0, 0);
             }
@@ -1013,7 +1042,7 @@ static cudaError_t sample_launch(const DrawArgs &a, int N, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(N) * CS);
     cfg.blockDim = dim3(DR_THREADS);
-    cfg.dynamicSmemBytes = sizeof(DrawShared) + (HELD ? static_cast<size_t>(a.chunk) * 4 : 0);
+    cfg.dynamicSmemBytes = sizeof(DrawShared<HELD>) + (HELD ? static_cast<size_t>(a.chunk) * 4 : 0);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1070,7 +1099,7 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // (two CTAs of an SM hold their logits in its shared memory where they fit)
-    const bool held = (sizeof(DrawShared) + static_cast<size_t>(a.chunk) * 4 + 1024) * 2 <= 228 * 1024;
+    const bool held = (sizeof(DrawShared<true>) + static_cast<size_t>(a.chunk) * 4 + 1024) * 2 <= 228 * 1024;
     auto run = [&](auto h) {
         constexpr bool H = decltype(h)::value;
         return ctas == 1 ? sample_launch<1, H>(a, N, s) : ctas == 2 ? sample_launch<2, H>(a, N, s)
