@@ -10,7 +10,7 @@
 // leaves its tokens out.  A filter's threshold is the token at a given count, or at a given sum of weights:
 //   a small top-k looks at the lanes' largest logits first: no more tokens than about k are as large as the k-th of those.
 //   They are listed in every CTA and ranked by comparing all with all, and everything else is done on the list;
-//   otherwise histograms over the distance d = m - l (128 bins per octave first; a bin with more than DR_LIST tokens
+//   otherwise histograms over the distance d = m - l (128 bins per octave first, or 512; a bin with more than DR_LIST tokens
 //   is cut again, by the bits of d, then of l, then of the index): each CTA makes its own, one exchange later every CTA adds
 //   up the few bins that decide.  Counts are exact; a bin's weights are 13- to 15-bit parts of its first token's, so their sum only
 //   says where to look (about a token off in a flat row): a pass over the tokens then takes the exact sum of all before the
@@ -31,7 +31,8 @@ namespace sdv {
 
 constexpr int DR_THREADS = 512, DR_WARPS = DR_THREADS / 32;
 // Bins of a histogram, 32 to a coarse one: 1024 beside a row that is held in shared memory; 4096 for one that is read again,
-// where a bin of the first level mostly has few enough tokens to be listed (a level more is a pass more).
+// where a bin of the first level mostly has few enough tokens to be listed (a level more is a pass more: 256 flat rows with
+// top-p 174 -> 141 us; beside a held row as many would leave no place for it).
 constexpr int bits_of(bool held) { return held ? 10 : 12; }
 constexpr int DR_LIST = 256;      // tokens that are ranked directly
 constexpr int DR_MOST_CTAS = 8;
@@ -1073,9 +1074,9 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     // As many CTAs per row as the GPU holds at once beside the other rows', two per SM; two at least where top-p may have to
-    // order a flat row (95 us for one CTA); no more than the row has 1024 tokens for.  256 rows of 151936 tokens by
-    // 1 / 2 / 4 / 8 CTAs: top-k of 50 54 / 59 / 74 / 103 us, each row with its own settings 132 / 86 / 86 / 116 us; 64 rows,
-    // top-k 29 / 20 / 18 / 26 us.
+    // order a flat row (77 us for one CTA); no more than the row has 1024 tokens for.  256 rows of 151936 tokens by
+    // 1 / 2 / 4 / 8 CTAs: top-k of 50 56 / 61 / 77 / 101 us, each row with its own settings 123 / 83 / 85 / 117 us; 64 rows,
+    // top-k 29 / 20 / 18 / 26 us, flat ones with top-p 78 / 47 / 41 / 65.
     const int slots = 2 * num_sms(), least = top_p ? 2 : 1;
     int ctas = DR_MOST_CTAS;
     while (ctas > 1 && (vocab <= static_cast<int64_t>(ctas) * 1024 || (ctas > least && static_cast<int64_t>(N) * ctas > slots)))
