@@ -544,8 +544,8 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
  * -1, and records SD_EDEVICE in a batch that is looked at.
  * Everything else is as in sd_paged_attn; the same call on the same inputs repeats bit for bit, and a sequence's
  * last bits depend on its neighbours.  out must not overlap q (out == q: SD_EINVAL).
- * workspace: sd_paged_attn_shared_workspace_bytes, zero-filled by the caller once; it serves every call of the same or a
- * smaller B, M, H and D.
+ * workspace: sd_paged_attn_shared_workspace_bytes, zero-filled by the caller once (and again after an SD_ETIMEOUT, or a
+ * call that returned SD_ECUDA); it serves every call of the same or a smaller B, M, H and D.
  */
 size_t sd_paged_attn_shared_workspace_bytes(int32_t B, int32_t M, int32_t H, int32_t H_kv, int32_t D);
 sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens,

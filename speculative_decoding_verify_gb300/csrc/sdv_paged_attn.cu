@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 || (MODE == PA_OWN && D ==
         *abort = 0;
         fence_barrier_init();
     }
-    // (PA_OWN: as in paged_wide_kernel)
-    if (MODE != PA_OWN || !a.beside) pdl_wait();
+    if constexpr (MODE == PA_OWN) after_plan(a, last);
+    else pdl_wait();
     pdl_launch_dependents();
     Sched sc;
     if (!make_sched<RPG, PA_THREADS, MODE>(a, prefix, ln, sc)) {
@@ -723,12 +723,15 @@ static cudaError_t pa_wide_run(PaMode mode, const PaCall &c, const PagedArgs &a,
 // a time, each with less ahead of its first tile.
 constexpr int PA_SHORT = 8;
 
+static bool pa_narrow_plan(PaMode mode, const PaCall &c, const PagedArgs &a, PaPlan &p) {
+    // (short runs: 8 rows of D <= 128 at a time, two CTAs per SM, hide more of each other's latency than 16)
+    const int rows = mode == PA_PREFIX ? 16 : mode == PA_OWN && c.D <= 128 && a.own_max == PA_SHORT ? 8 : a.M * a.g;
+    return pa_plan(c.type, a.B, rows, c.D, p);
+}
 static sd_status pa_narrow_run(PaMode mode, const PaCall &c, const PagedArgs &from, cudaStream_t s) {
     PaPlan p;
     PagedArgs a = from;
-    // (short runs: 8 rows of D <= 128 at a time, two CTAs per SM, hide more of each other's latency than 16)
-    const int rows = mode == PA_PREFIX ? 16 : mode == PA_OWN && c.D <= 128 && a.own_max == PA_SHORT ? 8 : a.M * a.g;
-    if (!pa_plan(c.type, a.B, rows, c.D, p)) return SD_ECUDA;
+    if (!pa_narrow_plan(mode, c, a, p)) return SD_ECUDA;
     a.nst = p.nst;
     cudaError_t e;
     if (mode == PA_PREFIX)
@@ -741,20 +744,27 @@ static sd_status pa_narrow_run(PaMode mode, const PaCall &c, const PagedArgs &fr
     return e == cudaSuccess ? SD_OK : SD_ECUDA;
 }
 
+// PA_OWN's first launch: of all sequences, or of those whose runs are short
+static PagedArgs pa_own_first(const PaCall &c) {
+    PagedArgs a = c.a;
+    a.own_min = 0;
+    a.own_max = pa_wide(a.M * a.g, c.D) ? PA_SHORT : INT32_MAX;
+    return a;
+}
+int pa_own_grid(const PaCall &c) {
+    PaPlan p;
+    return pa_narrow_plan(PA_OWN, c, pa_own_first(c), p) ? p.grid : 0;
+}
 sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s) {
     PagedArgs a = c.a;
     const int rows = a.M * a.g, B = a.B;
-    a.own_min = 0;
-    a.own_max = INT32_MAX;
-    a.beside = 1;
-    if (!pa_wide(rows, c.D)) return pa_narrow_run(mode, c, a, s);
+    if (mode == PA_ALL && !pa_wide(rows, c.D)) return pa_narrow_run(mode, c, a, s);
     if (mode == PA_OWN) {
-        a.own_max = PA_SHORT;
-        const sd_status st = pa_narrow_run(mode, c, a, s);
-        if (st != SD_OK) return st;
+        const PagedArgs first = pa_own_first(c);
+        const sd_status st = pa_narrow_run(mode, c, first, s);
+        if (st != SD_OK || first.own_max != PA_SHORT) return st;
         a.own_min = PA_SHORT + 1;
         a.own_max = INT32_MAX;
-        a.beside = 0;
     }
     const int part = B <= PA_WIDE_B ? B : (B + 1) / 2;
     static_assert(PG_MAX_B <= 2 * PA_WIDE_B, "two launches hold the most sequences");

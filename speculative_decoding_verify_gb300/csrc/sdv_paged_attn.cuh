@@ -42,7 +42,7 @@ struct PagedArgs {
     // stay as partials), PA_OWN [B * M][H]
     float2 *row_ml;
     const int32_t *skip;          // PA_OWN: [B] tiles of a sequence's prefix
-    int32_t beside;               // PA_OWN: 1 where nothing but the prefixes' launch may still run
+    int32_t *tickets;             // PA_OWN: [grid], 1 from the plan's end until the CTA takes it
     int32_t own_min, own_max;     // PA_OWN: the sequences of so many tiles behind their prefix
 };
 
@@ -66,6 +66,27 @@ template <int MODE>
 __device__ __forceinline__ void put_ml(const PagedArgs &a, int b, int i, int h, float m, float l) {
     if constexpr (MODE == PA_PREFIX) a.row_ml[static_cast<int64_t>(a.first[b] + i) * a.H + h] = make_float2(m, l);
     if constexpr (MODE == PA_OWN) a.row_ml[(static_cast<int64_t>(b) * a.M + i) * a.H + h] = make_float2(m, l);
+}
+
+// PA_OWN, the kernel of few rows: it runs beside the prefixes' launch, for whose end griddepcontrol.wait would wait.  What it
+// reads is the plan's, or older, and the plan has waited for all that is older: its last CTA releases a ticket per CTA behind
+// its lists, and the exchange that takes it acquires all of that (the proxy fence: for the tensor copies too).  A CTA that finds
+// none waits like any other.  The exchange leaves zero, so a ticket is never an earlier call's, replayed graphs
+// included.  `word` is in shared memory.  All threads call it, and griddepcontrol.wait ahead of their end: what comes next
+// finds the prefixes done as well.  (Waiting here instead: 106 -> 115 us for 4 x 16 + 8 sequences, 176 -> 180 for 64 x 5 rows.)
+__device__ __forceinline__ void after_plan(const PagedArgs &a, volatile int *word) {
+    int32_t *ticket = a.tickets + blockIdx.x;
+    if (threadIdx.x == 0) {
+        int32_t got;
+        asm volatile("atom.acquire.gpu.exch.b32 %0, [%1], %2;" : "=r"(got) : "l"(ticket), "r"(0) : "memory");
+        *word = got;
+    }
+    __syncthreads();
+    if (*word == 0) {
+        pdl_wait();
+        if (threadIdx.x == 0) *ticket = 0;
+    }
+    fence_proxy_async_global();
 }
 
 // the scales of 8-bit rows where there is no page
@@ -581,13 +602,15 @@ struct PaCall {
     int32_t type, D;
 };
 size_t pa_workspace(int D, size_t *off_ml, size_t *off_o);
-size_t pa_counters();  // bytes of counters at its start
+size_t pa_counters();  // bytes of a counter for each CTA of the largest grid (at the workspace's start)
 sd_status pa_call(const sd_kv_pages *pages, const int32_t *table, int32_t width, const int32_t *lens, const int32_t *n_new,
                   int32_t B, int32_t M, int32_t H, const float *q, int64_t q_seq_stride, int64_t q_row_stride,
                   const int32_t *parent, int32_t window, int32_t sinks, float *out, int64_t out_seq_stride,
                   int64_t out_row_stride, void *workspace, size_t ws_bytes, PaCall &c);
 // the new rows of the sequences of c.a (PA_ALL or PA_OWN)
 sd_status pa_rows(const PaCall &c, PaMode mode, cudaStream_t s);
+// CTAs of its first launch (PA_OWN): at most pa_counters() / 4
+int pa_own_grid(const PaCall &c);
 // the prefixes of the groups of c.a (at most PG_MAX_B / 2), of at most `rows` query rows per KV head each, and how their
 // partials are left: rows of one, the CTAs that share the line of tiles, and what the sums and outputs are in
 struct PrefixLayout {

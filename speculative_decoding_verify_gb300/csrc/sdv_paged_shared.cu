@@ -8,7 +8,8 @@
 //   the prefixes: the many-row kernel with all new rows of a group as the rows of one "sequence" (128 of them share each
 //   64-row tile of keys), into the workspace; a run that is cut between CTAs stays as partials (joined there, 128 rows
 //   of up to a dozen of them were one CTA's work: 17 us behind the others);
-//   each sequence's rows behind its prefix, as sd_paged_attn computes them, beside the prefixes as those leave the SMs;
+//   each sequence's rows behind its prefix, as sd_paged_attn computes them, beside the prefixes as those leave the SMs
+//   (after_plan: what orders them behind the plan);
 //   the join, a warp per query row and head: its prefix's partials and its own.
 // So a prefix is read from HBM once per group (per 128 query rows from L2), where sd_paged_attn reads it once per sequence.
 #include "sdv_paged_attn.cuh"
@@ -25,6 +26,7 @@ static int64_t g_share_from = 0;
 // The plan, in the workspace.
 struct SharedPlan {
     int32_t *head;  // [0] CTAs that are done (0 between calls), [1] rows of rows_of
+    int32_t *tickets;  // of the CTAs of the sequences' launch (0 between calls)
     int32_t *ref, *common;                       // [B]: a sequence's group as its lowest member (-1: none), slots that it shares with it
     int32_t *skip;                               // [B] tiles of the prefix
     int4 *at;                                    // [B] its group's first tile in the line of the prefixes' tiles (two words), row
@@ -53,6 +55,7 @@ static SharedWs shared_ws(void *base, int B, int M, int H, int D) {
     };
     auto ints = [&](size_t n) { return reinterpret_cast<int32_t *>(take(4 * n)); };
     w.p.head = reinterpret_cast<int32_t *>(p);
+    w.p.tickets = reinterpret_cast<int32_t *>(take(pa_counters()));
     w.attn = take(pa_workspace(D, nullptr, nullptr));
     w.partials = take(pa_workspace(D, nullptr, nullptr));
     w.p.ref = ints(B);
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(SP_THREADS) shared_plan_kernel(SharedPlan pl, 
                                                                  const int32_t *lens, const int32_t *n_new,
                                                                  const int32_t *group, int32_t B, int32_t M, int32_t P,
                                                                  int32_t H_kv, int32_t g, int32_t rp, int32_t n_pages,
-                                                                 int64_t worth_it, int *status) {
+                                                                 int64_t worth_it, int32_t n_tickets, int *status) {
     __shared__ int32_t s_ref[PG_MAX_B], s_n[PG_MAX_B], s_min[PG_MAX_B];
     __shared__ uint32_t s_at[PG_MAX_B], s_warp[SP_THREADS / 32];
     __shared__ int32_t s_low, s_last;
@@ -241,6 +244,10 @@ __global__ void __launch_bounds__(SP_THREADS) shared_plan_kernel(SharedPlan pl, 
         for (int i = 0; i < (s_n[j] & 31); ++i)
             if (SD_INB(to + i < B * M, status, 127)) pl.rows_of[to + i] = j * M + i;  // site 127: query row of a group
     }
+    __syncthreads();
+    __threadfence();  // (with it the stores release what the CTA has written and seen)
+    for (int i = tid; i < n_tickets; i += SP_THREADS)
+        asm volatile("st.relaxed.gpu.b32 [%0], %1;" ::"l"(pl.tickets + i), "r"(1) : "memory");
 }
 
 struct JoinArgs {
@@ -361,7 +368,7 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
                                int64_t out_seq_stride, int64_t out_row_stride, void *workspace, size_t ws_bytes,
                                sd_stream_t stream) {
     SD_NVTX("sd_paged_attn_shared");
-    const size_t ahead = 256;
+    const size_t ahead = 256 + pa_counters();
     if (!group || !workspace || !aligned(workspace, 256) || ws_bytes < ahead || (out && out == q)) return SD_EINVAL;
     PaCall c;
     const sd_status st = pa_call(pages, table, width, lens, n_new, B, M, H, q, q_seq_stride, q_row_stride, parent, 0, 0, out,
@@ -376,7 +383,7 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
     const int rows = B * M * c.a.g;
     const PrefixLayout lay = pa_prefix_layout(c, rows);
     if (launch(shared_plan_kernel, dim3(B), dim3(SP_THREADS), 0, s, w.p, table, width, lens, n_new, group, B, M, c.a.P, c.a.H_kv,
-               c.a.g, lay.rp, c.a.n_pages, g_share_from ? g_share_from : SP_WORTH, c.a.status) != cudaSuccess)
+               c.a.g, lay.rp, c.a.n_pages, g_share_from ? g_share_from : SP_WORTH, pa_own_grid(c), c.a.status) != cudaSuccess)
         return SD_ECUDA;
     PaCall g = c;
     size_t off_ml, off_o;
@@ -397,6 +404,7 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
     if (r != SD_OK) return r;
     c.a.skip = w.p.skip;
     c.a.row_ml = w.own_ml;
+    c.a.tickets = w.p.tickets;
     r = pa_rows(c, PA_OWN, s);
     if (r != SD_OK) return r;
     JoinArgs ja = {w.p, lay, w.prefix_ml, w.own_ml, g.a.part_ml, w.prefix_o, g.a.part_o, out, out_seq_stride, out_row_stride,

@@ -265,15 +265,10 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         for (int i = 0; i < 6; ++i) badw[i] = 0;
         fence_barrier_init();
     }
-    // (PA_OWN starts beside the prefixes' launch, whose CTAs have all seen what was before it; it waits for it ahead of its
-    // end alone, so that what comes next finds both done)
-    if (MODE != PA_OWN || !a.beside) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
     Sched sc;
-    if (!make_sched<RP, W::THREADS, MODE>(a, prefix, ln, sc)) {
-        if constexpr (MODE == PA_OWN) pdl_wait();
-        return;
-    }
+    if (!make_sched<RP, W::THREADS, MODE>(a, prefix, ln, sc)) return;
     if (warp == W::WARP_M) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tbase)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -962,7 +957,6 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
         }
     }
     // ---- every role is done
-    if constexpr (MODE == PA_OWN) pdl_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == W::WARP_M) {

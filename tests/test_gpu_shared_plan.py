@@ -1,0 +1,80 @@
+"""Attention over shared prefixes as a step of a running batch: what is shared, and what a replayed step reads."""
+import numpy as np
+import pytest
+import torch
+
+from _util import cuda, host, status_ok
+from test_gpu_paged import Cache, i32
+from test_gpu_shared import compare, share
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sdv():
+    from speculative_decoding_verify_gb300 import build as b
+    b.build()
+    import speculative_decoding_verify_gb300 as m
+    m.lib()
+    m.debug_share_from(1)  # small groups too
+    yield m
+    m.debug_share_from(0)
+
+
+# lengths, new rows, groups (members: shared slots of 16 rows)
+STEPS = [([640, 700, 650, 30], [2, 1, 2, 2], {(0, 1, 2): 40}),
+         ([100, 1000, 1010, 900], [1, 2, 2, 1], {(1, 2, 3): 56}),
+         ([320, 330, 500, 510], [2, 2, 1, 2], {(0, 1): 20, (2, 3): 31}),
+         ([70, 64, 800, 17], [2, 2, 2, 2], {}),
+         ([640, 640, 640, 640], [1, 1, 1, 2], {(0, 1, 2, 3): 40})]
+
+
+@pytest.mark.parametrize("H,D,dtype", [(2, 128, "f16"), (16, 64, "bf16"), (16, 128, "f16"), (4, 256, "bf16")])
+def test_a_replayed_step_reads_what_was_written_before_it(sdv, H, D, dtype):
+    """One graph of an append and the attention (few and many query rows), replayed without a pause while lengths, tables, groups, pages
+    and queries change under it: the prefixes' tiles, and so the tiles that each sequence skips, are others each time."""
+    M, H_kv, P, width, n_pages = 2, 1, 16, 70, 260
+    states = []
+    for i, (lens, news, groups) in enumerate(STEPS):
+        rng = np.random.default_rng(100 + i)
+        used = sum(-(-(a + n) // P) for a, n in zip(lens, news))
+        c = Cache(sdv, rng, lens, news, M, H_kv, D, P, dtype, spare=n_pages - used)
+        share(c, groups)
+        group = [next((m[0] for m in groups if b in m), -1) for b in range(4)]
+        table = torch.full((4, width), -1, dtype=torch.int32, device="cuda")
+        table[:, :c.table.shape[1]] = c.table
+        q = rng.standard_normal((4, M, H, D)).astype(np.float32)
+        new = [torch.zeros(4, M, H_kv, D, device="cuda") for _ in range(2)]
+        k, v = c.k.clone(), c.v.clone()
+        for b, (L, n) in enumerate(zip(lens, news)):
+            for to, pool, x in ((new[0], k, c.K), (new[1], v, c.V)):
+                to[b, :n] = torch.tensor(x[b][:, L:L + n].transpose(1, 0, 2)).float().cuda()
+                for j in range(L, L + n):  # the step's append brings them
+                    pool[int(table[b, j // P]), :, j % P] = 7.0
+        states.append((c, q, lens, news, (k, v, table, i32(lens), i32(news), i32(group), cuda(q), *new)))
+    fixed = [torch.zeros_like(x) for x in states[0][4]]
+    fk, fv, table, lens, n_new, group, q, k_new, v_new = fixed
+    pages, out = sdv.KvPages(fk, fv), torch.zeros(4, M, H, D, device="cuda")
+    ws = sdv.workspace(sdv.paged_attn_shared_workspace_bytes(4, M, H, H_kv, D))
+
+    def step():
+        sdv.paged_append(k_new, v_new, pages, table, lens, n_new=n_new)
+        sdv.paged_attn_shared(q, pages, table, lens, group, out, ws, n_new=n_new)
+
+    s, outs, order = torch.cuda.Stream(), [], [0, 1, 0, 2, 4, 3, 1, 4, 2, 0, 3, 2]
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+        for i in order:
+            for to, x in zip(fixed, states[i][4]):
+                to.copy_(x)
+            out.fill_(123.0)
+            graph.replay()
+            outs.append(out.clone())
+        s.synchronize()
+    status_ok()
+    for i, o in zip(order, outs):
+        c, q_, lens_, news_, _ = states[i]
+        compare(o, c, q_, lens_, news_)
