@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(256, 4) shared_join_kernel(const JoinArgs a) {
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = 1.0f / (sum + w);
+        const float all = sum + w, inv = all == 0.0f ? 0.0f : 1.0f / all;  // (no weight at all: every score is below fp32's range)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (on) to[32 * k] = make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv);

@@ -78,3 +78,36 @@ def test_a_replayed_step_reads_what_was_written_before_it(sdv, H, D, dtype):
     for i, o in zip(order, outs):
         c, q_, lens_, news_, _ = states[i]
         compare(o, c, q_, lens_, news_)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("H", [2, 16])
+def test_rows_whose_scores_are_all_below_the_range(sdv, D, H):
+    """Scores that overflow to minus infinity weigh nothing: zeros come out, shared or alone, as from sd_paged_attn.  (4 log2(e) /
+    sqrt(D) times -3e38, summed over D, is under -1e40 in its first 16-bit part; what the part leaves, at most 2^-8 of it on either side, adds up to
+    less than 2e38.)"""
+    P, lens = 16, [200, 230, 300]
+    rng = np.random.default_rng(20)
+    pages = 16 * 3
+    k = torch.full((pages, 1, P, D), -3e38, device="cuda", dtype=torch.bfloat16)
+    v = cuda(rng.standard_normal((pages, 1, P, D)).astype(np.float32)).bfloat16()
+    table = np.arange(pages, dtype=np.int32).reshape(3, 16)[:, ::-1].copy()
+    table = np.concatenate([table, np.full((3, 6), -1, np.int32)], 1)
+    table[:, 16:19] = table[:, :3]  # (300 rows take 19 pages)
+    table[1, :8] = table[0, :8]
+    q = torch.zeros(3, 1, H, D, device="cuda")
+    q[:, :, ::2] = 4.0  # the other heads' scores are 0: the mean of the rows
+    ws = sdv.workspace(sdv.paged_attn_shared_workspace_bytes(3, 1, H, 1, D))
+    pg, t = sdv.KvPages(k, v), torch.tensor(table).cuda()
+    for group in ([0, 0, -1], [-1, -1, -1]):
+        out, ref = torch.full_like(q, 123.0), torch.full_like(q, 123.0)
+        sdv.paged_attn_shared(q, pg, t, i32(lens), i32(group), out, ws)
+        sdv.paged_attn(q, pg, t, i32(lens), ref, ws)
+        status_ok()
+        for o in (host(out), host(ref)):
+            assert np.all(o[:, :, ::2] == 0.0)
+            for b, L in enumerate(lens):
+                rows = host(v.double())[table[b, np.arange(L + 1) // P], 0, np.arange(L + 1) % P]
+                # each weight is 1 and at most two roundings of u; the sums of up to 301 terms round 19 times in tiles and joins
+                tol = (L + 1 + 80) * 2.0 ** -24 * np.abs(rows).mean(0)
+                assert np.all(np.abs(o[b, 0, 1::2] - rows.mean(0)) <= tol)
