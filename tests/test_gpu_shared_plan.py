@@ -111,3 +111,101 @@ def test_rows_whose_scores_are_all_below_the_range(sdv, D, H):
                 # each weight is 1 and at most two roundings of u; the sums of up to 301 terms round 19 times in tiles and joins
                 tol = (L + 1 + 80) * 2.0 ** -24 * np.abs(rows).mean(0)
                 assert np.all(np.abs(o[b, 0, 1::2] - rows.mean(0)) <= tol)
+
+
+def expected(table, lens, news, group, P, H_kv, n_pages, least):
+    """Query rows that a prefix is computed for: of each group's sequences with new rows, the leading slots that name one page in all of
+    them, of whole committed pages, in whole 64-row tiles; nothing where all but one member of each group leave out too little."""
+    members = {}
+    for b, (n, g) in enumerate(zip(news, group)):
+        if n > 0 and 0 <= g < len(lens):
+            members.setdefault(g, []).append(b)
+    less, rows = 0, 0
+    for m in members.values():
+        if len(m) < 2:
+            continue
+        slots = min(lens[b] for b in m) // P
+        same = 0
+        while same < slots and 0 <= table[m[0]][same] < n_pages and all(table[b][same] == table[m[0]][same] for b in m):
+            same += 1
+        tiles = same * P // 64
+        less += (len(m) - 1) * tiles * H_kv
+        rows += sum(news[b] for b in m) if tiles else 0
+    return rows if less >= least else 0
+
+
+def joined(sdv, c, table, lens, news, group, M, H, D, ws, seen=None):
+    """Runs a call and returns the number of query rows that its plan gave a prefix (-7: it did not look)."""
+    ws.view(torch.int32)[1] = -7
+    q = torch.zeros(len(lens), M, H, D, device="cuda") if seen is None else seen
+    out = torch.full_like(q, 123.0)
+    sdv.paged_attn_shared(q, c, table, i32(lens), i32(group), out, ws, n_new=i32(news))
+    status_ok()
+    return int(ws.view(torch.int32)[1]), out
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_what_is_shared(sdv, seed):
+    """Groups of every kind over random tables: the plan gives a prefix to the rows that the tables say, and to no others."""
+    rng = np.random.default_rng(300 + seed)
+    P, H_kv, D = [(16, 2, 64), (8, 1, 128), (64, 2, 64), (128, 1, 64), (32, 3, 128), (16, 1, 256)][seed % 6]
+    B, M, n_pages, width = int(rng.integers(2, 40)), 3, 300, 1024 // P
+    k, v = (torch.randn(n_pages, H_kv, P, D, device="cuda").half() for _ in range(2))
+    pages = sdv.KvPages(k, v)
+    ws = sdv.workspace(sdv.paged_attn_shared_workspace_bytes(B, M, 2 * H_kv, H_kv, D))
+    some = 0
+    for _ in range(10):
+        lens = rng.integers(0, width * P - M + 1, B)
+        news = rng.integers(0, M + 1, B)
+        group = rng.integers(-1, max(1, B // 3), B)
+        table = rng.integers(0, n_pages, (B, width)).astype(np.int32)
+        for g in range(B):  # members share a random number of slots with the first one
+            m = np.flatnonzero(group == g)
+            for b in m[1:]:
+                n = int(rng.integers(0, width + 1))
+                table[b, :n] = table[m[0], :n]
+        want = expected(table, lens, news, group, P, H_kv, n_pages, 1)
+        some += want > 0
+        got, out = joined(sdv, pages, torch.tensor(table).cuda(), lens, news, group, M, 2 * H_kv, D, ws, torch.randn(B, M, 2 * H_kv, D, device="cuda"))
+        assert got == want
+        for b in range(B):  # (the sums over random rows are other tests')
+            assert torch.all(out[b, int(news[b]):] == 123.0) and torch.all(torch.isfinite(out[b]))
+    assert some >= 3
+
+
+@pytest.mark.parametrize("news,group,rows", [([2, 2, 2], [0, 0, 0], 6), ([2, 0, 1], [2, 2, 2], 3), ([2, 2, 2], [0, 0, -1], 4), ([0, 2, 1], [0, 0, 0], 3),
+                                             ([2, 2, 2], [0, 1, 2], 0), ([2, 2, 2], [-1, -1, -1], 0), ([1, 0, 0], [0, 0, 0], 0)])
+def test_who_joins_a_prefix(sdv, news, group, rows):
+    k = torch.randn(20, 1, 16, 64, device="cuda").half()
+    table = torch.tensor([[0, 1, 2, 3, 4, 5 + b] for b in range(3)], dtype=torch.int32).cuda()
+    ws = sdv.workspace(sdv.paged_attn_shared_workspace_bytes(3, 2, 1, 1, 64))
+    assert joined(sdv, sdv.KvPages(k, k), table, [80, 85, 81], news, group, 2, 1, 64, ws)[0] == rows
+
+
+@pytest.mark.parametrize("tiles", [29, 30, 31, 1 << 20])
+def test_the_least_that_a_prefix_has_to_save(sdv, tiles):
+    """3 other members of 2 heads by 5 tiles are 30: up to that least number they share; nobody looks where the tables (6 tiles)
+    cannot hold as much."""
+    k = torch.randn(60, 2, 8, 64, device="cuda").half()
+    table = torch.arange(49, dtype=torch.int32).repeat(4, 1).cuda()
+    ws = sdv.workspace(sdv.paged_attn_shared_workspace_bytes(4, 2, 4, 2, 64))
+    lens = [320, 321, 383, 320]
+    try:
+        sdv.debug_share_from(tiles)
+        got = joined(sdv, sdv.KvPages(k, k), table, lens, [2, 1, 2, 2], [1] * 4, 2, 4, 64, ws)[0]
+    finally:
+        sdv.debug_share_from(1)
+    assert got == (7 if tiles <= 30 else 0 if tiles <= 36 else -7)
+
+
+@pytest.mark.parametrize("rows,held,got", [(8000, 16000, 4), (7999, 16000, 0), (8000, 15936, -7), (15000, 15936, -7), (15000, 16000, 4)])
+def test_the_numbers_from_which_a_batch_shares(sdv, rows, held, got):
+    """Three other members of 8 heads: 125 tiles of 64 rows are 3000, and tables of 250 tiles could hold 6000."""
+    k = torch.randn(1, 8, 64, 64, device="cuda").half()
+    table = torch.zeros(4, held // 64, dtype=torch.int32, device="cuda")
+    ws = sdv.workspace(sdv.paged_attn_shared_workspace_bytes(4, 1, 8, 8, 64))
+    try:
+        sdv.debug_share_from(0)
+        assert joined(sdv, sdv.KvPages(k, k), table, [rows] * 4, [1] * 4, [0] * 4, 1, 8, 64, ws)[0] == got
+    finally:
+        sdv.debug_share_from(1)
