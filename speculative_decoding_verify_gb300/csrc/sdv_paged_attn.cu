@@ -28,7 +28,7 @@ namespace sdv {
 // form is held to that, 162 -> 125 us for 16 sequences of 16000 bf16 rows; at D = 128 it would spill 60 registers and
 // take 20 % longer.)
 template <int T, int D, int NT, int MODE>
-__global__ void __launch_bounds__(PA_THREADS, D == 64 || (MODE == PA_OWN && D == 128 && NT == 1) ? 2 : 0)
+__global__ void __launch_bounds__(PA_THREADS, D == 64 || (MODE == PA_OWN && D == 128) ? 2 : 0)
     paged_attn_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
     using LY = PaLayout<T, D>;
@@ -526,21 +526,22 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 || (MODE == PA_OWN && D ==
                 named_bar_sync(1, 32 * PA_CW);
             }
         }
-        if (MODE != PA_PREFIX && !complete) {
-            // the last of the run's CTAs to come here joins their partials, in the order of their keys
-            const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
-            __threadfence();
-            named_bar_sync(1, 32 * PA_CW);
-            if (tid == 0 && SD_INB(c0 >= 0 && c0 <= c1 && c1 < static_cast<int>(gridDim.x), a.status, 118)) {  // site 118: counter
-                const int was = atomicAdd(&a.counters[c0], 1);
-                *last = was == c1 - c0;
-                if (was == c1 - c0) a.counters[c0] = 0;
+        if constexpr (MODE != PA_PREFIX)  // (a prefix's partials go to the join behind it)
+            if (!complete) {
+                // the last of the run's CTAs to come here joins their partials, in the order of their keys
+                const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
+                __threadfence();
+                named_bar_sync(1, 32 * PA_CW);
+                if (tid == 0 && SD_INB(c0 >= 0 && c0 <= c1 && c1 < static_cast<int>(gridDim.x), a.status, 118)) {  // site 118: counter
+                    const int was = atomicAdd(&a.counters[c0], 1);
+                    *last = was == c1 - c0;
+                    if (was == c1 - c0) a.counters[c0] = 0;
+                }
+                named_bar_sync(1, 32 * PA_CW);
+                if (*last) {
+                    join_partials<RPG, D, 32 * PA_CW, MODE>(a, p, c0, c1, tid, sm_o, 1);
+                }
             }
-            named_bar_sync(1, 32 * PA_CW);
-            if (*last) {
-                join_partials<RPG, D, 32 * PA_CW, MODE>(a, p, c0, c1, tid, sm_o, 1);
-            }
-        }
         u = behind<MODE>(p, u);
     }
     if constexpr (MODE == PA_OWN) pdl_wait();
@@ -635,8 +636,11 @@ static cudaError_t pa_launch_d(int D, const PaPlan &p, const PagedArgs &a, const
                                const CUtensorMap &tmv, cudaStream_t s) {
     if (D == 256)
         return p.nt == 1 ? pa_launch<T, 256, 1, MODE>(p, a, tmk, tmv, s) : pa_launch<T, 256, 2, MODE>(p, a, tmk, tmv, s);
-    if (D == 128)
-        return p.nt == 1 ? pa_launch<T, 128, 1, MODE>(p, a, tmk, tmv, s) : pa_launch<T, 128, 2, MODE>(p, a, tmk, tmv, s);
+    if (D == 128) {
+        if constexpr (MODE != PA_OWN)  // (more than 8 rows of a sequence are the many-row kernel's, or short runs of 8)
+            if (p.nt == 2) return pa_launch<T, 128, 2, MODE>(p, a, tmk, tmv, s);
+        return pa_launch<T, 128, 1, MODE>(p, a, tmk, tmv, s);
+    }
     return p.nt == 1 ? pa_launch<T, 64, 1, MODE>(p, a, tmk, tmv, s) : pa_launch<T, 64, 2, MODE>(p, a, tmk, tmv, s);
 }
 template <int MODE>

@@ -539,7 +539,7 @@ __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1
 #pragma unroll
         for (int k = 0; k < NV; ++k) v[i][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (!SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RPG <= a.part_rows && rows <= RPG &&
-                    (p.rg * RPG + rows - 1) / a.g < (MODE == PA_PREFIX ? p.n : a.M),
+                    (p.rg * RPG + rows - 1) / a.g < a.M,
                 a.status, 116))  // site 116: partials of a join, its output rows
         c1 = c0 - 1;
     for (int x0 = c0; x0 <= c1; x0 += JC) {

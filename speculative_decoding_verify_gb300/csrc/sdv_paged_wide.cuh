@@ -896,61 +896,62 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     lanes[static_cast<int64_t>(pslot) * (RP * D / 4) + d * 128] =
                         make_float4(o[2 * d].x * unit, o[2 * d].y * unit, o[2 * d + 1].x * unit, o[2 * d + 1].y * unit);
             }
-            if (MODE != PA_PREFIX && !complete) {
-                const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
-                __threadfence();
-                named_bar_sync(5, PW_SOFT);
-                if (tid == 0 && SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RP <= a.part_rows,
-                                       a.status, 118)) {  // site 118: counter, partials
-                    const int was = atomicAdd(&a.counters[c0], 1);
-                    *last = was == c1 - c0;
-                    if (was == c1 - c0) a.counters[c0] = 0;
-                }
-                named_bar_sync(5, PW_SOFT);
-                if (*last) {
-                    if constexpr (C > 1) {
-                        join_partials<RP, D, PW_SOFT, MODE>(a, p, c0, c1, tid, scratch, 5, PW_UNIT);
-                    } else {
-                        // as join_partials: in the order of the keys, with a running maximum; two partials' loads in
-                        // flight at once
-                        __threadfence();
-                        float jm = PA_NEG, jl = 0.0f;
+            if constexpr (MODE != PA_PREFIX)
+                if (!complete) {
+                    const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
+                    __threadfence();
+                    named_bar_sync(5, PW_SOFT);
+                    if (tid == 0 && SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RP <= a.part_rows,
+                                           a.status, 118)) {  // site 118: counter, partials
+                        const int was = atomicAdd(&a.counters[c0], 1);
+                        *last = was == c1 - c0;
+                        if (was == c1 - c0) a.counters[c0] = 0;
+                    }
+                    named_bar_sync(5, PW_SOFT);
+                    if (*last) {
+                        if constexpr (C > 1) {
+                            join_partials<RP, D, PW_SOFT, MODE>(a, p, c0, c1, tid, scratch, 5, PW_UNIT);
+                        } else {
+                            // as join_partials: in the order of the keys, with a running maximum; two partials' loads in
+                            // flight at once
+                            __threadfence();
+                            float jm = PA_NEG, jl = 0.0f;
 #pragma unroll
-                        for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
-                        for (int x0 = c0; x0 <= c1; x0 += 2) {
-                            float2 ml[2];
-                            float4 y[2][W::DO / 4];
+                            for (int d = 0; d < W::DO / 2; ++d) o[d] = make_float2(0.0f, 0.0f);
+                            for (int x0 = c0; x0 <= c1; x0 += 2) {
+                                float2 ml[2];
+                                float4 y[2][W::DO / 4];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int x = min(x0 + h, c1);  // (past the last: read again, and weighed by 0)
-                                const int64_t sl = 2 * x + (x == c0);
-                                ml[h] = __ldcg(&a.part_ml[sl * RP + r]);
+                                for (int h = 0; h < 2; ++h) {
+                                    const int x = min(x0 + h, c1);  // (past the last: read again, and weighed by 0)
+                                    const int64_t sl = 2 * x + (x == c0);
+                                    ml[h] = __ldcg(&a.part_ml[sl * RP + r]);
 #pragma unroll
-                                for (int d = 0; d < W::DO / 4; ++d)
-                                    y[h][d] = __ldcg(lanes + sl * (RP * D / 4) + d * 128);
-                            }
+                                    for (int d = 0; d < W::DO / 4; ++d)
+                                        y[h][d] = __ldcg(lanes + sl * (RP * D / 4) + d * 128);
+                                }
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (x0 + h > c1) break;
-                                const float n = fmaxf(jm, ml[h].x), w0 = ex2(jm - n), w = ex2(ml[h].x - n);
-                                jm = n;
-                                jl = fmaf(jl, w0, ml[h].y * w);
+                                for (int h = 0; h < 2; ++h) {
+                                    if (x0 + h > c1) break;
+                                    const float n = fmaxf(jm, ml[h].x), w0 = ex2(jm - n), w = ex2(ml[h].x - n);
+                                    jm = n;
+                                    jl = fmaf(jl, w0, ml[h].y * w);
 #pragma unroll
-                                for (int d = 0; d < W::DO / 4; ++d) {
-                                    const float2 lo = fmul2_rn(o[2 * d], make_float2(w0, w0));
-                                    const float2 hi = fmul2_rn(o[2 * d + 1], make_float2(w0, w0));
-                                    o[2 * d] = ffma2_rn(make_float2(y[h][d].x, y[h][d].y), make_float2(w, w), lo);
-                                    o[2 * d + 1] = ffma2_rn(make_float2(y[h][d].z, y[h][d].w), make_float2(w, w), hi);
+                                    for (int d = 0; d < W::DO / 4; ++d) {
+                                        const float2 lo = fmul2_rn(o[2 * d], make_float2(w0, w0));
+                                        const float2 hi = fmul2_rn(o[2 * d + 1], make_float2(w0, w0));
+                                        o[2 * d] = ffma2_rn(make_float2(y[h][d].x, y[h][d].y), make_float2(w, w), lo);
+                                        o[2 * d + 1] = ffma2_rn(make_float2(y[h][d].z, y[h][d].w), make_float2(w, w), hi);
+                                    }
                                 }
                             }
+                            fac = jl == 0.0f ? 0.0f : 1.0f / jl;
+                            rows_ready = true;
+                            if constexpr (MODE == PA_OWN)
+                                if (real && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, jm, jl * PW_UNIT);
                         }
-                        fac = jl == 0.0f ? 0.0f : 1.0f / jl;
-                        rows_ready = true;
-                        if constexpr (MODE == PA_OWN)
-                            if (real && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, jm, jl * PW_UNIT);
                     }
                 }
-            }
             if constexpr (C == 1 && MODE != PA_PREFIX)
                 if (rows_ready) write_rows(true, fac);
             u = behind<MODE>(p, u);
