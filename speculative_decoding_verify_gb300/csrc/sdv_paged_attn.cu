@@ -799,7 +799,7 @@ PrefixLayout pa_prefix_layout(const PaCall &c, int rows) {
     }
     l.rp = rows <= 32 ? 32 : rows <= 64 && c.type != SD_KV_BF16 ? 64 : 128;
     l.grid = num_sms();
-    l.unit = 6.103515625e-05f;  // (the many-row kernel's weights are in units of 2^-14)
+    l.unit = PW_UNIT;
     return l;
 }
 sd_status pa_prefix(const PaCall &c, int rows, cudaStream_t s) {

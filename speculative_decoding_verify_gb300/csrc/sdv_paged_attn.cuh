@@ -11,6 +11,7 @@ constexpr int PA_CW = 4;           // consumer warps, 16 keys of a tile each
 constexpr int PA_THREADS = 32 * (PA_CW + 1);
 constexpr float PA_NEG = -3.402823466e38f;  // running-max start: finite, below every score
 constexpr float PA_PS = 16384.0f;  // fp16 weights are scaled by 2^14 (exact)
+constexpr float PW_UNIT = 6.103515625e-05f;  // 2^-14: what the many-row kernel's weights and their sums are in
 constexpr uint64_t PA_WAIT_NS = 2000000000ull;
 
 // What a launch goes over: whole sequences (sd_paged_attn); or of a batch that shares prefixes (sd_paged_attn_shared) each

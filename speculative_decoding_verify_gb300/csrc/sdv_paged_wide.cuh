@@ -30,8 +30,8 @@ namespace sdv {
 
 constexpr int PW_NG = 2;       // softmax groups of four warps (the lane quarters of tensor memory)
 constexpr int PW_SOFT = 128 * PW_NG;
-constexpr float PW_UP = 14.0f; // weights are in units of 2^-14 throughout (their sum too): fp16 parts stay normal
-constexpr float PW_UNIT = 6.103515625e-05f;  // 2^-14
+constexpr float PW_UP = 14.0f; // weights are in units of PW_UNIT = 2^-14 throughout (their sum too): fp16 parts stay normal
+static_assert(PW_UNIT * (1 << static_cast<int>(PW_UP)) == 1.0f, "the unit of the weights");
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }

@@ -35,3 +35,10 @@ def test_no_kernel_is_built_that_no_call_reaches():
     got = {tuple(int(x) for x in m) for m in re.findall(r"paged_attn_kernelILi(\d)ELi(\d+)ELi(\d)ELi(\d)EE", names)}
     want = {(t, d, nt, mode) for t in range(3) for d in (64, 128, 256) for nt in (1, 2) for mode in (0, 1) if (d, nt, mode) != (128, 2, 1)}
     assert got == want | {(t, 256, 2, 2) for t in range(3)}
+
+
+def test_the_weights_unit_stands_in_one_place():
+    """The join scales partials by the unit that the many-row kernel's weights are in."""
+    names = ["sdv_paged_attn.cu", "sdv_paged_attn.cuh", "sdv_paged_wide.cuh", "sdv_paged_shared.cu"]
+    assert sum(source(n).count("6.103515625e-05") for n in names) == 1
+    assert "l.unit = PW_UNIT;" in source("sdv_paged_attn.cu")
