@@ -504,7 +504,8 @@ sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
  *
  * sd_rope_rows: x, out fp32, row i at i * stride (elements, multiples of 4, 16-byte aligned), its `heads` heads of D
  * contiguous (D a multiple of 8, at most 1024); row i is turned to position pos[i] (device).  out may be x (with the same
- * stride), and must not overlap it otherwise.
+ * stride), and must not overlap it otherwise.  Heads of more than 65535 blocks (some 2 million of 128) are SD_EUNSUPPORTED,
+ * here and below.
  *
  * sd_paged_append_rope: sd_paged_append of keys turned to their positions and of values as they are, and the turned
  * queries beside it (8-bit rows are quantised after the turn).  Row i of sequence b stands at position lens[b] + depth(i),

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(RP_THREADS) paged_append_rope_kernel(const App
 // otherwise (the launch and the loads' latency are all there is).
 // (A block per row and turn: a grid that stays, 16 blocks per SM, took 118 us for 16384 rows of 40 heads and 148 us for 8
 // prompts of 2048 rows, this 97 and 131.)
-static int heads_per_block(int64_t rows, int heads, int slots) {
+static int heads_per_block(int64_t rows, int64_t heads, int slots) {
     const int64_t full = rows * ((heads + RP_HEADS * slots - 1) / (RP_HEADS * slots));
     return full >= 2 * num_sms() ? RP_HEADS * slots : slots;
 }
@@ -345,13 +345,14 @@ sd_status sd_rope_rows(const sd_rope *rope, const float *x, int64_t x_stride, co
     const int64_t line = static_cast<int64_t>(heads) * D;
     if ((N > 1 && (x_stride < line || out_stride < line)) || x_stride % 4 || out_stride % 4) return SD_EINVAL;
     if (!aligned(x, 16) || !aligned(out, 16)) return SD_EINVAL;
+    const int LR = D / 8, per = heads_per_block(N, heads, RP_THREADS / LR);
+    const int64_t turns = (static_cast<int64_t>(heads) + per - 1) / per;
+    if (turns > 65535) return SD_EUNSUPPORTED;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
-    const int LR = D / 8, per = heads_per_block(N, heads, RP_THREADS / LR);
-    if ((heads + per - 1) / per > 65535) return SD_EUNSUPPORTED;
     const RopeArgs r = {rope->turns, rope->rot, rope->interleaved, rope->scale};
-    return launch(rope_rows_kernel, dim3(N, (heads + per - 1) / per), dim3(RP_THREADS), 0, reinterpret_cast<cudaStream_t>(stream), r, x,
-                  x_stride, pos, N, heads, static_cast<int32_t>(LR), static_cast<int32_t>(per), out, out_stride,
+    return launch(rope_rows_kernel, dim3(N, static_cast<unsigned>(turns)), dim3(RP_THREADS), 0,
+                  reinterpret_cast<cudaStream_t>(stream), r, x, x_stride, pos, N, heads, static_cast<int32_t>(LR), static_cast<int32_t>(per), out, out_stride,
                   status) == cudaSuccess
                ? SD_OK
                : SD_ECUDA;
@@ -379,6 +380,10 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
         if (B > 1 && (q_seq_stride < qline || out_seq_stride < qline)) return SD_EINVAL;
     }
     if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 128) return SD_EUNSUPPORTED;
+    const int64_t rows = static_cast<int64_t>(B) * M, heads = static_cast<int64_t>(H) + 2 * static_cast<int64_t>(pages->H_kv);
+    const int per = heads_per_block(rows, heads, RP_THREADS / (pages->D / 8));
+    const int64_t turns = (heads + per - 1) / per;
+    if (rows > INT32_MAX || turns > 65535) return SD_EUNSUPPORTED;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     AppendRopeArgs a = {};
@@ -395,9 +400,7 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
     a.B = B;
     a.M = M;
     a.H = H;
-    const int64_t rows = static_cast<int64_t>(B) * M;
-    const int heads = H + 2 * pages->H_kv;
-    a.per = heads_per_block(rows, heads, RP_THREADS / (pages->D / 8));
+    a.per = per;
     a.q = q;
     a.k_new = k_new;
     a.v_new = v_new;
@@ -410,9 +413,7 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
     a.sm = row_stride;
     a.r = {rope->turns, rope->rot, rope->interleaved, rope->scale};
     a.status = status;
-    const int turns = (heads + a.per - 1) / a.per;
-    if (rows > INT32_MAX || turns > 65535) return SD_EUNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(rows), turns);
+    const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(turns));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = pages->type == SD_KV_F16    ? append_rope_launch<SD_KV_F16>(pages->D, a, grid, s)
                           : pages->type == SD_KV_BF16 ? append_rope_launch<SD_KV_BF16>(pages->D, a, grid, s)
