@@ -504,7 +504,7 @@ sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
  *
  * sd_rope_rows: x, out fp32, row i at i * stride (elements, multiples of 4, 16-byte aligned), its `heads` heads of D
  * contiguous (D a multiple of 8, at most 1024); row i is turned to position pos[i] (device).  out may be x (with the same
- * stride), and must not overlap it otherwise.  Heads of more than 65535 blocks (some 2 million of 128) are SD_EUNSUPPORTED,
+ * stride, else SD_EINVAL), and must not overlap it otherwise.  Heads of more than 65535 blocks (some 2 million of 128) are SD_EUNSUPPORTED,
  * here and below.
  *
  * sd_paged_append_rope: sd_paged_append of keys turned to their positions and of values as they are, and the turned
@@ -512,8 +512,9 @@ sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
  * the depth of node i in the sequence's tree (parent int32 [B][M] as for sd_paged_attn, M <= 16; NULL: chains, depth i, any
  * M); it is written to row lens[b] + i, so that a commit that moves an accepted path leaves every row at the place of its
  * position.  q, q_out fp32 [row i of sequence b at b * seq_stride + i * row_stride], H heads of D contiguous, H any number
- * (0: no queries); q_out may be q (with the same strides), and must not overlap the inputs otherwise.  q, k_new and v_new may be columns of one fused projection.  Rows from n_new[b] on of
- * q_out are left as they were.  Where a row's page is missing its query is turned all the same.
+ * (0: no queries); q_out may be q (with the same strides, else SD_EINVAL), and must not overlap the inputs otherwise.  q,
+ * k_new and v_new may be columns of one fused projection.  Rows from n_new[b] on of q_out are left as they were.  Where a
+ * row's page is missing its query is turned all the same.
  */
 typedef enum { SD_ROPE_PLAIN = 0, SD_ROPE_LINEAR = 1, SD_ROPE_NTK = 2, SD_ROPE_BANDS = 3, SD_ROPE_YARN = 4 } sd_rope_scaling;
 typedef struct {

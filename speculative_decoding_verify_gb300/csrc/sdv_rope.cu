@@ -345,6 +345,7 @@ sd_status sd_rope_rows(const sd_rope *rope, const float *x, int64_t x_stride, co
     const int64_t line = static_cast<int64_t>(heads) * D;
     if ((N > 1 && (x_stride < line || out_stride < line)) || x_stride % 4 || out_stride % 4) return SD_EINVAL;
     if (!aligned(x, 16) || !aligned(out, 16)) return SD_EINVAL;
+    if (x == out && N > 1 && x_stride != out_stride) return SD_EINVAL;  // (a row would go where another is still read)
     const int LR = D / 8, per = heads_per_block(N, heads, RP_THREADS / LR);
     const int64_t turns = (static_cast<int64_t>(heads) + per - 1) / per;
     if (turns > 65535) return SD_EUNSUPPORTED;
@@ -380,6 +381,7 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
         if (B > 1 && (q_seq_stride < qline || out_seq_stride < qline)) return SD_EINVAL;
     }
     if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 128) return SD_EUNSUPPORTED;
+    if (H > 0 && q == q_out && ((M > 1 && q_row_stride != out_row_stride) || (B > 1 && q_seq_stride != out_seq_stride))) return SD_EINVAL;
     const int64_t rows = static_cast<int64_t>(B) * M, heads = static_cast<int64_t>(H) + 2 * static_cast<int64_t>(pages->H_kv);
     const int per = heads_per_block(rows, heads, RP_THREADS / (pages->D / 8));
     const int64_t turns = (heads + per - 1) / per;

@@ -11,3 +11,12 @@ def test_more_heads_than_a_grid_has_places_are_refused(sdv, heads):  # noqa: F81
     for D in (64, 128, 256):
         p = pages(sdv, D=D, row_stride=D, head_stride=16 * D, page_stride=4 * 16 * D)
         assert append(sdv, p, rope(sdv, rot=8), B=1, M=1, H=heads) == EUNSUPPORTED
+
+
+def test_in_place_with_other_strides_is_refused(sdv):  # noqa: F811
+    """A row that is written where another one is still to be read."""
+    r, p = rope(sdv), pages(sdv)
+    assert rows(sdv, r, xs=1024, os=1028) == EINVAL and rows(sdv, r, xs=2048, os=1024) == EINVAL
+    assert append(sdv, p, r, o_sm=1028, o_sb=5 * 1028) == EINVAL
+    assert append(sdv, p, r, o_sb=6 * 1024) == EINVAL
+    assert append(sdv, p, r, B=1, o_sm=2048) == EINVAL
