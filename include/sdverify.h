@@ -573,7 +573,8 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
  * out_tokens int32 [N]; out_prob fp32 [N] (or NULL): the drawn token's probability among the kept; out_probs fp32 (or
  * NULL), row n at n * ld_probs: all of them, 0 where not kept (q_probs of sd_accept_sample for a drafter that samples).
  * A row with a setting out of range or without any token gets token -1, probability 0, and records SD_EDEVICE.
- * out_probs must not overlap the logits (out_probs == logits: SD_EINVAL); a difference l_c - m beyond fp32's range weighs
+ * out_probs must not overlap the logits, nor any output temperature, top_k or top_p (out_probs == logits, out_tokens == top_k,
+ * out_prob == temperature or top_p: SD_EINVAL); out_prob may be u or min_p.  A difference l_c - m beyond fp32's range weighs
  * nothing.  1 <= vocab <= 360448 (else SD_EUNSUPPORTED).  No workspace.
  */
 sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, const float *u, const float *temperature,

@@ -1071,6 +1071,9 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     if (!aligned(logits, 4) || (out_probs && !aligned(out_probs, 4))) return SD_EINVAL;
     if (vocab > DR_VOCAB || N > INT32_MAX / DR_MOST_CTAS) return SD_EUNSUPPORTED;
     if (out_probs == logits) return SD_EINVAL;
+    // (in a large batch every row's settings are read for its place in the order, by then rows may be drawn)
+    if (top_k && out_tokens == top_k) return SD_EINVAL;
+    if (out_prob && (out_prob == temperature || out_prob == top_p)) return SD_EINVAL;
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     // As many CTAs per row as the GPU holds at once beside the other rows', two per SM; two at least where top-p may have to
