@@ -209,3 +209,29 @@ def test_the_numbers_from_which_a_batch_shares(sdv, rows, held, got):
         assert joined(sdv, sdv.KvPages(k, k), table, [rows] * 4, [1] * 4, [0] * 4, 1, 8, 64, ws)[0] == got
     finally:
         sdv.debug_share_from(1)
+
+
+def test_no_ticket_is_left(sdv):
+    """Every CTA of the own rows' launch takes the ticket that the plan releases for it, whatever its grid is (two CTAs per SM or one), with and
+    without programmatic launches; the same bits either way."""
+    ws = sdv.workspace(sdv.paged_attn_shared_workspace_bytes(5, 2, 16, 2, 256))
+    try:
+        for D, H in ((64, 4), (256, 4), (128, 16), (64, 16), (128, 2)):
+            rng = np.random.default_rng(D + H)
+            lens, news = [320, 700, 333, 390, 41], [2, 1, 2, 2, 2]
+            c = Cache(sdv, rng, lens, news, 2, 2, D, 16, "f16")
+            share(c, {(0, 1, 2, 3): 20})
+            q = rng.standard_normal((5, 2, H, D)).astype(np.float32)
+            outs = []
+            for on in (1, 0, 1):
+                sdv.set_pdl(on)
+                out = torch.full(q.shape, 123.0, device="cuda")
+                sdv.paged_attn_shared(cuda(q), c.pages, c.table, i32(lens), i32([0, 0, 0, 0, -1]), out, ws, n_new=i32(news))
+                status_ok()
+                head = ws.view(torch.int32)[:64 + 2 * torch.cuda.get_device_properties(0).multi_processor_count]
+                assert int(head[0]) == 0 and int(head[1]) == 7 and torch.all(head[64:] == 0)
+                outs.append(out)
+            assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+            compare(outs[0], c, q, lens, news)
+    finally:
+        sdv.set_pdl(1)
