@@ -504,8 +504,8 @@ sd_status sd_pages_compact(const sd_kv_pages *pages, int32_t *refs, int32_t *tab
  *
  * sd_rope_rows: x, out fp32, row i at i * stride (elements, multiples of 4, 16-byte aligned), its `heads` heads of D
  * contiguous (D a multiple of 8, at most 1024); row i is turned to position pos[i] (device).  out may be x (with the same
- * stride, else SD_EINVAL), and must not overlap it otherwise.  Heads of more than 65535 blocks (some 2 million of 128) are SD_EUNSUPPORTED,
- * here and below.
+ * stride, else SD_EINVAL), and must not overlap it otherwise.  Heads of more than 65535 blocks (some 2 million of 128)
+ * are SD_EUNSUPPORTED, here and below.
  *
  * sd_paged_append_rope: sd_paged_append of keys turned to their positions and of values as they are, and the turned
  * queries beside it (8-bit rows are quantised after the turn).  Row i of sequence b stands at position lens[b] + depth(i),
@@ -542,8 +542,8 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
  * that name the same page in all of them, and whose rows are committed in all, in whole 64-row tiles), so that a group
  * that shares nothing, or a sequence that left its group, changes no result.  Where too little is shared for a launch of its
  * own to pay (about 3000 64-row tiles per KV head and member, one member of each group not counted), each sequence reads
- * all of its rows, and a batch whose tables cannot hold twice that much is not looked at.  A group number outside [-1, B) counts as
- * -1, and records SD_EDEVICE in a batch that is looked at.
+ * all of its rows, and a batch whose tables cannot hold twice that much is not looked at.  A group number outside [-1, B)
+ * counts as -1, and records SD_EDEVICE in a batch that is looked at.
  * Everything else is as in sd_paged_attn; the same call on the same inputs repeats bit for bit, and a sequence's
  * last bits depend on its neighbours.  out must not overlap q (out == q: SD_EINVAL).
  * workspace: sd_paged_attn_shared_workspace_bytes, zero-filled by the caller once (and again after an SD_ETIMEOUT, or a
@@ -573,9 +573,9 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
  * out_tokens int32 [N]; out_prob fp32 [N] (or NULL): the drawn token's probability among the kept; out_probs fp32 (or
  * NULL), row n at n * ld_probs: all of them, 0 where not kept (q_probs of sd_accept_sample for a drafter that samples).
  * A row with a setting out of range or without any token gets token -1, probability 0, and records SD_EDEVICE.
- * out_probs must not overlap the logits, nor any output temperature, top_k or top_p (out_probs == logits, out_tokens == top_k,
- * out_prob == temperature or top_p: SD_EINVAL); out_prob may be u or min_p.  A difference l_c - m beyond fp32's range weighs
- * nothing.  1 <= vocab <= 360448 (else SD_EUNSUPPORTED).  No workspace.
+ * out_probs must not overlap the logits, nor any output temperature, top_k or top_p (out_probs == logits, out_tokens ==
+ * top_k, out_prob == temperature or top_p: SD_EINVAL); out_prob may be u or min_p.  A difference l_c - m beyond fp32's
+ * range weighs nothing.  1 <= vocab <= 360448 (else SD_EUNSUPPORTED).  No workspace.
  */
 sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, const float *u, const float *temperature,
                     const int32_t *top_k, const float *top_p, const float *min_p, int32_t *out_tokens, float *out_prob,
@@ -796,7 +796,8 @@ sd_status sd_debug_block_dots(int qtype, const void *w, int64_t n_out, int64_t k
 /* The matmul's SiLU*mul requantisation applied to given g, u fp32 [M][F]. */
 sd_status sd_debug_silu_mul_requant(const float *g, const float *u, int32_t M, int64_t F, int8_t *q, float *scales,
                                     sd_stream_t stream);
-/* Tiles that sd_paged_attn_shared has to be able to leave out before it looks and shares (0: its own numbers, 6000 and 3000). */
+/* Tiles that sd_paged_attn_shared has to be able to leave out before it looks and shares (0: its own numbers, 6000 and
+ * 3000). */
 void sd_debug_share_from(int64_t tiles);
 /* The canonical exponential on n values. */
 sd_status sd_debug_cexp(const float *x, int64_t n, float *y, sd_stream_t stream);

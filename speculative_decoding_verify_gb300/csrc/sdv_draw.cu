@@ -12,8 +12,8 @@
 //   They are listed in every CTA and ranked by comparing all with all, and everything else is done on the list;
 //   otherwise histograms over the distance d = m - l (128 bins per octave first, or 512; a bin with more than DR_LIST tokens
 //   is cut again, by the bits of d, then of l, then of the index): each CTA makes its own, one exchange later every CTA adds
-//   up the few bins that decide.  Counts are exact; a bin's weights are 13- to 15-bit parts of its first token's, so their sum only
-//   says where to look (about a token off in a flat row): a pass over the tokens then takes the exact sum of all before the
+//   up the few bins that decide.  Counts are exact; a bin's weights are 13- to 15-bit parts of its first token's, so their
+//   sum only says where to look (about a token off in a flat row): a pass over the tokens then takes the exact sum of all before the
 //   bin and lists those in it and beside it, and where the threshold is not among them the search goes on at the next token
 //   before or behind, then by halves.
 // A pass leaves the sum of each warp's kept tokens, so the draw is a search among those and a scan of one run.
@@ -254,8 +254,8 @@ struct Draw {
         return clean_of(four_of(x, wide, i, n), infinite);
     }
 
-    // f(i, four logits from i on) for this lane's tokens.  Those that are read again come four loads at a time (a load that may
-    // be cut short would wait for the one before: two branches write the same registers)
+    // f(i, four logits from i on) for this lane's tokens.  Those that are read again come four loads at a time (a load that
+    // may be cut short would wait for the one before: two branches write the same registers)
     template <class F>
     __device__ __forceinline__ void each(F f) const {
         const int at = w0 + 4 * (static_cast<int>(threadIdx.x) & 31);
@@ -317,7 +317,8 @@ struct Draw {
                     if constexpr (FIRST) {
                         bin = first_bin(d);
                         if constexpr (MASS) {
-                            from = __uint_as_float(min(d & (0xffffffffu << DR_SHIFT), DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT)));
+                            constexpr uint32_t LAST = DR_FIRST + (static_cast<uint32_t>(DR_BINS - 1) << DR_SHIFT);
+                            from = __uint_as_float(min(d & (0xffffffffu << DR_SHIFT), LAST));
                             if (bin == 0) from = 0.0f;
                         }
                     } else {
@@ -346,7 +347,8 @@ struct Draw {
         share<true, false>(0, whole(), DR_SHIFT);
     }
     __device__ __forceinline__ static uint32_t first_bin(uint32_t d) {
-        return static_cast<uint32_t>(min(max((static_cast<int32_t>(d) - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT, 0), DR_BINS - 1));
+        const int bin = (static_cast<int32_t>(d) - static_cast<int32_t>(DR_FIRST)) >> DR_SHIFT;
+        return static_cast<uint32_t>(min(max(bin, 0), DR_BINS - 1));
     }
     // The coarse bins; every CTA gets them.
     template <bool FIRST, bool MASS>
@@ -423,7 +425,8 @@ struct Draw {
             Sum f[3], upto[3], mine = 0;
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                if constexpr (MASS) f[i] = static_cast<float>(raw[i]) * ex2_approx(-c_hi * edge(first, phase, r, shift, bin0 + i));
+                if constexpr (MASS)
+                    f[i] = static_cast<float>(raw[i]) * ex2_approx(-c_hi * edge(first, phase, r, shift, bin0 + i));
                 else f[i] = static_cast<uint32_t>(raw[i]);
                 mine += f[i];
                 upto[i] = mine;
@@ -444,7 +447,9 @@ struct Draw {
             some = __reduce_max_sync(0xffffffffu, some);
             const int who = hit != INT_MAX ? hit : max(some, 0);
             // value x[i] of bin k of the 96
-            auto of_bin = [&](auto (&x)[3], int k) { return __shfl_sync(0xffffffffu, k % 3 == 0 ? x[0] : k % 3 == 1 ? x[1] : x[2], k / 3); };
+            auto of_bin = [&](auto (&x)[3], int k) {
+                return __shfl_sync(0xffffffffu, k % 3 == 0 ? x[0] : k % 3 == 1 ? x[1] : x[2], k / 3);
+            };
             int lo = who, hi = who;
             uint32_t n[3], sum[3], all = 0;
 #pragma unroll
@@ -654,7 +659,8 @@ struct Draw {
     }
     __device__ __forceinline__ void put(int t, float l, int idx) {
         const uint32_t slot = atomicAdd(&sh.listed, 1u);
-        if (slot < DR_LIST && SD_INB(slot < DR_LIST, a.status, 124)) sh.list[t][slot] = place_of(l, idx);  // site 124: listed token
+        if (slot < DR_LIST && SD_INB(slot < DR_LIST, a.status, 124))  // site 124: listed token
+            sh.list[t][slot] = place_of(l, idx);
     }
     // how many tokens are before a range, in every CTA
     __device__ uint32_t count_before(const Range &r) {
@@ -750,6 +756,8 @@ __device__ __forceinline__ int row_in_order(const DrawArgs &a, uint32_t *heavies
     return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(row)));
 }
 
+// (Two CTAs per SM have 64 registers a thread: where a row is held nothing is spilled, where it is read again 32 to 64 bytes a
+// thread are, beside 176 to 192 of stack.)
 template <int CS, bool HELD>
 __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -855,7 +863,8 @@ __global__ void __launch_bounds__(DR_THREADS, 2) sample_kernel(const DrawArgs a)
             few = k <= DR_SMALL_K;
             if (few) {
                 w.histogram_of_tops();
-                w.gather(Draw<CS, HELD>::bin_end(w.template locate<false>(true, 0, none, Draw<CS, HELD>::DR_SHIFT, k, 0.0f).bin));
+                const Found f = w.template locate<false>(true, 0, none, Draw<CS, HELD>::DR_SHIFT, k, 0.0f);
+                w.gather(Draw<CS, HELD>::bin_end(f.bin));
                 few = w.fits;
                 w.ranks(0, 0);
             }
@@ -1077,12 +1086,16 @@ sd_status sd_sample(const float *logits, int64_t ld, int64_t vocab, int32_t N, c
     int *status = status_ptr();
     if (!status) return SD_ECUDA;
     // As many CTAs per row as the GPU holds at once beside the other rows', two per SM; two at least where top-p may have to
-    // order a flat row (77 us for one CTA); no more than the row has 1024 tokens for.  256 rows of 151936 tokens by
-    // 1 / 2 / 4 / 8 CTAs: top-k of 50 56 / 61 / 77 / 101 us, each row with its own settings 123 / 83 / 85 / 117 us; 64 rows,
-    // top-k 29 / 20 / 18 / 26 us, flat ones with top-p 78 / 47 / 41 / 65.
+    // order a flat row; no more than the row has 1024 tokens for.  us by 1 / 2 / 4 / 8 CTAs, rows of 151936 tokens:
+    //               64 rows            256 rows              1024 rows
+    //   top-k 50    30 / 20 / 18 / 26  58 / 62 / 78 / 100    209 / 210 / 268 / 376
+    //   T alone     36 / 22 / 21 / 27  76 / 74 / 76 / 93     252 / 233 / 277 / 348  (256 rows at once are read twice from HBM)
+    //   flat top-p  78 / 47 / 41 / 66  137 / 142 / 153 / 239 459 / 457 / 571 / 916
+    //   mixed                          123 / 83 / 85 / 117  (a setting of its own for each row)
     const int slots = 2 * num_sms(), least = top_p ? 2 : 1;
     int ctas = DR_MOST_CTAS;
-    while (ctas > 1 && (vocab <= static_cast<int64_t>(ctas) * 1024 || (ctas > least && static_cast<int64_t>(N) * ctas > slots)))
+    while (ctas > 1 &&
+           (vocab <= static_cast<int64_t>(ctas) * 1024 || (ctas > least && static_cast<int64_t>(N) * ctas > slots)))
         ctas /= 2;
     DrawArgs a = {};
     a.logits = logits;

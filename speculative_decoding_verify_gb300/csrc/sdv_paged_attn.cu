@@ -504,9 +504,11 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 || (MODE == PA_OWN && D ==
                     inv = lv == 0.0f ? 0.0f : 1.0f / lv;
                     if (!complete && tg < rows && (tid & 15) == 0) a.part_ml[pslot * RPG + tr] = make_float2(mx, lv);
                     if constexpr (MODE != PA_ALL)
-                        if (complete && tg < rows && (tid & 15) == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
+                        if (complete && tg < rows && (tid & 15) == 0)
+                            put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv);
                 }
-                if (tg < rows && SD_INB(p.b < a.B && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh < a.H_kv && (complete || (pslot + 1) * RPG <= a.part_rows),
+                if (tg < rows && SD_INB(p.b < a.B && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh < a.H_kv &&
+                                            (complete || (pslot + 1) * RPG <= a.part_rows),
                                         a.status, 117)) {  // site 117: rows of a piece
                     const int i = tg / a.g, h = p.kh * a.g + tg % a.g, d = 4 * (tid & 15);
                     float *op = complete ? out_row<MODE>(a, p.b, i, h, D)
@@ -532,7 +534,8 @@ __global__ void __launch_bounds__(PA_THREADS, D == 64 || (MODE == PA_OWN && D ==
                 const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
                 __threadfence();
                 named_bar_sync(1, 32 * PA_CW);
-                if (tid == 0 && SD_INB(c0 >= 0 && c0 <= c1 && c1 < static_cast<int>(gridDim.x), a.status, 118)) {  // site 118: counter
+                if (tid == 0 && SD_INB(c0 >= 0 && c0 <= c1 && c1 < static_cast<int>(gridDim.x), a.status,
+                                       118)) {  // site 118: counter
                     const int was = atomicAdd(&a.counters[c0], 1);
                     *last = was == c1 - c0;
                     if (was == c1 - c0) a.counters[c0] = 0;
@@ -723,8 +726,8 @@ static cudaError_t pa_wide_run(PaMode mode, const PaCall &c, const PagedArgs &a,
     return run(a, c.tmk, c.tmv, c.D, rows, grid, s);
 }
 
-// Tiles behind a prefix up to which the kernel of few rows takes a sequence whatever its query rows are: it holds more runs at
-// a time, each with less ahead of its first tile.
+// Tiles behind a prefix up to which the kernel of few rows takes a sequence whatever its query rows are: it holds more runs
+// at a time, each with less ahead of its first tile.
 constexpr int PA_SHORT = 8;
 
 static bool pa_narrow_plan(PaMode mode, const PaCall &c, const PagedArgs &a, PaPlan &p) {

@@ -39,8 +39,8 @@ struct PagedArgs {
     // PA_PREFIX: lens, n_new hold the groups' shared rows and numbers of new rows, first[v] where group v's begin in
     // rows_of (sequence * M + row), leader[v] a sequence whose table names the group's pages; out [row of rows_of][H][D]
     const int32_t *first, *leader, *rows_of;
-    // maximum and sum behind each row of out and head: PA_PREFIX [row of rows_of][H] (of runs inside one CTA; those that are cut
-    // stay as partials), PA_OWN [B * M][H]
+    // maximum and sum behind each row of out and head: PA_PREFIX [row of rows_of][H] (of runs inside one CTA; those that are
+    // cut stay as partials), PA_OWN [B * M][H]
     float2 *row_ml;
     const int32_t *skip;          // PA_OWN: [B] tiles of a sequence's prefix
     int32_t *tickets;             // PA_OWN: [grid], 1 from the plan's end until the CTA takes it
@@ -69,12 +69,13 @@ __device__ __forceinline__ void put_ml(const PagedArgs &a, int b, int i, int h, 
     if constexpr (MODE == PA_OWN) a.row_ml[(static_cast<int64_t>(b) * a.M + i) * a.H + h] = make_float2(m, l);
 }
 
-// PA_OWN, the kernel of few rows: it runs beside the prefixes' launch, for whose end griddepcontrol.wait would wait.  What it
-// reads is the plan's, or older, and the plan has waited for all that is older: its last CTA releases a ticket per CTA behind
-// its lists, and the exchange that takes it acquires all of that (the proxy fence: for the tensor copies too).  A CTA that finds
-// none waits like any other.  The exchange leaves zero, so a ticket is never an earlier call's, replayed graphs
+// PA_OWN, the kernel of few rows: it runs beside the prefixes' launch, for whose end griddepcontrol.wait would wait.  What
+// it reads is the plan's, or older, and the plan has waited for all that is older: its last CTA releases a ticket per CTA
+// behind its lists, and the exchange that takes it acquires all of that (the proxy fence: for the tensor copies too).  A CTA
+// that finds none waits like any other.  The exchange leaves zero, so a ticket is never an earlier call's, replayed graphs
 // included.  `word` is in shared memory.  All threads call it, and griddepcontrol.wait ahead of their end: what comes next
-// finds the prefixes done as well.  (Waiting here instead: 106 -> 115 us for 4 x 16 + 8 sequences, 176 -> 180 for 64 x 5 rows.)
+// finds the prefixes done as well.  (Waiting here instead: 106.5 -> 115 us for 4 x 16 + 8 sequences, 178 -> 180 for 64 x 5
+// rows.)
 __device__ __forceinline__ void after_plan(const PagedArgs &a, volatile int *word) {
     int32_t *ticket = a.tickets + blockIdx.x;
     if (threadIdx.x == 0) {
@@ -363,7 +364,8 @@ __device__ bool make_sched(const PagedArgs &a, int64_t *prefix, int2 *ln, Sched 
     sc.u0 = static_cast<int64_t>(blockIdx.x) * sc.W / sc.G;
     sc.u1 = static_cast<int64_t>(blockIdx.x + 1) * sc.W / sc.G;
     if constexpr (MODE == PA_OWN) {
-        // an end inside a short run moves to its start, which leaves the ends inside the others, and so cta_of there, as they are
+        // an end inside a short run moves to its start, which leaves the ends inside the others, and so cta_of there, as they
+        // are
         auto whole = [&](int64_t u) {
             if (u >= sc.W) return u;
             int lo = 0, hi = a.B - 1;
@@ -432,7 +434,8 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
             __syncwarp();
             for (int i = lane; i < n; i += 32) {
                 const int tg = p.rg * RPG + r0 + i;
-                if (!SD_INB(p.b >= 0 && p.b < a.B && tg >= 0 && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh >= 0 && p.kh < a.H_kv && slot < nst,
+                if (!SD_INB(p.b >= 0 && p.b < a.B && tg >= 0 && tg / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh >= 0 &&
+                                p.kh < a.H_kv && slot < nst,
                             a.status, 113))  // site 113: query row
                     continue;
                 bulk_g2s_l2keep(ring + static_cast<size_t>(slot) * LY::STAGE + i * (D * 4 + 16),
@@ -443,7 +446,8 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
         }
         if (!ok) break;
         const int32_t *tab = a.table + static_cast<int64_t>(MODE == PA_PREFIX ? a.leader[b] : b) * a.width;
-        const int total = MODE == PA_PREFIX ? p.len : p.len + p.n, lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
+        const int total = MODE == PA_PREFIX ? p.len : p.len + p.n;
+        const int lo = a.window > 0 ? max(0, p.len - a.window + 1) : 0, sink = a.window > 0 ? a.sinks : 0;
         // the pages of the piece's places in order, npt to a tile, 32 at a time and 32 more on their way: a table entry
         // fetched per tile would cost the tile its latency.  (A place without rows, or an entry that is no page, reads
         // as zeros.)
@@ -504,8 +508,9 @@ __device__ void produce_tiles(const PagedArgs &a, const Sched &sc, const CUtenso
 }
 
 // The partials of one run's CTAs c0 .. c1, joined in the order of their keys by the NTHR threads that call it (named
-// barrier `bar` among them; l_unit: what their sums are in).  A warp reads whole rows (a row of D = 64 half a warp), JC CTAs at a time: the weights of
-// all rows come first, through shared memory (RPG * (JC + 2) floats), then every load of a pass is in flight at once.
+// barrier `bar` among them; l_unit: what their sums are in).  A warp reads whole rows (a row of D = 64 half a warp), JC
+// CTAs at a time: the weights of all rows come first, through shared memory (RPG * (JC + 2) floats), then every load of a
+// pass is in flight at once.
 constexpr int JC = 8;
 template <int RPG, int D, int NTHR, int MODE>
 __device__ void join_partials(const PagedArgs &a, const Piece &p, int c0, int c1, int tid, float *sm, int bar,

@@ -17,9 +17,16 @@
 namespace sdv {
 
 constexpr int SP_THREADS = 256;
-// Tiles of keys (per KV head and member) that have to be left out for the prefixes' launch to pay: it and the join cost about
-// as long as 3000 of them.  Where the tables cannot hold SP_LOOK of them, which the plan costs too, nobody looks.  (A test
-// may set another number for both.)
+// Tiles of keys (per KV head and member) that have to be left out for the prefixes' launch to pay: it and the join cost
+// about as long as 3000 of them.  Where the tables cannot hold SP_LOOK of them, which the plan costs too, nobody looks.  (A
+// test may set another number for both.)  us of sd_paged_attn / with the prefix shared, 8 KV heads, one new row a member:
+//   tiles left out         D = 128 fp16   D = 64 int8    D = 256 fp16
+//    6000 (4 x 16000 rows)  42.4 / 42.1    42.8 / 42.9    96 / 81
+//    7440 (16 x 4000)       41.3 / 40.4    42.3 / 41.0    94 / 65
+//    7560 (64 x 1000)       45.9 / 51.6    45.6 / 49.9   104 / 84
+//   14000 (8 x 16000)       70.5 / 45.4    74.2 / 46.9   175 / 113
+// A tile counts the same whatever its bytes, its members' query rows and the number of members: many members of a short
+// prefix lose up to 12 % there, and D = 256 would gain from fewer tiles on.
 constexpr int64_t SP_WORTH = 3000, SP_LOOK = 6000;
 static int64_t g_share_from = 0;
 
@@ -27,13 +34,13 @@ static int64_t g_share_from = 0;
 struct SharedPlan {
     int32_t *head;  // [0] CTAs that are done (0 between calls), [1] rows of rows_of
     int32_t *tickets;  // of the CTAs of the sequences' launch (0 between calls)
-    int32_t *ref, *common;                       // [B]: a sequence's group as its lowest member (-1: none), slots that it shares with it
-    int32_t *skip;                               // [B] tiles of the prefix
-    int4 *at;                                    // [B] its group's first tile in the line of the prefixes' tiles (two words), row
-                                                 // groups per KV head, the sequence's first row in the group
-    int64_t *line;                               // that line's length
-    int32_t *first, *rows, *len, *leader;        // [B / 2]: the groups
-    int32_t *rows_of;                            // [B * M]
+    int32_t *ref, *common;  // [B]: a sequence's group as its lowest member (-1: none), slots that it shares with it
+    int32_t *skip;          // [B] tiles of the prefix
+    int4 *at;       // [B] its group's first tile in the line of the prefixes' tiles (two words), row groups per KV head, the
+                    // sequence's first row in the group
+    int64_t *line;  // that line's length
+    int32_t *first, *rows, *len, *leader;  // [B / 2]: the groups
+    int32_t *rows_of;                      // [B * M]
 };
 struct SharedWs {
     SharedPlan p;
@@ -166,19 +173,23 @@ __global__ void __launch_bounds__(SP_THREADS) shared_plan_kernel(SharedPlan pl, 
     if (tid == 0) s_low = 0;
     __syncthreads();
     for (int j = tid; j < B; j += SP_THREADS)
-        s_min[j] = s_ref[j] == j && s_min[j] != INT32_MAX ? static_cast<int32_t>(static_cast<int64_t>(s_min[j]) * P / PA_KT) : 0;
+        s_min[j] = s_ref[j] == j && s_min[j] != INT32_MAX
+                       ? static_cast<int32_t>(static_cast<int64_t>(s_min[j]) * P / PA_KT) : 0;
     __syncthreads();
     int64_t less = 0;
     for (int j = tid; j < B; j += SP_THREADS)
         if (s_ref[j] >= 0 && s_ref[j] != j) less += static_cast<int64_t>(s_min[s_ref[j]]) * H_kv;
-    if (less > 0) atomicAdd(&s_low, static_cast<int32_t>(min(less, static_cast<int64_t>(1 << 20))));  // (1024 of them at most)
+    // (256 threads' at most: no sum passes 32 bits)
+    if (less > 0) atomicAdd(&s_low, static_cast<int32_t>(min(less, static_cast<int64_t>(1 << 20))));
     __syncthreads();
     const bool worth = s_low >= worth_it;
     // groups in the order of their lowest members: each thread takes neighbours, (groups << 16 | rows) summed over all before
     const int per = (B + SP_THREADS - 1) / SP_THREADS, j0 = min(B, tid * per), j1 = min(B, j0 + per);
     uint32_t sum = 0;
     int64_t tiles_of = 0;  // and the tiles of their runs
-    auto group_tiles = [&](int j) { return static_cast<int64_t>((static_cast<int>(s_at[j]) * g + rp - 1) / rp) * H_kv * s_min[j]; };
+    auto group_tiles = [&](int j) {
+        return static_cast<int64_t>((static_cast<int>(s_at[j]) * g + rp - 1) / rp) * H_kv * s_min[j];
+    };
     for (int j = j0; j < j1; ++j) {
         if (!worth) s_min[j] = 0;
         if (s_min[j] > 0) {
@@ -219,7 +230,8 @@ __global__ void __launch_bounds__(SP_THREADS) shared_plan_kernel(SharedPlan pl, 
     for (int j = j0; j < j1; ++j)
         if (s_min[j] > 0) {
             const uint32_t n = s_at[j], v = at >> 16;
-            if (SD_INB(v < static_cast<uint32_t>(B) / 2 && (at & 0xffffu) + n <= static_cast<uint32_t>(B) * M, status, 126)) {  // site 126: group
+            if (SD_INB(v < static_cast<uint32_t>(B) / 2 && (at & 0xffffu) + n <= static_cast<uint32_t>(B) * M, status,
+                       126)) {  // site 126: group
                 pl.first[v] = static_cast<int32_t>(at & 0xffffu);
                 pl.rows[v] = static_cast<int32_t>(n);
                 pl.len[v] = s_min[j] * PA_KT;
@@ -237,9 +249,11 @@ __global__ void __launch_bounds__(SP_THREADS) shared_plan_kernel(SharedPlan pl, 
         const int r = s_ref[j], tiles = r >= 0 ? s_min[r] : 0;
         pl.skip[j] = tiles;
         if (tiles == 0) continue;
+        // (a walk over the group: 9 us in all for 72 sequences in groups of 16, 15 for 1024, 37 for 1024 in one group)
         int to = 0;
         for (int i = r; i < j; ++i) to += s_ref[i] == r ? s_n[i] & 31 : 0;
-        pl.at[j] = make_int4(static_cast<int32_t>(s_line[r] & 0xffffffff), static_cast<int32_t>(s_line[r] >> 32), s_n[r] >> 5, to);
+        pl.at[j] = make_int4(static_cast<int32_t>(s_line[r] & 0xffffffff), static_cast<int32_t>(s_line[r] >> 32),
+                             s_n[r] >> 5, to);
         to += static_cast<int>(s_at[r]);
         for (int i = 0; i < (s_n[j] & 31); ++i)
             if (SD_INB(to + i < B * M, status, 127)) pl.rows_of[to + i] = j * M + i;  // site 127: query row of a group
@@ -275,12 +289,14 @@ __global__ void __launch_bounds__(256, 4) shared_join_kernel(const JoinArgs a) {
     const bool on = lane < D / 4;
     const int64_t items = static_cast<int64_t>(__ldcg(&a.pl.head[1])) * a.H, W = *a.pl.line;
     const int64_t G = min(static_cast<int64_t>(a.lay.grid), W);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += static_cast<int64_t>(gridDim.x) * 8) {
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+         it += static_cast<int64_t>(gridDim.x) * 8) {
         const int x = static_cast<int>(it / a.H), h = static_cast<int>(it - static_cast<int64_t>(x) * a.H);
         const int code = a.pl.rows_of[x], b = code / a.M, i = code - b * a.M;
         if (!SD_INB(x < a.B * a.M && code >= 0 && b < a.B, a.status, 129)) continue;  // site 129: joined row
         const int4 y = a.pl.at[b];
-        const int T = a.pl.skip[b], kh = h / a.g, tg = (y.w + i) * a.g + h - kh * a.g, rg = tg / a.lay.rp, r = tg - rg * a.lay.rp;
+        const int T = a.pl.skip[b], kh = h / a.g, tg = (y.w + i) * a.g + h - kh * a.g;
+        const int rg = tg / a.lay.rp, r = tg - rg * a.lay.rp;
         const int64_t run0 = (static_cast<int64_t>(static_cast<uint32_t>(y.x)) | static_cast<int64_t>(y.y) << 32) +
                              (static_cast<int64_t>(kh) * y.z + rg) * T;
         const int c0 = static_cast<int>(((run0 + 1) * G - 1) / W), n = static_cast<int>(((run0 + T) * G - 1) / W) - c0 + 1;
@@ -342,7 +358,8 @@ __global__ void __launch_bounds__(256, 4) shared_join_kernel(const JoinArgs a) {
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float all = sum + w, inv = all == 0.0f ? 0.0f : 1.0f / all;  // (no weight at all: every score is below fp32's range)
+        // (no weight at all: every score is below fp32's range)
+        const float all = sum + w, inv = all == 0.0f ? 0.0f : 1.0f / all;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (on) to[32 * k] = make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv);

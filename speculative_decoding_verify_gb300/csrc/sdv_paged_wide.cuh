@@ -842,7 +842,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
             const float f = ex2(m - mx) * unit * (!complete ? 1.0f : lv == 0.0f ? 0.0f : 1.0f / lv);
             if (!complete && real && lg == 0 && grp == 0) a.part_ml[pslot * RP + r] = make_float2(mx, lv);
             if constexpr (MODE != PA_ALL)
-                if (complete && real && lg == 0 && grp == 0) put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * PW_UNIT);
+                if (complete && real && lg == 0 && grp == 0)
+                    put_ml<MODE>(a, p.b, tg / a.g, p.kh * a.g + tg % a.g, mx, lv * PW_UNIT);
             // rows of D floats from the threads' columns times fac, 16 columns of every group at a time through shared
             // memory: thread = 4 columns of row tid / 8 (and of the rows RW further on), group (tid / 4) % 2
             auto write_rows = [&](bool final, float fac) {
@@ -867,8 +868,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     named_bar_sync(5, PW_SOFT);
 #pragma unroll
                     for (int k = 0; k < NK; ++k)
-                        if (to[k] && SD_INB(p.b < a.B && (p.rg * RP + wr + RW * k) / a.g < (MODE == PA_PREFIX ? p.n : a.M) && p.kh < a.H_kv &&
-                                                (final || (pslot + 1) * RP <= a.part_rows),
+                        if (to[k] && SD_INB(p.b < a.B && (p.rg * RP + wr + RW * k) / a.g < (MODE == PA_PREFIX ? p.n : a.M) &&
+                                                p.kh < a.H_kv && (final || (pslot + 1) * RP <= a.part_rows),
                                             a.status, 117)) {  // site 117: rows of a piece
                             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -901,7 +902,8 @@ __global__ void __launch_bounds__(WideLayout<T, D, C>::THREADS, 1)
                     const int c0 = cta_of(sc, p.run0), c1 = cta_of(sc, p.run0 + p.st.T - 1);
                     __threadfence();
                     named_bar_sync(5, PW_SOFT);
-                    if (tid == 0 && SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) && (2 * c1 + 2) * RP <= a.part_rows,
+                    if (tid == 0 && SD_INB(c0 >= 0 && c0 < c1 && c1 < static_cast<int>(gridDim.x) &&
+                                               (2 * c1 + 2) * RP <= a.part_rows,
                                            a.status, 118)) {  // site 118: counter, partials
                         const int was = atomicAdd(&a.counters[c0], 1);
                         *last = was == c1 - c0;

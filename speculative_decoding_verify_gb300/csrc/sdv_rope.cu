@@ -73,8 +73,8 @@ __device__ __forceinline__ void turn_lane(float4 &x, float4 &y, const Turn &t, b
     }
 }
 
-// Rows: block (n, y) takes the y-th `per` heads of row n; the threads behind the last whole head of a block only help with the
-// sines.
+// Rows: block (n, y) takes the y-th `per` heads of row n; the threads behind the last whole head of a block only help with
+// the sines.
 __global__ void __launch_bounds__(RP_THREADS) rope_rows_kernel(RopeArgs r, const float *x, int64_t xs, const int32_t *pos,
                                                                int32_t N, int32_t heads, int32_t LR, int32_t per,
                                                                float *out, int64_t os, int *status) {
@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(RP_THREADS) rope_rows_kernel(RopeArgs r, const
     pdl_launch_dependents();
     const int slots = RP_THREADS / LR, slot = static_cast<int>(threadIdx.x) / LR, l = static_cast<int>(threadIdx.x) % LR;
     const int64_t n = blockIdx.x;
-    const int h0 = static_cast<int>(blockIdx.y) * per + slot, h1 = min(heads, static_cast<int>(blockIdx.y + 1) * per), D = 8 * LR;
+    const int h0 = static_cast<int>(blockIdx.y) * per + slot, h1 = min(heads, static_cast<int>(blockIdx.y + 1) * per);
+    const int D = 8 * LR;
     const int2 at = lane_at(r, l);
     const bool work = slot < slots;
     float4 a[RP_HEADS], b[RP_HEADS];
@@ -353,8 +354,8 @@ sd_status sd_rope_rows(const sd_rope *rope, const float *x, int64_t x_stride, co
     if (!status) return SD_ECUDA;
     const RopeArgs r = {rope->turns, rope->rot, rope->interleaved, rope->scale};
     return launch(rope_rows_kernel, dim3(N, static_cast<unsigned>(turns)), dim3(RP_THREADS), 0,
-                  reinterpret_cast<cudaStream_t>(stream), r, x, x_stride, pos, N, heads, static_cast<int32_t>(LR), static_cast<int32_t>(per), out, out_stride,
-                  status) == cudaSuccess
+                  reinterpret_cast<cudaStream_t>(stream), r, x, x_stride, pos, N, heads,
+                  static_cast<int32_t>(LR), static_cast<int32_t>(per), out, out_stride, status) == cudaSuccess
                ? SD_OK
                : SD_ECUDA;
 }
@@ -381,7 +382,8 @@ sd_status sd_paged_append_rope(const sd_kv_pages *pages, const int32_t *table, i
         if (B > 1 && (q_seq_stride < qline || out_seq_stride < qline)) return SD_EINVAL;
     }
     if (static_cast<int64_t>(width) * pages->page_rows > INT32_MAX - 128) return SD_EUNSUPPORTED;
-    if (H > 0 && q == q_out && ((M > 1 && q_row_stride != out_row_stride) || (B > 1 && q_seq_stride != out_seq_stride))) return SD_EINVAL;
+    if (H > 0 && q == q_out && ((M > 1 && q_row_stride != out_row_stride) || (B > 1 && q_seq_stride != out_seq_stride)))
+        return SD_EINVAL;
     const int64_t rows = static_cast<int64_t>(B) * M, heads = static_cast<int64_t>(H) + 2 * static_cast<int64_t>(pages->H_kv);
     const int per = heads_per_block(rows, heads, RP_THREADS / (pages->D / 8));
     const int64_t turns = (heads + per - 1) / per;
