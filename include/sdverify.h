@@ -561,8 +561,8 @@ sd_status sd_paged_attn_shared(const sd_kv_pages *pages, const int32_t *table, i
  * section, for rows that are drawn without a draft: a drafter's own tokens, the first token of a conversation, a batch of
  * samples; any top_k, and min-p).  logits fp32, row n at n * ld (any ld >= vocab).  Settings are one per row (device), each
  * pointer NULL for "off" in all rows:
- *   temperature fp32 >= 0 (NULL: 1; 0: the likeliest token), top_k int32 >= 0 (0 or >= vocab: off), top_p fp32 in (0, 1],
- *   min_p fp32 in [0, 1]; u fp32 in [0, 1) (required).
+ *   temperature fp32 >= 0 (NULL: 1; 0: the likeliest token; weights at one below 1.4427e-36 are as at that), top_k int32
+ *   >= 0 (0 or >= vocab: off), top_p fp32 in (0, 1], min_p fp32 in [0, 1]; u fp32 in [0, 1) (required).
  * With m the row's largest logit, w_c = exp((l_c - m) / T), tokens in the order of larger l first (lower index
  * among equals; -0 equals 0):
  *   the first top_k of them; of these the shortest prefix whose sum of w reaches top_p times their sum; of these the ones

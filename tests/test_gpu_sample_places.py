@@ -34,3 +34,22 @@ def test_probabilities_in_the_random_numbers_place(sdv, N):
         status_ok()
         assert torch.equal(again, token) and torch.equal(place, own)
         place.copy_(was)
+
+
+def test_the_smallest_temperatures(sdv):
+    """Temperatures above 0 and below 1.4e-36 count as that: logits of their size are weighed alike, others give the likeliest token."""
+    torch.manual_seed(3)
+    N, V = 6, 700
+    u, T = torch.rand(N, device="cuda") * 0.999, torch.tensor([1.4e-36, 1e-36, 1e-38, 1e-40, 1e-44, 1e-45], device="cuda")
+    token, prob = i32([0] * N), torch.zeros(N, device="cuda")
+    near = (torch.randn(1, V, device="cuda") * 1e-36).expand(N, V).contiguous()
+    u[:] = u[0]
+    sdv.sample(near, u, token, temperature=T, prob=prob)
+    status_ok()
+    assert torch.all(token == token[0]) and torch.all(prob == prob[0])
+    w = torch.softmax(near[0].double() / (1.4426950408889634e-36), 0)
+    assert abs(float(prob[0]) - float(w[int(token[0])])) <= 1e-5 * float(prob[0])
+    far = torch.randn(N, V, device="cuda")
+    sdv.sample(far, u, token, temperature=T, prob=prob)
+    status_ok()
+    assert torch.equal(token.long(), far.argmax(1)) and torch.all(prob == 1.0)
